@@ -286,6 +286,86 @@ gdn_status decode_impl(const gdn_shape *shape, const gdn_decode_io *io, void *st
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+gdn_status device_sms(int *sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || *sms < 1)
+    return GDN_ERR_CUDA;
+  return GDN_OK;
+}
+
+// Bytes from the first row's first element to the last row's last.
+size_t rows_bytes(long long rows, long long ld, long long cols, size_t el) {
+  return ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * el;
+}
+
+gdn_status linattn_impl(const gdn_shape *shape, const gdn_linattn_io *io, bool decode, void *stream) {
+  if (!shape || !io) return GDN_ERR_INVALID_ARG;
+  if (shape->B < 1 || shape->T < 1) return GDN_ERR_INVALID_ARG;
+  const bool packed = io->cu_seqlens != nullptr;
+  const long long tokens = packed ? (long long)shape->T : (long long)shape->B * shape->T;
+  gdn::Dims d;
+  Sizes sz;
+  gdn_status st = check_shape(shape, tokens, &d, &sz);
+  if (st != GDN_OK) return st;
+  if (!io->q || !io->k || !io->v || !io->o || !io->S_T) return GDN_ERR_INVALID_ARG;
+  if ((io->g != nullptr) == (io->log_decay != nullptr)) return GDN_ERR_INVALID_ARG;
+  if (decode && (io->S0 || packed || io->workspace)) return GDN_ERR_INVALID_ARG;
+  const long long wk = (long long)shape->Hk * gdn::kDHead, wv = (long long)shape->Hv * gdn::kDHead;
+  if (io->ldq < wk || io->ldk < wk || io->ldv < wv || io->ldo < wv) return GDN_ERR_INVALID_ARG;
+  const long long max_ld = 1LL << 32;
+  if (io->ldq > max_ld || io->ldk > max_ld || io->ldv > max_ld || io->ldo > max_ld) return GDN_ERR_UNSUPPORTED_SHAPE;
+  const void *ptrs[] = {io->q, io->k, io->v, io->o, io->S0, io->S_T};
+  const long long step = 16 / (long long)sz.io;
+  if (!all_aligned(ptrs, 6) || io->ldq % step || io->ldk % step || io->ldv % step || io->ldo % step ||
+      ((reinterpret_cast<uintptr_t>(io->g) | reinterpret_cast<uintptr_t>(io->log_decay) |
+        reinterpret_cast<uintptr_t>(io->cu_seqlens)) & 3u) != 0)
+    return GDN_ERR_ALIGNMENT;
+  Range in[7];
+  int n = 0;
+  in[n++] = range_of(io->q, rows_bytes(tokens, io->ldq, wk, sz.io));
+  in[n++] = range_of(io->k, rows_bytes(tokens, io->ldk, wk, sz.io));
+  in[n++] = range_of(io->v, rows_bytes(tokens, io->ldv, wv, sz.io));
+  in[n++] = range_of(io->g, sz.gb);
+  in[n++] = range_of(io->log_decay, sz.head);
+  in[n++] = range_of(io->cu_seqlens, ((size_t)shape->B + 1) * sizeof(int));
+  const bool in_place = decode || io->S0 == io->S_T;
+  in[n++] = range_of(io->S0, sz.S);
+  const Range ro = range_of(io->o, rows_bytes(tokens, io->ldo, wv, sz.io)), rs = range_of(io->S_T, sz.S);
+  for (int i = 0; i < n; ++i) {
+    if (overlap(ro, in[i])) return GDN_ERR_ALIAS;
+    if (!(i == n - 1 && in_place) && overlap(rs, in[i])) return GDN_ERR_ALIAS;
+  }
+  if (overlap(ro, rs)) return GDN_ERR_ALIAS;
+  // bf16 prompts run in chunks on the tensor cores; single tokens and fp32 io
+  // (fp32 arithmetic throughout) token by token.
+  const bool bf16 = shape->io_dtype == GDN_BF16;
+  const bool chunked = bf16 && !decode;
+  if (io->workspace && (reinterpret_cast<uintptr_t>(io->workspace) & 255u) != 0) return GDN_ERR_ALIGNMENT;
+  const Range rw = range_of(io->workspace, io->workspace_bytes);
+  for (int i = 0; i < n; ++i)
+    if (overlap(rw, in[i])) return GDN_ERR_ALIAS;
+  if (overlap(rw, ro) || overlap(rw, rs)) return GDN_ERR_ALIAS;
+  unsigned int *err = nullptr;
+  st = check_device(&err);
+  if (st != GDN_OK) return st;
+  int sms = 0;
+  st = device_sms(&sms);
+  if (st != GDN_OK) return st;
+  int nseg = 1;
+  if (chunked && io->workspace) {
+    nseg = gdn::linattn_segments(shape->B, shape->Hv, tokens, packed, sms);
+    if (io->workspace_bytes < gdn::linattn_ws_bytes(shape->B, shape->Hv, nseg)) return GDN_ERR_INVALID_ARG;
+  }
+  gdn::LinAttnArgs a{shape->B, shape->T,  shape->Hk, shape->Hv, d.q_scale, io->q,
+                     io->k,    io->v,     io->o,     io->ldq,   io->ldk,   io->ldv,
+                     io->ldo,  io->g,     io->log_decay, decode ? io->S_T : io->S0, io->S_T, io->cu_seqlens,
+                     nseg > 1 ? static_cast<float *>(io->workspace) : nullptr, nseg, err};
+  const cudaError_t e = chunked ? gdn::launch_linattn_chunked(a, (cudaStream_t)stream)
+                                : gdn::launch_linattn_recurrent(a, bf16, sms, (cudaStream_t)stream);
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -416,6 +496,82 @@ gdn_status gdn_linear(int M, int N, int K, const void *x, long long ldx, const v
     return GDN_ERR_CUDA;
   cudaError_t e = gdn::launch_gemm(a, sms, (cudaStream_t)stream);
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_linear_ex(int M, int N, int K, int gated, const void *x, long long ldx, const void *w,
+                         long long ldw, const void *bias, int n_out, const gdn_linear_ex_out *out, void *stream) {
+  if (M < 1 || N < 1 || K < 1 || !x || !w || !out || n_out < 1 || n_out > gdn::kGemmMaxOut)
+    return GDN_ERR_INVALID_ARG;
+  if (ldx < K || ldw < K) return GDN_ERR_INVALID_ARG;
+  if (M > (1 << 30) || N > (1 << 29) || K > (1 << 30) || ldx > (1LL << 32) || ldw > (1LL << 32))
+    return GDN_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(bias) || (ldx % 8) != 0 || (ldw % 8) != 0) return GDN_ERR_ALIGNMENT;
+  gdn::LinArgs a{};
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.x = x;
+  a.w = w;
+  a.ldx = ldx;
+  a.ldw = ldw;
+  a.bias = bias;
+  a.gated = gated != 0;
+  a.n_out = n_out;
+  const long long wrows = (long long)N * (gated ? 2 : 1);
+  const Range in[3] = {range_of(x, rows_bytes(M, ldx, K, 2)), range_of(w, rows_bytes(wrows, ldw, K, 2)),
+                       range_of(bias, (size_t)wrows * 2)};
+  Range ro[gdn::kGemmMaxOut], rr[gdn::kGemmMaxOut];
+  for (int o = 0; o < n_out; ++o) {
+    const gdn_linear_ex_out &q = out[o];
+    if (!q.ptr || q.col_begin < 0 || q.col_end <= q.col_begin || q.col_end > N || q.ld < q.col_end - q.col_begin ||
+        (q.residual && q.ldr < q.col_end - q.col_begin) || q.act < GDN_ACT_NONE || q.act > GDN_ACT_SIGMOID)
+      return GDN_ERR_INVALID_ARG;
+    for (int p = 0; p < o; ++p)
+      if (q.col_begin < out[p].col_end && out[p].col_begin < q.col_end) return GDN_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(q.ptr) | reinterpret_cast<uintptr_t>(q.residual)) & 1u) != 0)
+      return GDN_ERR_ALIGNMENT;
+    const long long cols = q.col_end - q.col_begin;
+    ro[o] = range_of(q.ptr, rows_bytes(M, q.ld, cols, 2));
+    rr[o] = range_of(q.residual, q.residual ? rows_bytes(M, q.ldr, cols, 2) : 0);
+    const bool vec = aligned16(q.ptr) && q.ld % 8 == 0 && q.col_begin % 8 == 0 &&
+                     (!q.residual || (aligned16(q.residual) && q.ldr % 8 == 0));
+    a.out[o] = gdn::LinOut{q.col_begin, q.col_end, q.ptr, q.ld, q.residual, q.ldr, q.act, vec ? 1 : 0};
+  }
+  for (int o = 0; o < n_out; ++o) {
+    for (const Range &r : in)
+      if (overlap(ro[o], r)) return GDN_ERR_ALIAS;
+    for (int p = 0; p < n_out; ++p) {
+      if (p < o && overlap(ro[o], ro[p])) return GDN_ERR_ALIAS;
+      const bool in_place = p == o && out[o].residual == out[o].ptr && out[o].ldr == out[o].ld;
+      if (!in_place && overlap(ro[o], rr[p])) return GDN_ERR_ALIAS;
+    }
+  }
+  unsigned int *err = nullptr;
+  gdn_status st = check_device(&err);
+  if (st != GDN_OK) return st;
+  a.err = err;
+  int sms = 0;
+  st = device_sms(&sms);
+  if (st != GDN_OK) return st;
+  return gdn::launch_linear_ex(a, sms, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_linattn_prefill(const gdn_shape *shape, const gdn_linattn_io *io, void *stream) {
+  return linattn_impl(shape, io, false, stream);
+}
+
+gdn_status gdn_linattn_decode(const gdn_shape *shape, const gdn_linattn_io *io, void *stream) {
+  return linattn_impl(shape, io, true, stream);
+}
+
+size_t gdn_linattn_workspace_bytes(const gdn_shape *shape, int packed) {
+  if (!shape || shape->B < 1 || shape->T < 1 || shape->io_dtype != GDN_BF16) return 0;
+  const long long tokens = packed ? (long long)shape->T : (long long)shape->B * shape->T;
+  gdn::Dims d;
+  Sizes sz;
+  int sms = 0;
+  if (check_shape(shape, tokens, &d, &sz) != GDN_OK || device_sms(&sms) != GDN_OK) return 0;
+  return gdn::linattn_ws_bytes(shape->B, shape->Hv, gdn::linattn_segments(shape->B, shape->Hv, tokens, packed != 0, sms));
 }
 
 gdn_status gdn_selftest_wait_timeout(int wait_us, void *stream) {

@@ -78,7 +78,56 @@ struct GemmArgs {
   unsigned int *err;
 };
 
+// y = act(x w^T + bias) (+ residual), or gated: act(p[:, n]) p[:, N + n] with
+// w [2N][K]; N counts output columns (gdn_linear_ex).
+struct LinOut {
+  int col_begin, col_end;
+  void *ptr;
+  long long ld;
+  const void *res;   // may be null; may be ptr itself
+  long long ldres;
+  int act;           // gdn_activation
+  int vec_ok;        // 16-byte accesses allowed at columns that are multiples of 8
+};
+struct LinArgs {
+  int M, N, K;
+  const void *x, *w;
+  long long ldx, ldw;
+  const void *bias;  // may be null: [N], gated [2N]
+  int gated, n_out;
+  LinOut out[kGemmMaxOut];
+  unsigned int *err;
+};
+
+// Linear attention with a log decay per value head: S <- e^g S + v k^T,
+// o = scale S q.  Token rows of q, k, v, o are ld* elements apart; sequence b
+// owns rows b*T .. b*T+T-1, or cu_seqlens[b] .. cu_seqlens[b+1]-1 (packed, T
+// the total).  Exactly one of g ([token][Hv]) and log_decay ([Hv]).
+struct LinAttnArgs {
+  int B, T, Hk, Hv;
+  float scale;
+  const void *q, *k, *v;
+  void *o;
+  long long ldq, ldk, ldv, ldo;
+  const float *g, *log_decay;
+  const float *S0;         // may be null (zeros); may be S_T
+  float *S_T;
+  const int *cu_seqlens;   // may be null
+  float *ws;               // may be null: the segments' states, then their decays
+  int nseg;                // segments per sequence (chunked kernel)
+  unsigned int *err;
+};
+constexpr int kLinAttnMaxSeg = 16;
+// Segments per sequence that the chunked kernel cuts a call into.
+int linattn_segments(int B, int Hv, long long tokens, bool packed, int sms);
+inline size_t linattn_ws_bytes(int B, int Hv, int nseg) {
+  return nseg < 2 ? 0 : (size_t)nseg * B * Hv * (kDHead * kDHead + 1) * sizeof(float);
+}
+
 // Each returns the cudaGetLastError() of its launch.
+cudaError_t launch_linear_ex(const LinArgs &a, int num_sms, cudaStream_t s);
+cudaError_t launch_linattn_recurrent(const LinAttnArgs &a, bool bf16, int num_sms, cudaStream_t s);
+cudaError_t launch_linattn_chunked(const LinAttnArgs &a, cudaStream_t s);  // bf16 io
 cudaError_t launch_decode(const DecodeArgs &a, bool bf16, cudaStream_t s);
 cudaError_t launch_prefill(const PrefillArgs &a, bool bf16, cudaStream_t s);          // token-serial
 cudaError_t launch_prefill_chunked(const PrefillArgs &a, bool bf16, cudaStream_t s);  // chunked WY, tcgen05

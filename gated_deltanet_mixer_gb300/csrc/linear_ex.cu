@@ -1,0 +1,534 @@
+// linear_ex.cu -- projections with their epilogue:
+//   p[t, n] = sum_k x[t, k] w[n, k] + bias[n]
+//   y[t, n] = act(p[t, n]) + residual[t, n]                     (plain)
+//   y[t, n] = act(p[t, n]) p[t, N + n] + residual[t, n]         (gated, w [2N][K])
+// bf16 in and out, fp32 accumulation on the tcgen05 tensor cores, everything
+// behind the sum in fp32 and rounded once.
+//
+// Two kernels:
+//   lin_tile_kernel   whole waves of 128 x 256 tiles: bound by the tensor
+//                     pipe.  Persistent, x tile rows on the MMA's M side, the
+//                     epilogue of a tile under the next tile's MMAs.
+//   lin_skinny_kernel fewer tiles than SMs (few tokens, or few columns): bound
+//                     by reading w once.  128 rows of w on the M side, the
+//                     tokens on the N side (16 .. 256), and the contraction
+//                     split over a cluster of CTAs, whose partial sums meet in
+//                     distributed shared memory in a fixed order: no workspace,
+//                     no second launch, the same result every time.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "gdn.h"
+#include "gdn_device.cuh"
+#include "launch.h"
+#include "tma_host.h"
+#include "umma.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace umma;
+using bf16 = __nv_bfloat16;
+
+constexpr int BK = 64;
+
+// Instruction descriptor, kind::f16 with bf16 A and B (format 1), fp32 D.
+constexpr uint32_t idesc_bf16(int M, int N) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The fast exponential and division are good to about 2^-21, far below the
+// bf16 rounding of the result.
+__device__ __forceinline__ float activate(float x, int act) {
+  switch (act) {
+    case GDN_ACT_SILU: return __fdividef(x, 1.0f + __expf(-x));
+    case GDN_ACT_GELU: return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
+    case GDN_ACT_SIGMOID: return __fdividef(1.0f, 1.0f + __expf(-x));
+    default: return x;
+  }
+}
+
+__device__ __forceinline__ void arrive(uint64_t *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// =============================================================================
+// lin_tile_kernel
+// =============================================================================
+constexpr int BM = 128, BN = 256;
+constexpr int kStages = 4;
+constexpr uint32_t kStageA = BM * BK * 2, kStageB = BN * BK * 2;
+constexpr uint32_t kStageBytes = kStageA + kStageB;
+constexpr uint32_t kBarOff = kStages * kStageBytes;
+constexpr uint32_t kTileSmem = kBarOff + 256 + 1024;
+constexpr int kTileThreads = 192;
+static_assert(kTileSmem <= 232448, "shared memory per CTA");
+
+struct Bars {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t tfull[2], tempty[2];
+  uint64_t end;
+  uint32_t tmem;
+};
+
+// Tile t of the persistent schedule: bands of 8 m tiles walk across n, so the
+// CTAs that run at once share their w tiles in L2.
+__device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int &mt, int &nt) {
+  constexpr int G = 8;
+  const int band = t / (G * tiles_n), r = t % (G * tiles_n);
+  const int rows = min(G, tiles_m - band * G);
+  mt = band * G + r % rows;
+  nt = r / rows;
+}
+
+// bias[at .. at + 31] added to v; columns from `limit` on are left alone.
+__device__ __forceinline__ void add_bias(float (&v)[32], const bf16 *bias, long long at, int limit) {
+  if (limit >= 32 && ((reinterpret_cast<uintptr_t>(bias + at) & 15u) == 0)) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(bias + at + 8 * q);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[8 * q + 2 * e] += __uint_as_float(w[e] << 16);
+        v[8 * q + 2 * e + 1] += __uint_as_float(w[e] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 32; ++q)
+      if (q < limit) v[q] += __bfloat162float(bias[at + q]);
+  }
+}
+
+// Columns col0 .. col0 + 31 of row `row`: v = p (bias added), u = the up half (gated).
+template <bool kGated>
+__device__ __forceinline__ void store_run(const LinArgs &g, long long row, int col0, float (&v)[32], const float (&u)[32]) {
+  for (int o = 0; o < g.n_out; ++o) {
+    const LinOut &out = g.out[o];
+    const int lo = max(col0, out.col_begin), hi = min(min(col0 + 32, out.col_end), g.N);
+    if (lo >= hi) continue;
+    bf16 *dst = static_cast<bf16 *>(out.ptr) + row * out.ld - out.col_begin;
+    const bf16 *res = static_cast<const bf16 *>(out.res) + row * out.ldres - out.col_begin;
+    if (lo == col0 && hi == col0 + 32 && out.vec_ok) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] = activate(v[8 * q + e], out.act);
+          if (kGated) y[e] *= u[8 * q + e];
+        }
+        if (out.res) {
+          const uint4 r = *reinterpret_cast<const uint4 *>(res + col0 + 8 * q);
+          const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[2 * e] += __uint_as_float(w[e] << 16);
+            y[2 * e + 1] += __uint_as_float(w[e] & 0xffff0000u);
+          }
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          __nv_bfloat162 t = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
+          w[e] = *reinterpret_cast<uint32_t *>(&t);
+        }
+        *reinterpret_cast<uint4 *>(dst + col0 + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 32; ++q)
+        if (col0 + q >= lo && col0 + q < hi) {
+          float y = activate(v[q], out.act);
+          if (kGated) y *= u[q];
+          if (out.res) y += __bfloat162float(res[col0 + q]);
+          dst[col0 + q] = __float2bfloat16_rn(y);
+        }
+    }
+  }
+}
+
+template <bool kGated>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    lin_tile_kernel(const LinArgs g, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w) {
+  constexpr int kCols = kGated ? BN / 2 : BN;  // output columns of a tile (gated: 128 gate rows of w, then 128 up rows)
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  Bars &B = *reinterpret_cast<Bars *>(sm + kBarOff);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + kCols - 1) / kCols;
+  const int ntiles = tiles_m * tiles_n;
+  const int nk = (g.K + BK - 1) / BK;
+  const uint32_t sbase = smem_u32(sm);
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      bar_init(&B.full[s], 1);
+      bar_init(&B.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      bar_init(&B.tfull[a], 1);
+      bar_init(&B.tempty[a], 4);
+    }
+    bar_init(&B.end, 1);
+  }
+  if (warp == 1) tmem_alloc(&B.tmem, 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = B.tmem;
+  bool ok = true;
+
+  if (warp == 0) {
+    // ---- TMA producer
+    if (lane == 0) {
+      uint32_t it = 0;
+      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+        int mt, nt;
+        tile_of(t, tiles_m, tiles_n, mt, nt);
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!bar_wait(&B.empty[s], ((it / kStages) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = sbase + s * kStageBytes;
+          bar_expect_tx(&B.full[s], kStageBytes);
+          tma_load_3d(dst, &tm_x, kb * BK, mt * BM, 0, &B.full[s]);
+          tma_load_3d(dst + kStageA, &tm_w, kb * BK, nt * kCols, 0, &B.full[s]);
+          tma_load_3d(dst + kStageA + kStageB / 2, &tm_w, kb * BK, nt * kCols + (kGated ? g.N : BN / 2), 0, &B.full[s]);
+        }
+      }
+      // Leave only when every stage issued has been consumed (bounded).
+      if (ok && it > 0)
+        for (uint32_t j = (it > kStages ? it - kStages : 0); j < it; ++j)
+          if (!bar_wait(&B.empty[j % kStages], (j / kStages) & 1)) {
+            ok = false;
+            break;
+          }
+      if (!ok) atomicOr(g.err, kErrTimeout);
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer
+    if (lane == 0) {
+      const uint32_t id = idesc_bf16(BM, BN);
+      uint32_t it = 0;
+      int local = 0;
+      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x, ++local) {
+        const int acc = local & 1;
+        if (!bar_wait(&B.tempty[acc], ((local >> 1) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc * BN);
+        for (int kb = 0; kb < nk; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!bar_wait(&B.full[s], (it / kStages) & 1)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          const uint32_t a0 = sbase + s * kStageBytes, b0 = a0 + kStageA;
+#pragma unroll
+          for (int ks = 0; ks < BK / 16; ++ks)
+            mma(d, desc_k(a0, ks, BM), desc_k(b0, ks, BN), id, (kb > 0 || ks > 0) ? 1u : 0u);
+          commit(&B.empty[s]);
+        }
+        if (!ok) break;
+        commit(&B.tfull[acc]);
+      }
+      commit(&B.end);  // every MMA issued is complete before TMEM is freed
+      if (!bar_wait(&B.end, 0)) ok = false;
+      if (!ok) atomicOr(g.err, kErrTimeout);
+    }
+  } else {
+    // ---- epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 = tile rows
+    const int quad = warp & 3;
+    const bf16 *bias = static_cast<const bf16 *>(g.bias);
+    int local = 0;
+    for (int t = blockIdx.x; t < ntiles; t += gridDim.x, ++local) {
+      int mt, nt;
+      tile_of(t, tiles_m, tiles_n, mt, nt);
+      const int acc = local & 1;
+      const bool got = bar_wait(&B.tfull[acc], (local >> 1) & 1);
+      if (!__all_sync(0xffffffffu, got)) {
+        if (lane == 0) atomicOr(g.err, kErrTimeout);
+        break;
+      }
+      fence_after();
+      const long long row = (long long)mt * BM + 32 * quad + lane;
+      const uint32_t taddr = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * BN);
+#pragma unroll 1
+      for (int c = 0; c < kCols; c += 32) {
+        float v[32], u[32];
+        tmem_ld32(taddr + c, v);  // every lane of the warp takes part
+        if (kGated) tmem_ld32(taddr + kCols + c, u);
+        const int col0 = nt * kCols + c;
+        if (row >= g.M || col0 >= g.N) continue;
+        if (bias) {
+          add_bias(v, bias, col0, g.N - col0);
+          if (kGated) add_bias(u, bias, (long long)g.N + col0, g.N - col0);
+        }
+        store_run<kGated>(g, row, col0, v, u);
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) arrive(&B.tempty[acc]);  // this warp has read its lanes: the accumulator may be refilled
+    }
+  }
+
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// =============================================================================
+// lin_skinny_kernel
+// =============================================================================
+constexpr int kRowsW = 128;  // rows of w per tile (gated: 64 gate, 64 up)
+constexpr int kSkinnyThreads = 192;
+
+template <int NT>
+struct Skinny {
+  static constexpr uint32_t kA = kRowsW * BK * 2, kB = NT * BK * 2;
+  static constexpr uint32_t kStage = kA + kB;
+  // Up to 64 tokens two CTAs share an SM (their loads and waits interleave).
+  static constexpr int kPerSm = NT <= 64 ? 2 : 1;
+  static constexpr int kRing = (int)((NT <= 64 ? 110u * 1024 : 200u * 1024) / kStage);
+  static constexpr uint32_t kBars = kRing * kStage;
+  static constexpr uint32_t kSmem = kBars + 256 + 1024;
+  static constexpr uint32_t kCols = NT < 32 ? 32 : NT;  // TMEM columns
+  static_assert(kRowsW * NT * 4 <= kBars, "the partial sums take the ring's place");
+  static_assert(kSmem * kPerSm + kPerSm * 1024 <= 233472, "shared memory per SM");
+};
+struct SkinnyBars {
+  uint64_t full[8], empty[8];
+  uint64_t done;
+  uint32_t tmem;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t saddr, uint32_t rank) {
+  float v;
+  asm volatile(
+      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}\n"
+      : "=f"(v)
+      : "r"(saddr), "r"(rank)
+      : "memory");
+  return v;
+}
+
+template <int NT, bool kGated>
+__global__ void __launch_bounds__(kSkinnyThreads)
+    lin_skinny_kernel(const LinArgs g, int split, const __grid_constant__ CUtensorMap tm_x,
+                      const __grid_constant__ CUtensorMap tm_w) {
+  using L = Skinny<NT>;
+  static_assert(L::kRing <= 8, "barriers");
+  constexpr int kOut = kGated ? kRowsW / 2 : kRowsW;  // output columns of a tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  SkinnyBars &B = *reinterpret_cast<SkinnyBars *>(sm + L::kBars);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x % split, tile = blockIdx.x / split;
+  const int tiles_n = (g.N + kOut - 1) / kOut;
+  const int n0 = (tile % tiles_n) * kOut, m0 = (tile / tiles_n) * NT;
+  const int nk = (g.K + BK - 1) / BK;
+  const int kb0 = (int)((long long)nk * rank / split), kb1 = (int)((long long)nk * (rank + 1) / split);
+  const uint32_t sbase = smem_u32(sm);
+
+  if (tid == 0) {
+    for (int s = 0; s < L::kRing; ++s) {
+      bar_init(&B.full[s], 1);
+      bar_init(&B.empty[s], 1);
+    }
+    bar_init(&B.done, 1);
+  }
+  if (warp == 1) tmem_alloc(&B.tmem, L::kCols);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = B.tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
+        const int s = it % L::kRing;
+        if (!bar_wait(&B.empty[s], ((it / L::kRing) & 1) ^ 1)) {
+          atomicOr(g.err, kErrTimeout);
+          break;
+        }
+        const uint32_t dst = sbase + s * L::kStage;
+        bar_expect_tx(&B.full[s], L::kStage);
+        tma_load_3d(dst, &tm_w, kb * BK, n0, 0, &B.full[s]);
+        tma_load_3d(dst + L::kA / 2, &tm_w, kb * BK, kGated ? g.N + n0 : n0 + kRowsW / 2, 0, &B.full[s]);
+        tma_load_3d(dst + L::kA, &tm_x, kb * BK, m0, 0, &B.full[s]);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id = idesc_bf16(kRowsW, NT);
+      for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
+        const int s = it % L::kRing;
+        if (!bar_wait(&B.full[s], (it / L::kRing) & 1)) {
+          atomicOr(g.err, kErrTimeout);
+          break;
+        }
+        fence_after();
+        const uint32_t a0 = sbase + s * L::kStage, b0 = a0 + L::kA;
+#pragma unroll
+        for (int ks = 0; ks < BK / 16; ++ks)
+          mma(tmem, desc_k(a0, ks, kRowsW), desc_k(b0, ks, NT), id, (kb > kb0 || ks > 0) ? 1u : 0u);
+        commit(&B.empty[s]);
+      }
+      commit(&B.done);
+    }
+  }
+  __syncwarp();
+  // Every load has landed and every MMA is complete (bounded): the ring is free.
+  const bool got = bar_wait(&B.done, 0);
+  if (!got && lane == 0) atomicOr(g.err, kErrTimeout);
+  __syncwarp();
+  fence_after();
+  const int rows = min(NT, g.M - m0);
+  float *part = reinterpret_cast<float *>(sm);  // [t][128]
+  if (warp >= 2) {
+    const int n = 32 * (warp & 3) + lane;
+    const uint32_t taddr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    if (NT == 16) {
+      uint32_t r[32];
+      tmem_ld32_nw(taddr, r);  // 32 columns are allocated; the upper 16 are not used
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (e < rows) part[e * kRowsW + n] = __uint_as_float(r[e]);
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < NT; c += 32) {
+        if (c >= rows) break;
+        uint32_t r[32];
+        tmem_ld32_nw(taddr + c, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (c + e < rows) part[(c + e) * kRowsW + n] = __uint_as_float(r[e]);
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    tmem_dealloc(tmem, L::kCols);
+  }
+  cluster_sync();
+  // This CTA's share of the tile: output columns n0 + rank * width .., every token.
+  const int width = kOut / split;
+  const bf16 *bias = static_cast<const bf16 *>(g.bias);
+  for (int i = tid; i < rows * width; i += kSkinnyThreads) {
+    const int t = i / width, c = rank * width + i % width, col = n0 + c;
+    if (col >= g.N) continue;
+    const uint32_t at = sbase + (uint32_t)(t * kRowsW + c) * 4;
+    float p = 0.f, u = 0.f;
+    for (int r = 0; r < split; ++r) {
+      p += ld_cluster(at, r);
+      if (kGated) u += ld_cluster(at + kOut * 4, r);
+    }
+    if (bias) {
+      p += __bfloat162float(bias[col]);
+      if (kGated) u += __bfloat162float(bias[(long long)g.N + col]);
+    }
+    for (int o = 0; o < g.n_out; ++o) {
+      const LinOut &out = g.out[o];
+      if (col < out.col_begin || col >= out.col_end) continue;
+      float y = activate(p, out.act);
+      if (kGated) y *= u;
+      const long long row = m0 + t;
+      if (out.res) y += __bfloat162float(static_cast<const bf16 *>(out.res)[row * out.ldres + col - out.col_begin]);
+      static_cast<bf16 *>(out.ptr)[row * out.ld + col - out.col_begin] = __float2bfloat16_rn(y);
+    }
+  }
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while another reads its partial sums
+}
+
+// A row-major [rows][K] bf16 matrix as a 3-d map (third extent 1) with
+// 128-byte-swizzled boxes of 64 columns x box_rows rows.
+bool encode_kmajor(CUtensorMap *m, const void *base, long long rows, long long K, long long ld, int box_rows) {
+  EncodeTiled enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)rows, 1};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)rows};
+  const cuuint32_t box[3] = {(cuuint32_t)BK, (cuuint32_t)box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kGated>
+cudaError_t launch_tile(const LinArgs &a, long long ntiles, int num_sms, cudaStream_t s) {
+  CUtensorMap tm_x, tm_w;
+  if (!encode_kmajor(&tm_x, a.x, a.M, a.K, a.ldx, BM) ||
+      !encode_kmajor(&tm_w, a.w, (long long)a.N * (kGated ? 2 : 1), a.K, a.ldw, BN / 2))
+    return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(lin_tile_kernel<kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTileSmem);
+  if (e != cudaSuccess) return e;
+  lin_tile_kernel<kGated><<<(int)(ntiles < num_sms ? ntiles : num_sms), kTileThreads, kTileSmem, s>>>(a, tm_x, tm_w);
+  return cudaGetLastError();
+}
+
+template <int NT, bool kGated>
+cudaError_t launch_skinny(const LinArgs &a, int num_sms, cudaStream_t s) {
+  using L = Skinny<NT>;
+  CUtensorMap tm_x, tm_w;
+  if (!encode_kmajor(&tm_x, a.x, a.M, a.K, a.ldx, NT) ||
+      !encode_kmajor(&tm_w, a.w, (long long)a.N * (kGated ? 2 : 1), a.K, a.ldw, kRowsW / 2))
+    return cudaErrorInvalidValue;
+  auto *kernel = lin_skinny_kernel<NT, kGated>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
+  if (e != cudaSuccess) return e;
+  constexpr int kOut = kGated ? kRowsW / 2 : kRowsW;
+  const long long tiles = (long long)((a.N + kOut - 1) / kOut) * ((a.M + NT - 1) / NT);
+  const int nk = (a.K + BK - 1) / BK;
+  // The widest split whose CTAs are all resident at once, each with a few k steps.
+  int split = 8;
+  while (split > 1 && (tiles * split > (long long)num_sms * L::kPerSm || nk < 2 * split)) split >>= 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3(kSkinnyThreads);
+  cfg.dynamicSmemBytes = L::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, split, tm_x, tm_w);
+}
+
+template <bool kGated>
+cudaError_t launch(const LinArgs &a, int num_sms, cudaStream_t s) {
+  const int cols = kGated ? BN / 2 : BN;
+  const long long ntiles = (long long)((a.M + BM - 1) / BM) * ((a.N + cols - 1) / cols);
+  if (ntiles >= num_sms) return launch_tile<kGated>(a, ntiles, num_sms, s);
+  if (a.M <= 16) return launch_skinny<16, kGated>(a, num_sms, s);
+  if (a.M <= 32) return launch_skinny<32, kGated>(a, num_sms, s);
+  if (a.M <= 64) return launch_skinny<64, kGated>(a, num_sms, s);
+  return launch_skinny<128, kGated>(a, num_sms, s);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_ex(const LinArgs &a, int num_sms, cudaStream_t s) {
+  return a.gated ? launch<true>(a, num_sms, s) : launch<false>(a, num_sms, s);
+}
+
+}  // namespace gdn

@@ -61,6 +61,20 @@ class gdn_decode_io(ctypes.Structure):
                                   "S_snap", "conv_in", "conv_out", "o")]
 
 
+class gdn_linear_ex_out(ctypes.Structure):
+    _fields_ = [("col_begin", ctypes.c_int), ("col_end", ctypes.c_int), ("ptr", vp), ("ld", ctypes.c_longlong),
+                ("act", ctypes.c_int), ("residual", vp), ("ldr", ctypes.c_longlong)]
+
+
+class gdn_linattn_io(ctypes.Structure):
+    _fields_ = [(n, vp) for n in ("q", "k", "v")] + \
+               [(n, ctypes.c_longlong) for n in ("ldq", "ldk", "ldv", "ldo")] + \
+               [(n, vp) for n in ("g", "log_decay", "S0", "o", "S_T", "cu_seqlens", "workspace")] + \
+               [("workspace_bytes", ctypes.c_size_t)]
+
+
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "sigmoid": 3}
+
 _lib = None
 
 
@@ -90,6 +104,14 @@ def lib():
         L.gdn_linear.restype = ctypes.c_int
         L.gdn_linear.argtypes = [ctypes.c_int] * 3 + [vp, ctypes.c_longlong, vp, ctypes.c_longlong, ctypes.c_int,
                                                       ctypes.POINTER(gdn_linear_out), vp]
+        L.gdn_linear_ex.restype = ctypes.c_int
+        L.gdn_linear_ex.argtypes = [ctypes.c_int] * 4 + [vp, ctypes.c_longlong, vp, ctypes.c_longlong, vp, ctypes.c_int,
+                                                         ctypes.POINTER(gdn_linear_ex_out), vp]
+        for name in ("gdn_linattn_prefill", "gdn_linattn_decode"):
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = [ctypes.POINTER(gdn_shape), ctypes.POINTER(gdn_linattn_io), vp]
+        L.gdn_linattn_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_linattn_workspace_bytes.argtypes = [ctypes.POINTER(gdn_shape), ctypes.c_int]
         L.gdn_selftest_wait_timeout.restype = ctypes.c_int
         L.gdn_selftest_wait_timeout.argtypes = [ctypes.c_int, vp]
         L.gdn_prefill_static.restype = ctypes.c_int
@@ -262,6 +284,110 @@ def gdn_linear(x, w, outs, stream=None):
                           _stream(stream))
     if st != GDN_OK:
         raise GdnError(st, "gdn_linear")
+
+
+def gdn_linear_ex(x, w, outs, *, bias=None, gated=False, stream=None):
+    """y = act(x w^T + bias) + residual for bf16 x [M, K] and w [N, K], or,
+    gated, y = act(p[:, :N]) * p[:, N:] + residual with w [2N, K] and bias
+    [2N].  ``outs`` lists (col_begin, col_end, tensor[, act[, residual]]):
+    ranges of the N output columns with their bf16 [M, >= width] tensors (row
+    strides from the tensors), act one of ACTIVATIONS (default "none"),
+    residual a tensor like the output, or the output itself (added in place)."""
+    M, K = x.shape
+    N, K2 = w.shape
+    if K2 != K:
+        raise ValueError("x and w disagree on K")
+    if gated and N % 2:
+        raise ValueError("gated: w has 2N rows")
+    N = N // 2 if gated else N
+    if bias is not None and bias.numel() != (2 * N if gated else N):
+        raise ValueError("bias has one value per row of w")
+    for t in (x, w, bias) + tuple(o[2] for o in outs) + tuple(o[4] for o in outs if len(o) > 4):
+        if t is not None and (t.dtype != torch.bfloat16 or t.stride(-1) != 1 and t.shape[-1] > 1):
+            raise TypeError("tensors are bfloat16 with contiguous rows")
+    arr = (gdn_linear_ex_out * len(outs))()
+    for e, o in zip(arr, outs):
+        res = o[4] if len(o) > 4 else None
+        if o[2].shape[0] != M or o[2].shape[1] < o[1] - o[0] or res is not None and (
+                res.shape[0] != M or res.shape[1] < o[1] - o[0]):
+            raise ValueError("an output or residual is smaller than its columns")
+        e.col_begin, e.col_end, e.ptr, e.ld = o[0], o[1], o[2].data_ptr(), _row_stride(o[2])
+        e.act = ACTIVATIONS[o[3]] if len(o) > 3 else 0
+        if res is not None:
+            e.residual, e.ldr = res.data_ptr(), _row_stride(res)
+    st = lib().gdn_linear_ex(M, N, K, 1 if gated else 0, x.data_ptr(), _row_stride(x), w.data_ptr(), _row_stride(w),
+                             _ptr(bias), len(outs), arr, _stream(stream))
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_linear_ex")
+
+
+def _row_stride(t):
+    """Elements between the rows of a 2-d tensor (one row: its width rounded up to 16 bytes or more)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), -(-t.shape[1] // 8) * 8)
+
+
+def _token_stride(t, what):
+    """Elements between consecutive token rows of [tokens, C] or [B, T, C] (batches back to back)."""
+    if t.stride(-1) != 1:
+        raise ValueError("%s: the last dimension must be contiguous" % what)
+    if t.dim() == 3:
+        B, T, C = t.shape
+        if T == 1:
+            return t.stride(0) if B > 1 else -(-C // 8) * 8
+        if B > 1 and t.stride(0) != T * t.stride(1):
+            raise ValueError("%s: sequences must follow each other at the token stride" % what)
+        return t.stride(1)
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+def _linattn(entry, q, k, v, o, S0, S_T, Hk, Hv, g, log_decay, cu_seqlens, workspace, scale, stream):
+    io_dtype = _io_code(q.dtype)
+    if not (k.dtype == v.dtype == o.dtype == q.dtype):
+        raise TypeError("q, k, v and o have one dtype")
+    D = _head_width(q.shape[-1] + k.shape[-1] + v.shape[-1], Hk, Hv)
+    if q.shape != k.shape or v.shape != o.shape or v.shape[:-1] != q.shape[:-1] or q.shape[-1] != Hk * D:
+        raise ValueError("q and k are [.., Hk * D], v and o [.., Hv * D], over the same tokens")
+    if cu_seqlens is not None:
+        if q.dim() != 2 or cu_seqlens.dtype != torch.int32:
+            raise ValueError("packed: q is [tokens, Hk * D], cu_seqlens int32 [B + 1]")
+        B, T = cu_seqlens.numel() - 1, q.shape[0]
+    else:
+        B, T = q.shape[0], q.shape[1]
+    tokens = T if cu_seqlens is not None else B * T
+    for t, n, what in ((g, tokens * Hv, "g"), (log_decay, Hv, "log_decay"), (S0, B * Hv * D * D, "S0"),
+                       (S_T, B * Hv * D * D, "S_T")):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous()):
+            raise ValueError("%s: %d contiguous float32 values are wanted" % (what, n))
+    sh = make_shape(B, T, Hk, Hv, D, io_dtype, q_scale=scale)
+    io = gdn_linattn_io(q.data_ptr(), k.data_ptr(), v.data_ptr(), _token_stride(q, "q"), _token_stride(k, "k"),
+                        _token_stride(v, "v"), _token_stride(o, "o"), _ptr(g), _ptr(log_decay), _ptr(S0), o.data_ptr(),
+                        S_T.data_ptr(), _ptr(cu_seqlens), None, 0)
+    if workspace is not None and workspace.numel():
+        io.workspace, io.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = getattr(lib(), entry)(ctypes.byref(sh), ctypes.byref(io), _stream(stream))
+    if st != GDN_OK:
+        raise GdnError(st, entry)
+
+
+def gdn_linattn_prefill(q, k, v, S0, o, S_T, *, Hk, Hv, g=None, log_decay=None, cu_seqlens=None, workspace=None,
+                        scale=0.0, stream=None):
+    """Linear attention with decay over prompts (gdn_linattn_prefill): q, k
+    [B, T, Hk*D], v and o [B, T, Hv*D] (packed: [tokens, ..] with cu_seqlens
+    int32 [B+1]), rows possibly strided; g [.., Hv] or log_decay [Hv]; S0 (or
+    None) and S_T [B, Hv, D, D]; a workspace of gdn_linattn_workspace_bytes()."""
+    _linattn("gdn_linattn_prefill", q, k, v, o, S0, S_T, Hk, Hv, g, log_decay, cu_seqlens, workspace, scale, stream)
+
+
+def gdn_linattn_decode(q, k, v, S, o, *, Hk, Hv, g=None, log_decay=None, scale=0.0, stream=None):
+    """T >= 1 new tokens per sequence from the cached state S [B, Hv, D, D],
+    updated in place (gdn_linattn_decode); q, k [B, T, Hk*D], v, o [B, T, Hv*D]."""
+    _linattn("gdn_linattn_decode", q, k, v, o, None, S, Hk, Hv, g, log_decay, None, None, scale, stream)
+
+
+def gdn_linattn_workspace_bytes(B, T, Hk, Hv, packed=False, D=128, io_dtype=None):
+    """Workspace bytes of gdn_linattn_prefill (packed: T is the total token count)."""
+    sh = make_shape(B, T, Hk, Hv, D, GDN_BF16 if io_dtype is None else io_dtype)
+    return lib().gdn_linattn_workspace_bytes(ctypes.byref(sh), 1 if packed else 0)
 
 
 def gdn_device_status(stream=None, reset=False):

@@ -63,11 +63,13 @@
 #ifndef GDN_H
 #define GDN_H
 
+#include <stddef.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 4
+#define GDN_ABI_VERSION 5
 
 typedef enum {
   GDN_OK = 0,
@@ -313,6 +315,94 @@ typedef struct {
 
 gdn_status gdn_linear(int M, int N, int K, const void *x, long long ldx, const void *w, long long ldw,
                       int n_out, const gdn_linear_out *out, void *stream);
+
+/*
+ * gdn_linear with an epilogue, for the projections around a linear-attention
+ * mixer and the gated feed-forward behind it:
+ *   p[t, n] = sum_k x[t, k] w[n, k] + bias[n]
+ *   y[t, n] = act(p[t, n]) + residual[t, n]                 t < M, n < N
+ * or, gated != 0, with w [2N][K] and bias [2N] (gate rows first, up rows after):
+ *   y[t, n] = act(p[t, n]) p[t, N + n] + residual[t, n]
+ * bf16 tensors, fp32 accumulation on the tensor cores; bias, activation,
+ * product and residual in fp32, rounded once.
+ *   x, w, ldx, ldw   as for gdn_linear
+ *   bias             16-byte aligned, or NULL
+ *   out[0 .. n_out-1], 1 <= n_out <= 4: disjoint ranges of the N output
+ *     columns; each has its own activation and, or NULL, its own residual
+ *     [M][ldr] whose column 0 is col_begin.  A residual may be exactly the
+ *     range's output (same pointer and stride: y is then added in place); it
+ *     must not otherwise overlap an output.
+ * Columns not covered by any range are computed and dropped.
+ */
+typedef enum {
+  GDN_ACT_NONE = 0,
+  GDN_ACT_SILU = 1,    /* x sigmoid(x) */
+  GDN_ACT_GELU = 2,    /* x Phi(x), Phi by erf */
+  GDN_ACT_SIGMOID = 3
+} gdn_activation;
+
+typedef struct {
+  int col_begin, col_end;
+  void *ptr;
+  long long ld;
+  int act;              /* gdn_activation */
+  const void *residual; /* or NULL */
+  long long ldr;
+} gdn_linear_ex_out;
+
+gdn_status gdn_linear_ex(int M, int N, int K, int gated, const void *x, long long ldx, const void *w,
+                         long long ldw, const void *bias, int n_out, const gdn_linear_ex_out *out, void *stream);
+
+/*
+ * Linear attention with a decay for each head ("How Qwen3.5 works" section
+ * 9.1 gives the ungated form, section 9.6 the decay):
+ *   S_t = e^{g_t} S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t
+ * per sequence and value head (value head h reads key head h / (Hv / Hk)).
+ * shape gives B, T, Hk, Hv, Dk = Dv = 128 and io_dtype; q_scale is `scale`
+ * (0 means 1/sqrt(Dk)); the eps fields are not used.
+ *   q, k [tokens][ldq], [tokens][ldk]   Hk heads of 128, io dtype
+ *   v, o [tokens][ldv], [tokens][ldo]   Hv heads of 128, io dtype
+ *        Rows may be further apart than they are wide (views of one fused
+ *        buffer): ld >= heads * 128 elements, rows 16-byte aligned.
+ *   g         [tokens][Hv] fp32 log decay per token, or NULL
+ *   log_decay [Hv] fp32 constant log decay of a head, or NULL; exactly one of
+ *        the two.  Values are <= 0 (-inf resets the state).
+ *   S0, S_T, cu_seqlens as for gdn_prefill_ex: S_T may be exactly S0; packed
+ *        sequences of any length from 0; o must not overlap any other tensor.
+ *   workspace 256-byte aligned scratch of at least
+ *        gdn_linattn_workspace_bytes(), or NULL.  With few sequences x value
+ *        heads it lets a prompt be cut into segments that run side by side.
+ *
+ * bf16 io runs in chunks of 64 tokens on the tensor cores: operands that are
+ * not bf16 already enter as sums of bf16 pieces (24 bits of what feeds the
+ * state, 16 bits of what feeds o only), the state itself is summed in fp32.
+ * Log decays below -80 act as -80 there.  q, k and v are finite: a NaN or
+ * infinity spreads over its chunk and into the state (never into another
+ * sequence).  fp32 io runs token by token in fp32.
+ */
+typedef struct {
+  const void *q, *k, *v;
+  long long ldq, ldk, ldv, ldo;
+  const float *g, *log_decay;
+  const float *S0;
+  void *o;
+  float *S_T;
+  const int *cu_seqlens;
+  void *workspace;
+  size_t workspace_bytes;
+} gdn_linattn_io;
+
+gdn_status gdn_linattn_prefill(const gdn_shape *shape, const gdn_linattn_io *io, void *stream);
+
+/* Bytes of workspace of gdn_linattn_prefill for this shape on the current
+ * device (packed: shape->T is the total token count); 0 where the call uses
+ * none or the shape is invalid. */
+size_t gdn_linattn_workspace_bytes(const gdn_shape *shape, int packed);
+
+/* shape->T >= 1 new tokens for each of B sequences from the cached state:
+ * io->S_T is the state, updated in place; io->S0, cu_seqlens and workspace
+ * are NULL.  The state is read and written once, whatever T is. */
+gdn_status gdn_linattn_decode(const gdn_shape *shape, const gdn_linattn_io *io, void *stream);
 
 /*
  * Synchronise `stream` and report device-side failures recorded since the
