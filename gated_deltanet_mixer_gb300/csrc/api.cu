@@ -1,7 +1,9 @@
 // api.cu -- the C ABI of libgdn (declared in include/gdn.h): argument checks,
 // aliasing rules, and the launch of the kernels on the caller's stream.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "gdn.h"
 #include "launch.h"
@@ -286,11 +288,31 @@ gdn_status decode_impl(const gdn_shape *shape, const gdn_decode_io *io, void *st
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-gdn_status device_sms(int *sms) {
+// What check_device finds, and the SM count, looked up once per device: the
+// smallest calls take a few microseconds, of which the look-up would be one.
+struct DeviceInfo {
+  unsigned int *err;
+  int sms;
+};
+gdn_status device_info(DeviceInfo *out) {
+  constexpr int kMax = 64;
+  static std::mutex mu;
+  static DeviceInfo info[kMax];
+  static std::atomic<bool> known[kMax];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || *sms < 1)
-    return GDN_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess) return GDN_ERR_CUDA;
+  if (dev < 0 || dev >= kMax) return GDN_ERR_CUDA;
+  if (!known[dev].load(std::memory_order_acquire)) {
+    DeviceInfo d{};
+    const gdn_status st = check_device(&d.err);
+    if (st != GDN_OK) return st;
+    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || d.sms < 1)
+      return GDN_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(mu);
+    info[dev] = d;
+    known[dev].store(true, std::memory_order_release);
+  }
+  *out = info[dev];
   return GDN_OK;
 }
 
@@ -346,23 +368,20 @@ gdn_status linattn_impl(const gdn_shape *shape, const gdn_linattn_io *io, bool d
   for (int i = 0; i < n; ++i)
     if (overlap(rw, in[i])) return GDN_ERR_ALIAS;
   if (overlap(rw, ro) || overlap(rw, rs)) return GDN_ERR_ALIAS;
-  unsigned int *err = nullptr;
-  st = check_device(&err);
+  DeviceInfo dev;
+  st = device_info(&dev);
   if (st != GDN_OK) return st;
-  int sms = 0;
-  st = device_sms(&sms);
-  if (st != GDN_OK) return st;
-  int nseg = 1;
+  gdn::LinAttnCut cut{1, 1};
   if (chunked && io->workspace) {
-    nseg = gdn::linattn_segments(shape->B, shape->Hv, tokens, packed, sms);
-    if (io->workspace_bytes < gdn::linattn_ws_bytes(shape->B, shape->Hv, nseg)) return GDN_ERR_INVALID_ARG;
+    cut = gdn::linattn_cut(shape->B, shape->Hv, tokens, dev.sms);
+    if (io->workspace_bytes < gdn::linattn_ws_bytes(shape->B, shape->Hv, cut)) return GDN_ERR_INVALID_ARG;
   }
   gdn::LinAttnArgs a{shape->B, shape->T,  shape->Hk, shape->Hv, d.q_scale, io->q,
                      io->k,    io->v,     io->o,     io->ldq,   io->ldk,   io->ldv,
                      io->ldo,  io->g,     io->log_decay, decode ? io->S_T : io->S0, io->S_T, io->cu_seqlens,
-                     nseg > 1 ? static_cast<float *>(io->workspace) : nullptr, nseg, err};
+                     cut.nseg > 1 ? static_cast<float *>(io->workspace) : nullptr, cut.nseg, cut.sub, dev.err};
   const cudaError_t e = chunked ? gdn::launch_linattn_chunked(a, (cudaStream_t)stream)
-                                : gdn::launch_linattn_recurrent(a, bf16, sms, (cudaStream_t)stream);
+                                : gdn::launch_linattn_recurrent(a, bf16, dev.sms, (cudaStream_t)stream);
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -546,14 +565,11 @@ gdn_status gdn_linear_ex(int M, int N, int K, int gated, const void *x, long lon
       if (!in_place && overlap(ro[o], rr[p])) return GDN_ERR_ALIAS;
     }
   }
-  unsigned int *err = nullptr;
-  gdn_status st = check_device(&err);
+  DeviceInfo dev;
+  const gdn_status st = device_info(&dev);
   if (st != GDN_OK) return st;
-  a.err = err;
-  int sms = 0;
-  st = device_sms(&sms);
-  if (st != GDN_OK) return st;
-  return gdn::launch_linear_ex(a, sms, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  a.err = dev.err;
+  return gdn::launch_linear_ex(a, dev.sms, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 gdn_status gdn_linattn_prefill(const gdn_shape *shape, const gdn_linattn_io *io, void *stream) {
@@ -569,9 +585,9 @@ size_t gdn_linattn_workspace_bytes(const gdn_shape *shape, int packed) {
   const long long tokens = packed ? (long long)shape->T : (long long)shape->B * shape->T;
   gdn::Dims d;
   Sizes sz;
-  int sms = 0;
-  if (check_shape(shape, tokens, &d, &sz) != GDN_OK || device_sms(&sms) != GDN_OK) return 0;
-  return gdn::linattn_ws_bytes(shape->B, shape->Hv, gdn::linattn_segments(shape->B, shape->Hv, tokens, packed != 0, sms));
+  DeviceInfo dev;
+  if (check_shape(shape, tokens, &d, &sz) != GDN_OK || device_info(&dev) != GDN_OK) return 0;
+  return gdn::linattn_ws_bytes(shape->B, shape->Hv, gdn::linattn_cut(shape->B, shape->Hv, tokens, dev.sms));
 }
 
 gdn_status gdn_selftest_wait_timeout(int wait_us, void *stream) {

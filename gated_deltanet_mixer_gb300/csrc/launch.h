@@ -114,14 +114,20 @@ struct LinAttnArgs {
   float *S_T;
   const int *cu_seqlens;   // may be null
   float *ws;               // may be null: the segments' states, then their decays
-  int nseg;                // segments per sequence (chunked kernel)
+  int nseg, sub;           // segments per sequence and parts per segment (chunked kernel)
   unsigned int *err;
 };
 constexpr int kLinAttnMaxSeg = 16;
-// Segments per sequence that the chunked kernel cuts a call into.
-int linattn_segments(int B, int Hv, long long tokens, bool packed, int sms);
-inline size_t linattn_ws_bytes(int B, int Hv, int nseg) {
-  return nseg < 2 ? 0 : (size_t)nseg * B * Hv * (kDHead * kDHead + 1) * sizeof(float);
+// How the chunked kernel cuts a call's sequences: segments side by side, and
+// parts of a segment in the launch that forms the states between them.
+struct LinAttnCut {
+  int nseg, sub;
+};
+LinAttnCut linattn_cut(int B, int Hv, long long tokens, int sms);
+// States kept between the launches: S0 and one per part but the last segment's.
+__host__ __device__ inline long long linattn_slots(int nseg, int sub) { return (long long)(nseg - 1) * sub + 1; }
+inline size_t linattn_ws_bytes(int B, int Hv, LinAttnCut c) {
+  return c.nseg < 2 ? 0 : (size_t)linattn_slots(c.nseg, c.sub) * B * Hv * (kDHead * kDHead + 1) * sizeof(float);
 }
 
 // Each returns the cudaGetLastError() of its launch.

@@ -5,22 +5,27 @@
 // recurrence S_t = e^{g_t} S_{t-1} + v_t k_t^T, o_t = S_t q_t becomes, kept
 // value-major (S[v][k]) and with tokens along the columns,
 //   O^T = e^{G_i} (S Q^T) + V^T P^T,  P_ij = e^{G_i - G_j} q_i . k_j (j <= i),
-//   S'  = e^{G_last} S + V^T (Gamma K),  Gamma_j = e^{G_last - G_j}.
+//   S'  = e^{G_last} S + (Gamma V)^T K,  Gamma_j = e^{G_last - G_j}.
 // Every exponent is <= 0.  Only S Q^T and the sum of S' carry the state: the
-// products P, V^T P^T and V^T (Gamma K) of a chunk do not wait for it.
+// products P, V^T P^T and (Gamma V)^T K of a chunk do not wait for it.
 //
 // One CTA walks the chunks of one (sequence, value head, segment):
-//   warp 16      TMA: q, k, v tiles into a 3-stage ring; the chunk's decays
-//   warp 17      issues the MMAs
-//   warps 8-11   Gamma K into shared memory; P from TMEM into shared memory
+//   warp 20      TMA: q, k, v tiles into a 4-stage ring; the chunk's decays
+//   warp 21      issues the MMAs
+//   warps 16-19  (Gamma V)^T from shared memory into TMEM (a transposing load
+//                hands each thread the words that its TMEM lanes hold)
+//   warps 8-11   P from TMEM into shared memory
 //   warps 0-7    the state, fp32 in registers: copies it to TMEM as the MMA
 //                operand, then adds the chunk's update
 //   warps 12-15  the output
 // Precision: bf16 holds 8 significant bits, so what is not bf16 already goes
-// to the MMA as a sum of bf16 pieces.  Gamma K, which feeds the carried fp32
-// state, takes three (24 bits); P and S, which feed the bf16 output only, two
-// (16 bits).  Every product starts from a zero accumulator and the state is
-// summed in fp32 registers, because an MMA truncates what it adds to.
+// to the MMA as a sum of bf16 pieces.  P and S, which feed the bf16 output
+// only, take two (16 bits).  Gamma V feeds the carried fp32 state and takes
+// four, which packed bf16 arithmetic forms without a conversion: with
+// Gamma = c0 + c1 + c2 in bf16, v c0 = fl(v c0) + fma(v, c0, -fl(v c0)) exactly,
+// v c1 likewise, and the last rest takes v c2 along (24 bits in all).  Every
+// product starts from a zero accumulator and the state is summed in fp32
+// registers, because an MMA truncates what it adds to.
 //
 // Few units (sequences x value heads) leave SMs idle, so a sequence can be cut
 // into segments: a first launch (kStateOnly) forms each segment's state from
@@ -40,36 +45,49 @@ namespace {
 using namespace umma;
 
 constexpr int kC = 64;  // tokens per chunk
-constexpr int kStages = 3;
+constexpr int kStages = 4;
 constexpr int kVecs = 8;  // chunk vectors in flight (the output warps lag the loads by less)
 constexpr float kMinLogDecay = -80.f;  // a decay below e^-80 acts as e^-80: sums of it stay finite
 
 constexpr uint32_t kTile = kC * kD * 2;             // 16 KB: 64 tokens x 128
 constexpr uint32_t kStageBytes = 3 * kTile;         // q, k, v
-constexpr uint32_t kGk = kStages * kStageBytes;     // Gamma K, three pieces
-constexpr uint32_t kP = kGk + 3 * kTile;            // P, two pieces of 8 KB
+constexpr uint32_t kP = kStages * kStageBytes;      // P, two pieces of 8 KB
 constexpr uint32_t kPTile = kC * kC * 2;
 constexpr uint32_t kShared = kP + 2 * kPTile;
 
 struct ChunkVec {
-  float G[kC];    // sums of the log decays from the chunk's first token
-  float eG[kC];   // e^G
-  float gam[kC];  // e^{G_last - G}, 0 past the sequence's end
-  float d;        // e^{G_last}
+  float G[kC];   // sums of the log2 decays from the chunk's first token
+  float eG[kC];  // e^G
+  // e^{G_last - G} of the tokens 2 i, 2 i + 1 as bf16 pairs (c0, 0) and (c1, c2)
+  // with c0 + c1 + c2 = it to 24 bits; 0 past the sequence's end
+  uint2 gam[2][kC / 2];
+  float d;       // e^{G_last}
   float pad[3];
 };
 struct Shared {
   ChunkVec vec[kVecs];
   uint64_t full[kStages], empty[kStages];
-  uint64_t qk_done, p_ready, gk_ready, su_done, ds_free, s_ready, o_done, o_free, end;
+  uint64_t qk_done, p_loaded, p_ready, gv_ready[2], su_done[2], ds_free[2], s_ready, o_done, o_free, end;
   uint32_t tmem;
 };
 constexpr uint32_t kSmem = kShared + ((sizeof(Shared) + 127) / 128) * 128 + 1024;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 
-constexpr int kThreads = 18 * 32;
-// TMEM columns (fp32, or bf16 pairs for the state operand).
-constexpr uint32_t kTDs = 0, kTSh = 128, kTSl = 192, kTO1 = 256, kTO2 = 320, kTP = 384;
+// Six warpgroups; the last one's warps 22 and 23 only take part in barriers.
+// Registers per thread: launched with 80, then split by what a group holds
+// (256 x 136 + 128 x (56 + 48 + 64 + 40) = 768 x 80).
+constexpr int kThreads = 24 * 32;
+constexpr int kRegsState = 136, kRegsP = 56, kRegsOut = 48, kRegsGv = 64, kRegsIssue = 40;
+static_assert(256 * kRegsState + 128 * (kRegsP + kRegsOut + kRegsGv + kRegsIssue) <= kThreads * 80, "register split");
+// TMEM columns (fp32, or bf16 pairs for the operands).  Two of the four pieces
+// of Gamma V take the place of P once its threads have loaded it.  The
+// state-only form has the space to double-buffer both the update and Gamma V.
+constexpr uint32_t kTDs = 0, kTSh = 128, kTSl = 192, kTO1 = 256, kTO2 = 320, kTP = 384, kTG = kTP;
+constexpr int kPieces = 4;
+template <bool kStateOnly>
+__device__ __forceinline__ uint32_t ds_col(int n) { return kStateOnly && (n & 1) ? 128u : kTDs; }
+template <bool kStateOnly>
+__device__ __forceinline__ uint32_t gv_col(int n) { return kStateOnly && (n & 1) ? 256u : kTG; }
 
 // Instruction descriptor, kind::f16 with bf16 A and B (format 1), fp32 D.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn) {
@@ -83,8 +101,47 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t *>(&t);
 }
+template <int R>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+__device__ __forceinline__ float ex2(float x) {  // 2^x to about 2^-22
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// The bf16 pair nearest to x; x keeps the rest.
+__device__ __forceinline__ uint32_t take_bf16(float2 &x) {
+  const uint32_t w = pack_bf16(x.x, x.y);
+  x = __ffma2_rn(make_float2(lo_f(w), hi_f(w)), make_float2(-1.f, -1.f), x);
+  return w;
+}
+// Packed bf16 products: rounded once, exact where the result fits.
+__device__ __forceinline__ uint32_t bf16_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// 16 consecutive 32-bit columns of this warp's 32 lanes, without the wait.
+__device__ __forceinline__ void tmem_ld16_nw(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 
 // 64 columns of 16 lanes: register 4 b + (0, 1) holds columns 8 b + 2 (lane % 4)
 // + (0, 1) of row lane / 4, registers 4 b + (2, 3) the same of row lane / 4 + 8.
@@ -101,9 +158,41 @@ __device__ __forceinline__ void tmem_ld16x64(uint32_t taddr, uint32_t (&r)[32]) 
   tmem_wait_ld();
 }
 
-// Warp-wide bounded wait: every lane looks at the barrier.
+// Four 8 x 8 bf16 matrices of shared memory, transposed: lane L gives the
+// address of row L % 8 of matrix L / 8 and gets, of each, the word
+// (rows 2 (L % 4), + 1) of column L / 4 (a: matrix 0, .. d: matrix 3).
+__device__ __forceinline__ void ldsm4t(uint32_t saddr, uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(saddr));
+}
+// 16 columns of 16 lanes: register 2 b + r holds column 4 b + lane % 4 of row lane / 4 + 8 r.
+__device__ __forceinline__ void tmem_st16x16(uint32_t taddr, const uint32_t (&w)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]));
+}
+
+// Warp-wide wait, bounded to a second; short, because it is inlined often and
+// the roles' loops together have to stay within the instruction cache.
+__device__ __forceinline__ uint32_t global_ns_lo() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, bar_wait(bar, parity));
+  bool ok = bar_try_wait(bar, parity);
+  if (!ok) {
+    const uint32_t t0 = global_ns_lo();
+#pragma unroll 1
+    do ok = bar_try_wait(bar, parity);
+    while (!ok && global_ns_lo() - t0 < 1000000000u);
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+// One arrival per warp, behind all of its lanes.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) arrive(bar);
 }
 
 // The decays of a chunk, by one warp: lane L holds tokens L and L + 32.
@@ -123,12 +212,24 @@ __device__ __forceinline__ void chunk_vec(ChunkVec &cv, float g0, float g1, int 
   float e0 = __shfl_down_sync(0xffffffffu, s0, 1), e1 = __shfl_down_sync(0xffffffffu, s1, 1);
   const float first1 = __shfl_sync(0xffffffffu, s1, 0);
   if (lane == 31) e0 = first1, e1 = 0.f;
-  cv.G[lane] = p0;
-  cv.G[lane + 32] = p1;
+  constexpr float kLog2e = 1.44269504088896341f;
+  cv.G[lane] = p0 * kLog2e;
+  cv.G[lane + 32] = p1 * kLog2e;
   cv.eG[lane] = expf(p0);
   cv.eG[lane + 32] = expf(p1);
-  cv.gam[lane] = lane < len ? expf(e0) : 0.f;
-  cv.gam[lane + 32] = lane + 32 < len ? expf(e1) : 0.f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = lane + 32 * i;
+    const float x = t < len ? expf(i ? e1 : e0) : 0.f;
+    const __nv_bfloat16 g0 = __float2bfloat16_rn(x);
+    const __nv_bfloat16 g1 = __float2bfloat16_rn(x - __bfloat162float(g0));
+    const __nv_bfloat16 g2 = __float2bfloat16_rn(x - __bfloat162float(g0) - __bfloat162float(g1));
+    __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(&cv.gam[0][t >> 1]) + (t & 1);
+    to[0] = g0;
+    to[2] = __float2bfloat16_rn(0.f);
+    to[4 * (kC / 2)] = g1;
+    to[4 * (kC / 2) + 2] = g2;
+  }
   if (lane == 0) cv.d = expf(s0);
 }
 
@@ -140,10 +241,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   Shared &B = *reinterpret_cast<Shared *>(sm + kShared);
   const uint32_t sbase = smem_u32(sm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   // ---- the work of this CTA; consecutive CTAs are the heads of one segment
-  const int launched_seg = kStateOnly ? a.nseg - 1 : a.nseg;
+  // A segment is a.sub parts of `per` chunks; the state-only launch has a CTA
+  // for each part of all segments but the last.
+  const int launched_seg = kStateOnly ? (a.nseg - 1) * a.sub : a.nseg;
   const int h = blockIdx.x % a.Hv, kh = h / (a.Hv / a.Hk);
   const int seg = (blockIdx.x / a.Hv) % launched_seg;
   int b = blockIdx.x / (a.Hv * launched_seg);
@@ -164,8 +267,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int unit = b * a.Hv + h;
   const long long units = (long long)a.B * a.Hv;
-  const int nch = (T + kC - 1) / kC, per = (nch + a.nseg - 1) / a.nseg;
-  const int c0 = min(nch, seg * per), c1 = min(nch, c0 + per);
+  const int nch = (T + kC - 1) / kC, per = (nch + a.nseg * a.sub - 1) / (a.nseg * a.sub);
+  const int len_seg = kStateOnly ? per : per * a.sub;
+  const int c0 = min(nch, seg * len_seg), c1 = min(nch, c0 + len_seg);
   const int n_chunks = c1 - c0;
   constexpr long long kState = kD * kD;
 
@@ -175,23 +279,110 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(&B.empty[s], 1);
     }
     bar_init(&B.qk_done, 1);
-    bar_init(&B.p_ready, 128);
-    bar_init(&B.gk_ready, 128);
-    bar_init(&B.su_done, 1);
-    bar_init(&B.ds_free, 256);
-    bar_init(&B.s_ready, 256);
+    bar_init(&B.p_loaded, 4);
+    bar_init(&B.p_ready, 4);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&B.gv_ready[i], 4);
+      bar_init(&B.su_done[i], 1);
+      bar_init(&B.ds_free[i], 8);
+    }
+    bar_init(&B.s_ready, 8);
     bar_init(&B.o_done, 1);
-    bar_init(&B.o_free, 128);
+    bar_init(&B.o_free, 4);
     bar_init(&B.end, 1);
   }
-  if (warp == 17) tmem_alloc(&B.tmem, 512);
+  if (warp == 21) tmem_alloc(&B.tmem, 512);
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = B.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);  // known to be the same in every lane
   bool ok = true;
 
-  if (warp == 16) {
+  // ---- Gamma V of the chunks first, first + step, ..: 32 tokens x 16 value indices of a warp's 32 at a time
+  auto gamma_v = [&](int first, int step) {
+    const int j = tid & 63, half = (tid >> 6) & 1;
+    const uint32_t jrow = (uint32_t)(half * (kTile / 2) + (j >> 3) * 1024 + (j & 7) * 128);
+    const int w = warp & 3;  // TMEM quarter: value indices 32 w .. 32 w + 31
+    const uint32_t tw = tmem + ((uint32_t)(32 * w) << 16);
+    // This lane's row of the transposing loads: token lane % 8 (+ 8), value indices 8 (4 w + lane / 8 % 2) ..
+    const uint32_t vrow = (uint32_t)((lane >> 4) * 1024 + (lane & 7) * 128);
+    const int vchunk = 4 * w + ((lane >> 3) & 1), cc = 2 * (lane & 3);
+    for (int n = first; n < n_chunks; n += step) {
+      const int s = n % kStages;
+      const ChunkVec &cv = B.vec[n % kVecs];
+      const int len = T - (c0 + n) * kC;
+      ok = warp_wait(&B.full[s], (n / kStages) & 1);
+      // the update that read these columns
+      if (kStateOnly) {
+        if (n > 1) ok = ok && warp_wait(&B.su_done[n & 1], ((n >> 1) & 1) ^ 1);
+      } else {
+        if (n > 0) ok = ok && warp_wait(&B.su_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
+      }
+      if (!ok) break;
+      fence_after();
+      if (j >= len) {  // rows past the end (another sequence's, or none) must count as 0, whatever they hold
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          *reinterpret_cast<uint4 *>(sm + s * kStageBytes + kTile + jrow + 16 * c) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(sm + s * kStageBytes + 2 * kTile + jrow + 16 * c) = make_uint4(0, 0, 0, 0);
+        }
+      }
+      const uint32_t vbase = sbase + s * kStageBytes + 2 * kTile + vrow;
+      // Two pieces at a time: the first two, then those in the columns of P.
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        if (pass == 1 && !kStateOnly) {
+          ok = warp_wait(&B.p_loaded, n & 1);
+          if (!ok) break;
+          fence_after();
+        }
+#pragma unroll 1
+        for (int jh = 0; jh < 2; ++jh) {
+          uint32_t v[2][8];
+#pragma unroll
+          for (int vh = 0; vh < 2; ++vh) {
+            const int ch = vchunk + 2 * vh;
+            const uint32_t at = vbase + (uint32_t)((ch >> 3) * (kTile / 2) + (((ch & 7) ^ (lane & 7)) << 4) + jh * 4096);
+            ldsm4t(at, v[vh][0], v[vh][1], v[vh][2], v[vh][3]);
+            ldsm4t(at + 2048, v[vh][4], v[vh][5], v[vh][6], v[vh][7]);
+          }
+          if (len < kC) {  // rows past the end are being zeroed by other threads
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int token = 32 * jh + 8 * ((i & 7) >> 1) + cc;
+              uint32_t &x = v[i >> 3][i & 7];
+              x = token + 1 < len ? x : token < len ? x & 0xffffu : 0u;
+            }
+          }
+          uint2 g[4];  // the factors of this pass: (c0, 0) or (c1, c2)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) g[e] = cv.gam[pass][16 * jh + 4 * e + (lane & 3)];
+          const uint32_t to = tw + gv_col<kStateOnly>(n) + (1 - pass) * kC + 16 * jh;
+#pragma unroll
+          for (int vh = 0; vh < 2; ++vh) {
+            uint32_t a0[8], a1[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t x = v[vh][i];
+              a1[i] = bf16_mul(x, g[i >> 1].x);
+              a0[i] = bf16_fma(x, g[i >> 1].y, bf16_fma(x, g[i >> 1].x, a1[i] ^ 0x80008000u));
+            }
+            tmem_st16x16(to + ((uint32_t)(16 * vh) << 16), a0);
+            tmem_st16x16(to + ((uint32_t)(16 * vh) << 16) + kC / 2, a1);
+          }
+        }
+      }
+      if (!ok) break;
+      tmem_wait_st();
+      fence_before();
+      fence_smem_to_async();
+      warp_arrive(&B.gv_ready[n & 1]);
+    }
+  };
+
+  if (warp >= 20) {
+    regs_dec<kRegsIssue>();
+   if (warp == 20) {
     // ---- TMA producer and the chunk vectors
     auto load_g = [&](int c, float &g0, float &g1) {
       g0 = g1 = 0.f;
@@ -235,46 +426,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Leave only when every tile issued has been consumed (bounded).
     for (int j = max(0, n - kStages); ok && j < n; ++j)
       if (!warp_wait(&B.empty[j % kStages], (j / kStages) & 1)) ok = false;
-  } else if (warp == 17) {
+   } else if (warp == 21) {
     // ---- MMA issuer (the whole warp; lane 0 issues)
     const uint32_t id_p = idesc_bf16(64, 64, 0, 0);     // Q K^T
     const uint32_t id_o1 = idesc_bf16(128, 64, 0, 0);   // S Q^T
     const uint32_t id_o2 = idesc_bf16(128, 64, 1, 0);   // V^T P^T
-    const uint32_t id_su = idesc_bf16(128, 128, 1, 1);  // V^T (Gamma K)
+    const uint32_t id_su = idesc_bf16(128, 128, 0, 1);  // (Gamma V)^T K
     auto issue_qk = [&](int s) {
       const uint32_t q = sbase + s * kStageBytes, k = q + kTile;
 #pragma unroll
-      for (int ks = 0; ks < kD / 16; ++ks) mma_w(tmem + kTP, desc_k(q, ks, kC), desc_k(k, ks, kC), id_p, ks > 0);
+      for (int kb = 0; kb < 2; ++kb)  // 64 of the 128 columns at a time
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_w(tmem + kTP, desc_k(q + kb * (kTile / 2), ks, kC), desc_k(k + kb * (kTile / 2), ks, kC), id_p, kb > 0 || ks > 0);
       commit_w(&B.qk_done);
     };
-    auto issue_su = [&](int s) {
-      const uint32_t v = sbase + s * kStageBytes + 2 * kTile;
+    auto issue_su = [&](int n) {
+      const uint32_t k = sbase + (n % kStages) * kStageBytes + kTile;
 #pragma unroll
-      for (int p = 2; p >= 0; --p)  // small pieces first
+      for (int p = 0; p < kPieces; ++p)  // small pieces first
 #pragma unroll
         for (int ks = 0; ks < kC / 16; ++ks)
-          mma_w(tmem + kTDs, desc_mn(v, ks, kC), desc_mn(sbase + kGk + p * kTile, ks, kC), id_su, p < 2 || ks > 0);
-      commit_w(&B.su_done);
+          mma_ta_w(tmem + ds_col<kStateOnly>(n), tmem + gv_col<kStateOnly>(n) + p * (kC / 2) + ks * 8, desc_mn(k, ks, kC),
+                   id_su, p > 0 || ks > 0);
+      commit_w(&B.su_done[n & 1]);
     };
     if (n_chunks > 0) {
       ok = warp_wait(&B.full[0], 0);
+      fence_after();
       if (ok && !kStateOnly) issue_qk(0);
-      if (ok) ok = warp_wait(&B.gk_ready, 0);
+      if (ok) ok = warp_wait(&B.gv_ready[0], 0);
       fence_after();
       if (ok) issue_su(0);
     }
     for (int n = 0; n < n_chunks && ok; ++n) {
       const int s = n % kStages, s1 = (n + 1) % kStages;
-      const uint32_t par = n & 1;
+      const uint32_t par = n & 1, par2 = (n >> 1) & 1;
       const bool more = n + 1 < n_chunks;
       if (!kStateOnly) {
-        ok = warp_wait(&B.p_ready, par);  // P(n) is in shared memory, its TMEM columns are free
-        if (ok && more) {
-          ok = warp_wait(&B.full[s1], ((n + 1) / kStages) & 1);
+        if (more) {  // the next P, once the update has read the Gamma V in its columns
+          ok = warp_wait(&B.full[s1], ((n + 1) / kStages) & 1) && warp_wait(&B.p_loaded, par) &&
+               warp_wait(&B.su_done[n & 1], par2);
           fence_after();
           if (ok) issue_qk(s1);
         }
-        if (ok) ok = warp_wait(&B.o_free, par ^ 1);
+        ok = ok && warp_wait(&B.p_ready, par) && warp_wait(&B.o_free, par ^ 1);
         if (!ok) break;
         fence_after();
         const uint32_t q = sbase + s * kStageBytes, v = q + 2 * kTile;
@@ -283,224 +479,224 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int ks = 0; ks < kC / 16; ++ks)
             mma_w(tmem + kTO2, desc_mn(v, ks, kC), desc_k(sbase + kP + p * kPTile, ks, kC), id_o2, p < 1 || ks > 0);
-        ok = warp_wait(&B.s_ready, par);
+        ok = ok && warp_wait(&B.s_ready, par);
         if (!ok) break;
         fence_after();
 #pragma unroll
-        for (int p = 1; p >= 0; --p)
+        for (int p = 3; p >= 0; --p) {  // the second piece's two halves, then the first's
+          const uint32_t qh = q + (p & 1) * (kTile / 2);
 #pragma unroll
-          for (int ks = 0; ks < kD / 16; ++ks)
-            mma_ta_w(tmem + kTO1, tmem + (p ? kTSl : kTSh) + ks * 8, desc_k(q, ks, kC), id_o1, p < 1 || ks > 0);
+          for (int ks = 0; ks < 4; ++ks)
+            mma_ta_w(tmem + kTO1, tmem + kTSh + p * 32 + ks * 8, desc_k(qh, ks, kC), id_o1, p < 3 || ks > 0);
+        }
         commit_w(&B.o_done);
       }
       commit_w(&B.empty[s]);  // the update of chunk n was issued before
       if (more) {
         if (kStateOnly) ok = warp_wait(&B.full[s1], ((n + 1) / kStages) & 1);
-        ok = ok && warp_wait(&B.gk_ready, par ^ 1) && warp_wait(&B.ds_free, par);
+        ok = ok && warp_wait(&B.gv_ready[(n + 1) & 1], ((n + 1) >> 1) & 1);
+        // the columns that the update goes to have been read
+        if (!kStateOnly) ok = ok && warp_wait(&B.ds_free[n & 1], par2);
+        if (kStateOnly && n > 0) ok = ok && warp_wait(&B.ds_free[(n - 1) & 1], ((n - 1) >> 1) & 1);
         fence_after();
-        if (ok) issue_su(s1);
+        if (ok) issue_su(n + 1);
       }
     }
     commit_w(&B.end);  // every MMA issued is complete before TMEM is freed
     if (!warp_wait(&B.end, 0)) ok = false;
+   }
+  } else if (warp >= 16) {
+    regs_dec<kRegsGv>();
+    gamma_v(0, kStateOnly ? 2 : 1);
   } else if (warp >= 8 && warp < 12) {
-    // ---- Gamma K and P
-    const int t = tid - 256, j = t & 63, half = t >> 6;
-    const uint32_t krow = (uint32_t)(half * (kTile / 2) + (j >> 3) * 1024 + (j & 7) * 128);
-    const int w = warp - 8;  // TMEM quarter: rows 16 w .. 16 w + 15 of P
-    const int i0 = 16 * w + (lane >> 2), cc = 2 * (lane & 3);
-    if (!kStateOnly) {  // P above the diagonal block stays zero
-      for (int blk = 2 * w + 2; blk < 8; ++blk)
-        for (int p = 0; p < 2; ++p)
-          for (int r = 0; r < 2; ++r)
-            *reinterpret_cast<uint32_t *>(sm + kP + p * kPTile + kmaj(i0 + 8 * r, 8 * blk + cc, kC)) = 0;
-    }
-    for (int n = 0; n < n_chunks; ++n) {
-      const int s = n % kStages;
-      const uint32_t par = n & 1;
-      const ChunkVec &cv = B.vec[n % kVecs];
-      ok = warp_wait(&B.full[s], (n / kStages) & 1);
-      if (ok && n > 0) ok = warp_wait(&B.su_done, par ^ 1);  // the last update has read its Gamma K
-      if (!ok) break;
-      {
-        const uint8_t *src = sm + s * kStageBytes + kTile + krow;
-        uint8_t *dst = sm + kGk + krow;
-        const float gam = cv.gam[j];
-        const bool inside = (c0 + n) * kC + j < T;
+    regs_dec<kRegsP>();
+    if (kStateOnly) {
+      gamma_v(1, 2);
+    } else {
+      // ---- P, rows 16 w .. 16 w + 15 in TMEM quarter w
+      const int w = warp - 8, i0 = 16 * w + (lane >> 2), cc = 2 * (lane & 3);
+      uint8_t *prow = sm + kP + (i0 >> 3) * 1024 + (i0 & 7) * 128 + cc * 2;
+      for (int n = 0; n < n_chunks; ++n) {
+        const uint32_t par = n & 1;
+        const ChunkVec &cv = B.vec[n % kVecs];
+        ok = warp_wait(&B.full[n % kStages], (n / kStages) & 1) && warp_wait(&B.qk_done, par);
+        if (!ok) break;
+        fence_after();
+        uint32_t r[32];
+        tmem_ld16x64(tmem + ((uint32_t)(32 * w) << 16) + kTP, r);
+        fence_before();
+        warp_arrive(&B.p_loaded);
+        const float ga = cv.G[i0], gb = cv.G[i0 + 8];
+        // r becomes the pieces: register 4 b + 2 q the first of row i0 + 8 q, the next one the second.
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint32_t at = (uint32_t)((c ^ (j & 7)) << 4);
-          const uint4 u = *reinterpret_cast<const uint4 *>(src + at);
-          const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-          uint32_t p0[4], p1[4], p2[4];
+        for (int blk = 0; blk < 8; ++blk) {
+          const int jc = 8 * blk + cc;
+          const float2 gj = *reinterpret_cast<const float2 *>(&cv.G[jc]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = inside ? lo_f(in[e]) * gam : 0.f, y = inside ? hi_f(in[e]) * gam : 0.f;
-            p0[e] = pack_bf16(x, y);
-            const float x1 = x - lo_f(p0[e]), y1 = y - hi_f(p0[e]);
-            p1[e] = pack_bf16(x1, y1);
-            p2[e] = pack_bf16(x1 - lo_f(p1[e]), y1 - hi_f(p1[e]));
+          for (int q = 0; q < 2; ++q) {
+            const float gi = q ? gb : ga;
+            const int i = i0 + 8 * q;
+            float2 x = __fmul2_rn(make_float2(__uint_as_float(r[4 * blk + 2 * q]), __uint_as_float(r[4 * blk + 2 * q + 1])),
+                                  make_float2(ex2(gi - gj.x), ex2(gi - gj.y)));
+            if (jc > i) x.x = 0.f;
+            if (jc + 1 > i) x.y = 0.f;
+            r[4 * blk + 2 * q] = take_bf16(x);
+            r[4 * blk + 2 * q + 1] = pack_bf16(x.x, x.y);
           }
-          *reinterpret_cast<uint4 *>(dst + at) = make_uint4(p0[0], p0[1], p0[2], p0[3]);
-          *reinterpret_cast<uint4 *>(dst + kTile + at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
-          *reinterpret_cast<uint4 *>(dst + 2 * kTile + at) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
         }
-        if (!inside) {  // rows past the end (another sequence's, or none): 0 x value must be 0
-          uint8_t *v = sm + s * kStageBytes + 2 * kTile + krow;
+        if (n > 0) ok = warp_wait(&B.o_done, par ^ 1);  // the last output has read its P
+        if (!ok) break;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4 *>(v + 16 * c) = make_uint4(0, 0, 0, 0);
+        for (int blk = 0; blk < 8; ++blk) {
+          uint8_t *dst = prow + ((blk ^ (i0 & 7)) << 4);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) *reinterpret_cast<uint32_t *>(dst + q * 1024 + p * kPTile) = r[4 * blk + 2 * q + p];
         }
+        fence_smem_to_async();
+        warp_arrive(&B.p_ready);
       }
-      fence_smem_to_async();
-      arrive(&B.gk_ready);
-      if (kStateOnly) continue;
-      ok = warp_wait(&B.qk_done, par);
-      if (ok && n > 0) ok = warp_wait(&B.o_done, par ^ 1);  // the last output has read its P
-      if (!ok) break;
-      fence_after();
-      uint32_t r[32];
-      tmem_ld16x64(tmem + ((uint32_t)(32 * w) << 16) + kTP, r);
-      const float ga = cv.G[i0], gb = cv.G[i0 + 8];
-#pragma unroll
-      for (int blk = 0; blk < 8; ++blk) {
-        if (blk > 2 * w + 1) break;
-        const int jc = 8 * blk + cc;
-        const float2 gj = *reinterpret_cast<const float2 *>(&cv.G[jc]);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int i = i0 + 8 * q;
-          const float gi = q ? gb : ga;
-          const float x = jc <= i ? __uint_as_float(r[4 * blk + 2 * q]) * __expf(gi - gj.x) : 0.f;
-          const float y = jc + 1 <= i ? __uint_as_float(r[4 * blk + 2 * q + 1]) * __expf(gi - gj.y) : 0.f;
-          const uint32_t p0 = pack_bf16(x, y);
-          uint8_t *dst = sm + kP + kmaj(i, jc, kC);
-          *reinterpret_cast<uint32_t *>(dst) = p0;
-          *reinterpret_cast<uint32_t *>(dst + kPTile) = pack_bf16(x - lo_f(p0), y - hi_f(p0));
-        }
-      }
-      fence_before();
-      fence_smem_to_async();
-      arrive(&B.p_ready);
     }
   } else if (warp < 8) {
+    regs_inc<kRegsState>();
     // ---- the state: row v, columns 64 half .. 64 half + 63
     const int v = 32 * (warp & 3) + lane, half = warp >> 2;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const long long at = (long long)unit * kState + v * kD + 64 * half;
-    float *dec = a.ws + a.nseg * units * kState;  // [nseg][units]
+    float *dec = a.ws + linattn_slots(a.nseg, a.sub) * units * kState;  // [slot][units]
     float S[64];
-    auto read = [&](const float *src, float mul, bool add) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float4 x = *reinterpret_cast<const float4 *>(src + 4 * i);
-        S[4 * i] = add ? fmaf(mul, S[4 * i], x.x) : x.x;
-        S[4 * i + 1] = add ? fmaf(mul, S[4 * i + 1], x.y) : x.y;
-        S[4 * i + 2] = add ? fmaf(mul, S[4 * i + 2], x.z) : x.z;
-        S[4 * i + 3] = add ? fmaf(mul, S[4 * i + 3], x.w) : x.w;
-      }
-    };
-    auto write = [&](float *dst) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        *reinterpret_cast<float4 *>(dst + 4 * i) = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
-    };
 #pragma unroll
     for (int i = 0; i < 64; ++i) S[i] = 0.f;
     if (kStateOnly) {
       // The call's S_T may be S0 itself: the second launch reads S0 from slot 0.
-      if (seg == 0 && a.S0) {
-        read(a.S0 + at, 0.f, false);
-        write(a.ws + at);
+      if (seg == 0 && a.S0)
+        for (int i = 0; i < 64; i += 4)
+          *reinterpret_cast<float4 *>(a.ws + at + i) = *reinterpret_cast<const float4 *>(a.S0 + at + i);
+    } else {
+      // S0, then the parts before this segment: S <- decay S + (their state from zero)
+      const int last = a.nseg > 1 ? seg * a.sub : 0;
+#pragma unroll 1
+      for (int m = a.S0 ? 0 : 1; m <= last; ++m) {
+        const float *src = (a.nseg > 1 ? a.ws + m * units * kState : a.S0) + at;
+        const float mul = m > 0 ? dec[m * units + unit] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) S[i] = 0.f;
+        for (int i = 0; i < 64; i += 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(src + i);
+          S[i] = fmaf(mul, S[i], x.x);
+          S[i + 1] = fmaf(mul, S[i + 1], x.y);
+          S[i + 2] = fmaf(mul, S[i + 2], x.z);
+          S[i + 3] = fmaf(mul, S[i + 3], x.w);
+        }
       }
-    } else if (a.nseg > 1) {
-      if (a.S0) read(a.ws + at, 0.f, false);
-      for (int m = 1; m <= seg; ++m) read(a.ws + m * units * kState + at, dec[m * units + unit], true);
-    } else if (a.S0) {
-      read(a.S0 + at, 0.f, false);
     }
     float dtot = 1.f;
+    uint32_t hi[32], lo[32];  // the state as two bf16 pieces
+    auto pieces = [&]() {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        float2 x = make_float2(S[2 * i], S[2 * i + 1]);
+        hi[i] = take_bf16(x);
+        lo[i] = pack_bf16(x.x, x.y);
+      }
+    };
+    if (!kStateOnly) pieces();
     for (int n = 0; n < n_chunks; ++n) {
       const uint32_t par = n & 1;
       if (!kStateOnly) {
         if (n > 0) ok = warp_wait(&B.o_done, par ^ 1);  // the last output has read its state
         if (!ok) break;
-        uint32_t hi[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) hi[i] = pack_bf16(S[2 * i], S[2 * i + 1]);
         tmem_st32w_nw(tl + kTSh + 32 * half, hi);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) hi[i] = pack_bf16(S[2 * i] - lo_f(hi[i]), S[2 * i + 1] - hi_f(hi[i]));
-        tmem_st32w_nw(tl + kTSl + 32 * half, hi);
+        tmem_st32w_nw(tl + kTSl + 32 * half, lo);
         tmem_wait_st();
         fence_before();
-        arrive(&B.s_ready);
+        warp_arrive(&B.s_ready);
       }
-      ok = warp_wait(&B.su_done, par);
+      ok = warp_wait(&B.su_done[n & 1], (n >> 1) & 1);
       if (!ok) break;
       fence_after();
       const float d = B.vec[n % kVecs].d;
       if (kStateOnly) dtot *= d;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t r[32];
-        tmem_ld32_nw(tl + kTDs + 64 * half + 32 * i, r);
+      for (int i = 0; i < 4; ++i) {
+        uint32_t r[16];
+        tmem_ld16_nw(tl + ds_col<kStateOnly>(n) + 64 * half + 16 * i, r);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) S[32 * i + e] = fmaf(d, S[32 * i + e], __uint_as_float(r[e]));
+        for (int e = 0; e < 8; ++e) {
+          const int x = 16 * i + 2 * e;
+          const float2 y = __ffma2_rn(make_float2(d, d), make_float2(S[x], S[x + 1]),
+                                      make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])));
+          S[x] = y.x;
+          S[x + 1] = y.y;
+        }
       }
       fence_before();
-      arrive(&B.ds_free);
+      warp_arrive(&B.ds_free[n & 1]);
+      if (!kStateOnly) pieces();
     }
-    if (kStateOnly) {
-      write(a.ws + (seg + 1) * units * kState + at);
-      if (tid == 0) dec[(seg + 1) * units + unit] = dtot;
-    } else if (seg == a.nseg - 1) {
-      if (in_bounds(at + 64, units * kState, a.err)) write(a.S_T + at);
+    if (kStateOnly && tid == 0) dec[(seg + 1) * units + unit] = dtot;
+    if (kStateOnly || (seg == a.nseg - 1 && in_bounds(at + 64, units * kState, a.err))) {
+      float *dst = (kStateOnly ? a.ws + (seg + 1) * units * kState : a.S_T) + at;
+#pragma unroll
+      for (int i = 0; i < 64; i += 4) *reinterpret_cast<float4 *>(dst + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
     }
-  } else if (!kStateOnly) {
-    // ---- the output: lane = value index, one column per token
+  } else {
+    regs_dec<kRegsOut>();
+   if (!kStateOnly) {
+    // ---- the output: lane = value index, one column per token.  Neighbouring
+    // lanes swap halves of a token pair, so that a lane stores two values of one
+    // token: even lanes of the pair's first token, odd lanes of its second.
     const int v = 32 * (warp & 3) + lane;
+    const bool odd = lane & 1;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + (row0 + (long long)c0 * kC) * a.ldo + h * kD + v;
-    const long long o_at = (row0 + (long long)c0 * kC) * a.ldo + h * kD + v;
     const long long o_size = ((a.cu_seqlens ? a.T : (long long)a.B * a.T) - 1) * a.ldo + (long long)a.Hv * kD;
+    long long at = (row0 + (long long)c0 * kC + odd) * a.ldo + h * kD + (v & ~1);
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o);
+    const float2 scale = make_float2(a.scale, a.scale);
     for (int n = 0; n < n_chunks; ++n) {
       ok = warp_wait(&B.o_done, n & 1);
       if (!ok) break;
       fence_after();
       const ChunkVec &cv = B.vec[n % kVecs];
-      const int len = min(kC, T - (c0 + n) * kC);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t r1[32], r2[32];
-        tmem_ld32_nw(tl + kTO1 + 32 * i, r1);
-        tmem_ld32_nw(tl + kTO2 + 32 * i, r2);
+      const int len = T - (c0 + n) * kC - odd;  // this lane's tokens are those below it
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        uint32_t r1[16], r2[16];
+        tmem_ld16_nw(tl + kTO1 + 16 * i, r1);
+        tmem_ld16_nw(tl + kTO2 + 16 * i, r2);
         tmem_wait_ld();
-        if (i == 1) {
+        if (i == 3) {
           fence_before();
-          arrive(&B.o_free);
+          warp_arrive(&B.o_free);
         }
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int tk = 32 * i + e;
-          const float y = a.scale * fmaf(cv.eG[tk], __uint_as_float(r1[e]), __uint_as_float(r2[e]));
-          const long long off = (long long)(n * kC + tk) * a.ldo;
-          if (tk < len && in_bounds(o_at + off + 1, o_size, a.err)) o[off] = __float2bfloat16_rn(y);
+        for (int e = 0; e < 16; e += 2) {
+          const float2 y = __fmul2_rn(
+              scale, __ffma2_rn(*reinterpret_cast<const float2 *>(&cv.eG[16 * i + e]),
+                                make_float2(__uint_as_float(r1[e]), __uint_as_float(r1[e + 1])),
+                                make_float2(__uint_as_float(r2[e]), __uint_as_float(r2[e + 1]))));
+          const float other = __shfl_xor_sync(0xffffffffu, odd ? y.x : y.y, 1);
+          const uint32_t w = odd ? pack_bf16(other, y.y) : pack_bf16(y.x, other);
+          if (16 * i + e < len && in_bounds(at + 2, o_size, a.err)) *reinterpret_cast<uint32_t *>(o + at) = w;
+          at += 2 * a.ldo;
         }
       }
     }
   }
+   }
   if (!ok && lane == 0) atomicOr(a.err, kErrTimeout);
 
   fence_before();
   __syncthreads();
-  if (warp == 17) {
+  if (warp == 21) {
     fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
+
+template <bool kStateOnly>
+struct ChunkTag {};
 
 // Token rows of a [rows][cols] bf16 tensor, ld elements apart: boxes of 64
 // columns x 64 rows, 128-byte swizzle (third extent 1).
@@ -518,14 +714,25 @@ bool encode_rows(CUtensorMap *m, const void *base, long long rows, long long col
 
 }  // namespace
 
-int linattn_segments(int B, int Hv, long long tokens, bool packed, int sms) {
+LinAttnCut linattn_cut(int B, int Hv, long long tokens, int sms) {
   const long long units = (long long)B * Hv;
-  // The chunks of a sequence (packed: of the average one).
-  const long long nch = packed ? (tokens / B + kC - 1) / kC : (tokens / B + kC - 1) / kC;
-  long long n = sms / units;  // one CTA per SM
+  const long long nch = (tokens / B + kC - 1) / kC;  // of a sequence (packed: of the average one)
+  long long n = sms / units;                         // one CTA per SM
   if (n > nch / 4) n = nch / 4;
   if (n > kLinAttnMaxSeg) n = kLinAttnMaxSeg;
-  return n < 2 ? 1 : (int)n;
+  if (n < 2) return {1, 1};
+  // The state-only launch has (n - 1) k parts per unit: the k whose waves of
+  // parts take the least time.
+  int best = 1;
+  long long best_waves = 0;
+  for (int k = 1; k <= 4 && n * k * 4 <= nch; ++k) {
+    const long long waves = ((n - 1) * k * units + sms - 1) / sms;
+    if (k == 1 || waves * best < best_waves * k) {
+      best = k;
+      best_waves = waves;
+    }
+  }
+  return {(int)n, best};
 }
 
 cudaError_t launch_linattn_chunked(const LinAttnArgs &a, cudaStream_t s) {
@@ -535,11 +742,11 @@ cudaError_t launch_linattn_chunked(const LinAttnArgs &a, cudaStream_t s) {
       !encode_rows(&tm_k, a.k, rows, (long long)a.Hk * kD, a.ldk) ||
       !encode_rows(&tm_v, a.v, rows, (long long)a.Hv * kD, a.ldv))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(linattn_chunked_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  cudaError_t e = allow_smem<ChunkTag<false>>(linattn_chunked_kernel<false>, kSmem);
   if (e == cudaSuccess && a.nseg > 1) {
-    e = cudaFuncSetAttribute(linattn_chunked_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    e = allow_smem<ChunkTag<true>>(linattn_chunked_kernel<true>, kSmem);
     if (e != cudaSuccess) return e;
-    linattn_chunked_kernel<true><<<(unsigned)((long long)a.B * a.Hv * (a.nseg - 1)), kThreads, kSmem, s>>>(a, tm_q, tm_k, tm_v);
+    linattn_chunked_kernel<true><<<(unsigned)((long long)a.B * a.Hv * (a.nseg - 1) * a.sub), kThreads, kSmem, s>>>(a, tm_q, tm_k, tm_v);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;

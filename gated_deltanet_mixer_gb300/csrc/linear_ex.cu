@@ -473,12 +473,17 @@ bool encode_kmajor(CUtensorMap *m, const void *base, long long rows, long long K
 }
 
 template <bool kGated>
+struct TileTag {};
+template <int NT, bool kGated>
+struct SkinnyTag {};
+
+template <bool kGated>
 cudaError_t launch_tile(const LinArgs &a, long long ntiles, int num_sms, cudaStream_t s) {
   CUtensorMap tm_x, tm_w;
   if (!encode_kmajor(&tm_x, a.x, a.M, a.K, a.ldx, BM) ||
       !encode_kmajor(&tm_w, a.w, (long long)a.N * (kGated ? 2 : 1), a.K, a.ldw, BN / 2))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(lin_tile_kernel<kGated>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTileSmem);
+  cudaError_t e = allow_smem<TileTag<kGated>>(lin_tile_kernel<kGated>, kTileSmem);
   if (e != cudaSuccess) return e;
   lin_tile_kernel<kGated><<<(int)(ntiles < num_sms ? ntiles : num_sms), kTileThreads, kTileSmem, s>>>(a, tm_x, tm_w);
   return cudaGetLastError();
@@ -492,7 +497,7 @@ cudaError_t launch_skinny(const LinArgs &a, int num_sms, cudaStream_t s) {
       !encode_kmajor(&tm_w, a.w, (long long)a.N * (kGated ? 2 : 1), a.K, a.ldw, kRowsW / 2))
     return cudaErrorInvalidValue;
   auto *kernel = lin_skinny_kernel<NT, kGated>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem);
+  cudaError_t e = allow_smem<SkinnyTag<NT, kGated>>(kernel, L::kSmem);
   if (e != cudaSuccess) return e;
   constexpr int kOut = kGated ? kRowsW / 2 : kRowsW;
   const long long tiles = (long long)((a.N + kOut - 1) / kOut) * ((a.M + NT - 1) / NT);

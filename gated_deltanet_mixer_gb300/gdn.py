@@ -297,76 +297,104 @@ def gdn_linear_ex(x, w, outs, *, bias=None, gated=False, stream=None):
     N, K2 = w.shape
     if K2 != K:
         raise ValueError("x and w disagree on K")
-    if gated and N % 2:
-        raise ValueError("gated: w has 2N rows")
-    N = N // 2 if gated else N
-    if bias is not None and bias.numel() != (2 * N if gated else N):
-        raise ValueError("bias has one value per row of w")
-    for t in (x, w, bias) + tuple(o[2] for o in outs) + tuple(o[4] for o in outs if len(o) > 4):
-        if t is not None and (t.dtype != torch.bfloat16 or t.stride(-1) != 1 and t.shape[-1] > 1):
-            raise TypeError("tensors are bfloat16 with contiguous rows")
-    arr = (gdn_linear_ex_out * len(outs))()
+    if bias is not None:
+        if bias.numel() != N or not bias.is_contiguous():
+            raise ValueError("bias has one value per row of w")
+        if bias.dtype != _BF16:
+            raise TypeError("bias must be bfloat16")
+    if gated:
+        if N % 2:
+            raise ValueError("gated: w has 2N rows")
+        N //= 2
+    n = len(outs)
+    arr = (gdn_linear_ex_out * n)()
     for e, o in zip(arr, outs):
-        res = o[4] if len(o) > 4 else None
-        if o[2].shape[0] != M or o[2].shape[1] < o[1] - o[0] or res is not None and (
-                res.shape[0] != M or res.shape[1] < o[1] - o[0]):
-            raise ValueError("an output or residual is smaller than its columns")
-        e.col_begin, e.col_end, e.ptr, e.ld = o[0], o[1], o[2].data_ptr(), _row_stride(o[2])
-        e.act = ACTIVATIONS[o[3]] if len(o) > 3 else 0
-        if res is not None:
-            e.residual, e.ldr = res.data_ptr(), _row_stride(res)
-    st = lib().gdn_linear_ex(M, N, K, 1 if gated else 0, x.data_ptr(), _row_stride(x), w.data_ptr(), _row_stride(w),
-                             _ptr(bias), len(outs), arr, _stream(stream))
+        begin, end, t = o[0], o[1], o[2]
+        e.col_begin, e.col_end, e.ptr, e.ld = begin, end, t.data_ptr(), _rows(t, M, end - begin, "output")
+        if len(o) > 3:
+            e.act = ACTIVATIONS[o[3]]
+            if len(o) > 4 and o[4] is not None:
+                e.residual, e.ldr = o[4].data_ptr(), _rows(o[4], M, end - begin, "residual")
+    st = (_lib or lib()).gdn_linear_ex(M, N, K, 1 if gated else 0, x.data_ptr(), _rows(x, M, K, "x"), w.data_ptr(),
+                                       _rows(w, 0, K, "w"), None if bias is None else bias.data_ptr(), n, arr,
+                                       _raw_stream(stream, x))
     if st != GDN_OK:
         raise GdnError(st, "gdn_linear_ex")
 
 
-def _row_stride(t):
-    """Elements between the rows of a 2-d tensor (one row: its width rounded up to 16 bytes or more)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), -(-t.shape[1] // 8) * 8)
+_BF16 = torch.bfloat16
+
+
+def _raw_stream(stream, t):
+    """The stream handle of a call on `t`'s device (the current stream if none is given)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.device.index) if t.is_cuda else None
+    return _stream(stream)
+
+
+def _rows(t, M, cols, what):
+    """Elements between the rows of a bf16 matrix of at least M rows of `cols` (one row: at least its width,
+    in whole 16 bytes)."""
+    shape = t.shape
+    if t.dtype != _BF16:
+        raise TypeError("%s must be bfloat16" % what)
+    if len(shape) != 2 or shape[0] < M or shape[1] < cols:
+        raise ValueError("%s is smaller than its columns" % what)
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError("%s: rows must be contiguous" % what)
+    return ld if shape[0] > 1 else max(ld, -(-shape[1] // 8) * 8)
 
 
 def _token_stride(t, what):
-    """Elements between consecutive token rows of [tokens, C] or [B, T, C] (batches back to back)."""
-    if t.stride(-1) != 1:
+    """Elements between consecutive token rows of [tokens, C] or [B, T, C] (sequences back to back)."""
+    st, shape = t.stride(), t.shape
+    if st[-1] != 1:
         raise ValueError("%s: the last dimension must be contiguous" % what)
-    if t.dim() == 3:
-        B, T, C = t.shape
+    if len(shape) == 3:
+        B, T = shape[0], shape[1]
         if T == 1:
-            return t.stride(0) if B > 1 else -(-C // 8) * 8
-        if B > 1 and t.stride(0) != T * t.stride(1):
+            return st[0] if B > 1 else -(-shape[2] // 8) * 8
+        if B > 1 and st[0] != T * st[1]:
             raise ValueError("%s: sequences must follow each other at the token stride" % what)
-        return t.stride(1)
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+        return st[1]
+    return st[0] if shape[0] > 1 else -(-shape[1] // 8) * 8
 
 
 def _linattn(entry, q, k, v, o, S0, S_T, Hk, Hv, g, log_decay, cu_seqlens, workspace, scale, stream):
-    io_dtype = _io_code(q.dtype)
-    if not (k.dtype == v.dtype == o.dtype == q.dtype):
+    dtype, shape, D = q.dtype, q.shape, q.shape[-1] // Hk
+    if not (k.dtype == dtype and v.dtype == dtype and o.dtype == dtype):
         raise TypeError("q, k, v and o have one dtype")
-    D = _head_width(q.shape[-1] + k.shape[-1] + v.shape[-1], Hk, Hv)
-    if q.shape != k.shape or v.shape != o.shape or v.shape[:-1] != q.shape[:-1] or q.shape[-1] != Hk * D:
+    if k.shape != shape or o.shape != v.shape or v.shape[:-1] != shape[:-1] or shape[-1] != Hk * D or v.shape[-1] != Hv * D:
         raise ValueError("q and k are [.., Hk * D], v and o [.., Hv * D], over the same tokens")
     if cu_seqlens is not None:
-        if q.dim() != 2 or cu_seqlens.dtype != torch.int32:
-            raise ValueError("packed: q is [tokens, Hk * D], cu_seqlens int32 [B + 1]")
-        B, T = cu_seqlens.numel() - 1, q.shape[0]
+        if len(shape) != 2 or cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_contiguous():
+            raise ValueError("packed: q is [tokens, Hk * D], cu_seqlens contiguous int32 [B + 1]")
+        B, T = cu_seqlens.numel() - 1, shape[0]
+        tokens = T
     else:
-        B, T = q.shape[0], q.shape[1]
-    tokens = T if cu_seqlens is not None else B * T
-    for t, n, what in ((g, tokens * Hv, "g"), (log_decay, Hv, "log_decay"), (S0, B * Hv * D * D, "S0"),
-                       (S_T, B * Hv * D * D, "S_T")):
-        if t is not None and (t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous()):
-            raise ValueError("%s: %d contiguous float32 values are wanted" % (what, n))
-    sh = make_shape(B, T, Hk, Hv, D, io_dtype, q_scale=scale)
+        B, T = shape[0], shape[1]
+        tokens = B * T
+    gate, n = (g, tokens * Hv) if g is not None else (log_decay, Hv)
+    _fp32(gate, n, "the log decays")
+    _fp32(S_T, B * Hv * D * D, "the state")
+    if S0 is not None:
+        _fp32(S0, B * Hv * D * D, "S0")
+    sh = gdn_shape(B, T, Hk, Hv, D, D, _io_code(dtype), 0.0, 0.0, scale)
     io = gdn_linattn_io(q.data_ptr(), k.data_ptr(), v.data_ptr(), _token_stride(q, "q"), _token_stride(k, "k"),
-                        _token_stride(v, "v"), _token_stride(o, "o"), _ptr(g), _ptr(log_decay), _ptr(S0), o.data_ptr(),
-                        S_T.data_ptr(), _ptr(cu_seqlens), None, 0)
+                        _token_stride(v, "v"), _token_stride(o, "o"), None if g is None else g.data_ptr(),
+                        None if log_decay is None else log_decay.data_ptr(), None if S0 is None else S0.data_ptr(),
+                        o.data_ptr(), S_T.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr())
     if workspace is not None and workspace.numel():
         io.workspace, io.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    st = getattr(lib(), entry)(ctypes.byref(sh), ctypes.byref(io), _stream(stream))
+    st = getattr(_lib or lib(), entry)(sh, io, _raw_stream(stream, q))
     if st != GDN_OK:
         raise GdnError(st, entry)
+
+
+def _fp32(t, n, what):
+    if t is None or t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s: %d contiguous float32 values are wanted" % (what, n))
 
 
 def gdn_linattn_prefill(q, k, v, S0, o, S_T, *, Hk, Hv, g=None, log_decay=None, cu_seqlens=None, workspace=None,

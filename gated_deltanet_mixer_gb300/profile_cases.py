@@ -6,6 +6,9 @@
     python -m gated_deltanet_mixer_gb300.profile_cases linear --T 2048 --K 5120 --N 16480 --calls 2
     python -m gated_deltanet_mixer_gb300.profile_cases decode_multi --B 64 --T 4 --calls 2 [--snap]
     python -m gated_deltanet_mixer_gb300.profile_cases serial --B 4 --T 1024 --Hv 32 --calls 2
+    python -m gated_deltanet_mixer_gb300.profile_cases linattn --B 4 --T 2048 --calls 2
+    python -m gated_deltanet_mixer_gb300.profile_cases linattn_decode --B 48 --T 1 --calls 2
+    python -m gated_deltanet_mixer_gb300.profile_cases linear_ex --T 64 --K 6144 --N 5120 --calls 2 [--gated]
 
 Inputs are the seeded synthetic ones of ``inputs.py``; each case is sized so
 that its working set is larger than L2 (129 MB) but only a few GB at most.
@@ -90,9 +93,40 @@ def linear(T, K, N, calls):
         gdn.gdn_linear(x, w, [(0, N, y)])
 
 
+def linattn(B, T, Hk, Hv, calls):
+    """Linear attention with decay over prompts (the chunked kernel)."""
+    t = torch.bfloat16
+    q, k = (torch.randn(B, T, Hk * 128, device="cuda", dtype=t) for _ in range(2))
+    v = torch.randn(B, T, Hv * 128, device="cuda", dtype=t)
+    g = -torch.nn.functional.softplus(-(3.0 + torch.randn(B, T, Hv, device="cuda")))
+    o, S_T = torch.empty_like(v), torch.empty(B, Hv, 128, 128, device="cuda")
+    ws = torch.empty(gdn.gdn_linattn_workspace_bytes(B, T, Hk, Hv), dtype=torch.uint8, device="cuda")
+    for _ in range(calls):
+        gdn.gdn_linattn_prefill(q, k, v, None, o, S_T, Hk=Hk, Hv=Hv, g=g, workspace=ws)
+
+
+def linattn_decode(B, T, Hk, Hv, calls):
+    t = torch.bfloat16
+    q, k = (torch.randn(B, T, Hk * 128, device="cuda", dtype=t) for _ in range(2))
+    v = torch.randn(B, T, Hv * 128, device="cuda", dtype=t)
+    S, o = torch.zeros(B, Hv, 128, 128, device="cuda"), torch.empty_like(v)
+    d = torch.full((Hv,), -0.05, device="cuda")
+    for _ in range(calls):
+        gdn.gdn_linattn_decode(q, k, v, S, o, Hk=Hk, Hv=Hv, log_decay=d)
+
+
+def linear_ex(T, K, N, calls, gated):
+    xa, wa = I.linear_problem(T, N * (2 if gated else 1), K, case=205)
+    x, w = _dev(xa, torch.bfloat16), _dev(wa, torch.bfloat16)
+    y = torch.empty(T, N, device="cuda", dtype=torch.bfloat16)
+    for _ in range(calls):
+        gdn.gdn_linear_ex(x, w, [(0, N, y, "silu")], gated=gated)
+
+
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("kernel", choices=["decode", "prefill", "linear", "decode_multi", "serial"])
+    ap.add_argument("kernel", choices=["decode", "prefill", "linear", "decode_multi", "serial", "linattn",
+                                       "linattn_decode", "linear_ex"])
     ap.add_argument("--B", type=int, default=None)
     ap.add_argument("--T", type=int, default=2048)
     ap.add_argument("--Hk", type=int, default=16)
@@ -103,6 +137,7 @@ def main():
     ap.add_argument("--form", choices=["fused", "staged", "split"], default="fused",
                     help="prefill: no workspace, the staged q^/k^ workspace, or the chunk-parallel workspace")
     ap.add_argument("--g-mu", type=float, default=3.0, help="prefill: mean of the log-decay logits")
+    ap.add_argument("--gated", action="store_true", help="linear_ex: the gated form")
     ap.add_argument("--snap", action="store_true", help="decode_multi: a state snapshot after every token")
     a = ap.parse_args()
     gdn.lib()
@@ -112,6 +147,12 @@ def main():
         linear(a.T, a.K, a.N, a.calls)
     elif a.kernel == "decode_multi":
         decode_multi(a.B or 64, a.T, a.Hk, a.Hv or 48, a.calls, a.snap)
+    elif a.kernel == "linattn":
+        linattn(a.B or 4, a.T, a.Hk, a.Hv or 32, a.calls)
+    elif a.kernel == "linattn_decode":
+        linattn_decode(a.B or 48, a.T, a.Hk, a.Hv or 48, a.calls)
+    elif a.kernel == "linear_ex":
+        linear_ex(a.T, a.K, a.N, a.calls, a.gated)
     elif a.kernel == "serial":
         serial(a.B or 4, a.T, a.Hk, a.Hv or 32, a.calls)
     else:
