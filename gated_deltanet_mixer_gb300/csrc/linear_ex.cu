@@ -9,12 +9,13 @@
 //   lin_tile_kernel   whole waves of 128 x 256 tiles: bound by the tensor
 //                     pipe.  Persistent, x tile rows on the MMA's M side, the
 //                     epilogue of a tile under the next tile's MMAs.
-//   lin_skinny_kernel fewer tiles than SMs (few tokens, or few columns): bound
-//                     by reading w once.  128 rows of w on the M side, the
-//                     tokens on the N side (16 .. 256), and the contraction
-//                     split over a cluster of CTAs, whose partial sums meet in
-//                     distributed shared memory in a fixed order: no workspace,
-//                     no second launch, the same result every time.
+//   lin_skinny_kernel fewer tiles (few tokens, or few columns): bound by
+//                     reading w once.  128 rows of w on the M side, the tokens
+//                     on the N side (16 .. 256), and the contraction split over
+//                     a cluster of CTAs, which hand each other their partial
+//                     sums through distributed shared memory and add them in a
+//                     fixed order: no workspace, no second launch, the same
+//                     result every time.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -295,19 +296,21 @@ constexpr int kSkinnyThreads = 192;
 
 template <int NT>
 struct Skinny {
+  // 64-wide k blocks per stage: two for the smallest, whose blocks are short
+  // against a wait (16 tokens, 6144 -> 5120: 14.4 us against 15.0 with one).
+  static constexpr int kSteps = NT <= 16 ? 2 : 1;
   static constexpr uint32_t kA = kRowsW * BK * 2, kB = NT * BK * 2;
-  static constexpr uint32_t kStage = kA + kB;
-  // Up to 64 tokens two CTAs share an SM (their loads and waits interleave).
-  static constexpr int kPerSm = NT <= 64 ? 2 : 1;
-  static constexpr int kRing = (int)((NT <= 64 ? 110u * 1024 : 200u * 1024) / kStage);
+  static constexpr uint32_t kBlock = kA + kB;
+  static constexpr uint32_t kStage = kSteps * kBlock;
+  static constexpr int kRing = (int)(200u * 1024 / kStage);
   static constexpr uint32_t kBars = kRing * kStage;
-  static constexpr uint32_t kSmem = kBars + 256 + 1024;
+  static constexpr uint32_t kSmem = kBars + 512 + 1024;
   static constexpr uint32_t kCols = NT < 32 ? 32 : NT;  // TMEM columns
   static_assert(kRowsW * NT * 4 <= kBars, "the partial sums take the ring's place");
-  static_assert(kSmem * kPerSm + kPerSm * 1024 <= 233472, "shared memory per SM");
+  static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 struct SkinnyBars {
-  uint64_t full[8], empty[8];
+  uint64_t full[12], empty[12];
   uint64_t done;
   uint32_t tmem;
 };
@@ -315,27 +318,98 @@ struct SkinnyBars {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t saddr, uint32_t rank) {
-  float v;
-  asm volatile(
-      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}\n"
-      : "=f"(v)
-      : "r"(saddr), "r"(rank)
-      : "memory");
-  return v;
+// The address of this CTA's `saddr` in CTA `rank` of the cluster, and a store there.
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// 8 consecutive columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Where output column `col` goes: its range's activation and its pointers, row 0.
+struct LinCol {
+  bf16 *y;
+  const bf16 *res;
+  long long ld, ldres;
+  int act;
+};
+__device__ __forceinline__ LinCol column(const LinArgs &g, int col) {
+  LinCol c{nullptr, nullptr, 0, 0, 0};
+  if (col >= g.N) return c;
+  for (int o = 0; o < g.n_out; ++o) {
+    const LinOut &out = g.out[o];
+    if (col < out.col_begin || col >= out.col_end) continue;
+    c.y = static_cast<bf16 *>(out.ptr) + (col - out.col_begin);
+    c.res = out.res ? static_cast<const bf16 *>(out.res) + (col - out.col_begin) : nullptr;
+    c.ld = out.ld;
+    c.ldres = out.ldres;
+    c.act = out.act;
+  }
+  return c;
+}
+template <int R>
+__device__ __forceinline__ void activate_run(float (&v)[R], int act) {
+  if (act == GDN_ACT_NONE) return;
+#pragma unroll
+  for (int e = 0; e < R; ++e) v[e] = activate(v[e], act);
+}
+// p (and u) of R rows, row0, row0 + step, .. of which the first `count` exist:
+// the rows are independent work, so nothing branches on one of them alone.
+template <bool kGated, int R>
+__device__ __forceinline__ void finish(const LinCol &c, long long row0, int step, int count, float (&p)[R],
+                                       const float (&u)[R]) {
+  switch (c.act) {  // outside the rows' loop
+    case GDN_ACT_SILU: activate_run(p, GDN_ACT_SILU); break;
+    case GDN_ACT_GELU: activate_run(p, GDN_ACT_GELU); break;
+    case GDN_ACT_SIGMOID: activate_run(p, GDN_ACT_SIGMOID); break;
+    default: break;
+  }
+  if (kGated) {
+#pragma unroll
+    for (int e = 0; e < R; ++e) p[e] *= u[e];
+  }
+  if (c.res) {
+    const bf16 *res = c.res + row0 * c.ldres;
+    const long long d = step * c.ldres;
+    bf16 r[R];
+#pragma unroll
+    for (int e = 0; e < R; ++e)
+      if (e < count) r[e] = res[e * d];
+#pragma unroll
+    for (int e = 0; e < R; ++e)
+      if (e < count) p[e] += __bfloat162float(r[e]);
+  }
+  bf16 *y = c.y + row0 * c.ld;
+  const long long d = step * c.ld;
+#pragma unroll
+  for (int e = 0; e < R; ++e)
+    if (e < count) y[e * d] = __float2bfloat16_rn(p[e]);
 }
 
 template <int NT, bool kGated>
-__global__ void __launch_bounds__(kSkinnyThreads)
+__global__ void __launch_bounds__(kSkinnyThreads, 1)
     lin_skinny_kernel(const LinArgs g, int split, const __grid_constant__ CUtensorMap tm_x,
                       const __grid_constant__ CUtensorMap tm_w) {
   using L = Skinny<NT>;
-  static_assert(L::kRing <= 8, "barriers");
+  static_assert(L::kRing <= 12, "barriers");
   constexpr int kOut = kGated ? kRowsW / 2 : kRowsW;  // output columns of a tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   SkinnyBars &B = *reinterpret_cast<SkinnyBars *>(sm + L::kBars);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rank = blockIdx.x % split, tile = blockIdx.x / split;
   const int tiles_n = (g.N + kOut - 1) / kOut;
   const int n0 = (tile % tiles_n) * kOut, m0 = (tile / tiles_n) * NT;
@@ -356,68 +430,84 @@ __global__ void __launch_bounds__(kSkinnyThreads)
   fence_after();
   const uint32_t tmem = B.tmem;
 
+  // The loads' and the MMAs' warps stay converged, lane 0 issuing: their operands
+  // then live in uniform registers (a lone thread issues at about half the rate).
+  bool ok = true;
+  const int nst = (kb1 - kb0 + L::kSteps - 1) / L::kSteps;
   if (warp == 0) {
-    if (lane == 0) {
-      for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
-        const int s = it % L::kRing;
-        if (!bar_wait(&B.empty[s], ((it / L::kRing) & 1) ^ 1)) {
-          atomicOr(g.err, kErrTimeout);
-          break;
-        }
-        const uint32_t dst = sbase + s * L::kStage;
-        bar_expect_tx(&B.full[s], L::kStage);
-        tma_load_3d(dst, &tm_w, kb * BK, n0, 0, &B.full[s]);
-        tma_load_3d(dst + L::kA / 2, &tm_w, kb * BK, kGated ? g.N + n0 : n0 + kRowsW / 2, 0, &B.full[s]);
-        tma_load_3d(dst + L::kA, &tm_x, kb * BK, m0, 0, &B.full[s]);
+    for (int it = 0; it < nst && ok; ++it) {
+      const int s = it % L::kRing;
+      ok = __all_sync(0xffffffffu, bar_wait(&B.empty[s], ((it / L::kRing) & 1) ^ 1));
+      if (!ok) break;
+      const int n = min(L::kSteps, kb1 - kb0 - it * L::kSteps);
+      bar_expect_tx_w(&B.full[s], n * L::kBlock);
+      for (int i = 0; i < n; ++i) {
+        const uint32_t dst = sbase + s * L::kStage + i * L::kBlock;
+        const int k = (kb0 + it * L::kSteps + i) * BK;
+        tma_load_3d_w(dst, &tm_w, k, n0, 0, &B.full[s]);
+        tma_load_3d_w(dst + L::kA / 2, &tm_w, k, kGated ? g.N + n0 : n0 + kRowsW / 2, 0, &B.full[s]);
+        tma_load_3d_w(dst + L::kA, &tm_x, k, m0, 0, &B.full[s]);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t id = idesc_bf16(kRowsW, NT);
-      for (int kb = kb0, it = 0; kb < kb1; ++kb, ++it) {
-        const int s = it % L::kRing;
-        if (!bar_wait(&B.full[s], (it / L::kRing) & 1)) {
-          atomicOr(g.err, kErrTimeout);
-          break;
-        }
-        fence_after();
-        const uint32_t a0 = sbase + s * L::kStage, b0 = a0 + L::kA;
+    const uint32_t id = idesc_bf16(kRowsW, NT), d = __shfl_sync(0xffffffffu, tmem, 0);
+    for (int it = 0; it < nst && ok; ++it) {
+      const int s = it % L::kRing;
+      ok = __all_sync(0xffffffffu, bar_wait(&B.full[s], (it / L::kRing) & 1));
+      if (!ok) break;
+      fence_after();
+      const int n = min(L::kSteps, kb1 - kb0 - it * L::kSteps);
+#pragma unroll
+      for (int i = 0; i < L::kSteps; ++i) {
+        if (i >= n) break;
+        const uint32_t a0 = sbase + s * L::kStage + i * L::kBlock, b0 = a0 + L::kA;
 #pragma unroll
         for (int ks = 0; ks < BK / 16; ++ks)
-          mma(tmem, desc_k(a0, ks, kRowsW), desc_k(b0, ks, NT), id, (kb > kb0 || ks > 0) ? 1u : 0u);
-        commit(&B.empty[s]);
+          mma_w(d, desc_k(a0, ks, kRowsW), desc_k(b0, ks, NT), id, (it > 0 || i > 0 || ks > 0) ? 1u : 0u);
       }
-      commit(&B.done);
+      commit_w(&B.empty[s]);
     }
+    commit_w(&B.done);
   }
   __syncwarp();
   // Every load has landed and every MMA is complete (bounded): the ring is free.
-  const bool got = bar_wait(&B.done, 0);
-  if (!got && lane == 0) atomicOr(g.err, kErrTimeout);
+  if (!bar_wait(&B.done, 0)) ok = false;
+  if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicOr(g.err, kErrTimeout);
   __syncwarp();
   fence_after();
   const int rows = min(NT, g.M - m0);
-  float *part = reinterpret_cast<float *>(sm);  // [t][128]
+  const bf16 *bias = static_cast<const bf16 *>(g.bias);
+  if (split > 1) cluster_sync();  // every CTA's ring is free: its first part takes the partial sums
+  // Token t is finished by CTA t % split of the cluster, in place t / split.
+  const int per = (rows + split - 1) / split;
+  float *part = reinterpret_cast<float *>(sm);  // [source CTA][place][128]
   if (warp >= 2) {
     const int n = 32 * (warp & 3) + lane;
     const uint32_t taddr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    if (NT == 16) {
-      uint32_t r[32];
-      tmem_ld32_nw(taddr, r);  // 32 columns are allocated; the upper 16 are not used
-      tmem_wait_ld();
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        if (e < rows) part[e * kRowsW + n] = __uint_as_float(r[e]);
-    } else {
+    const bool direct = split == 1 && !kGated;  // this lane already holds its column's sums
+    LinCol c{};
+    float b = 0.f;
+    if (direct) {
+      c = column(g, n0 + n);
+      if (bias && n0 + n < g.N) b = __bfloat162float(bias[n0 + n]);
+    }
+    uint32_t to = 0, at = sbase + (uint32_t)(rank * per * kRowsW + n) * 4;
 #pragma unroll 1
-      for (int c = 0; c < NT; c += 32) {
-        if (c >= rows) break;
-        uint32_t r[32];
-        tmem_ld32_nw(taddr + c, r);
-        tmem_wait_ld();
+    for (int t0 = 0; t0 < rows; t0 += 8) {
+      float v[8];
+      tmem_ld8(taddr + t0, v);
+      if (direct) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (c + e < rows) part[(c + e) * kRowsW + n] = __uint_as_float(r[e]);
+        for (int e = 0; e < 8; ++e) v[e] += b;
+        if (c.y) finish<false>(c, (long long)m0 + t0, 1, rows - t0, v, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (t0 + e < rows) st_cluster(map_rank(at, to), v[e]);
+          const bool wrap = ++to == (uint32_t)split;
+          to = wrap ? 0u : to;
+          at += wrap ? kRowsW * 4 : 0;
+        }
       }
     }
   }
@@ -427,35 +517,35 @@ __global__ void __launch_bounds__(kSkinnyThreads)
     fence_after();
     tmem_dealloc(tmem, L::kCols);
   }
-  cluster_sync();
-  // This CTA's share of the tile: output columns n0 + rank * width .., every token.
-  const int width = kOut / split;
-  const bf16 *bias = static_cast<const bf16 *>(g.bias);
-  for (int i = tid; i < rows * width; i += kSkinnyThreads) {
-    const int t = i / width, c = rank * width + i % width, col = n0 + c;
-    if (col >= g.N) continue;
-    const uint32_t at = sbase + (uint32_t)(t * kRowsW + c) * 4;
-    float p = 0.f, u = 0.f;
-    for (int r = 0; r < split; ++r) {
-      p += ld_cluster(at, r);
-      if (kGated) u += ld_cluster(at + kOut * 4, r);
-    }
-    if (bias) {
-      p += __bfloat162float(bias[col]);
-      if (kGated) u += __bfloat162float(bias[(long long)g.N + col]);
-    }
-    for (int o = 0; o < g.n_out; ++o) {
-      const LinOut &out = g.out[o];
-      if (col < out.col_begin || col >= out.col_end) continue;
-      float y = activate(p, out.act);
-      if (kGated) y *= u;
-      const long long row = m0 + t;
-      if (out.res) y += __bfloat162float(static_cast<const bf16 *>(out.res)[row * out.ldres + col - out.col_begin]);
-      static_cast<bf16 *>(out.ptr)[row * out.ld + col - out.col_begin] = __float2bfloat16_rn(y);
-    }
+  if (split == 1 && !kGated) return;
+  if (split > 1) cluster_sync();
+  // This CTA's tokens, every column of the tile: a thread keeps to one column.
+  const int mine = (rows - rank + split - 1) / split;
+  const int n = tid % kOut;
+  constexpr int kShare = kSkinnyThreads / kOut;  // 1 or 3 threads per column
+  if (tid >= kShare * kOut) return;
+  const LinCol c = column(g, n0 + n);
+  if (!c.y) return;
+  float b = 0.f, bu = 0.f;
+  if (bias) {
+    b = __bfloat162float(bias[n0 + n]);
+    if (kGated) bu = __bfloat162float(bias[(long long)g.N + n0 + n]);
   }
-  __syncwarp();
-  cluster_sync();  // no CTA leaves while another reads its partial sums
+  for (int t = 4 * (tid / kOut); t < mine; t += 4 * kShare) {
+    float p[4], u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] = b, u[e] = bu;
+    for (int r = 0; r < split; ++r) {
+      const float *src = part + (r * per + t) * kRowsW + n;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (t + e < mine) {
+          p[e] += src[e * kRowsW];
+          if (kGated) u[e] += src[e * kRowsW + kOut];
+        }
+    }
+    finish<kGated>(c, (long long)m0 + rank + (long long)t * split, split, mine - t, p, u);
+  }
 }
 
 // A row-major [rows][K] bf16 matrix as a 3-d map (third extent 1) with
@@ -502,9 +592,13 @@ cudaError_t launch_skinny(const LinArgs &a, int num_sms, cudaStream_t s) {
   constexpr int kOut = kGated ? kRowsW / 2 : kRowsW;
   const long long tiles = (long long)((a.N + kOut - 1) / kOut) * ((a.M + NT - 1) / NT);
   const int nk = (a.K + BK - 1) / BK;
-  // The widest split whose CTAs are all resident at once, each with a few k steps.
-  int split = 8;
-  while (split > 1 && (tiles * split > (long long)num_sms * L::kPerSm || nk < 2 * split)) split >>= 1;
+  // The widest split whose CTAs are all resident at once, each with some k steps
+  // and (the partial sums' space) whole tokens.
+  long long split = (long long)num_sms / tiles;
+  if (split > nk / 2) split = nk / 2;
+  if (split > 8) split = 8;
+  if (split < 1) split = 1;
+  while (split > 1 && (long long)split * ((NT + split - 1) / split) * kRowsW * 4 > L::kBars) --split;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * split));
   cfg.blockDim = dim3(kSkinnyThreads);
@@ -512,22 +606,25 @@ cudaError_t launch_skinny(const LinArgs &a, int num_sms, cudaStream_t s) {
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.x = (unsigned)split;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, split, tm_x, tm_w);
+  return cudaLaunchKernelEx(&cfg, kernel, a, (int)split, tm_x, tm_w);
 }
 
 template <bool kGated>
 cudaError_t launch(const LinArgs &a, int num_sms, cudaStream_t s) {
   const int cols = kGated ? BN / 2 : BN;
   const long long ntiles = (long long)((a.M + BM - 1) / BM) * ((a.N + cols - 1) / cols);
-  if (ntiles >= num_sms) return launch_tile<kGated>(a, ntiles, num_sms, s);
+  // Where w is read many times over and there is no SM to spare for a split
+  // contraction: the tile kernel.
+  if (a.M > 128 && 2 * ntiles > num_sms) return launch_tile<kGated>(a, ntiles, num_sms, s);
   if (a.M <= 16) return launch_skinny<16, kGated>(a, num_sms, s);
   if (a.M <= 32) return launch_skinny<32, kGated>(a, num_sms, s);
   if (a.M <= 64) return launch_skinny<64, kGated>(a, num_sms, s);
-  return launch_skinny<128, kGated>(a, num_sms, s);
+  if (a.M <= 128) return launch_skinny<128, kGated>(a, num_sms, s);
+  return launch_skinny<256, kGated>(a, num_sms, s);
 }
 
 }  // namespace
