@@ -6,12 +6,13 @@
 // independent: a warp owns kRows of them in fp32 registers, lane L holding
 // columns 4L .. 4L+3, and a CTA of 8 warps covers 8 kRows rows of one
 // (sequence, value head).  The state is read once and written once per call,
-// whatever the number of tokens.  Tokens are staged kTB at a time: while a
-// block is worked on, the next one's q, k, v and decays are on their way into
-// registers, then into the other half of a double buffer in shared memory.
+// whatever the number of tokens.  Tokens are copied kTB at a time into a ring in
+// shared memory, three blocks ahead of the one worked on.
 //
 // One token is bound by the state's traffic (128 KB per unit against 128 x 128
-// fused multiply-adds); long runs by the fp32 multiply-adds.
+// fused multiply-adds); long runs by the latency of a token's loads and sums.
+#include <type_traits>
+
 #include "gdn_device.cuh"
 #include "launch.h"
 
@@ -20,7 +21,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTB = 8;  // tokens staged at a time: one 4-wide load of q and of k per thread
+constexpr int kTB = 8;    // tokens per block
+constexpr int kRing = 4;  // blocks in the ring
 
 // Sums part[0 .. R) over the warp; lane L returns the total of part[L / (32 / R)].
 template <int R>
@@ -44,6 +46,11 @@ __device__ __forceinline__ float reduce_rows(float (&part)[R], int lane) {
   return part[0];
 }
 
+__device__ __forceinline__ void copy16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+
 __device__ __forceinline__ float4 decayed(float4 s, float a, float v, float4 k) {
   const float2 x = __ffma2_rn(make_float2(a, a), make_float2(s.x, s.y),
                               __fmul2_rn(make_float2(v, v), make_float2(k.x, k.y)));
@@ -52,13 +59,13 @@ __device__ __forceinline__ float4 decayed(float4 s, float a, float v, float4 k) 
   return make_float4(x.x, x.y, y.x, y.y);
 }
 
-template <typename IO, int kRows>
+// kGroup: tokens whose sums are reduced together.
+template <typename IO, int kRows, int kGroup>
 __global__ void __launch_bounds__(kThreads) linattn_recurrent_kernel(LinAttnArgs a) {
   constexpr int kSplit = kD / (kWarps * kRows);  // CTAs per unit
   constexpr int kCtaRows = kWarps * kRows;
-  __shared__ __align__(16) float s_q[2][kTB][kD], s_k[2][kTB][kD];
-  __shared__ __align__(16) float s_v[2][kTB][kCtaRows];
-  __shared__ float s_a[2][kTB];
+  __shared__ __align__(16) IO s_q[kRing][kTB][kD], s_k[kRing][kTB][kD], s_v[kRing][kTB][kCtaRows];
+  __shared__ float s_a[kRing][kTB];  // e^g
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int unit = blockIdx.x / kSplit, part = blockIdx.x % kSplit;
   const int b = unit / a.Hv, h = unit % a.Hv, kh = h / (a.Hv / a.Hk);
@@ -79,64 +86,68 @@ __global__ void __launch_bounds__(kThreads) linattn_recurrent_kernel(LinAttnArgs
   const long long total_rows = a.cu_seqlens ? a.T : (long long)a.B * a.T;
   const int r0 = part * kCtaRows + warp * kRows;  // this warp's first state row
 
-  // This thread's share of a block's staging: token tb, columns c4 .. c4 + 3 of q and k.
-  const int tb = tid / (kD / 4), c4 = 4 * (tid % (kD / 4));
-  constexpr int kVLoads = kTB * kCtaRows / 4;  // 4-wide loads of v (at most one per thread)
-  static_assert(kVLoads <= kThreads, "v staging");
-  const int vb = tid / (kCtaRows / 4), v4 = 4 * (tid % (kCtaRows / 4));
+  constexpr int kPiece = 16 / sizeof(IO);  // values per 16-byte copy
   const IO *q = static_cast<const IO *>(a.q) + row0 * a.ldq + kh * kD;
   const IO *k = static_cast<const IO *>(a.k) + row0 * a.ldk + kh * kD;
   const IO *v = static_cast<const IO *>(a.v) + row0 * a.ldv + h * kD + part * kCtaRows;
-  float4 nq, nk, nv;
-  float na = 0.f;
-  auto fetch = [&](int t0) {
-    if (t0 + tb < T) {
-      nq = ld_io4(q + (t0 + tb) * a.ldq + c4);
-      nk = ld_io4(k + (t0 + tb) * a.ldk + c4);
+  auto fetch = [&](int block) {  // copies block `block` into its place in the ring
+    const int t0 = block * kTB, slot = block % kRing;
+    constexpr int kWide = kD / kPiece, kNarrow = kCtaRows / kPiece;  // copies per row of q, k; of v
+    const int t = tid / kWide, c = tid % kWide * kPiece;
+    if (t < kTB && t0 + t < T) {
+      copy16(&s_q[slot][t][c], q + (t0 + t) * a.ldq + c);
+      copy16(&s_k[slot][t][c], k + (t0 + t) * a.ldk + c);
     }
-    if (tid < kVLoads && t0 + vb < T) nv = ld_io4(v + (t0 + vb) * a.ldv + v4);
-    if (tid < kTB && t0 + tid < T) na = expf(a.g ? a.g[(row0 + t0 + tid) * a.Hv + h] : a.log_decay[h]);
+    const int tv = tid / kNarrow, cv = tid % kNarrow * kPiece;
+    if (tv < kTB && t0 + tv < T) copy16(&s_v[slot][tv][cv], v + (t0 + tv) * a.ldv + cv);
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto stage = [&](int buf) {
-    *reinterpret_cast<float4 *>(&s_q[buf][tb][c4]) = nq;
-    *reinterpret_cast<float4 *>(&s_k[buf][tb][c4]) = nk;
-    if (tid < kVLoads) *reinterpret_cast<float4 *>(&s_v[buf][vb][v4]) = nv;
-    if (tid < kTB) s_a[buf][tid] = na;
-  };
-  nq = nk = nv = make_float4(0.f, 0.f, 0.f, 0.f);
-  fetch(0);
+  static_assert(kTB * kD / kPiece <= kThreads, "one copy of q and of k per thread");
+  auto decay = [&](int t) { return a.g ? a.g[(row0 + t) * a.Hv + h] : a.log_decay[h]; };
+  for (int b = 0; b < kRing - 1; ++b) fetch(b);
+  if (tid < kTB * (kRing - 1) && tid < T) s_a[tid / kTB][tid % kTB] = expf(decay(tid));
   const long long s_at = ((long long)unit * kD + r0) * kD + 4 * lane;
   float4 S[kRows];
 #pragma unroll
   for (int r = 0; r < kRows; ++r)
     S[r] = a.S0 ? ld_stream(a.S0 + s_at + r * kD) : make_float4(0.f, 0.f, 0.f, 0.f);
-  stage(0);
-  __syncthreads();
   IO *o = static_cast<IO *>(a.o) + row0 * a.ldo + h * kD + r0;
   const long long o_size = (total_rows - 1) * a.ldo + (long long)a.Hv * kD;
-  for (int t0 = 0, buf = 0; t0 < T; t0 += kTB, buf ^= 1) {
-    if (t0 + kTB < T) fetch(t0 + kTB);
-    const int n = min(kTB, T - t0);
-    for (int t = 0; t < n; ++t) {
-      const float al = s_a[buf][t];
-      const float4 kv = *reinterpret_cast<const float4 *>(&s_k[buf][t][4 * lane]);
-      const float4 qv = *reinterpret_cast<const float4 *>(&s_q[buf][t][4 * lane]);
-      float p[kRows];
+  // N tokens from `t` on: their sums over the columns are reduced together, so
+  // that the shuffles of one do not hold up the next one's update.
+  auto tokens = [&](auto count, int buf, int t0, int t) {
+    constexpr int N = decltype(count)::value;
+    float p[N * kRows];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float al = s_a[buf][t + i];
+      const float4 kv = ld_io4(&s_k[buf][t + i][4 * lane]);
+      const float4 qv = ld_io4(&s_q[buf][t + i][4 * lane]);
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
-        S[r] = decayed(S[r], al, s_v[buf][t][warp * kRows + r], kv);
-        p[r] = dot4(S[r], qv);
+        S[r] = decayed(S[r], al, ld_io(&s_v[buf][t + i][warp * kRows + r]), kv);
+        p[i * kRows + r] = dot4(S[r], qv);
       }
-      const float sum = reduce_rows<kRows>(p, lane);
-      constexpr int kPer = 32 / kRows;  // lanes per row
-      const int r = lane / kPer;
-      const long long at = (long long)(t0 + t) * a.ldo + r;
-      if (lane % kPer == 0 && in_bounds(row0 * a.ldo + h * kD + r0 + at + 1, o_size, a.err)) st_io(o + at, sum * a.scale);
     }
-    if (t0 + kTB < T) {
-      stage(buf ^ 1);
-      __syncthreads();
-    }
+    const float sum = reduce_rows<N * kRows>(p, lane);
+    constexpr int kPer = 32 / (N * kRows);  // lanes per sum
+    const int i = lane / kPer / kRows, r = lane / kPer % kRows;
+    const long long at = (long long)(t0 + t + i) * a.ldo + r;
+    if (lane % kPer == 0 && in_bounds(row0 * a.ldo + h * kD + r0 + at + 1, o_size, a.err)) st_io(o + at, sum * a.scale);
+  };
+  for (int t0 = 0, block = 0; t0 < T; t0 += kTB, ++block) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");  // this block has landed
+    __syncthreads();  // for every thread; and the block before this one is done with
+    fetch(block + kRing - 1);
+    const int next = t0 + (kRing - 1) * kTB + tid;
+    float na = 0.f;
+    if (tid < kTB && next < T) na = decay(next);  // used after this block's work
+    const int n = min(kTB, T - t0), buf = block % kRing;
+    int t = 0;
+    if (kGroup > 1)
+      for (; t + kGroup <= n; t += kGroup) tokens(std::integral_constant<int, kGroup>(), buf, t0, t);
+    for (; t < n; ++t) tokens(std::integral_constant<int, 1>(), buf, t0, t);
+    if (tid < kTB && next < T) s_a[(block + kRing - 1) % kRing][tid] = expf(na);
   }
   const long long s_size = (long long)a.B * a.Hv * kD * kD;
 #pragma unroll
@@ -146,20 +157,25 @@ __global__ void __launch_bounds__(kThreads) linattn_recurrent_kernel(LinAttnArgs
 
 template <typename IO, int kRows>
 void launch(const LinAttnArgs &a, cudaStream_t s) {
-  const long long units = (long long)a.B * a.Hv;
-  linattn_recurrent_kernel<IO, kRows><<<(unsigned)(units * (kD / (kWarps * kRows))), kThreads, 0, s>>>(a);
+  const unsigned grid = (unsigned)((long long)a.B * a.Hv * (kD / (kWarps * kRows)));
+  // A few tokens are bound by the state's traffic: no groups, and the registers
+  // of more CTAs per SM instead (64 x 48 heads, 4 tokens: 76 us, in groups 81; 8
+  // tokens: 101 us, in groups 99).
+  if (a.T < 8)
+    linattn_recurrent_kernel<IO, kRows, 1><<<grid, kThreads, 0, s>>>(a);
+  else
+    linattn_recurrent_kernel<IO, kRows, 4><<<grid, kThreads, 0, s>>>(a);
 }
 
 template <typename IO>
 void launch_rows(const LinAttnArgs &a, int num_sms, cudaStream_t s) {
-  // Few units: the rows of a unit over more CTAs, so that every SM has one.
+  // Few units: the rows of a unit over more CTAs.  (1 x 16 heads, one token: 2.5
+  // us with 2 rows per warp, 2.8 with 4, 3.0 with 8; 64 x 48 heads: 71, 60, 61 us.)
   const long long units = (long long)a.B * a.Hv;
   if (units * 4 <= num_sms)
     launch<IO, 2>(a, s);
-  else if (units <= num_sms)
-    launch<IO, 4>(a, s);
   else
-    launch<IO, 8>(a, s);
+    launch<IO, 4>(a, s);
 }
 
 }  // namespace

@@ -7,6 +7,7 @@ There is no fallback: if ``libgdn.so`` is missing, loading it raises.
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -105,11 +106,10 @@ def lib():
         L.gdn_linear.argtypes = [ctypes.c_int] * 3 + [vp, ctypes.c_longlong, vp, ctypes.c_longlong, ctypes.c_int,
                                                       ctypes.POINTER(gdn_linear_out), vp]
         L.gdn_linear_ex.restype = ctypes.c_int
-        L.gdn_linear_ex.argtypes = [ctypes.c_int] * 4 + [vp, ctypes.c_longlong, vp, ctypes.c_longlong, vp, ctypes.c_int,
-                                                         ctypes.POINTER(gdn_linear_ex_out), vp]
+        L.gdn_linear_ex.argtypes = [ctypes.c_int] * 4 + [vp, ctypes.c_longlong, vp, ctypes.c_longlong, vp, ctypes.c_int, vp, vp]
         for name in ("gdn_linattn_prefill", "gdn_linattn_decode"):
             getattr(L, name).restype = ctypes.c_int
-            getattr(L, name).argtypes = [ctypes.POINTER(gdn_shape), ctypes.POINTER(gdn_linattn_io), vp]
+            getattr(L, name).argtypes = [vp, vp, vp]  # structures by reference, or packed bytes
         L.gdn_linattn_workspace_bytes.restype = ctypes.c_size_t
         L.gdn_linattn_workspace_bytes.argtypes = [ctypes.POINTER(gdn_shape), ctypes.c_int]
         L.gdn_selftest_wait_timeout.restype = ctypes.c_int
@@ -306,29 +306,30 @@ def gdn_linear_ex(x, w, outs, *, bias=None, gated=False, stream=None):
         if N % 2:
             raise ValueError("gated: w has 2N rows")
         N //= 2
-    n = len(outs)
-    arr = (gdn_linear_ex_out * n)()
-    for e, o in zip(arr, outs):
+    packed = []
+    for o in outs:
         begin, end, t = o[0], o[1], o[2]
-        e.col_begin, e.col_end, e.ptr, e.ld = begin, end, t.data_ptr(), _rows(t, M, end - begin, "output")
-        if len(o) > 3:
-            e.act = ACTIVATIONS[o[3]]
-            if len(o) > 4 and o[4] is not None:
-                e.residual, e.ldr = o[4].data_ptr(), _rows(o[4], M, end - begin, "residual")
+        act = ACTIVATIONS[o[3]] if len(o) > 3 else 0
+        res = o[4] if len(o) > 4 else None
+        packed.append(_PACK_LINEAR_OUT.pack(
+            begin, end, t.data_ptr(), _rows(t, M, end - begin, "output"), act, 0 if res is None else res.data_ptr(),
+            0 if res is None else _rows(res, M, end - begin, "residual")))
     st = (_lib or lib()).gdn_linear_ex(M, N, K, 1 if gated else 0, x.data_ptr(), _rows(x, M, K, "x"), w.data_ptr(),
-                                       _rows(w, 0, K, "w"), None if bias is None else bias.data_ptr(), n, arr,
-                                       _raw_stream(stream, x))
+                                       _rows(w, 0, K, "w"), None if bias is None else bias.data_ptr(), len(packed),
+                                       b"".join(packed), _raw_stream(stream, x))
     if st != GDN_OK:
         raise GdnError(st, "gdn_linear_ex")
 
 
 _BF16 = torch.bfloat16
+_PACK_LINEAR_OUT = struct.Struct("=2iQqi4xQq")  # gdn_linear_ex_out
 
 
 def _raw_stream(stream, t):
     """The stream handle of a call on `t`'s device (the current stream if none is given)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.device.index) if t.is_cuda else None
+        dev = t.get_device()
+        return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
     return _stream(stream)
 
 
@@ -346,54 +347,77 @@ def _rows(t, M, cols, what):
     return ld if shape[0] > 1 else max(ld, -(-shape[1] // 8) * 8)
 
 
-def _token_stride(t, what):
-    """Elements between consecutive token rows of [tokens, C] or [B, T, C] (sequences back to back)."""
-    st, shape = t.stride(), t.shape
-    if st[-1] != 1:
-        raise ValueError("%s: the last dimension must be contiguous" % what)
+def _token_rows(t, what):
+    """(tokens per sequence or in all, width, elements between token rows) of [B, T, C] (sequences back to back)
+    or [tokens, C]."""
+    shape, st = t.shape, t.stride()
     if len(shape) == 3:
-        B, T = shape[0], shape[1]
+        B, T, C = shape
+        s0, ld, one = st
         if T == 1:
-            return st[0] if B > 1 else -(-shape[2] // 8) * 8
-        if B > 1 and st[0] != T * st[1]:
+            ld = s0 if B > 1 else (C + 7) // 8 * 8
+        elif B > 1 and s0 != T * ld:
             raise ValueError("%s: sequences must follow each other at the token stride" % what)
-        return st[1]
-    return st[0] if shape[0] > 1 else -(-shape[1] // 8) * 8
+    else:
+        B, T, C = 0, *shape
+        ld, one = st
+        if T == 1:
+            ld = (C + 7) // 8 * 8
+    if one != 1:
+        raise ValueError("%s: the last dimension must be contiguous" % what)
+    return B, T, C, ld
+
+
+# The layouts of gdn_shape and gdn_linattn_io, packed in one go: the smallest
+# calls take a few microseconds, of which filling the structures would be two.
+_PACK_SHAPE = struct.Struct("=7i3f")
+_PACK_LINATTN = struct.Struct("=3Q4q8Q")
+_F32 = torch.float32
+_IO_CODES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
 
 
 def _linattn(entry, q, k, v, o, S0, S_T, Hk, Hv, g, log_decay, cu_seqlens, workspace, scale, stream):
-    dtype, shape, D = q.dtype, q.shape, q.shape[-1] // Hk
-    if not (k.dtype == dtype and v.dtype == dtype and o.dtype == dtype):
-        raise TypeError("q, k, v and o have one dtype")
-    if k.shape != shape or o.shape != v.shape or v.shape[:-1] != shape[:-1] or shape[-1] != Hk * D or v.shape[-1] != Hv * D:
+    dtype = q.dtype
+    if not (k.dtype == dtype and v.dtype == dtype and o.dtype == dtype) or dtype not in _IO_CODES:
+        raise TypeError("q, k, v and o have one dtype, bfloat16 or float32")
+    B, T, C, ldq = _token_rows(q, "q")
+    Bk, Tk, Ck, ldk = _token_rows(k, "k")
+    Bv, Tv, Cv, ldv = _token_rows(v, "v")
+    Bo, To, Co, ldo = _token_rows(o, "o")
+    D = C // Hk
+    if not (B == Bk == Bv == Bo and T == Tk == Tv == To and C == Ck == Hk * D and Cv == Co == Hv * D):
         raise ValueError("q and k are [.., Hk * D], v and o [.., Hv * D], over the same tokens")
+    tokens = B * T
     if cu_seqlens is not None:
-        if len(shape) != 2 or cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_contiguous():
+        if B or cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_contiguous():
             raise ValueError("packed: q is [tokens, Hk * D], cu_seqlens contiguous int32 [B + 1]")
-        B, T = cu_seqlens.numel() - 1, shape[0]
-        tokens = T
-    else:
-        B, T = shape[0], shape[1]
-        tokens = B * T
-    gate, n = (g, tokens * Hv) if g is not None else (log_decay, Hv)
-    _fp32(gate, n, "the log decays")
-    _fp32(S_T, B * Hv * D * D, "the state")
+        B, tokens = cu_seqlens.numel() - 1, T
+    elif not B:
+        raise ValueError("q is [B, T, Hk * D]")
+    if g is not None:
+        _fp32(g, tokens * Hv, "g")
+    if log_decay is not None:
+        _fp32(log_decay, Hv, "log_decay")
+    n = B * Hv * D * D
+    _fp32(S_T, n, "the state")
     if S0 is not None:
-        _fp32(S0, B * Hv * D * D, "S0")
-    sh = gdn_shape(B, T, Hk, Hv, D, D, _io_code(dtype), 0.0, 0.0, scale)
-    io = gdn_linattn_io(q.data_ptr(), k.data_ptr(), v.data_ptr(), _token_stride(q, "q"), _token_stride(k, "k"),
-                        _token_stride(v, "v"), _token_stride(o, "o"), None if g is None else g.data_ptr(),
-                        None if log_decay is None else log_decay.data_ptr(), None if S0 is None else S0.data_ptr(),
-                        o.data_ptr(), S_T.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr())
+        _fp32(S0, n, "S0")
+    ws = ws_bytes = 0
     if workspace is not None and workspace.numel():
-        io.workspace, io.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    st = getattr(_lib or lib(), entry)(sh, io, _raw_stream(stream, q))
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = getattr(_lib or lib(), entry)(
+        _PACK_SHAPE.pack(B, T, Hk, Hv, D, D, _IO_CODES[dtype], 0.0, 0.0, scale),
+        _PACK_LINATTN.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ldk, ldv, ldo,
+                           0 if g is None else g.data_ptr(), 0 if log_decay is None else log_decay.data_ptr(),
+                           0 if S0 is None else S0.data_ptr(), o.data_ptr(), S_T.data_ptr(),
+                           0 if cu_seqlens is None else cu_seqlens.data_ptr(), ws, ws_bytes),
+        _raw_stream(stream, q))
     if st != GDN_OK:
         raise GdnError(st, entry)
 
 
 def _fp32(t, n, what):
-    if t is None or t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+    if t.dtype != _F32 or t.numel() != n or not t.is_contiguous():
         raise ValueError("%s: %d contiguous float32 values are wanted" % (what, n))
 
 

@@ -133,3 +133,13 @@ def test_binding_refuses_what_it_can_see():
         with pytest.raises(err):
             gdn.gdn_linear_ex(x, kw.get("w", w), [(0, 6, kw.get("y", y), kw.get("act", "none"))], bias=kw.get("bias"),
                               gated=kw.get("gated", False))
+
+
+def test_packed_layouts_are_the_structures():
+    """What the binding packs by hand lies where the C structures have it."""
+    for fmt, cls in ((gdn._PACK_SHAPE, gdn.gdn_shape), (gdn._PACK_LINATTN, gdn.gdn_linattn_io),
+                     (gdn._PACK_LINEAR_OUT, gdn.gdn_linear_ex_out)):
+        assert fmt.size == ctypes.sizeof(cls)
+        vals = [float(i) if t is ctypes.c_float else i for i, (_, t) in enumerate(cls._fields_, 1)]
+        got = cls.from_buffer_copy(fmt.pack(*vals))
+        assert [getattr(got, f) for f, _ in cls._fields_] == vals
