@@ -359,10 +359,9 @@ gdn_status linattn_impl(const gdn_shape *shape, const gdn_linattn_io *io, bool d
     if (!(i == n - 1 && in_place) && overlap(rs, in[i])) return GDN_ERR_ALIAS;
   }
   if (overlap(ro, rs)) return GDN_ERR_ALIAS;
-  // bf16 prompts run in chunks on the tensor cores; single tokens and fp32 io
-  // (fp32 arithmetic throughout) token by token.
+  // bf16 prompts run in chunks on the tensor cores; the shortest ones, tokens
+  // from the cache and fp32 io (fp32 arithmetic throughout) token by token.
   const bool bf16 = shape->io_dtype == GDN_BF16;
-  const bool chunked = bf16 && !decode;
   if (io->workspace && (reinterpret_cast<uintptr_t>(io->workspace) & 255u) != 0) return GDN_ERR_ALIGNMENT;
   const Range rw = range_of(io->workspace, io->workspace_bytes);
   for (int i = 0; i < n; ++i)
@@ -371,9 +370,10 @@ gdn_status linattn_impl(const gdn_shape *shape, const gdn_linattn_io *io, bool d
   DeviceInfo dev;
   st = device_info(&dev);
   if (st != GDN_OK) return st;
+  const bool chunked = bf16 && !decode && !gdn::linattn_recurrent_pays(shape->B, shape->Hv, shape->T, dev.sms);
   gdn::LinAttnCut cut{1, 1};
   if (chunked && io->workspace) {
-    cut = gdn::linattn_cut(shape->B, shape->Hv, tokens, dev.sms);
+    cut = gdn::linattn_cut(shape->B, shape->Hv, tokens, packed, dev.sms);
     if (io->workspace_bytes < gdn::linattn_ws_bytes(shape->B, shape->Hv, cut)) return GDN_ERR_INVALID_ARG;
   }
   gdn::LinAttnArgs a{shape->B, shape->T,  shape->Hk, shape->Hv, d.q_scale, io->q,
@@ -587,7 +587,7 @@ size_t gdn_linattn_workspace_bytes(const gdn_shape *shape, int packed) {
   Sizes sz;
   DeviceInfo dev;
   if (check_shape(shape, tokens, &d, &sz) != GDN_OK || device_info(&dev) != GDN_OK) return 0;
-  return gdn::linattn_ws_bytes(shape->B, shape->Hv, gdn::linattn_cut(shape->B, shape->Hv, tokens, dev.sms));
+  return gdn::linattn_ws_bytes(shape->B, shape->Hv, gdn::linattn_cut(shape->B, shape->Hv, tokens, packed != 0, dev.sms));
 }
 
 gdn_status gdn_selftest_wait_timeout(int wait_us, void *stream) {

@@ -117,13 +117,15 @@ struct LinAttnArgs {
   int nseg, sub;           // segments per sequence and parts per segment (chunked kernel)
   unsigned int *err;
 };
-constexpr int kLinAttnMaxSeg = 16;
+constexpr int kLinAttnMaxSeg = 32;
 // How the chunked kernel cuts a call's sequences: segments side by side, and
 // parts of a segment in the launch that forms the states between them.
 struct LinAttnCut {
   int nseg, sub;
 };
-LinAttnCut linattn_cut(int B, int Hv, long long tokens, int sms);
+LinAttnCut linattn_cut(int B, int Hv, long long tokens, bool packed, int sms);
+// Whether the recurrent kernel is the faster one for bf16 sequences of up to `longest` tokens.
+bool linattn_recurrent_pays(int B, int Hv, long long longest, int sms);
 // States kept between the launches: S0 and one per part but the last segment's.
 __host__ __device__ inline long long linattn_slots(int nseg, int sub) { return (long long)(nseg - 1) * sub + 1; }
 inline size_t linattn_ws_bytes(int B, int Hv, LinAttnCut c) {

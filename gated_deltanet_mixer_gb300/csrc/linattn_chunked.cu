@@ -28,9 +28,9 @@
 // registers, because an MMA truncates what it adds to.
 //
 // Few units (sequences x value heads) leave SMs idle, so a sequence can be cut
-// into segments: a first launch (kStateOnly) forms each segment's state from
-// zero, a second starts every segment from the decayed sum of those before it.
-// Cost: k and v are read twice.
+// into segments: a first launch (kStateOnly) forms the state of each segment's
+// parts from zero, a small one turns those into the state before every segment,
+// and a third starts every segment from its own.  Cost: k and v are read twice.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -574,19 +574,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 64; i += 4)
           *reinterpret_cast<float4 *>(a.ws + at + i) = *reinterpret_cast<const float4 *>(a.S0 + at + i);
     } else {
-      // S0, then the parts before this segment: S <- decay S + (their state from zero)
-      const int last = a.nseg > 1 ? seg * a.sub : 0;
-#pragma unroll 1
-      for (int m = a.S0 ? 0 : 1; m <= last; ++m) {
-        const float *src = (a.nseg > 1 ? a.ws + m * units * kState : a.S0) + at;
-        const float mul = m > 0 ? dec[m * units + unit] : 0.f;
+      const float *src = a.nseg == 1 ? a.S0 : seg > 0 || a.S0 ? a.ws + (long long)seg * a.sub * units * kState : nullptr;
+      if (src) {
 #pragma unroll
         for (int i = 0; i < 64; i += 4) {
-          const float4 x = *reinterpret_cast<const float4 *>(src + i);
-          S[i] = fmaf(mul, S[i], x.x);
-          S[i + 1] = fmaf(mul, S[i + 1], x.y);
-          S[i + 2] = fmaf(mul, S[i + 2], x.z);
-          S[i + 3] = fmaf(mul, S[i + 3], x.w);
+          const float4 x = *reinterpret_cast<const float4 *>(src + at + i);
+          S[i] = x.x;
+          S[i + 1] = x.y;
+          S[i + 2] = x.z;
+          S[i + 3] = x.w;
         }
       }
     }
@@ -695,6 +691,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// The state before every segment but the first, in place of that of the part
+// before it: S <- decay of the part S + its state from zero, from S0 on.
+constexpr int kCombineThreads = 256;
+__global__ void __launch_bounds__(kCombineThreads) linattn_combine_kernel(LinAttnArgs a) {
+  const long long units = (long long)a.B * a.Hv, unit = blockIdx.y;
+  const long long at = unit * kD * kD + 4 * (blockIdx.x * kCombineThreads + threadIdx.x), step = units * kD * kD;
+  const int parts = (a.nseg - 1) * a.sub;
+  const float *dec = a.ws + linattn_slots(a.nseg, a.sub) * step;
+  float4 S = a.S0 ? *reinterpret_cast<const float4 *>(a.ws + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kAhead = 8;
+  for (int m0 = 1; m0 <= parts; m0 += kAhead) {
+    float4 x[kAhead];
+    float d[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (m0 + i <= parts) {
+        x[i] = *reinterpret_cast<const float4 *>(a.ws + (m0 + i) * step + at);
+        d[i] = dec[(m0 + i) * units + unit];
+      }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (m0 + i <= parts) {
+        S = make_float4(fmaf(d[i], S.x, x[i].x), fmaf(d[i], S.y, x[i].y), fmaf(d[i], S.z, x[i].z), fmaf(d[i], S.w, x[i].w));
+        if ((m0 + i) % a.sub == 0) *reinterpret_cast<float4 *>(a.ws + (m0 + i) * step + at) = S;
+      }
+  }
+}
+
 template <bool kStateOnly>
 struct ChunkTag {};
 
@@ -714,25 +738,39 @@ bool encode_rows(CUtensorMap *m, const void *base, long long rows, long long col
 
 }  // namespace
 
-LinAttnCut linattn_cut(int B, int Hv, long long tokens, int sms) {
+// Microseconds, measured: a CTA's start and end, a chunk with its output, a
+// chunk's state alone, a token of the recurrent kernel (one CTA per SM; above
+// that by the unit).
+namespace {
+constexpr float kStart = 9.f, kChunkOut = 2.1f, kChunkState = 1.2f, kToken = 0.11f, kTokenUnit = 0.0033f;
+}
+
+LinAttnCut linattn_cut(int B, int Hv, long long tokens, bool packed, int sms) {
   const long long units = (long long)B * Hv;
-  const long long nch = (tokens / B + kC - 1) / kC;  // of a sequence (packed: of the average one)
-  long long n = sms / units;                         // one CTA per SM
-  if (n > nch / 4) n = nch / 4;
-  if (n > kLinAttnMaxSeg) n = kLinAttnMaxSeg;
-  if (n < 2) return {1, 1};
-  // The state-only launch has (n - 1) k parts per unit: the k whose waves of
-  // parts take the least time.
-  int best = 1;
-  long long best_waves = 0;
-  for (int k = 1; k <= 4 && n * k * 4 <= nch; ++k) {
-    const long long waves = ((n - 1) * k * units + sms - 1) / sms;
-    if (k == 1 || waves * best < best_waves * k) {
-      best = k;
-      best_waves = waves;
+  // The chunks of a sequence; of a packed batch, whose lengths the host does not
+  // know, those of one three times the average.
+  const long long len = packed ? (tokens < 3 * (tokens / B + 1) ? tokens : 3 * (tokens / B + 1)) : tokens / B;
+  const long long nch = (len + kC - 1) / kC;
+  LinAttnCut best{1, 1};
+  float least = (float)((units + sms - 1) / sms) * (kStart + kChunkOut * nch);
+  for (int n = 2; n <= kLinAttnMaxSeg && n <= nch && units * n <= 2LL * sms; ++n)
+    for (int k = 1; k <= 3 && n * k <= nch; ++k) {
+      const long long per = (nch + n * k - 1) / (n * k);
+      const float out = (float)((units * n + sms - 1) / sms) * (kStart + kChunkOut * per * k);
+      const float state = (float)((units * (n - 1) * k + sms - 1) / sms) * (kStart + kChunkState * per);
+      if (out + state + 4.f < least) {  // 4: the launch between them
+        least = out + state + 4.f;
+        best = {n, k};
+      }
     }
-  }
-  return {(int)n, best};
+  return best;
+}
+
+bool linattn_recurrent_pays(int B, int Hv, long long longest, int sms) {
+  const float units = (float)B * Hv, nch = (float)((longest + kC - 1) / kC);
+  const float token = kToken > kTokenUnit * units ? kToken : kTokenUnit * units;
+  const float waves = (float)(((long long)B * Hv + sms - 1) / sms);
+  return 3.f + token * longest < waves * (kStart + kChunkOut * nch);
 }
 
 cudaError_t launch_linattn_chunked(const LinAttnArgs &a, cudaStream_t s) {
@@ -747,6 +785,7 @@ cudaError_t launch_linattn_chunked(const LinAttnArgs &a, cudaStream_t s) {
     e = allow_smem<ChunkTag<true>>(linattn_chunked_kernel<true>, kSmem);
     if (e != cudaSuccess) return e;
     linattn_chunked_kernel<true><<<(unsigned)((long long)a.B * a.Hv * (a.nseg - 1) * a.sub), kThreads, kSmem, s>>>(a, tm_q, tm_k, tm_v);
+    linattn_combine_kernel<<<dim3(kD * kD / (4 * kCombineThreads), (unsigned)(a.B * a.Hv)), kCombineThreads, 0, s>>>(a);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;

@@ -56,21 +56,29 @@ __device__ __forceinline__ void arrive(uint64_t *bar) {
 // =============================================================================
 // lin_tile_kernel
 // =============================================================================
-constexpr int BM = 128, BN = 256;
-constexpr int kStages = 4;
-constexpr uint32_t kStageA = BM * BK * 2, kStageB = BN * BK * 2;
-constexpr uint32_t kStageBytes = kStageA + kStageB;
-constexpr uint32_t kBarOff = kStages * kStageBytes;
-constexpr uint32_t kTileSmem = kBarOff + 256 + 1024;
-constexpr int kTileThreads = 192;
-static_assert(kTileSmem <= 232448, "shared memory per CTA");
+constexpr int BM = 128;
+constexpr int kEpiWarps = 8;  // two per TMEM quarter, a half of the columns each
+constexpr int kTileThreads = 64 + 32 * kEpiWarps;
+constexpr int kMaxStages = 8;
 
+// Tiles 256 columns wide carry the most arithmetic per byte; narrower ones give
+// small problems more CTAs and shorter epilogues.
+template <int BN>
+struct Tile {
+  static constexpr uint32_t kA = BM * BK * 2, kB = BN * BK * 2, kStage = kA + kB;
+  static constexpr int kStages = 192 * 1024 / kStage < kMaxStages ? (int)(192 * 1024 / kStage) : kMaxStages;
+  static constexpr uint32_t kBars = kStages * kStage;
+  static constexpr uint32_t kRun = kBars + 256;  // per epilogue warp: a 32 x 32 run of the tile, rows 33 apart
+  static constexpr uint32_t kSmem = kRun + kEpiWarps * 32 * 33 * 4 + 1024;
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+};
 struct Bars {
-  uint64_t full[kStages], empty[kStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t tfull[2], tempty[2];
   uint64_t end;
   uint32_t tmem;
 };
+static_assert(sizeof(Bars) <= 256, "barriers");
 
 // Tile t of the persistent schedule: bands of 8 m tiles walk across n, so the
 // CTAs that run at once share their w tiles in L2.
@@ -102,62 +110,134 @@ __device__ __forceinline__ void add_bias(float (&v)[32], const bf16 *bias, long 
   }
 }
 
-// Columns col0 .. col0 + 31 of row `row`: v = p (bias added), u = the up half (gated).
+template <int R>
+__device__ __forceinline__ void activate_run(float (&v)[R], int act) {
+  switch (act) {  // outside the loop
+    case GDN_ACT_SILU:
+#pragma unroll
+      for (int e = 0; e < R; ++e) v[e] = activate(v[e], GDN_ACT_SILU);
+      break;
+    case GDN_ACT_GELU:
+#pragma unroll
+      for (int e = 0; e < R; ++e) v[e] = activate(v[e], GDN_ACT_GELU);
+      break;
+    case GDN_ACT_SIGMOID:
+#pragma unroll
+      for (int e = 0; e < R; ++e) v[e] = activate(v[e], GDN_ACT_SIGMOID);
+      break;
+    default: break;
+  }
+}
+
+__device__ __forceinline__ bool whole_run(const LinOut &out, int col0, int N) {
+  return col0 >= out.col_begin && col0 + 32 <= min(out.col_end, N) && out.vec_ok;
+}
+// The residual of range `out` under columns col0 .. col0 + 31 of rows row0 ..
+// row0 + 31: 32 bf16 of this lane's row (whole runs) or of its column.
+__device__ __forceinline__ void load_residual(const LinArgs &g, const LinOut &out, long long row0, int lane, int col0,
+                                              uint32_t (&x)[16]) {
+  const int rows = (int)min(32LL, g.M - row0), col = col0 + lane;
+  const bf16 *res = static_cast<const bf16 *>(out.res) - out.col_begin;
+  if (whole_run(out, col0, g.N)) {
+    const uint4 *src = reinterpret_cast<const uint4 *>(res + (row0 + min(lane, rows - 1)) * out.ldres + col0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4 r = src[q];
+      x[4 * q] = r.x, x[4 * q + 1] = r.y, x[4 * q + 2] = r.z, x[4 * q + 3] = r.w;
+    }
+  } else if (col >= out.col_begin && col < min(out.col_end, g.N)) {
+    const uint16_t *src = reinterpret_cast<const uint16_t *>(res + row0 * out.ldres + col);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint32_t r0 = 2 * e < rows ? src[2 * e * out.ldres] : 0;
+      const uint32_t r1 = 2 * e + 1 < rows ? src[(2 * e + 1) * out.ldres] : 0;
+      x[e] = r0 | r1 << 16;
+    }
+  }
+}
+// The first range with a residual under these columns, loaded ahead into x; -1: none.
+__device__ __forceinline__ int prefetch_residual(const LinArgs &g, long long row0, int lane, int col0, uint32_t (&x)[16]) {
+  if (row0 >= g.M) return -1;
+  for (int o = 0; o < g.n_out; ++o) {
+    const LinOut &out = g.out[o];
+    if (!out.res || max(col0, out.col_begin) >= min(min(col0 + 32, out.col_end), g.N)) continue;
+    load_residual(g, out, row0, lane, col0, x);
+    return o;
+  }
+  return -1;
+}
+
+// Columns col0 .. col0 + 31 of the warp's rows row0 .. row0 + 31, lane = row:
+// v = p (bias added), u = the up half (gated), x = the residual of range
+// `loaded`.  Whole aligned runs are stored 16 bytes per lane.  Others go through
+// shared memory, so that a warp stores 32 neighbouring columns of one row at a
+// time: a lane storing its own row would touch 32 rows with every 2-byte store
+// (4069 x 6549 x 144 with a residual: 601 us so, 110 this way).
 template <bool kGated>
-__device__ __forceinline__ void store_run(const LinArgs &g, long long row, int col0, float (&v)[32], const float (&u)[32]) {
+__device__ __forceinline__ void store_run(const LinArgs &g, long long row0, int lane, int col0, const float (&v)[32],
+                                          const float (&u)[32], float *run, int loaded, uint32_t (&x)[16]) {
   for (int o = 0; o < g.n_out; ++o) {
     const LinOut &out = g.out[o];
     const int lo = max(col0, out.col_begin), hi = min(min(col0 + 32, out.col_end), g.N);
     if (lo >= hi) continue;
-    bf16 *dst = static_cast<bf16 *>(out.ptr) + row * out.ld - out.col_begin;
-    const bf16 *res = static_cast<const bf16 *>(out.res) + row * out.ldres - out.col_begin;
-    if (lo == col0 && hi == col0 + 32 && out.vec_ok) {
+    const int rows = (int)min(32LL, g.M - row0), col = col0 + lane;
+    const bool whole = whole_run(out, col0, g.N), inside = col >= lo && col < hi;
+    if (out.res && o != loaded) load_residual(g, out, row0, lane, col0, x);
+    float y[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) y[e] = v[e];
+    activate_run(y, out.act);
+    if (kGated) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) y[e] *= u[e];
+    }
+    bf16 *dst = static_cast<bf16 *>(out.ptr) - out.col_begin;
+    if (whole) {
+      if (lane >= rows) continue;
+      uint4 *to = reinterpret_cast<uint4 *>(dst + (row0 + lane) * out.ld + col0);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          y[e] = activate(v[8 * q + e], out.act);
-          if (kGated) y[e] *= u[8 * q + e];
-        }
-        if (out.res) {
-          const uint4 r = *reinterpret_cast<const uint4 *>(res + col0 + 8 * q);
-          const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            y[2 * e] += __uint_as_float(w[e] << 16);
-            y[2 * e + 1] += __uint_as_float(w[e] & 0xffff0000u);
-          }
-        }
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          __nv_bfloat162 t = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
+          float a = y[8 * q + 2 * e], b = y[8 * q + 2 * e + 1];
+          if (out.res) a += __uint_as_float(x[4 * q + e] << 16), b += __uint_as_float(x[4 * q + e] & 0xffff0000u);
+          __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
           w[e] = *reinterpret_cast<uint32_t *>(&t);
         }
-        *reinterpret_cast<uint4 *>(dst + col0 + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+        to[q] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-    } else {
+      continue;
+    }
+    __syncwarp();  // the run before this one has been read
 #pragma unroll
-      for (int q = 0; q < 32; ++q)
-        if (col0 + q >= lo && col0 + q < hi) {
-          float y = activate(v[q], out.act);
-          if (kGated) y *= u[q];
-          if (out.res) y += __bfloat162float(res[col0 + q]);
-          dst[col0 + q] = __float2bfloat16_rn(y);
+    for (int e = 0; e < 32; ++e) run[lane * 33 + e] = y[e];
+    __syncwarp();
+    if (inside) {
+      bf16 *to = dst + row0 * out.ld + col;
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (e < rows) {
+          float z = run[e * 33 + lane];
+          if (out.res) z += __uint_as_float(e & 1 ? x[e / 2] & 0xffff0000u : x[e / 2] << 16);
+          *to = __float2bfloat16_rn(z);
+          to += out.ld;
         }
     }
   }
 }
 
-template <bool kGated>
+template <int BN, bool kGated>
 __global__ void __launch_bounds__(kTileThreads, 1)
     lin_tile_kernel(const LinArgs g, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w) {
-  constexpr int kCols = kGated ? BN / 2 : BN;  // output columns of a tile (gated: 128 gate rows of w, then 128 up rows)
+  using L = Tile<BN>;
+  constexpr int kStages = L::kStages;
+  constexpr int kCols = kGated ? BN / 2 : BN;  // output columns of a tile (gated: the gate rows of w, then the up rows)
+  static_assert(kCols >= 64, "two runs of 32 columns at least");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  Bars &B = *reinterpret_cast<Bars *>(sm + kBarOff);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Bars &B = *reinterpret_cast<Bars *>(sm + L::kBars);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + kCols - 1) / kCols;
   const int ntiles = tiles_m * tiles_n;
   const int nk = (g.K + BK - 1) / BK;
@@ -170,109 +250,107 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       bar_init(&B.tfull[a], 1);
-      bar_init(&B.tempty[a], 4);
+      bar_init(&B.tempty[a], kEpiWarps);
     }
     bar_init(&B.end, 1);
   }
-  if (warp == 1) tmem_alloc(&B.tmem, 512);
+  if (warp == 1) tmem_alloc(&B.tmem, 2 * BN);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = B.tmem;
   bool ok = true;
 
+  // The loads' and the MMAs' warps stay converged, lane 0 issuing: their operands
+  // then live in uniform registers (a lone thread issues at about half the rate).
   if (warp == 0) {
     // ---- TMA producer
-    if (lane == 0) {
-      uint32_t it = 0;
-      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
-        int mt, nt;
-        tile_of(t, tiles_m, tiles_n, mt, nt);
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!bar_wait(&B.empty[s], ((it / kStages) & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
-          const uint32_t dst = sbase + s * kStageBytes;
-          bar_expect_tx(&B.full[s], kStageBytes);
-          tma_load_3d(dst, &tm_x, kb * BK, mt * BM, 0, &B.full[s]);
-          tma_load_3d(dst + kStageA, &tm_w, kb * BK, nt * kCols, 0, &B.full[s]);
-          tma_load_3d(dst + kStageA + kStageB / 2, &tm_w, kb * BK, nt * kCols + (kGated ? g.N : BN / 2), 0, &B.full[s]);
-        }
+    uint32_t it = 0;
+    for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+      int mt, nt;
+      tile_of(t, tiles_m, tiles_n, mt, nt);
+      for (int kb = 0; kb < nk && ok; ++kb, ++it) {
+        const int s = it % kStages;
+        ok = __all_sync(0xffffffffu, bar_wait(&B.empty[s], ((it / kStages) & 1) ^ 1));
+        if (!ok) break;
+        const uint32_t dst = sbase + s * L::kStage;
+        bar_expect_tx_w(&B.full[s], L::kStage);
+        tma_load_3d_w(dst, &tm_x, kb * BK, mt * BM, 0, &B.full[s]);
+        tma_load_3d_w(dst + L::kA, &tm_w, kb * BK, nt * kCols, 0, &B.full[s]);
+        if (kGated) tma_load_3d_w(dst + L::kA + L::kB / 2, &tm_w, kb * BK, g.N + nt * kCols, 0, &B.full[s]);
       }
-      // Leave only when every stage issued has been consumed (bounded).
-      if (ok && it > 0)
-        for (uint32_t j = (it > kStages ? it - kStages : 0); j < it; ++j)
-          if (!bar_wait(&B.empty[j % kStages], (j / kStages) & 1)) {
-            ok = false;
-            break;
-          }
-      if (!ok) atomicOr(g.err, kErrTimeout);
     }
+    // Leave only when every stage issued has been consumed (bounded).
+    for (uint32_t j = (it > kStages ? it - kStages : 0); ok && j < it; ++j)
+      ok = __all_sync(0xffffffffu, bar_wait(&B.empty[j % kStages], (j / kStages) & 1));
+    if (!ok && lane == 0) atomicOr(g.err, kErrTimeout);
   } else if (warp == 1) {
     // ---- MMA issuer
-    if (lane == 0) {
-      const uint32_t id = idesc_bf16(BM, BN);
-      uint32_t it = 0;
-      int local = 0;
-      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x, ++local) {
-        const int acc = local & 1;
-        if (!bar_wait(&B.tempty[acc], ((local >> 1) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        fence_after();
-        const uint32_t d = tmem + (uint32_t)(acc * BN);
-        for (int kb = 0; kb < nk; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!bar_wait(&B.full[s], (it / kStages) & 1)) {
-            ok = false;
-            break;
-          }
-          fence_after();
-          const uint32_t a0 = sbase + s * kStageBytes, b0 = a0 + kStageA;
-#pragma unroll
-          for (int ks = 0; ks < BK / 16; ++ks)
-            mma(d, desc_k(a0, ks, BM), desc_k(b0, ks, BN), id, (kb > 0 || ks > 0) ? 1u : 0u);
-          commit(&B.empty[s]);
-        }
+    const uint32_t id = idesc_bf16(BM, BN), td = __shfl_sync(0xffffffffu, tmem, 0);
+    uint32_t it = 0;
+    int local = 0;
+    for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x, ++local) {
+      const int acc = local & 1;
+      ok = __all_sync(0xffffffffu, bar_wait(&B.tempty[acc], ((local >> 1) & 1) ^ 1));
+      if (!ok) break;
+      fence_after();
+      const uint32_t d = td + (uint32_t)(acc * BN);
+      for (int kb = 0; kb < nk; ++kb, ++it) {
+        const int s = it % kStages;
+        ok = __all_sync(0xffffffffu, bar_wait(&B.full[s], (it / kStages) & 1));
         if (!ok) break;
-        commit(&B.tfull[acc]);
+        fence_after();
+        const uint32_t a0 = sbase + s * L::kStage, b0 = a0 + L::kA;
+#pragma unroll
+        for (int ks = 0; ks < BK / 16; ++ks)
+          mma_w(d, desc_k(a0, ks, BM), desc_k(b0, ks, BN), id, (kb > 0 || ks > 0) ? 1u : 0u);
+        commit_w(&B.empty[s]);
       }
-      commit(&B.end);  // every MMA issued is complete before TMEM is freed
-      if (!bar_wait(&B.end, 0)) ok = false;
-      if (!ok) atomicOr(g.err, kErrTimeout);
+      if (!ok) break;
+      commit_w(&B.tfull[acc]);
     }
+    commit_w(&B.end);  // every MMA issued is complete before TMEM is freed
+    if (!__all_sync(0xffffffffu, bar_wait(&B.end, 0))) ok = false;
+    if (!ok && lane == 0) atomicOr(g.err, kErrTimeout);
   } else {
     // ---- epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 = tile rows
-    const int quad = warp & 3;
+    const int quad = warp & 3, half = (warp - 2) >> 2;
     const bf16 *bias = static_cast<const bf16 *>(g.bias);
+    float *run = reinterpret_cast<float *>(sm + L::kRun) + (warp - 2) * 32 * 33;
     int local = 0;
     for (int t = blockIdx.x; t < ntiles; t += gridDim.x, ++local) {
       int mt, nt;
       tile_of(t, tiles_m, tiles_n, mt, nt);
       const int acc = local & 1;
+      const long long row0 = (long long)mt * BM + 32 * quad;
+      const int first = half * (kCols / 2);
+      // The residual is loaded one run ahead, the first one under the MMAs.
+      uint32_t ahead[16];
+      int loaded = prefetch_residual(g, row0, lane, nt * kCols + first, ahead);
       const bool got = bar_wait(&B.tfull[acc], (local >> 1) & 1);
       if (!__all_sync(0xffffffffu, got)) {
         if (lane == 0) atomicOr(g.err, kErrTimeout);
         break;
       }
       fence_after();
-      const long long row = (long long)mt * BM + 32 * quad + lane;
       const uint32_t taddr = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * BN);
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 32) {
+      for (int c = first; c < first + kCols / 2; c += 32) {
+        uint32_t x[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = ahead[e];
+        const int now = loaded;
+        const int col0 = nt * kCols + c;
+        if (c + 32 < first + kCols / 2) loaded = prefetch_residual(g, row0, lane, col0 + 32, ahead);
         float v[32], u[32];
         tmem_ld32(taddr + c, v);  // every lane of the warp takes part
         if (kGated) tmem_ld32(taddr + kCols + c, u);
-        const int col0 = nt * kCols + c;
-        if (row >= g.M || col0 >= g.N) continue;
+        if (row0 >= g.M || col0 >= g.N) continue;
         if (bias) {
           add_bias(v, bias, col0, g.N - col0);
           if (kGated) add_bias(u, bias, (long long)g.N + col0, g.N - col0);
         }
-        store_run<kGated>(g, row, col0, v, u);
+        store_run<kGated>(g, row0, lane, col0, v, u, run, now, x);
       }
       fence_before();
       __syncwarp();
@@ -284,7 +362,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   if (warp == 1) {
     fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 2 * BN);
   }
 }
 
@@ -360,23 +438,12 @@ __device__ __forceinline__ LinCol column(const LinArgs &g, int col) {
   }
   return c;
 }
-template <int R>
-__device__ __forceinline__ void activate_run(float (&v)[R], int act) {
-  if (act == GDN_ACT_NONE) return;
-#pragma unroll
-  for (int e = 0; e < R; ++e) v[e] = activate(v[e], act);
-}
 // p (and u) of R rows, row0, row0 + step, .. of which the first `count` exist:
 // the rows are independent work, so nothing branches on one of them alone.
 template <bool kGated, int R>
 __device__ __forceinline__ void finish(const LinCol &c, long long row0, int step, int count, float (&p)[R],
                                        const float (&u)[R]) {
-  switch (c.act) {  // outside the rows' loop
-    case GDN_ACT_SILU: activate_run(p, GDN_ACT_SILU); break;
-    case GDN_ACT_GELU: activate_run(p, GDN_ACT_GELU); break;
-    case GDN_ACT_SIGMOID: activate_run(p, GDN_ACT_SIGMOID); break;
-    default: break;
-  }
+  activate_run(p, c.act);
   if (kGated) {
 #pragma unroll
     for (int e = 0; e < R; ++e) p[e] *= u[e];
@@ -531,14 +598,15 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     b = __bfloat162float(bias[n0 + n]);
     if (kGated) bu = __bfloat162float(bias[(long long)g.N + n0 + n]);
   }
-  for (int t = 4 * (tid / kOut); t < mine; t += 4 * kShare) {
-    float p[4], u[4];
+  constexpr int kRun = NT <= 64 ? 4 : 8;  // tokens finished side by side
+  for (int t = kRun * (tid / kOut); t < mine; t += kRun * kShare) {
+    float p[kRun], u[kRun];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) p[e] = b, u[e] = bu;
+    for (int e = 0; e < kRun; ++e) p[e] = b, u[e] = bu;
     for (int r = 0; r < split; ++r) {
       const float *src = part + (r * per + t) * kRowsW + n;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < kRun; ++e)
         if (t + e < mine) {
           p[e] += src[e * kRowsW];
           if (kGated) u[e] += src[e * kRowsW + kOut];
@@ -562,20 +630,23 @@ bool encode_kmajor(CUtensorMap *m, const void *base, long long rows, long long K
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kGated>
+template <int BN, bool kGated>
 struct TileTag {};
 template <int NT, bool kGated>
 struct SkinnyTag {};
 
-template <bool kGated>
-cudaError_t launch_tile(const LinArgs &a, long long ntiles, int num_sms, cudaStream_t s) {
+template <int BN, bool kGated>
+cudaError_t launch_tile(const LinArgs &a, int num_sms, cudaStream_t s) {
   CUtensorMap tm_x, tm_w;
   if (!encode_kmajor(&tm_x, a.x, a.M, a.K, a.ldx, BM) ||
-      !encode_kmajor(&tm_w, a.w, (long long)a.N * (kGated ? 2 : 1), a.K, a.ldw, BN / 2))
+      !encode_kmajor(&tm_w, a.w, (long long)a.N * (kGated ? 2 : 1), a.K, a.ldw, kGated ? BN / 2 : BN))
     return cudaErrorInvalidValue;
-  cudaError_t e = allow_smem<TileTag<kGated>>(lin_tile_kernel<kGated>, kTileSmem);
+  constexpr size_t kSmem = Tile<BN>::kSmem;
+  cudaError_t e = allow_smem<TileTag<BN, kGated>>(lin_tile_kernel<BN, kGated>, kSmem);
   if (e != cudaSuccess) return e;
-  lin_tile_kernel<kGated><<<(int)(ntiles < num_sms ? ntiles : num_sms), kTileThreads, kTileSmem, s>>>(a, tm_x, tm_w);
+  constexpr int kCols = kGated ? BN / 2 : BN;
+  const long long ntiles = (long long)((a.M + BM - 1) / BM) * ((a.N + kCols - 1) / kCols);
+  lin_tile_kernel<BN, kGated><<<(int)(ntiles < num_sms ? ntiles : num_sms), kTileThreads, kSmem, s>>>(a, tm_x, tm_w);
   return cudaGetLastError();
 }
 
@@ -613,13 +684,37 @@ cudaError_t launch_skinny(const LinArgs &a, int num_sms, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, a, (int)split, tm_x, tm_w);
 }
 
+// Microseconds of the tile kernel with tiles of BN w rows: a wave's k steps or
+// its epilogue, whichever is longer, and the last epilogue.  Measured: 0.36 us per
+// 64-wide k step at 256, which falls less than the tile does; 1.5 us per 64
+// columns of epilogue.
+template <bool kGated>
+float tile_cost(const LinArgs &a, int BN, int num_sms) {
+  const int cols = kGated ? BN / 2 : BN, nk = (a.K + BK - 1) / BK;
+  const long long tiles = (long long)((a.M + BM - 1) / BM) * ((a.N + cols - 1) / cols);
+  const float loop = (BN == 256 ? 0.36f : BN == 128 ? 0.24f : 0.19f) * nk, epi = 1.5f * cols / 64;
+  return (float)((tiles + num_sms - 1) / num_sms) * (loop > epi ? loop : epi) + epi;
+}
+
 template <bool kGated>
 cudaError_t launch(const LinArgs &a, int num_sms, cudaStream_t s) {
-  const int cols = kGated ? BN / 2 : BN;
-  const long long ntiles = (long long)((a.M + BM - 1) / BM) * ((a.N + cols - 1) / cols);
-  // Where w is read many times over and there is no SM to spare for a split
-  // contraction: the tile kernel.
-  if (a.M > 128 && 2 * ntiles > num_sms) return launch_tile<kGated>(a, ntiles, num_sms, s);
+  // Up to 128 tokens w is read once either way.  Above, the tile kernel against
+  // the split form, where a wave of it fits: 0.6 us per k step of its 128 x 256
+  // tiles, and 8 us for the meeting in the cluster (14 with a residual).
+  if (a.M > 128) {
+    const int nk = (a.K + BK - 1) / BK, out = kGated ? kRowsW / 2 : kRowsW;
+    const long long tiles2 = (long long)((a.N + out - 1) / out) * ((a.M + 255) / 256), split = num_sms / tiles2;
+    bool residual = false;
+    for (int o = 0; o < a.n_out; ++o) residual |= a.out[o].res != nullptr;
+    const float skinny = split < 2 ? 1e30f : 0.6f * nk / (split > 8 ? 8 : split) + (residual ? 14.f : 8.f);
+    const float t256 = tile_cost<kGated>(a, 256, num_sms), t128 = tile_cost<kGated>(a, 128, num_sms);
+    const float t64 = kGated ? 1e30f : tile_cost<kGated>(a, 64, num_sms);
+    if (skinny > t256 || skinny > t128 || skinny > t64) {
+      if (t256 <= t128 && t256 <= t64) return launch_tile<256, kGated>(a, num_sms, s);
+      if (t128 <= t64) return launch_tile<128, kGated>(a, num_sms, s);
+      return launch_tile<kGated ? 128 : 64, kGated>(a, num_sms, s);
+    }
+  }
   if (a.M <= 16) return launch_skinny<16, kGated>(a, num_sms, s);
   if (a.M <= 32) return launch_skinny<32, kGated>(a, num_sms, s);
   if (a.M <= 64) return launch_skinny<64, kGated>(a, num_sms, s);

@@ -373,7 +373,8 @@ gdn_status gdn_linear_ex(int M, int N, int K, int gated, const void *x, long lon
  *        gdn_linattn_workspace_bytes(), or NULL.  With few sequences x value
  *        heads it lets a prompt be cut into segments that run side by side.
  *
- * bf16 io runs in chunks of 64 tokens on the tensor cores: operands that are
+ * bf16 io runs in chunks of 64 tokens on the tensor cores (the shortest
+ * prompts, up to about a hundred tokens, token by token as fp32 io does): operands that are
  * not bf16 already enter as sums of bf16 pieces (24 bits of what feeds the
  * state, 16 bits of what feeds o only), the state itself is summed in fp32.
  * Log decays below -80 act as -80 there.  q, k and v are finite: a NaN or
