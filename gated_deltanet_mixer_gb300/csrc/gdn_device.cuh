@@ -86,6 +86,22 @@ __device__ __forceinline__ int longest_first(const int *cu, int B, int slot, int
   return res;
 }
 
+// A decay e^g as S -> m S + w S: m = e^g - 1 and w = 1 where e^g is above a
+// half, else m = e^g and w = 0.  Rounded to fp32, e^g itself is off by up to
+// 2^-24 of S with every application, always the same way for a constant decay:
+// over the 100,000 tokens of a slow one that is 0.6 %.  m keeps 24 bits of
+// what is taken away.
+struct Decay {
+  float m, w;
+  static __device__ __forceinline__ Decay of(float g) {
+    return g > -0.69f ? Decay{expm1f(g), 1.f} : Decay{expf(g), 0.f};
+  }
+  // e^g s + x, for a pair
+  __device__ __forceinline__ float2 apply(float2 s, float2 x) const {
+    return __ffma2_rn(make_float2(w, w), s, __ffma2_rn(make_float2(m, m), s, x));
+  }
+};
+
 // silu(x) = x * sigmoid(x)
 __device__ __forceinline__ float silu(float x) { return x / (1.0f + expf(-x)); }
 

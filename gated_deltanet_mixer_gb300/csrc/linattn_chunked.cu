@@ -61,8 +61,9 @@ struct ChunkVec {
   // e^{G_last - G} of the tokens 2 i, 2 i + 1 as bf16 pairs (c0, 0) and (c1, c2)
   // with c0 + c1 + c2 = it to 24 bits; 0 past the sequence's end
   uint2 gam[2][kC / 2];
-  float d;       // e^{G_last}
-  float pad[3];
+  Decay d;       // e^{G_last}
+  float total;   // G_last (natural)
+  float pad;
 };
 struct Shared {
   ChunkVec vec[kVecs];
@@ -230,7 +231,10 @@ __device__ __forceinline__ void chunk_vec(ChunkVec &cv, float g0, float g1, int 
     to[4 * (kC / 2)] = g1;
     to[4 * (kC / 2) + 2] = g2;
   }
-  if (lane == 0) cv.d = expf(s0);
+  if (lane == 0) {
+    cv.d = Decay::of(s0);
+    cv.total = s0;
+  }
 }
 
 template <bool kStateOnly>
@@ -564,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int v = 32 * (warp & 3) + lane, half = warp >> 2;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const long long at = (long long)unit * kState + v * kD + 64 * half;
-    float *dec = a.ws + linattn_slots(a.nseg, a.sub) * units * kState;  // [slot][units]
+    float *dec = a.ws + linattn_slots(a.nseg, a.sub) * units * kState;  // [slot][units]: log decays
     float S[64];
 #pragma unroll
     for (int i = 0; i < 64; ++i) S[i] = 0.f;
@@ -586,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    float dtot = 1.f;
+    float total = 0.f;  // the log decay over the part
     uint32_t hi[32], lo[32];  // the state as two bf16 pieces
     auto pieces = [&]() {
 #pragma unroll
@@ -611,8 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = warp_wait(&B.su_done[n & 1], (n >> 1) & 1);
       if (!ok) break;
       fence_after();
-      const float d = B.vec[n % kVecs].d;
-      if (kStateOnly) dtot *= d;
+      const Decay d = B.vec[n % kVecs].d;
+      if (kStateOnly) total += B.vec[n % kVecs].total;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t r[16];
@@ -621,8 +625,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int x = 16 * i + 2 * e;
-          const float2 y = __ffma2_rn(make_float2(d, d), make_float2(S[x], S[x + 1]),
-                                      make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])));
+          const float2 y = d.apply(make_float2(S[x], S[x + 1]),
+                                   make_float2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])));
           S[x] = y.x;
           S[x + 1] = y.y;
         }
@@ -631,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(&B.ds_free[n & 1]);
       if (!kStateOnly) pieces();
     }
-    if (kStateOnly && tid == 0) dec[(seg + 1) * units + unit] = dtot;
+    if (kStateOnly && tid == 0) dec[(seg + 1) * units + unit] = total;
     if (kStateOnly || (seg == a.nseg - 1 && in_bounds(at + 64, units * kState, a.err))) {
       float *dst = (kStateOnly ? a.ws + (seg + 1) * units * kState : a.S_T) + at;
 #pragma unroll
@@ -698,7 +702,7 @@ __global__ void __launch_bounds__(kCombineThreads) linattn_combine_kernel(LinAtt
   const long long units = (long long)a.B * a.Hv, unit = blockIdx.y;
   const long long at = unit * kD * kD + 4 * (blockIdx.x * kCombineThreads + threadIdx.x), step = units * kD * kD;
   const int parts = (a.nseg - 1) * a.sub;
-  const float *dec = a.ws + linattn_slots(a.nseg, a.sub) * step;
+  const float *dec = a.ws + linattn_slots(a.nseg, a.sub) * step;  // log decays
   float4 S = a.S0 ? *reinterpret_cast<const float4 *>(a.ws + at) : make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int kAhead = 8;
   for (int m0 = 1; m0 <= parts; m0 += kAhead) {
@@ -713,7 +717,10 @@ __global__ void __launch_bounds__(kCombineThreads) linattn_combine_kernel(LinAtt
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
       if (m0 + i <= parts) {
-        S = make_float4(fmaf(d[i], S.x, x[i].x), fmaf(d[i], S.y, x[i].y), fmaf(d[i], S.z, x[i].z), fmaf(d[i], S.w, x[i].w));
+        const Decay e = Decay::of(d[i]);
+        const float2 lo = e.apply(make_float2(S.x, S.y), make_float2(x[i].x, x[i].y));
+        const float2 hi = e.apply(make_float2(S.z, S.w), make_float2(x[i].z, x[i].w));
+        S = make_float4(lo.x, lo.y, hi.x, hi.y);
         if ((m0 + i) % a.sub == 0) *reinterpret_cast<float4 *>(a.ws + (m0 + i) * step + at) = S;
       }
   }

@@ -51,11 +51,11 @@ __device__ __forceinline__ void copy16(void *dst, const void *src) {
                : "memory");
 }
 
-__device__ __forceinline__ float4 decayed(float4 s, float a, float v, float4 k) {
-  const float2 x = __ffma2_rn(make_float2(a, a), make_float2(s.x, s.y),
-                              __fmul2_rn(make_float2(v, v), make_float2(k.x, k.y)));
-  const float2 y = __ffma2_rn(make_float2(a, a), make_float2(s.z, s.w),
-                              __fmul2_rn(make_float2(v, v), make_float2(k.z, k.w)));
+// e^g s + v k
+__device__ __forceinline__ float4 decayed(float4 s, Decay a, float v, float4 k) {
+  const float2 v2 = make_float2(v, v);
+  const float2 x = a.apply(make_float2(s.x, s.y), __fmul2_rn(v2, make_float2(k.x, k.y)));
+  const float2 y = a.apply(make_float2(s.z, s.w), __fmul2_rn(v2, make_float2(k.z, k.w)));
   return make_float4(x.x, x.y, y.x, y.y);
 }
 
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThreads) linattn_recurrent_kernel(LinAttnArgs
   constexpr int kSplit = kD / (kWarps * kRows);  // CTAs per unit
   constexpr int kCtaRows = kWarps * kRows;
   __shared__ __align__(16) IO s_q[kRing][kTB][kD], s_k[kRing][kTB][kD], s_v[kRing][kTB][kCtaRows];
-  __shared__ float s_a[kRing][kTB];  // e^g
+  __shared__ Decay s_a[kRing][kTB];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int unit = blockIdx.x / kSplit, part = blockIdx.x % kSplit;
   const int b = unit / a.Hv, h = unit % a.Hv, kh = h / (a.Hv / a.Hk);
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads) linattn_recurrent_kernel(LinAttnArgs
   static_assert(kTB * kD / kPiece <= kThreads, "one copy of q and of k per thread");
   auto decay = [&](int t) { return a.g ? a.g[(row0 + t) * a.Hv + h] : a.log_decay[h]; };
   for (int b = 0; b < kRing - 1; ++b) fetch(b);
-  if (tid < kTB * (kRing - 1) && tid < T) s_a[tid / kTB][tid % kTB] = expf(decay(tid));
+  if (tid < kTB * (kRing - 1) && tid < T) s_a[tid / kTB][tid % kTB] = Decay::of(decay(tid));
   const long long s_at = ((long long)unit * kD + r0) * kD + 4 * lane;
   float4 S[kRows];
 #pragma unroll
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) linattn_recurrent_kernel(LinAttnArgs
     float p[N * kRows];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float al = s_a[buf][t + i];
+      const Decay al = s_a[buf][t + i];
       const float4 kv = ld_io4(&s_k[buf][t + i][4 * lane]);
       const float4 qv = ld_io4(&s_q[buf][t + i][4 * lane]);
 #pragma unroll
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) linattn_recurrent_kernel(LinAttnArgs
     if (kGroup > 1)
       for (; t + kGroup <= n; t += kGroup) tokens(std::integral_constant<int, kGroup>(), buf, t0, t);
     for (; t < n; ++t) tokens(std::integral_constant<int, 1>(), buf, t0, t);
-    if (tid < kTB && next < T) s_a[(block + kRing - 1) % kRing][tid] = expf(na);
+    if (tid < kTB && next < T) s_a[(block + kRing - 1) % kRing][tid] = Decay::of(na);
   }
   const long long s_size = (long long)a.B * a.Hv * kD * kD;
 #pragma unroll

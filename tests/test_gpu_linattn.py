@@ -272,3 +272,21 @@ def test_side_stream_and_graph():
     torch.cuda.synchronize()
     assert gdn.gdn_device_status() == 0
     assert torch.equal(o[0, 1:], want[0][1:])
+
+
+@pytest.mark.parametrize("io,T", [("bf16", 4096), ("bf16", 90), ("f32", 512)])
+def test_very_slow_constant_decay(io, T):
+    """A half-life of 100,000 tokens, q = v = 0: the state is S0 e^{T g}, up to
+    two roundings of the state per application of a decay (2^-24 each, worst
+    case all one way: a constant decay takes the same step every time)."""
+    g = -6.9e-6
+    q = torch.zeros(1, T, D, dtype=torch.bfloat16 if io == "bf16" else torch.float32, device="cuda")
+    S0 = torch.rand(1, 1, D, D, device="cuda", generator=torch.Generator("cuda").manual_seed(1)) + 0.5
+    S, o = torch.empty_like(S0), torch.empty_like(q)
+    for ws in (False, True):
+        n = gdn.gdn_linattn_workspace_bytes(1, T, 1, 1) if io == "bf16" else 0
+        gdn.gdn_linattn_prefill(q, q, q, S0, o, S, Hk=1, Hv=1, log_decay=torch.tensor([g], device="cuda"),
+                                workspace=torch.empty(n, dtype=torch.uint8, device="cuda") if ws and n else None)
+        torch.cuda.synchronize()
+        ratio = (S.double() / S0.double()) / math.exp(T * float(torch.tensor(g)))
+        assert (ratio - 1).abs().max().item() < 2 * T * 2.0 ** -24
