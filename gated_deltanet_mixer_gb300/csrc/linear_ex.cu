@@ -438,23 +438,27 @@ __device__ __forceinline__ LinCol column(const LinArgs &g, int col) {
   }
   return c;
 }
-// p (and u) of R rows, row0, row0 + step, .. of which the first `count` exist:
-// the rows are independent work, so nothing branches on one of them alone.
+// The residual of R rows, row0, row0 + step, .. of which the first `count` exist.
+template <int R>
+__device__ __forceinline__ void load_rows(const LinCol &c, long long row0, int step, int count, bf16 (&r)[R]) {
+  if (!c.res) return;
+  const bf16 *res = c.res + row0 * c.ldres;
+  const long long d = step * c.ldres;
+#pragma unroll
+  for (int e = 0; e < R; ++e)
+    if (e < count) r[e] = res[e * d];
+}
+// p (and u, and the residual r) of those rows: independent work, so nothing
+// branches on one of them alone.
 template <bool kGated, int R>
 __device__ __forceinline__ void finish(const LinCol &c, long long row0, int step, int count, float (&p)[R],
-                                       const float (&u)[R]) {
+                                       const float (&u)[R], const bf16 (&r)[R]) {
   activate_run(p, c.act);
   if (kGated) {
 #pragma unroll
     for (int e = 0; e < R; ++e) p[e] *= u[e];
   }
   if (c.res) {
-    const bf16 *res = c.res + row0 * c.ldres;
-    const long long d = step * c.ldres;
-    bf16 r[R];
-#pragma unroll
-    for (int e = 0; e < R; ++e)
-      if (e < count) r[e] = res[e * d];
 #pragma unroll
     for (int e = 0; e < R; ++e)
       if (e < count) p[e] += __bfloat162float(r[e]);
@@ -566,7 +570,11 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
       if (direct) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += b;
-        if (c.y) finish<false>(c, (long long)m0 + t0, 1, rows - t0, v, v);
+        if (c.y) {
+          bf16 r[8];
+          load_rows(c, (long long)m0 + t0, 1, rows - t0, r);
+          finish<false>(c, (long long)m0 + t0, 1, rows - t0, v, v, r);
+        }
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -585,21 +593,30 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     tmem_dealloc(tmem, L::kCols);
   }
   if (split == 1 && !kGated) return;
-  if (split > 1) cluster_sync();
   // This CTA's tokens, every column of the tile: a thread keeps to one column.
+  // The residual is loaded one run of tokens ahead.
   const int mine = (rows - rank + split - 1) / split;
   const int n = tid % kOut;
   constexpr int kShare = kSkinnyThreads / kOut;  // 1 or 3 threads per column
-  if (tid >= kShare * kOut) return;
-  const LinCol c = column(g, n0 + n);
+  constexpr int kRun = NT <= 32 ? 4 : 8;         // tokens finished side by side
+  const LinCol c = tid < kShare * kOut ? column(g, n0 + n) : LinCol{};
+  const long long row0 = (long long)m0 + rank;
+  bf16 ahead[kRun];
+  int t = kRun * (tid / kOut);
+  if (c.y) load_rows(c, row0 + (long long)t * split, split, mine - t, ahead);
+  if (split > 1) cluster_sync();
   if (!c.y) return;
   float b = 0.f, bu = 0.f;
   if (bias) {
     b = __bfloat162float(bias[n0 + n]);
     if (kGated) bu = __bfloat162float(bias[(long long)g.N + n0 + n]);
   }
-  constexpr int kRun = NT <= 64 ? 4 : 8;  // tokens finished side by side
-  for (int t = kRun * (tid / kOut); t < mine; t += kRun * kShare) {
+  for (; t < mine; t += kRun * kShare) {
+    bf16 res[kRun];
+#pragma unroll
+    for (int e = 0; e < kRun; ++e) res[e] = ahead[e];
+    const int next = t + kRun * kShare;
+    load_rows(c, row0 + (long long)next * split, split, mine - next, ahead);
     float p[kRun], u[kRun];
 #pragma unroll
     for (int e = 0; e < kRun; ++e) p[e] = b, u[e] = bu;
@@ -612,7 +629,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
           if (kGated) u[e] += src[e * kRowsW + kOut];
         }
     }
-    finish<kGated>(c, (long long)m0 + rank + (long long)t * split, split, mine - t, p, u);
+    finish<kGated>(c, row0 + (long long)t * split, split, mine - t, p, u, res);
   }
 }
 
