@@ -321,6 +321,14 @@ size_t rows_bytes(long long rows, long long ld, long long cols, size_t el) {
   return ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * el;
 }
 
+// Whether rows of wa bytes at a and of wb bytes at b, both `pitch` bytes apart,
+// are disjoint column blocks of one buffer.
+bool column_blocks(const void *a, size_t wa, const void *b, size_t wb, size_t pitch) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  const size_t d = x <= y ? (y - x) % pitch : (pitch - (x - y) % pitch) % pitch;  // b's column, from a's
+  return d >= wa && d + wb <= pitch;
+}
+
 gdn_status linattn_impl(const gdn_shape *shape, const gdn_linattn_io *io, bool decode, void *stream) {
   if (!shape || !io) return GDN_ERR_INVALID_ARG;
   if (shape->B < 1 || shape->T < 1) return GDN_ERR_INVALID_ARG;
@@ -559,10 +567,16 @@ gdn_status gdn_linear_ex(int M, int N, int K, int gated, const void *x, long lon
   for (int o = 0; o < n_out; ++o) {
     for (const Range &r : in)
       if (overlap(ro[o], r)) return GDN_ERR_ALIAS;
+    const size_t w = (size_t)(out[o].col_end - out[o].col_begin) * 2, pitch = (size_t)out[o].ld * 2;
     for (int p = 0; p < n_out; ++p) {
-      if (p < o && overlap(ro[o], ro[p])) return GDN_ERR_ALIAS;
+      const size_t wp = (size_t)(out[p].col_end - out[p].col_begin) * 2;
+      if (p < o && overlap(ro[o], ro[p]) &&
+          !(out[p].ld == out[o].ld && column_blocks(out[o].ptr, w, out[p].ptr, wp, pitch)))
+        return GDN_ERR_ALIAS;
       const bool in_place = p == o && out[o].residual == out[o].ptr && out[o].ldr == out[o].ld;
-      if (!in_place && overlap(ro[o], rr[p])) return GDN_ERR_ALIAS;
+      if (!in_place && overlap(ro[o], rr[p]) &&
+          !(out[p].ldr == out[o].ld && column_blocks(out[o].ptr, w, out[p].residual, wp, pitch)))
+        return GDN_ERR_ALIAS;
     }
   }
   DeviceInfo dev;

@@ -227,6 +227,43 @@ __device__ __forceinline__ void store_run(const LinArgs &g, long long row0, int 
   }
 }
 
+// One epilogue warp's share of a tile: rows row0 .. row0 + 31 (the TMEM lanes at
+// taddr), kCols / 2 output columns from tile0 + first.  `wait` waits for the
+// accumulator; the residual is loaded one run ahead, the first one before it.
+template <int kCols, bool kGated, typename Wait>
+__device__ __forceinline__ bool tile_epilogue(const LinArgs &g, float *run, int lane, long long row0, int tile0, int first,
+                                              uint32_t taddr, Wait wait) {
+  const bf16 *bias = static_cast<const bf16 *>(g.bias);
+  uint32_t ahead[16];
+  int loaded = prefetch_residual(g, row0, lane, tile0 + first, ahead);
+  if (!wait()) {
+    if (lane == 0) atomicOr(g.err, kErrTimeout);
+    return false;
+  }
+  fence_after();
+#pragma unroll 1
+  for (int c = first; c < first + kCols / 2; c += 32) {
+    uint32_t x[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = ahead[e];
+    const int now = loaded;
+    const int col0 = tile0 + c;
+    if (c + 32 < first + kCols / 2) loaded = prefetch_residual(g, row0, lane, col0 + 32, ahead);
+    float v[32], u[32];
+    tmem_ld32(taddr + c, v);  // every lane of the warp takes part
+    if (kGated) tmem_ld32(taddr + kCols + c, u);
+    if (row0 >= g.M || col0 >= g.N) continue;
+    if (bias) {
+      add_bias(v, bias, col0, g.N - col0);
+      if (kGated) add_bias(u, bias, (long long)g.N + col0, g.N - col0);
+    }
+    store_run<kGated>(g, row0, lane, col0, v, u, run, now, x);
+  }
+  fence_before();
+  __syncwarp();
+  return true;
+}
+
 template <int BN, bool kGated>
 __global__ void __launch_bounds__(kTileThreads, 1)
     lin_tile_kernel(const LinArgs g, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w) {
@@ -315,45 +352,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   } else {
     // ---- epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 = tile rows
     const int quad = warp & 3, half = (warp - 2) >> 2;
-    const bf16 *bias = static_cast<const bf16 *>(g.bias);
     float *run = reinterpret_cast<float *>(sm + L::kRun) + (warp - 2) * 32 * 33;
     int local = 0;
     for (int t = blockIdx.x; t < ntiles; t += gridDim.x, ++local) {
       int mt, nt;
       tile_of(t, tiles_m, tiles_n, mt, nt);
       const int acc = local & 1;
-      const long long row0 = (long long)mt * BM + 32 * quad;
-      const int first = half * (kCols / 2);
-      // The residual is loaded one run ahead, the first one under the MMAs.
-      uint32_t ahead[16];
-      int loaded = prefetch_residual(g, row0, lane, nt * kCols + first, ahead);
-      const bool got = bar_wait(&B.tfull[acc], (local >> 1) & 1);
-      if (!__all_sync(0xffffffffu, got)) {
-        if (lane == 0) atomicOr(g.err, kErrTimeout);
-        break;
-      }
-      fence_after();
+      const auto wait = [&]() { return __all_sync(0xffffffffu, bar_wait(&B.tfull[acc], (local >> 1) & 1)); };
       const uint32_t taddr = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * BN);
-#pragma unroll 1
-      for (int c = first; c < first + kCols / 2; c += 32) {
-        uint32_t x[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = ahead[e];
-        const int now = loaded;
-        const int col0 = nt * kCols + c;
-        if (c + 32 < first + kCols / 2) loaded = prefetch_residual(g, row0, lane, col0 + 32, ahead);
-        float v[32], u[32];
-        tmem_ld32(taddr + c, v);  // every lane of the warp takes part
-        if (kGated) tmem_ld32(taddr + kCols + c, u);
-        if (row0 >= g.M || col0 >= g.N) continue;
-        if (bias) {
-          add_bias(v, bias, col0, g.N - col0);
-          if (kGated) add_bias(u, bias, (long long)g.N + col0, g.N - col0);
-        }
-        store_run<kGated>(g, row0, lane, col0, v, u, run, now, x);
-      }
-      fence_before();
-      __syncwarp();
+      if (!tile_epilogue<kCols, kGated>(g, run, lane, (long long)mt * BM + 32 * quad, nt * kCols, half * (kCols / 2), taddr, wait))
+        break;
       if (lane == 0) arrive(&B.tempty[acc]);  // this warp has read its lanes: the accumulator may be refilled
     }
   }
@@ -363,6 +371,175 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (warp == 1) {
     fence_after();
     tmem_dealloc(tmem, 2 * BN);
+  }
+}
+
+// =============================================================================
+// lin_pair_kernel: 256 x 256 tiles by pairs of CTAs (cta_group::2).  Each CTA
+// loads half of x's rows and half of w's; one MMA of the pair reads both, so that
+// a CTA moves a third fewer bytes per flop than with a 128 x 256 tile of its own.
+// Each CTA's TMEM holds its 128 rows of the result.  Gated: CTA 0's rows of w are
+// the gate's, CTA 1's the up half's.
+// =============================================================================
+constexpr int kPairStages = 6;
+constexpr uint32_t kPairHalf = 128 * BK * 2;          // 16 KB: this CTA's rows of x, or of w
+constexpr uint32_t kPairStage = 2 * kPairHalf;
+constexpr uint32_t kPairBars = kPairStages * kPairStage;
+constexpr uint32_t kPairRun = kPairBars + 256;
+constexpr uint32_t kPairSmem = kPairRun + kEpiWarps * 32 * 33 * 4 + 1024;
+static_assert(kPairSmem <= 232448, "shared memory per CTA");
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this CTA's `saddr` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+// Lane 0 of a converged warp: a 3-d box into this CTA, completing on the mbarrier
+// at the cluster address `bar`, which may be the pair's other CTA's.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void *map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .u32 l;\n\tmov.u32 l, %%laneid;\n\tsetp.eq.u32 e, l, 0;\n\t"
+      "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];\n\t}\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(0), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .u32 l;\n\tmov.u32 l, %%laneid;\n\tsetp.eq.u32 e, l, 0;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate));
+}
+// Arrive on `bar` in both CTAs once every MMA issued before is complete.
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t.reg .u32 l;\n\tmov.u32 l, %%laneid;\n\tsetp.eq.u32 e, l, 0;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+template <bool kGated>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    lin_pair_kernel(const LinArgs g, const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w) {
+  constexpr int kCols = kGated ? 128 : 256;  // output columns of a tile
+  extern __shared__ uint8_t smem_raw[];
+  // The same offset in both CTAs: the descriptors of one serve the other's tiles.
+  uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  Bars &B = *reinterpret_cast<Bars *>(sm + kPairBars);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int tiles_m = (g.M + 255) / 256, tiles_n = (g.N + kCols - 1) / kCols;
+  const int ntiles = tiles_m * tiles_n;
+  const int nk = (g.K + BK - 1) / BK;
+  const uint32_t sbase = smem_u32(sm);
+
+  if (tid == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      bar_init(&B.full[s], 1);
+      bar_init(&B.empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      bar_init(&B.tfull[a], 1);
+      bar_init(&B.tempty[a], 2 * kEpiWarps);  // both CTAs' (used in CTA 0)
+    }
+    bar_init(&B.end, 1);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B.tmem)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  cluster_sync();  // the other CTA's barriers are ready too
+  fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);
+  bool ok = true;
+
+  if (warp == 0) {
+    // ---- TMA producer: both CTAs' tiles complete on CTA 0's barriers
+    uint32_t it = 0;
+    for (int t = pair; t < ntiles && ok; t += pairs) {
+      int mt, nt;
+      tile_of(t, tiles_m, tiles_n, mt, nt);
+      const int xrow = mt * 256 + 128 * rank;
+      const int wrow = kGated ? rank * g.N + nt * kCols : nt * kCols + 128 * rank;
+      for (int kb = 0; kb < nk && ok; ++kb, ++it) {
+        const int s = it % kPairStages;
+        ok = __all_sync(0xffffffffu, bar_wait(&B.empty[s], ((it / kPairStages) & 1) ^ 1));
+        if (!ok) break;
+        const uint32_t dst = sbase + s * kPairStage, bar = map_rank(smem_u32(&B.full[s]), 0);
+        if (rank == 0) bar_expect_tx_w(&B.full[s], 2 * kPairStage);
+        tma_load_3d_pair(dst, &tm_x, kb * BK, xrow, bar);
+        tma_load_3d_pair(dst + kPairHalf, &tm_w, kb * BK, wrow, bar);
+      }
+    }
+    // Leave only when every stage issued has been consumed (bounded).
+    for (uint32_t j = (it > kPairStages ? it - kPairStages : 0); ok && j < it; ++j)
+      ok = __all_sync(0xffffffffu, bar_wait(&B.empty[j % kPairStages], (j / kPairStages) & 1));
+    if (!ok && lane == 0) atomicOr(g.err, kErrTimeout);
+  } else if (warp == 1 && rank == 0) {
+    // ---- MMA issuer of the pair
+    const uint32_t id = idesc_bf16(256, 256);
+    uint32_t it = 0;
+    int local = 0;
+    for (int t = pair; t < ntiles && ok; t += pairs, ++local) {
+      const int acc = local & 1;
+      ok = __all_sync(0xffffffffu, bar_wait(&B.tempty[acc], ((local >> 1) & 1) ^ 1));
+      if (!ok) break;
+      fence_after();
+      const uint32_t d = tmem + (uint32_t)(acc * 256);
+      for (int kb = 0; kb < nk; ++kb, ++it) {
+        const int s = it % kPairStages;
+        ok = __all_sync(0xffffffffu, bar_wait(&B.full[s], (it / kPairStages) & 1));
+        if (!ok) break;
+        fence_after();
+        const uint32_t a0 = sbase + s * kPairStage, b0 = a0 + kPairHalf;
+#pragma unroll
+        for (int ks = 0; ks < BK / 16; ++ks)
+          mma_pair(d, desc_k(a0, ks, 128), desc_k(b0, ks, 128), id, (kb > 0 || ks > 0) ? 1u : 0u);
+        commit_pair(&B.empty[s]);
+      }
+      if (!ok) break;
+      commit_pair(&B.tfull[acc]);
+    }
+    commit_pair(&B.end);  // every MMA issued is complete before TMEM is freed
+    if (!__all_sync(0xffffffffu, bar_wait(&B.end, 0))) ok = false;
+    if (!ok && lane == 0) atomicOr(g.err, kErrTimeout);
+  } else if (warp >= 2) {
+    // ---- epilogue of this CTA's 128 rows
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    float *run = reinterpret_cast<float *>(sm + kPairRun) + (warp - 2) * 32 * 33;
+    int local = 0;
+    for (int t = pair; t < ntiles; t += pairs, ++local) {
+      int mt, nt;
+      tile_of(t, tiles_m, tiles_n, mt, nt);
+      const int acc = local & 1;
+      const auto wait = [&]() { return __all_sync(0xffffffffu, bar_wait(&B.tfull[acc], (local >> 1) & 1)); };
+      const uint32_t taddr = tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * 256);
+      if (!tile_epilogue<kCols, kGated>(g, run, lane, (long long)mt * 256 + 128 * rank + 32 * quad, nt * kCols,
+                                        half * (kCols / 2), taddr, wait))
+        break;
+      if (lane == 0)  // this warp has read its lanes: the accumulator may be refilled
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                         map_rank(smem_u32(&B.tempty[acc]), 0))
+                     : "memory");
+    }
+  }
+  __syncwarp();
+
+  fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other reads its tiles or arrives on its barriers
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }
 }
 
@@ -393,15 +570,7 @@ struct SkinnyBars {
   uint32_t tmem;
 };
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address of this CTA's `saddr` in CTA `rank` of the cluster, and a store there.
-__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
+// A store to an address of the cluster (map_rank).
 __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -652,6 +821,35 @@ struct TileTag {};
 template <int NT, bool kGated>
 struct SkinnyTag {};
 
+template <bool kGated>
+struct PairTag {};
+
+template <bool kGated>
+cudaError_t launch_pair(const LinArgs &a, int num_sms, cudaStream_t s) {
+  CUtensorMap tm_x, tm_w;
+  if (!encode_kmajor(&tm_x, a.x, a.M, a.K, a.ldx, 128) ||
+      !encode_kmajor(&tm_w, a.w, (long long)a.N * (kGated ? 2 : 1), a.K, a.ldw, 128))
+    return cudaErrorInvalidValue;
+  auto *kernel = lin_pair_kernel<kGated>;
+  cudaError_t e = allow_smem<PairTag<kGated>>(kernel, kPairSmem);
+  if (e != cudaSuccess) return e;
+  constexpr int kCols = kGated ? 128 : 256;
+  const long long ntiles = (long long)((a.M + 255) / 256) * ((a.N + kCols - 1) / kCols);
+  const long long pairs = ntiles < num_sms / 2 ? ntiles : num_sms / 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, tm_x, tm_w);
+}
+
 template <int BN, bool kGated>
 cudaError_t launch_tile(const LinArgs &a, int num_sms, cudaStream_t s) {
   CUtensorMap tm_x, tm_w;
@@ -702,14 +900,14 @@ cudaError_t launch_skinny(const LinArgs &a, int num_sms, cudaStream_t s) {
 }
 
 // Microseconds of the tile kernel with tiles of BN w rows: a wave's k steps or
-// its epilogue, whichever is longer, and the last epilogue.  Measured: 0.36 us per
+// its epilogue, whichever is longer, and the last epilogue.  Measured: 0.40 us per
 // 64-wide k step at 256, which falls less than the tile does; 1.5 us per 64
 // columns of epilogue.
 template <bool kGated>
 float tile_cost(const LinArgs &a, int BN, int num_sms) {
   const int cols = kGated ? BN / 2 : BN, nk = (a.K + BK - 1) / BK;
   const long long tiles = (long long)((a.M + BM - 1) / BM) * ((a.N + cols - 1) / cols);
-  const float loop = (BN == 256 ? 0.36f : BN == 128 ? 0.24f : 0.19f) * nk, epi = 1.5f * cols / 64;
+  const float loop = (BN == 256 ? 0.40f : BN == 128 ? 0.24f : 0.19f) * nk, epi = 1.5f * cols / 64;
   return (float)((tiles + num_sms - 1) / num_sms) * (loop > epi ? loop : epi) + epi;
 }
 
@@ -726,6 +924,12 @@ cudaError_t launch(const LinArgs &a, int num_sms, cudaStream_t s) {
     const float skinny = split < 2 ? 1e30f : 0.6f * nk / (split > 8 ? 8 : split) + (residual ? 14.f : 8.f);
     const float t256 = tile_cost<kGated>(a, 256, num_sms), t128 = tile_cost<kGated>(a, 128, num_sms);
     const float t64 = kGated ? 1e30f : tile_cost<kGated>(a, 64, num_sms);
+    // Pairs: 0.37 us per k step of a wave of their 256 x 256 tiles.
+    const int cols = kGated ? 128 : 256;
+    const long long tiles = (long long)((a.M + 255) / 256) * ((a.N + cols - 1) / cols);
+    const float loop = 0.37f * nk, epi = 1.5f * cols / 64;
+    const float pair = (float)((tiles + num_sms / 2 - 1) / (num_sms / 2)) * (loop > epi ? loop : epi) + epi;
+    if (pair <= t256 && pair <= t128 && pair <= t64 && pair <= skinny) return launch_pair<kGated>(a, num_sms, s);
     if (skinny > t256 || skinny > t128 || skinny > t64) {
       if (t256 <= t128 && t256 <= t64) return launch_tile<256, kGated>(a, num_sms, s);
       if (t128 <= t64) return launch_tile<128, kGated>(a, num_sms, s);

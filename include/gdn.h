@@ -330,8 +330,9 @@ gdn_status gdn_linear(int M, int N, int K, const void *x, long long ldx, const v
  *   out[0 .. n_out-1], 1 <= n_out <= 4: disjoint ranges of the N output
  *     columns; each has its own activation and, or NULL, its own residual
  *     [M][ldr] whose column 0 is col_begin.  A residual may be exactly the
- *     range's output (same pointer and stride: y is then added in place); it
- *     must not otherwise overlap an output.
+ *     range's output (same pointer and stride: y is then added in place).
+ *     Otherwise outputs and residuals must not overlap, except as disjoint
+ *     column blocks of one buffer (the same stride).
  * Columns not covered by any range are computed and dropped.
  */
 typedef enum {

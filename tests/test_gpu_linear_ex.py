@@ -139,3 +139,9 @@ def test_repeats_bit_for_bit_on_a_side_stream_and_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y[0], y[1]) and torch.equal(y[0], y[2])
+
+
+@pytest.mark.parametrize("M,N,K", [(4096, 4096, 320), (2049, 5000, 1000), (8192, 2056, 64)])
+def test_pairs_of_ctas(M, N, K):
+    check(M, N, K, seed=20, residual=True)
+    check(M, N, K, gated=True, seed=21, bias=K != 64)

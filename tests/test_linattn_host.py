@@ -143,3 +143,18 @@ def test_packed_layouts_are_the_structures():
         vals = [float(i) if t is ctypes.c_float else i for i, (_, t) in enumerate(cls._fields_, 1)]
         got = cls.from_buffer_copy(fmt.pack(*vals))
         assert [getattr(got, f) for f, _ in cls._fields_] == vals
+
+
+def test_linear_ex_outputs_may_be_column_blocks_of_one_buffer(L):
+    def two(off, wa=8, wb=8, ld=24, ld2=None):
+        return [(0, wa, fake(2), ld, 0, None, 0), (16 - wb, 16, fake(2, off), ld2 or ld, 0, None, 0)]
+    assert linear(L, outs=two(16)) in OK_ON_HOST                  # right behind the first block
+    assert linear(L, outs=two(32)) in OK_ON_HOST                  # the last 8 of 24 columns
+    assert linear(L, outs=two(48 * 3 + 16)) in OK_ON_HOST         # the same block, three rows further down
+    assert linear(L, outs=two(14)) == 4                           # one column shared
+    assert linear(L, outs=two(34)) == 4                           # the last column is the next row's first
+    assert linear(L, outs=two(16, ld2=32)) == 4                   # another stride
+    # the earlier block behind the later one, and a residual next to an output
+    assert linear(L, outs=[(8, 16, fake(2, 16), 24, 0, None, 0), (0, 8, fake(2), 24, 0, None, 0)]) in OK_ON_HOST
+    assert linear(L, outs=[(0, 8, fake(2), 24, 0, fake(2, 16), 24)]) in OK_ON_HOST
+    assert linear(L, outs=[(0, 8, fake(2), 24, 0, fake(2, 8), 24)]) == 4
