@@ -190,6 +190,19 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
   }
   return __all_sync(0xffffffffu, ok);
 }
+// Two barriers: both are looked at before either answer is needed.
+__device__ __forceinline__ bool warp_wait2(uint64_t *bar0, uint32_t parity0, uint64_t *bar1, uint32_t parity1) {
+  bool ok0 = bar_try_wait(bar0, parity0), ok1 = bar_try_wait(bar1, parity1);
+  if (!(ok0 && ok1)) {
+    const uint32_t t0 = global_ns_lo();
+#pragma unroll 1
+    do {
+      ok0 = ok0 || bar_try_wait(bar0, parity0);
+      ok1 = ok1 || bar_try_wait(bar1, parity1);
+    } while (!(ok0 && ok1) && global_ns_lo() - t0 < 1000000000u);
+  }
+  return __all_sync(0xffffffffu, ok0 && ok1);
+}
 // One arrival per warp, behind all of its lanes.
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
   __syncwarp();
@@ -469,12 +482,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool more = n + 1 < n_chunks;
       if (!kStateOnly) {
         if (more) {  // the next P, once the update has read the Gamma V in its columns
-          ok = warp_wait(&B.full[s1], ((n + 1) / kStages) & 1) && warp_wait(&B.p_loaded, par) &&
-               warp_wait(&B.su_done[n & 1], par2);
+          // (P itself has been loaded: Gamma V, and so the update, waited for that)
+          ok = warp_wait2(&B.full[s1], ((n + 1) / kStages) & 1, &B.su_done[n & 1], par2);
           fence_after();
           if (ok) issue_qk(s1);
         }
-        ok = ok && warp_wait(&B.p_ready, par) && warp_wait(&B.o_free, par ^ 1);
+        ok = ok && warp_wait2(&B.p_ready, par, &B.o_free, par ^ 1);
         if (!ok) break;
         fence_after();
         const uint32_t q = sbase + s * kStageBytes, v = q + 2 * kTile;
@@ -498,10 +511,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       commit_w(&B.empty[s]);  // the update of chunk n was issued before
       if (more) {
         if (kStateOnly) ok = warp_wait(&B.full[s1], ((n + 1) / kStages) & 1);
-        ok = ok && warp_wait(&B.gv_ready[(n + 1) & 1], ((n + 1) >> 1) & 1);
-        // the columns that the update goes to have been read
-        if (!kStateOnly) ok = ok && warp_wait(&B.ds_free[n & 1], par2);
-        if (kStateOnly && n > 0) ok = ok && warp_wait(&B.ds_free[(n - 1) & 1], ((n - 1) >> 1) & 1);
+        // Gamma V is there, and the columns that the update goes to have been read
+        const int before = kStateOnly ? n - 1 : n;
+        if (before >= 0)
+          ok = ok && warp_wait2(&B.gv_ready[(n + 1) & 1], ((n + 1) >> 1) & 1, &B.ds_free[before & 1], (before >> 1) & 1);
+        else
+          ok = ok && warp_wait(&B.gv_ready[(n + 1) & 1], ((n + 1) >> 1) & 1);
         fence_after();
         if (ok) issue_su(n + 1);
       }
@@ -654,6 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long at = (row0 + (long long)c0 * kC + odd) * a.ldo + h * kD + (v & ~1);
     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o);
     const float2 scale = make_float2(a.scale, a.scale);
+    const uint32_t take = odd ? 0x3276 : 0x5410;  // (other's, own) high halves, or (own, other's) low halves
     for (int n = 0; n < n_chunks; ++n) {
       ok = warp_wait(&B.o_done, n & 1);
       if (!ok) break;
@@ -676,8 +692,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               scale, __ffma2_rn(*reinterpret_cast<const float2 *>(&cv.eG[16 * i + e]),
                                 make_float2(__uint_as_float(r1[e]), __uint_as_float(r1[e + 1])),
                                 make_float2(__uint_as_float(r2[e]), __uint_as_float(r2[e + 1]))));
-          const float other = __shfl_xor_sync(0xffffffffu, odd ? y.x : y.y, 1);
-          const uint32_t w = odd ? pack_bf16(other, y.y) : pack_bf16(y.x, other);
+          const uint32_t own = pack_bf16(y.x, y.y), other = __shfl_xor_sync(0xffffffffu, own, 1);
+          const uint32_t w = __byte_perm(own, other, take);
           if (16 * i + e < len && in_bounds(at + 2, o_size, a.err)) *reinterpret_cast<uint32_t *>(o + at) = w;
           at += 2 * a.ldo;
         }
