@@ -532,6 +532,8 @@ gdn_status gdn_linear_ex(int M, int N, int K, int gated, const void *x, long lon
   if (ldx < K || ldw < K) return GDN_ERR_INVALID_ARG;
   if (M > (1 << 30) || N > (1 << 29) || K > (1 << 30) || ldx > (1LL << 32) || ldw > (1LL << 32))
     return GDN_ERR_UNSUPPORTED_SHAPE;
+  // The kernels count their tiles (128 x 64 the smallest) in 31 bits.
+  if (((M + 127LL) / 128) * ((N + 63LL) / 64) >= (1LL << 31)) return GDN_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(x) || !aligned16(w) || !aligned16(bias) || (ldx % 8) != 0 || (ldw % 8) != 0) return GDN_ERR_ALIGNMENT;
   gdn::LinArgs a{};
   a.M = M;

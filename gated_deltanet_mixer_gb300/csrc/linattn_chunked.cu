@@ -31,6 +31,14 @@
 // into segments: a first launch (kStateOnly) forms the state of each segment's
 // parts from zero, a small one turns those into the state before every segment,
 // and a third starts every segment from its own.  Cost: k and v are read twice.
+//
+// Bound: a chunk of 64 tokens takes about 3,900 cycles of its SM, of which the
+// tensor pipe works 1,900 (47 %) and instruction issue 50 %; what paces it is the
+// chain update -> P and Gamma V -> next update, not memory (4 x 8192 tokens, 16/32
+// heads: 258 us, 3.1 TB/s of the 0.81 GB that the call cannot do without, where
+// a copy runs at 6.8; 65536 tokens, 16/48 heads: 940 us).  The loops of the roles
+// share one instruction cache: unrolled further, from 56 to 65 KB of code, the
+// kernel took 10 % longer.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -399,131 +407,131 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 20) {
     regs_dec<kRegsIssue>();
-   if (warp == 20) {
-    // ---- TMA producer and the chunk vectors
-    auto load_g = [&](int c, float &g0, float &g1) {
-      g0 = g1 = 0.f;
-      const int t = c * kC + lane;
-      if (a.g) {
-        if (t < T) g0 = a.g[(row0 + t) * a.Hv + h];
-        if (t + 32 < T) g1 = a.g[(row0 + t + 32) * a.Hv + h];
-      } else {
-        const float gh = a.log_decay[h];
-        if (t < T) g0 = gh;
-        if (t + 32 < T) g1 = gh;
-      }
-      g0 = fmaxf(g0, kMinLogDecay);
-      g1 = fmaxf(g1, kMinLogDecay);
-    };
-    float g0 = 0.f, g1 = 0.f;
-    if (n_chunks > 0) load_g(c0, g0, g1);
-    int n = 0;
-    for (; n < n_chunks; ++n) {
-      const int s = n % kStages;
-      if (!warp_wait(&B.empty[s], ((n / kStages) & 1) ^ 1)) {
-        ok = false;
-        break;
-      }
-      const int c = c0 + n;
-      if (lane == 0) {
-        const uint32_t dst = sbase + s * kStageBytes;
-        const int row = (int)(row0 + (long long)c * kC);
-        bar_expect_tx(&B.full[s], kStateOnly ? 2 * kTile : 3 * kTile);
-        for (int x = 0; x < 2; ++x) {
-          if (!kStateOnly) tma_load_3d(dst + x * (kTile / 2), &tm_q, kh * kD + 64 * x, row, 0, &B.full[s]);
-          tma_load_3d(dst + kTile + x * (kTile / 2), &tm_k, kh * kD + 64 * x, row, 0, &B.full[s]);
-          tma_load_3d(dst + 2 * kTile + x * (kTile / 2), &tm_v, h * kD + 64 * x, row, 0, &B.full[s]);
+    if (warp == 20) {
+      // ---- TMA producer and the chunk vectors
+      auto load_g = [&](int c, float &g0, float &g1) {
+        g0 = g1 = 0.f;
+        const int t = c * kC + lane;
+        if (a.g) {
+          if (t < T) g0 = a.g[(row0 + t) * a.Hv + h];
+          if (t + 32 < T) g1 = a.g[(row0 + t + 32) * a.Hv + h];
+        } else {
+          const float gh = a.log_decay[h];
+          if (t < T) g0 = gh;
+          if (t + 32 < T) g1 = gh;
         }
-      }
-      chunk_vec(B.vec[n % kVecs], g0, g1, T - c * kC, lane);
-      __syncwarp();
-      if (lane == 0) arrive(&B.full[s]);
-      if (n + 1 < n_chunks) load_g(c + 1, g0, g1);
-    }
-    // Leave only when every tile issued has been consumed (bounded).
-    for (int j = max(0, n - kStages); ok && j < n; ++j)
-      if (!warp_wait(&B.empty[j % kStages], (j / kStages) & 1)) ok = false;
-   } else if (warp == 21) {
-    // ---- MMA issuer (the whole warp; lane 0 issues)
-    const uint32_t id_p = idesc_bf16(64, 64, 0, 0);     // Q K^T
-    const uint32_t id_o1 = idesc_bf16(128, 64, 0, 0);   // S Q^T
-    const uint32_t id_o2 = idesc_bf16(128, 64, 1, 0);   // V^T P^T
-    const uint32_t id_su = idesc_bf16(128, 128, 0, 1);  // (Gamma V)^T K
-    auto issue_qk = [&](int s) {
-      const uint32_t q = sbase + s * kStageBytes, k = q + kTile;
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)  // 64 of the 128 columns at a time
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_w(tmem + kTP, desc_k(q + kb * (kTile / 2), ks, kC), desc_k(k + kb * (kTile / 2), ks, kC), id_p, kb > 0 || ks > 0);
-      commit_w(&B.qk_done);
-    };
-    auto issue_su = [&](int n) {
-      const uint32_t k = sbase + (n % kStages) * kStageBytes + kTile;
-#pragma unroll
-      for (int p = 0; p < kPieces; ++p)  // small pieces first
-#pragma unroll
-        for (int ks = 0; ks < kC / 16; ++ks)
-          mma_ta_w(tmem + ds_col<kStateOnly>(n), tmem + gv_col<kStateOnly>(n) + p * (kC / 2) + ks * 8, desc_mn(k, ks, kC),
-                   id_su, p > 0 || ks > 0);
-      commit_w(&B.su_done[n & 1]);
-    };
-    if (n_chunks > 0) {
-      ok = warp_wait(&B.full[0], 0);
-      fence_after();
-      if (ok && !kStateOnly) issue_qk(0);
-      if (ok) ok = warp_wait(&B.gv_ready[0], 0);
-      fence_after();
-      if (ok) issue_su(0);
-    }
-    for (int n = 0; n < n_chunks && ok; ++n) {
-      const int s = n % kStages, s1 = (n + 1) % kStages;
-      const uint32_t par = n & 1, par2 = (n >> 1) & 1;
-      const bool more = n + 1 < n_chunks;
-      if (!kStateOnly) {
-        if (more) {  // the next P, once the update has read the Gamma V in its columns
-          // (P itself has been loaded: Gamma V, and so the update, waited for that)
-          ok = warp_wait2(&B.full[s1], ((n + 1) / kStages) & 1, &B.su_done[n & 1], par2);
-          fence_after();
-          if (ok) issue_qk(s1);
+        g0 = fmaxf(g0, kMinLogDecay);
+        g1 = fmaxf(g1, kMinLogDecay);
+      };
+      float g0 = 0.f, g1 = 0.f;
+      if (n_chunks > 0) load_g(c0, g0, g1);
+      int n = 0;
+      for (; n < n_chunks; ++n) {
+        const int s = n % kStages;
+        if (!warp_wait(&B.empty[s], ((n / kStages) & 1) ^ 1)) {
+          ok = false;
+          break;
         }
-        ok = ok && warp_wait2(&B.p_ready, par, &B.o_free, par ^ 1);
-        if (!ok) break;
-        fence_after();
-        const uint32_t q = sbase + s * kStageBytes, v = q + 2 * kTile;
+        const int c = c0 + n;
+        if (lane == 0) {
+          const uint32_t dst = sbase + s * kStageBytes;
+          const int row = (int)(row0 + (long long)c * kC);
+          bar_expect_tx(&B.full[s], kStateOnly ? 2 * kTile : 3 * kTile);
+          for (int x = 0; x < 2; ++x) {
+            if (!kStateOnly) tma_load_3d(dst + x * (kTile / 2), &tm_q, kh * kD + 64 * x, row, 0, &B.full[s]);
+            tma_load_3d(dst + kTile + x * (kTile / 2), &tm_k, kh * kD + 64 * x, row, 0, &B.full[s]);
+            tma_load_3d(dst + 2 * kTile + x * (kTile / 2), &tm_v, h * kD + 64 * x, row, 0, &B.full[s]);
+          }
+        }
+        chunk_vec(B.vec[n % kVecs], g0, g1, T - c * kC, lane);
+        __syncwarp();
+        if (lane == 0) arrive(&B.full[s]);
+        if (n + 1 < n_chunks) load_g(c + 1, g0, g1);
+      }
+      // Leave only when every tile issued has been consumed (bounded).
+      for (int j = max(0, n - kStages); ok && j < n; ++j)
+        if (!warp_wait(&B.empty[j % kStages], (j / kStages) & 1)) ok = false;
+    } else if (warp == 21) {
+      // ---- MMA issuer (the whole warp; lane 0 issues)
+      const uint32_t id_p = idesc_bf16(64, 64, 0, 0);     // Q K^T
+      const uint32_t id_o1 = idesc_bf16(128, 64, 0, 0);   // S Q^T
+      const uint32_t id_o2 = idesc_bf16(128, 64, 1, 0);   // V^T P^T
+      const uint32_t id_su = idesc_bf16(128, 128, 0, 1);  // (Gamma V)^T K
+      auto issue_qk = [&](int s) {
+        const uint32_t q = sbase + s * kStageBytes, k = q + kTile;
 #pragma unroll
-        for (int p = 1; p >= 0; --p)
-#pragma unroll
-          for (int ks = 0; ks < kC / 16; ++ks)
-            mma_w(tmem + kTO2, desc_mn(v, ks, kC), desc_k(sbase + kP + p * kPTile, ks, kC), id_o2, p < 1 || ks > 0);
-        ok = ok && warp_wait(&B.s_ready, par);
-        if (!ok) break;
-        fence_after();
-#pragma unroll
-        for (int p = 3; p >= 0; --p) {  // the second piece's two halves, then the first's
-          const uint32_t qh = q + (p & 1) * (kTile / 2);
+        for (int kb = 0; kb < 2; ++kb)  // 64 of the 128 columns at a time
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            mma_ta_w(tmem + kTO1, tmem + kTSh + p * 32 + ks * 8, desc_k(qh, ks, kC), id_o1, p < 3 || ks > 0);
-        }
-        commit_w(&B.o_done);
-      }
-      commit_w(&B.empty[s]);  // the update of chunk n was issued before
-      if (more) {
-        if (kStateOnly) ok = warp_wait(&B.full[s1], ((n + 1) / kStages) & 1);
-        // Gamma V is there, and the columns that the update goes to have been read
-        const int before = kStateOnly ? n - 1 : n;
-        if (before >= 0)
-          ok = ok && warp_wait2(&B.gv_ready[(n + 1) & 1], ((n + 1) >> 1) & 1, &B.ds_free[before & 1], (before >> 1) & 1);
-        else
-          ok = ok && warp_wait(&B.gv_ready[(n + 1) & 1], ((n + 1) >> 1) & 1);
+            mma_w(tmem + kTP, desc_k(q + kb * (kTile / 2), ks, kC), desc_k(k + kb * (kTile / 2), ks, kC), id_p, kb > 0 || ks > 0);
+        commit_w(&B.qk_done);
+      };
+      auto issue_su = [&](int n) {
+        const uint32_t k = sbase + (n % kStages) * kStageBytes + kTile;
+#pragma unroll
+        for (int p = 0; p < kPieces; ++p)  // small pieces first
+#pragma unroll
+          for (int ks = 0; ks < kC / 16; ++ks)
+            mma_ta_w(tmem + ds_col<kStateOnly>(n), tmem + gv_col<kStateOnly>(n) + p * (kC / 2) + ks * 8, desc_mn(k, ks, kC),
+                     id_su, p > 0 || ks > 0);
+        commit_w(&B.su_done[n & 1]);
+      };
+      if (n_chunks > 0) {
+        ok = warp_wait(&B.full[0], 0);
         fence_after();
-        if (ok) issue_su(n + 1);
+        if (ok && !kStateOnly) issue_qk(0);
+        if (ok) ok = warp_wait(&B.gv_ready[0], 0);
+        fence_after();
+        if (ok) issue_su(0);
       }
+      for (int n = 0; n < n_chunks && ok; ++n) {
+        const int s = n % kStages, s1 = (n + 1) % kStages;
+        const uint32_t par = n & 1, par2 = (n >> 1) & 1;
+        const bool more = n + 1 < n_chunks;
+        if (!kStateOnly) {
+          if (more) {  // the next P, once the update has read the Gamma V in its columns
+            // (P itself has been loaded: Gamma V, and so the update, waited for that)
+            ok = warp_wait2(&B.full[s1], ((n + 1) / kStages) & 1, &B.su_done[n & 1], par2);
+            fence_after();
+            if (ok) issue_qk(s1);
+          }
+          ok = ok && warp_wait2(&B.p_ready, par, &B.o_free, par ^ 1);
+          if (!ok) break;
+          fence_after();
+          const uint32_t q = sbase + s * kStageBytes, v = q + 2 * kTile;
+#pragma unroll
+          for (int p = 1; p >= 0; --p)
+#pragma unroll
+            for (int ks = 0; ks < kC / 16; ++ks)
+              mma_w(tmem + kTO2, desc_mn(v, ks, kC), desc_k(sbase + kP + p * kPTile, ks, kC), id_o2, p < 1 || ks > 0);
+          ok = ok && warp_wait(&B.s_ready, par);
+          if (!ok) break;
+          fence_after();
+#pragma unroll
+          for (int p = 3; p >= 0; --p) {  // the second piece's two halves, then the first's
+            const uint32_t qh = q + (p & 1) * (kTile / 2);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ta_w(tmem + kTO1, tmem + kTSh + p * 32 + ks * 8, desc_k(qh, ks, kC), id_o1, p < 3 || ks > 0);
+          }
+          commit_w(&B.o_done);
+        }
+        commit_w(&B.empty[s]);  // the update of chunk n was issued before
+        if (more) {
+          if (kStateOnly) ok = warp_wait(&B.full[s1], ((n + 1) / kStages) & 1);
+          // Gamma V is there, and the columns that the update goes to have been read
+          const int before = kStateOnly ? n - 1 : n;
+          if (before >= 0)
+            ok = ok && warp_wait2(&B.gv_ready[(n + 1) & 1], ((n + 1) >> 1) & 1, &B.ds_free[before & 1], (before >> 1) & 1);
+          else
+            ok = ok && warp_wait(&B.gv_ready[(n + 1) & 1], ((n + 1) >> 1) & 1);
+          fence_after();
+          if (ok) issue_su(n + 1);
+        }
+      }
+      commit_w(&B.end);  // every MMA issued is complete before TMEM is freed
+      if (!warp_wait(&B.end, 0)) ok = false;
     }
-    commit_w(&B.end);  // every MMA issued is complete before TMEM is freed
-    if (!warp_wait(&B.end, 0)) ok = false;
-   }
   } else if (warp >= 16) {
     regs_dec<kRegsGv>();
     gamma_v(0, kStateOnly ? 2 : 1);
@@ -658,49 +666,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     regs_dec<kRegsOut>();
-   if (!kStateOnly) {
-    // ---- the output: lane = value index, one column per token.  Neighbouring
-    // lanes swap halves of a token pair, so that a lane stores two values of one
-    // token: even lanes of the pair's first token, odd lanes of its second.
-    const int v = 32 * (warp & 3) + lane;
-    const bool odd = lane & 1;
-    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const long long o_size = ((a.cu_seqlens ? a.T : (long long)a.B * a.T) - 1) * a.ldo + (long long)a.Hv * kD;
-    long long at = (row0 + (long long)c0 * kC + odd) * a.ldo + h * kD + (v & ~1);
-    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o);
-    const float2 scale = make_float2(a.scale, a.scale);
-    const uint32_t take = odd ? 0x3276 : 0x5410;  // (other's, own) high halves, or (own, other's) low halves
-    for (int n = 0; n < n_chunks; ++n) {
-      ok = warp_wait(&B.o_done, n & 1);
-      if (!ok) break;
-      fence_after();
-      const ChunkVec &cv = B.vec[n % kVecs];
-      const int len = T - (c0 + n) * kC - odd;  // this lane's tokens are those below it
+    if (!kStateOnly) {
+      // ---- the output: lane = value index, one column per token.  Neighbouring
+      // lanes swap halves of a token pair, so that a lane stores two values of one
+      // token: even lanes of the pair's first token, odd lanes of its second.
+      const int v = 32 * (warp & 3) + lane;
+      const bool odd = lane & 1;
+      const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+      const long long o_size = ((a.cu_seqlens ? a.T : (long long)a.B * a.T) - 1) * a.ldo + (long long)a.Hv * kD;
+      long long at = (row0 + (long long)c0 * kC + odd) * a.ldo + h * kD + (v & ~1);
+      __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o);
+      const float2 scale = make_float2(a.scale, a.scale);
+      const uint32_t take = odd ? 0x3276 : 0x5410;  // (other's, own) high halves, or (own, other's) low halves
+      for (int n = 0; n < n_chunks; ++n) {
+        ok = warp_wait(&B.o_done, n & 1);
+        if (!ok) break;
+        fence_after();
+        const ChunkVec &cv = B.vec[n % kVecs];
+        const int len = T - (c0 + n) * kC - odd;  // this lane's tokens are those below it
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        uint32_t r1[16], r2[16];
-        tmem_ld16_nw(tl + kTO1 + 16 * i, r1);
-        tmem_ld16_nw(tl + kTO2 + 16 * i, r2);
-        tmem_wait_ld();
-        if (i == 3) {
-          fence_before();
-          warp_arrive(&B.o_free);
-        }
+        for (int i = 0; i < 4; ++i) {
+          uint32_t r1[16], r2[16];
+          tmem_ld16_nw(tl + kTO1 + 16 * i, r1);
+          tmem_ld16_nw(tl + kTO2 + 16 * i, r2);
+          tmem_wait_ld();
+          if (i == 3) {
+            fence_before();
+            warp_arrive(&B.o_free);
+          }
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const float2 y = __fmul2_rn(
-              scale, __ffma2_rn(*reinterpret_cast<const float2 *>(&cv.eG[16 * i + e]),
-                                make_float2(__uint_as_float(r1[e]), __uint_as_float(r1[e + 1])),
-                                make_float2(__uint_as_float(r2[e]), __uint_as_float(r2[e + 1]))));
-          const uint32_t own = pack_bf16(y.x, y.y), other = __shfl_xor_sync(0xffffffffu, own, 1);
-          const uint32_t w = __byte_perm(own, other, take);
-          if (16 * i + e < len && in_bounds(at + 2, o_size, a.err)) *reinterpret_cast<uint32_t *>(o + at) = w;
-          at += 2 * a.ldo;
+          for (int e = 0; e < 16; e += 2) {
+            const float2 y = __fmul2_rn(
+                scale, __ffma2_rn(*reinterpret_cast<const float2 *>(&cv.eG[16 * i + e]),
+                                  make_float2(__uint_as_float(r1[e]), __uint_as_float(r1[e + 1])),
+                                  make_float2(__uint_as_float(r2[e]), __uint_as_float(r2[e + 1]))));
+            const uint32_t own = pack_bf16(y.x, y.y), other = __shfl_xor_sync(0xffffffffu, own, 1);
+            const uint32_t w = __byte_perm(own, other, take);
+            if (16 * i + e < len && in_bounds(at + 2, o_size, a.err)) *reinterpret_cast<uint32_t *>(o + at) = w;
+            at += 2 * a.ldo;
+          }
         }
       }
     }
-  }
-   }
+    }
   if (!ok && lane == 0) atomicOr(a.err, kErrTimeout);
 
   fence_before();

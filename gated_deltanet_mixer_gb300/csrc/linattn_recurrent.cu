@@ -9,8 +9,11 @@
 // whatever the number of tokens.  Tokens are copied kTB at a time into a ring in
 // shared memory, three blocks ahead of the one worked on.
 //
-// One token is bound by the state's traffic (128 KB per unit against 128 x 128
-// fused multiply-adds); long runs by the latency of a token's loads and sums.
+// One token is bound by the state's traffic, 128 KB per unit against 128 x 128
+// fused multiply-adds (256 sequences x 48 heads: 233 us, 6.9 TB/s; 1 x 16 heads:
+// 2.6 us); a few tokens by that and by instruction issue (64 x 48 heads, 4
+// tokens: 74 us, 5.5 TB/s); long runs by the latency of a token's sums (2 x 1001
+// tokens, 8 heads, fp32: 120 us, 0.12 us per token).
 #include <type_traits>
 
 #include "gdn_device.cuh"
@@ -126,7 +129,15 @@ __global__ void __launch_bounds__(kThreads) linattn_recurrent_kernel(LinAttnArgs
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
         S[r] = decayed(S[r], al, ld_io(&s_v[buf][t + i][warp * kRows + r]), kv);
-        p[i * kRows + r] = dot4(S[r], qv);
+        // Groups of bf16 tokens: in packed pairs (64 x 48 heads, 4 tokens: 74 us, 80
+        // without; groups of fp32 tokens and single ones are slower with them).
+        if (kGroup > 1 && sizeof(IO) == 2) {
+          const float2 pq = __ffma2_rn(make_float2(S[r].x, S[r].y), make_float2(qv.x, qv.y),
+                                       __fmul2_rn(make_float2(S[r].z, S[r].w), make_float2(qv.z, qv.w)));
+          p[i * kRows + r] = pq.x + pq.y;
+        } else {
+          p[i * kRows + r] = dot4(S[r], qv);
+        }
       }
     }
     const float sum = reduce_rows<N * kRows>(p, lane);
@@ -158,10 +169,10 @@ __global__ void __launch_bounds__(kThreads) linattn_recurrent_kernel(LinAttnArgs
 template <typename IO, int kRows>
 void launch(const LinAttnArgs &a, cudaStream_t s) {
   const unsigned grid = (unsigned)((long long)a.B * a.Hv * (kD / (kWarps * kRows)));
-  // A few tokens are bound by the state's traffic: no groups, and the registers
-  // of more CTAs per SM instead (64 x 48 heads, 4 tokens: 76 us, in groups 81; 8
-  // tokens: 101 us, in groups 99).
-  if (a.T < 8)
+  // Up to three tokens are bound by the state's traffic: no groups, and the
+  // registers of more CTAs per SM instead (64 x 48 heads, 3 tokens: 72 us, in
+  // groups 75).
+  if (a.T < 4)
     linattn_recurrent_kernel<IO, kRows, 1><<<grid, kThreads, 0, s>>>(a);
   else
     linattn_recurrent_kernel<IO, kRows, 4><<<grid, kThreads, 0, s>>>(a);

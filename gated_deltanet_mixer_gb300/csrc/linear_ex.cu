@@ -5,10 +5,13 @@
 // bf16 in and out, fp32 accumulation on the tcgen05 tensor cores, everything
 // behind the sum in fp32 and rounded once.
 //
-// Two kernels:
-//   lin_tile_kernel   whole waves of 128 x 256 tiles: bound by the tensor
-//                     pipe.  Persistent, x tile rows on the MMA's M side, the
+// Three kernels:
+//   lin_pair_kernel   256 x 256 tiles by pairs of CTAs: bound by the tensor pipe,
+//                     92 % active (8192 tokens 5120 -> 16480: 817 us, 1692
+//                     TFLOP/s; the tile kernel below: 912 us).  Persistent, the
 //                     epilogue of a tile under the next tile's MMAs.
+//   lin_tile_kernel   128 x 64 .. 256 tiles of one CTA, where pairs' tiles are too
+//                     few for the SMs (1024 x 2048 x 2048: 12 us).
 //   lin_skinny_kernel fewer tiles (few tokens, or few columns): bound by
 //                     reading w once.  128 rows of w on the M side, the tokens
 //                     on the N side (16 .. 256), and the contraction split over

@@ -373,6 +373,8 @@ gdn_status gdn_linear_ex(int M, int N, int K, int gated, const void *x, long lon
  *   workspace 256-byte aligned scratch of at least
  *        gdn_linattn_workspace_bytes(), or NULL.  With few sequences x value
  *        heads it lets a prompt be cut into segments that run side by side.
+ *        Undefined after the call; not to be shared by calls that may overlap
+ *        in time.
  *
  * bf16 io runs in chunks of 64 tokens on the tensor cores (the shortest
  * prompts, up to about a hundred tokens, token by token as fp32 io does): operands that are

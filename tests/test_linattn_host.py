@@ -92,6 +92,7 @@ def test_linear_ex_arguments(L):
                 dict(outs=[(2 * i, 2 * i + 2, fake(2 + i), 8, 0, None, 0) for i in range(5)])):
         assert linear(L, **bad) == 1, bad
     assert linear(L, ldx=1 << 33) == 2
+    assert linear(L, M=1 << 30, N=1 << 28) == 2                  # more tiles than 31 bits count
     for bad in (dict(x=fake(0, 8)), dict(ldw=68), dict(bias=fake(5, 2)), dict(outs=[(0, 8, fake(2, 1), 8, 0, None, 0)]),
                 dict(outs=[(0, 8, fake(2), 8, 0, fake(3, 1), 8)])):
         assert linear(L, **bad) == 3, bad
