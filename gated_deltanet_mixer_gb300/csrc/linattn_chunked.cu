@@ -37,8 +37,8 @@
 // chain update -> P and Gamma V -> next update, not memory (4 x 8192 tokens, 16/32
 // heads: 258 us, 3.1 TB/s of the 0.81 GB that the call cannot do without, where
 // a copy runs at 6.8; 65536 tokens, 16/48 heads: 940 us).  The loops of the roles
-// share one instruction cache: unrolled further, from 56 to 65 KB of code, the
-// kernel took 10 % longer.
+// share one instruction cache: a form with 82 KB of code instead of 58 waited for
+// instructions in a third of its samples and took 1.4 times as long.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -78,15 +78,16 @@ struct Shared {
   uint64_t full[kStages], empty[kStages];
   uint64_t qk_done, p_loaded, p_ready, gv_ready[2], su_done[2], ds_free[2], s_ready, o_done, o_free, end;
   uint32_t tmem;
+  int unit, seg;  // for the state's warps, whose registers are full
 };
 constexpr uint32_t kSmem = kShared + ((sizeof(Shared) + 127) / 128) * 128 + 1024;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 
 // Six warpgroups; the last one's warps 22 and 23 only take part in barriers.
 // Registers per thread: launched with 80, then split by what a group holds
-// (256 x 136 + 128 x (56 + 48 + 64 + 40) = 768 x 80).
+// (256 x 136 + 128 x (56 + 56 + 56 + 40) = 768 x 80).
 constexpr int kThreads = 24 * 32;
-constexpr int kRegsState = 136, kRegsP = 56, kRegsOut = 48, kRegsGv = 64, kRegsIssue = 40;
+constexpr int kRegsState = 136, kRegsP = 56, kRegsOut = 56, kRegsGv = 56, kRegsIssue = 40;
 static_assert(256 * kRegsState + 128 * (kRegsP + kRegsOut + kRegsGv + kRegsIssue) <= kThreads * 80, "register split");
 // TMEM columns (fp32, or bf16 pairs for the operands).  Two of the four pieces
 // of Gamma V take the place of P once its threads have loaded it.  The
@@ -298,7 +299,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n_chunks = c1 - c0;
   constexpr long long kState = kD * kD;
 
+  // The log decays of chunk c, tokens lane and lane + 32; the first chunk's are
+  // asked for before anything else.
+  auto load_g = [&](int c, float &g0, float &g1) {
+    g0 = g1 = 0.f;
+    const int t = c * kC + lane;
+    if (a.g) {
+      if (t < T) g0 = a.g[(row0 + t) * a.Hv + h];
+      if (t + 32 < T) g1 = a.g[(row0 + t + 32) * a.Hv + h];
+    } else {
+      const float gh = a.log_decay[h];
+      if (t < T) g0 = gh;
+      if (t + 32 < T) g1 = gh;
+    }
+    g0 = fmaxf(g0, kMinLogDecay);
+    g1 = fmaxf(g1, kMinLogDecay);
+  };
+  float g0 = 0.f, g1 = 0.f;
+  if (warp == 20 && n_chunks > 0) load_g(c0, g0, g1);
+
   if (tid == 0) {
+    auto bar_init = [](uint64_t *bar, uint32_t count) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
+    };
     for (int s = 0; s < kStages; ++s) {
       bar_init(&B.full[s], 2);
       bar_init(&B.empty[s], 1);
@@ -315,6 +338,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     bar_init(&B.o_done, 1);
     bar_init(&B.o_free, 4);
     bar_init(&B.end, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");  // one for all of them
+    B.unit = unit;
+    B.seg = seg;
+  }
+  if (warp == 20 && lane < 3) {
+    const CUtensorMap *map = lane == 0 ? &tm_k : lane == 1 ? &tm_v : &tm_q;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
   }
   if (warp == 21) tmem_alloc(&B.tmem, 512);
   fence_before();
@@ -409,22 +439,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<kRegsIssue>();
     if (warp == 20) {
       // ---- TMA producer and the chunk vectors
-      auto load_g = [&](int c, float &g0, float &g1) {
-        g0 = g1 = 0.f;
-        const int t = c * kC + lane;
-        if (a.g) {
-          if (t < T) g0 = a.g[(row0 + t) * a.Hv + h];
-          if (t + 32 < T) g1 = a.g[(row0 + t + 32) * a.Hv + h];
-        } else {
-          const float gh = a.log_decay[h];
-          if (t < T) g0 = gh;
-          if (t + 32 < T) g1 = gh;
-        }
-        g0 = fmaxf(g0, kMinLogDecay);
-        g1 = fmaxf(g1, kMinLogDecay);
-      };
-      float g0 = 0.f, g1 = 0.f;
-      if (n_chunks > 0) load_g(c0, g0, g1);
       int n = 0;
       for (; n < n_chunks; ++n) {
         const int s = n % kStages;
@@ -591,7 +605,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int v = 32 * (warp & 3) + lane, half = warp >> 2;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const long long at = (long long)unit * kState + v * kD + 64 * half;
-    float *dec = a.ws + linattn_slots(a.nseg, a.sub) * units * kState;  // [slot][units]: log decays
+    const auto dec_at = [&](int slot, int u) -> float & {  // [slot][units]: the parts' log decays
+      return a.ws[linattn_slots(a.nseg, a.sub) * units * kState + slot * units + u];
+    };
     float S[64];
 #pragma unroll
     for (int i = 0; i < 64; ++i) S[i] = 0.f;
@@ -658,11 +674,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       warp_arrive(&B.ds_free[n & 1]);
       if (!kStateOnly) pieces();
     }
-    if (kStateOnly && tid == 0) dec[(seg + 1) * units + unit] = total;
-    if (kStateOnly || (seg == a.nseg - 1 && in_bounds(at + 64, units * kState, a.err))) {
-      float *dst = (kStateOnly ? a.ws + (seg + 1) * units * kState : a.S_T) + at;
+    // From here on with values read anew, so that none is held through the loop.
+    int t;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+    const int seg_ = *const_cast<volatile int *>(&B.seg), unit_ = *const_cast<volatile int *>(&B.unit);
+    if (kStateOnly && t == 0) dec_at(seg_ + 1, unit_) = total;
+    if (kStateOnly || seg_ == a.nseg - 1) {
+      // Through shared memory, so that a warp stores whole rows: 16-byte piece c of
+      // row v lies at piece c ^ (v % 32) there, and neither side has a bank
+      // conflict.  The stages that the last chunk does not use are free.
+      float4 *buf = reinterpret_cast<float4 *>(sm + (n_chunks > 0 && (n_chunks - 1) % kStages < 2 ? 2 * kStageBytes : 0));
+      const int l = t & 31, row_ = t & 127, piece = t >> 7 << 4;
 #pragma unroll
-      for (int i = 0; i < 64; i += 4) *reinterpret_cast<float4 *>(dst + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+      for (int i = 0; i < 16; ++i)
+        buf[row_ * 32 + ((piece + i) ^ l)] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      float *dst = kStateOnly ? a.ws + (seg_ + 1) * units * kState : a.S_T;
+#pragma unroll 1
+      for (int i = 0; i < 16; ++i) {
+        const int row = 16 * (t >> 5) + i;
+        const long long to = (long long)unit_ * kState + row * kD + 4 * l;
+        if (in_bounds(to + 4, units * kState, a.err))
+          *reinterpret_cast<float4 *>(dst + to) = buf[row * 32 + (l ^ (row & 31))];
+      }
     }
   } else {
     regs_dec<kRegsOut>();
