@@ -4,10 +4,13 @@
 // With G_i the sum of the log decays of the chunk's tokens up to i, the
 // recurrence S_t = e^{g_t} S_{t-1} + v_t k_t^T, o_t = S_t q_t becomes, kept
 // value-major (S[v][k]) and with tokens along the columns,
-//   O^T = e^{G_i} (S Q^T) + V^T P^T,  P_ij = e^{G_i - G_j} q_i . k_j (j <= i),
-//   S'  = e^{G_last} S + (Gamma V)^T K,  Gamma_j = e^{G_last - G_j}.
-// Every exponent is <= 0.  Only S Q^T and the sum of S' carry the state: the
-// products P, V^T P^T and (Gamma V)^T K of a chunk do not wait for it.
+//   O^T = e^{F_i} (S Q^T + V^T P^T),  P_ij = e^{G_i - F_i - G_j} q_i . k_j (j <= i),
+//   S'  = e^{G_last} S + (Gamma V)^T K,  Gamma_j = e^{G_last - G_j},
+// with F_i = max(G_i, -40), so that one accumulator takes both products of an
+// output: P grows to e^40 at most, and an output of a token 40 below the chunk's
+// start in log decay sees e^-40 of the state where it should see less.  Only S Q^T
+// and the sum of S' carry the state: the products P, V^T P^T and (Gamma V)^T K of a
+// chunk do not wait for it.
 //
 // One CTA walks the chunks of one (sequence, value head, segment):
 //   warp 20      TMA: q, k, v tiles into a 4-stage ring; the chunk's decays
@@ -55,6 +58,7 @@ using namespace umma;
 constexpr int kC = 64;  // tokens per chunk
 constexpr int kStages = 4;
 constexpr int kVecs = 8;  // chunk vectors in flight (the output warps lag the loads by less)
+constexpr float kFloor = -40.f;  // of the sum of a chunk's log decays in front of an output (below)
 constexpr float kMinLogDecay = -80.f;  // a decay below e^-80 acts as e^-80: sums of it stay finite
 
 constexpr uint32_t kTile = kC * kD * 2;             // 16 KB: 64 tokens x 128
@@ -65,7 +69,8 @@ constexpr uint32_t kShared = kP + 2 * kPTile;
 
 struct ChunkVec {
   float G[kC];   // sums of the log2 decays from the chunk's first token
-  float eG[kC];  // e^G
+  float over[kC];  // G - F where G is below it, else 0 (log2)
+  float eF[kC];  // scale e^F, F = max(natural G, kFloor)
   // e^{G_last - G} of the tokens 2 i, 2 i + 1 as bf16 pairs (c0, 0) and (c1, c2)
   // with c0 + c1 + c2 = it to 24 bits; 0 past the sequence's end
   uint2 gam[2][kC / 2];
@@ -76,7 +81,7 @@ struct ChunkVec {
 struct Shared {
   ChunkVec vec[kVecs];
   uint64_t full[kStages], empty[kStages];
-  uint64_t qk_done, p_loaded, p_ready, gv_ready[2], su_done[2], ds_free[2], s_ready, o_done, o_free, end;
+  uint64_t qk_done, p_loaded, p_ready, gv_ready[2], su_half[2], su_done[2], ds_free[2], s_ready, o_done, o_free, end;
   uint32_t tmem;
   int unit, seg;  // for the state's warps, whose registers are full
 };
@@ -89,10 +94,9 @@ static_assert(kSmem <= 232448, "shared memory per CTA");
 constexpr int kThreads = 24 * 32;
 constexpr int kRegsState = 136, kRegsP = 56, kRegsOut = 56, kRegsGv = 56, kRegsIssue = 40;
 static_assert(256 * kRegsState + 128 * (kRegsP + kRegsOut + kRegsGv + kRegsIssue) <= kThreads * 80, "register split");
-// TMEM columns (fp32, or bf16 pairs for the operands).  Two of the four pieces
-// of Gamma V take the place of P once its threads have loaded it.  The
-// state-only form has the space to double-buffer both the update and Gamma V.
-constexpr uint32_t kTDs = 0, kTSh = 128, kTSl = 192, kTO1 = 256, kTO2 = 320, kTP = 384, kTG = kTP;
+// TMEM columns (fp32, or bf16 pairs for the operands): all 512 are used.  The
+// state-only form double-buffers both the update and Gamma V.
+constexpr uint32_t kTDs = 0, kTSh = 128, kTSl = 192, kTO = 256, kTP = 320, kTG = 384;
 constexpr int kPieces = 4;
 template <bool kStateOnly>
 __device__ __forceinline__ uint32_t ds_col(int n) { return kStateOnly && (n & 1) ? 128u : kTDs; }
@@ -219,7 +223,7 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
 }
 
 // The decays of a chunk, by one warp: lane L holds tokens L and L + 32.
-__device__ __forceinline__ void chunk_vec(ChunkVec &cv, float g0, float g1, int len, int lane) {
+__device__ __forceinline__ void chunk_vec(ChunkVec &cv, float g0, float g1, float scale, int len, int lane) {
   float p0 = g0, p1 = g1;  // inclusive sums from the front
   float s0 = g0, s1 = g1;  // and from the back: no cancellation in e^{G_last - G_j}
 #pragma unroll
@@ -238,8 +242,10 @@ __device__ __forceinline__ void chunk_vec(ChunkVec &cv, float g0, float g1, int 
   constexpr float kLog2e = 1.44269504088896341f;
   cv.G[lane] = p0 * kLog2e;
   cv.G[lane + 32] = p1 * kLog2e;
-  cv.eG[lane] = expf(p0);
-  cv.eG[lane + 32] = expf(p1);
+  cv.over[lane] = fminf(p0 - kFloor, 0.f) * kLog2e;
+  cv.over[lane + 32] = fminf(p1 - kFloor, 0.f) * kLog2e;
+  cv.eF[lane] = scale * expf(fmaxf(p0, kFloor));
+  cv.eF[lane + 32] = scale * expf(fmaxf(p1, kFloor));
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = lane + 32 * i;
@@ -331,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bar_init(&B.p_ready, 4);
     for (int i = 0; i < 2; ++i) {
       bar_init(&B.gv_ready[i], 4);
+      bar_init(&B.su_half[i], 1);
       bar_init(&B.su_done[i], 1);
       bar_init(&B.ds_free[i], 8);
     }
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (kStateOnly) {
         if (n > 1) ok = ok && warp_wait(&B.su_done[n & 1], ((n >> 1) & 1) ^ 1);
       } else {
-        if (n > 0) ok = ok && warp_wait(&B.su_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
+        if (n > 0) ok = ok && warp_wait(&B.su_half[(n - 1) & 1], ((n - 1) >> 1) & 1);
       }
       if (!ok) break;
       fence_after();
@@ -383,11 +390,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const uint32_t vbase = sbase + s * kStageBytes + 2 * kTile + vrow;
-      // Two pieces at a time: the first two, then those in the columns of P.
+      // Two pieces at a time, the small ones first: the last update has read those.
 #pragma unroll 1
-      for (int pass = 0; pass < 2; ++pass) {
-        if (pass == 1 && !kStateOnly) {
-          ok = warp_wait(&B.p_loaded, n & 1);
+      for (int pass = 1; pass >= 0; --pass) {
+        if (pass == 0 && !kStateOnly && n > 0) {
+          ok = warp_wait(&B.su_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
           if (!ok) break;
           fence_after();
         }
@@ -457,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(dst + 2 * kTile + x * (kTile / 2), &tm_v, h * kD + 64 * x, row, 0, &B.full[s]);
           }
         }
-        chunk_vec(B.vec[n % kVecs], g0, g1, T - c * kC, lane);
+        chunk_vec(B.vec[n % kVecs], g0, g1, a.scale, T - c * kC, lane);
         __syncwarp();
         if (lane == 0) arrive(&B.full[s]);
         if (n + 1 < n_chunks) load_g(c + 1, g0, g1);
@@ -483,11 +490,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto issue_su = [&](int n) {
         const uint32_t k = sbase + (n % kStages) * kStageBytes + kTile;
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p)  // small pieces first
+        for (int p = 0; p < kPieces; ++p) {  // small pieces first
 #pragma unroll
           for (int ks = 0; ks < kC / 16; ++ks)
             mma_ta_w(tmem + ds_col<kStateOnly>(n), tmem + gv_col<kStateOnly>(n) + p * (kC / 2) + ks * 8, desc_mn(k, ks, kC),
                      id_su, p > 0 || ks > 0);
+          if (p == 1 && !kStateOnly) commit_w(&B.su_half[n & 1]);  // the next chunk's may take their place
+        }
         commit_w(&B.su_done[n & 1]);
       };
       if (n_chunks > 0) {
@@ -500,12 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       for (int n = 0; n < n_chunks && ok; ++n) {
         const int s = n % kStages, s1 = (n + 1) % kStages;
-        const uint32_t par = n & 1, par2 = (n >> 1) & 1;
+        const uint32_t par = n & 1;
         const bool more = n + 1 < n_chunks;
         if (!kStateOnly) {
-          if (more) {  // the next P, once the update has read the Gamma V in its columns
-            // (P itself has been loaded: Gamma V, and so the update, waited for that)
-            ok = warp_wait2(&B.full[s1], ((n + 1) / kStages) & 1, &B.su_done[n & 1], par2);
+          if (more) {  // the next P
+            ok = warp_wait2(&B.full[s1], ((n + 1) / kStages) & 1, &B.p_loaded, par);
             fence_after();
             if (ok) issue_qk(s1);
           }
@@ -517,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int p = 1; p >= 0; --p)
 #pragma unroll
             for (int ks = 0; ks < kC / 16; ++ks)
-              mma_w(tmem + kTO2, desc_mn(v, ks, kC), desc_k(sbase + kP + p * kPTile, ks, kC), id_o2, p < 1 || ks > 0);
+              mma_w(tmem + kTO, desc_mn(v, ks, kC), desc_k(sbase + kP + p * kPTile, ks, kC), id_o2, p < 1 || ks > 0);
           ok = ok && warp_wait(&B.s_ready, par);
           if (!ok) break;
           fence_after();
@@ -526,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t qh = q + (p & 1) * (kTile / 2);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              mma_ta_w(tmem + kTO1, tmem + kTSh + p * 32 + ks * 8, desc_k(qh, ks, kC), id_o1, p < 3 || ks > 0);
+              mma_ta_w(tmem + kTO, tmem + kTSh + p * 32 + ks * 8, desc_k(qh, ks, kC), id_o1, 1);
           }
           commit_w(&B.o_done);
         }
@@ -567,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16x64(tmem + ((uint32_t)(32 * w) << 16) + kTP, r);
         fence_before();
         warp_arrive(&B.p_loaded);
-        const float ga = cv.G[i0], gb = cv.G[i0 + 8];
+        const float ga = cv.over[i0], gb = cv.over[i0 + 8];
         // r becomes the pieces: register 4 b + 2 q the first of row i0 + 8 q, the next one the second.
 #pragma unroll
         for (int blk = 0; blk < 8; ++blk) {
@@ -710,7 +718,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const long long o_size = ((a.cu_seqlens ? a.T : (long long)a.B * a.T) - 1) * a.ldo + (long long)a.Hv * kD;
       long long at = (row0 + (long long)c0 * kC + odd) * a.ldo + h * kD + (v & ~1);
       __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o);
-      const float2 scale = make_float2(a.scale, a.scale);
       const uint32_t take = odd ? 0x3276 : 0x5410;  // (other's, own) high halves, or (own, other's) low halves
       for (int n = 0; n < n_chunks; ++n) {
         ok = warp_wait(&B.o_done, n & 1);
@@ -720,9 +727,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int len = T - (c0 + n) * kC - odd;  // this lane's tokens are those below it
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
-          uint32_t r1[16], r2[16];
-          tmem_ld16_nw(tl + kTO1 + 16 * i, r1);
-          tmem_ld16_nw(tl + kTO2 + 16 * i, r2);
+          uint32_t r[16];
+          tmem_ld16_nw(tl + kTO + 16 * i, r);
           tmem_wait_ld();
           if (i == 3) {
             fence_before();
@@ -730,10 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
-            const float2 y = __fmul2_rn(
-                scale, __ffma2_rn(*reinterpret_cast<const float2 *>(&cv.eG[16 * i + e]),
-                                  make_float2(__uint_as_float(r1[e]), __uint_as_float(r1[e + 1])),
-                                  make_float2(__uint_as_float(r2[e]), __uint_as_float(r2[e + 1]))));
+            const float2 y = __fmul2_rn(*reinterpret_cast<const float2 *>(&cv.eF[16 * i + e]),
+                                        make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
             const uint32_t own = pack_bf16(y.x, y.y), other = __shfl_xor_sync(0xffffffffu, own, 1);
             const uint32_t w = __byte_perm(own, other, take);
             if (16 * i + e < len && in_bounds(at + 2, o_size, a.err)) *reinterpret_cast<uint32_t *>(o + at) = w;
