@@ -19,6 +19,7 @@
 //                     sums through distributed shared memory and add them in a
 //                     fixed order: no workspace, no second launch, the same
 //                     result every time.
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -150,11 +151,14 @@ __device__ __forceinline__ void load_residual(const LinArgs &g, const LinOut &ou
     }
   } else if (col >= out.col_begin && col < min(out.col_end, g.N)) {
     const uint16_t *src = reinterpret_cast<const uint16_t *>(res + row0 * out.ldres + col);
+    const long long ld = out.ldres;
+    if (rows == 32) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const uint32_t r0 = 2 * e < rows ? src[2 * e * out.ldres] : 0;
-      const uint32_t r1 = 2 * e + 1 < rows ? src[(2 * e + 1) * out.ldres] : 0;
-      x[e] = r0 | r1 << 16;
+      for (int e = 0; e < 16; ++e, src += 2 * ld) x[e] = (uint32_t)src[0] | (uint32_t)src[ld] << 16;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e, src += 2 * ld)
+        x[e] = (2 * e < rows ? src[0] : 0u) | (2 * e + 1 < rows ? (uint32_t)src[ld] << 16 : 0u);
     }
   }
 }
@@ -162,7 +166,7 @@ __device__ __forceinline__ void load_residual(const LinArgs &g, const LinOut &ou
 __device__ __forceinline__ int prefetch_residual(const LinArgs &g, long long row0, int lane, int col0, uint32_t (&x)[16]) {
   if (row0 >= g.M) return -1;
   for (int o = 0; o < g.n_out; ++o) {
-    const LinOut &out = g.out[o];
+    const LinOut out = g.out[o];  // in registers: the parameters are indexed once
     if (!out.res || max(col0, out.col_begin) >= min(min(col0 + 32, out.col_end), g.N)) continue;
     load_residual(g, out, row0, lane, col0, x);
     return o;
@@ -175,12 +179,14 @@ __device__ __forceinline__ int prefetch_residual(const LinArgs &g, long long row
 // `loaded`.  Whole aligned runs are stored 16 bytes per lane.  Others go through
 // shared memory, so that a warp stores 32 neighbouring columns of one row at a
 // time: a lane storing its own row would touch 32 rows with every 2-byte store
-// (4069 x 6549 x 144 with a residual: 601 us so, 110 this way).
+// (4069 x 6549 x 144 with a residual: 601 us so, 67 this way).  What bounds these
+// loops is instructions: with the fields of a range read from the parameters at
+// each use, and every row tested against the last one, the same call took 121 us.
 template <bool kGated>
 __device__ __forceinline__ void store_run(const LinArgs &g, long long row0, int lane, int col0, const float (&v)[32],
                                           const float (&u)[32], float *run, int loaded, uint32_t (&x)[16]) {
   for (int o = 0; o < g.n_out; ++o) {
-    const LinOut &out = g.out[o];
+    const LinOut out = g.out[o];
     const int lo = max(col0, out.col_begin), hi = min(min(col0 + 32, out.col_end), g.N);
     if (lo >= hi) continue;
     const int rows = (int)min(32LL, g.M - row0), col = col0 + lane;
@@ -195,16 +201,18 @@ __device__ __forceinline__ void store_run(const LinArgs &g, long long row0, int 
       for (int e = 0; e < 32; ++e) y[e] *= u[e];
     }
     bf16 *dst = static_cast<bf16 *>(out.ptr) - out.col_begin;
+    const long long ld = out.ld;
+    const bool add = out.res != nullptr;
     if (whole) {
       if (lane >= rows) continue;
-      uint4 *to = reinterpret_cast<uint4 *>(dst + (row0 + lane) * out.ld + col0);
+      uint4 *to = reinterpret_cast<uint4 *>(dst + (row0 + lane) * ld + col0);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           float a = y[8 * q + 2 * e], b = y[8 * q + 2 * e + 1];
-          if (out.res) a += __uint_as_float(x[4 * q + e] << 16), b += __uint_as_float(x[4 * q + e] & 0xffff0000u);
+          if (add) a += __uint_as_float(x[4 * q + e] << 16), b += __uint_as_float(x[4 * q + e] & 0xffff0000u);
           __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
           w[e] = *reinterpret_cast<uint32_t *>(&t);
         }
@@ -217,15 +225,21 @@ __device__ __forceinline__ void store_run(const LinArgs &g, long long row0, int 
     for (int e = 0; e < 32; ++e) run[lane * 33 + e] = y[e];
     __syncwarp();
     if (inside) {
-      bf16 *to = dst + row0 * out.ld + col;
+      bf16 *to = dst + row0 * ld + col;
+      auto column = [&](auto full) {
 #pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (e < rows) {
-          float z = run[e * 33 + lane];
-          if (out.res) z += __uint_as_float(e & 1 ? x[e / 2] & 0xffff0000u : x[e / 2] << 16);
-          *to = __float2bfloat16_rn(z);
-          to += out.ld;
-        }
+        for (int e = 0; e < 32; ++e)
+          if (full || e < rows) {
+            float z = run[e * 33 + lane];
+            if (add) z += __uint_as_float(e & 1 ? x[e / 2] & 0xffff0000u : x[e / 2] << 16);
+            *to = __float2bfloat16_rn(z);
+            to += ld;
+          }
+      };
+      if (rows == 32)
+        column(std::true_type{});
+      else
+        column(std::false_type{});
     }
   }
 }
