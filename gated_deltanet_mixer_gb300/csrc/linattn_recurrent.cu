@@ -4,16 +4,17 @@
 //
 // Row i of S (value index i) needs only v_t[i], so the 128 rows are
 // independent: a warp owns kRows of them in fp32 registers, lane L holding
-// columns 4L .. 4L+3, and a CTA of 8 warps covers 8 kRows rows of one
+// columns 4L .. 4L+3, and a CTA covers kWarps kRows rows of one
 // (sequence, value head).  The state is read once and written once per call,
 // whatever the number of tokens.  Tokens are copied kTB at a time into a ring in
 // shared memory, three blocks ahead of the one worked on.
 //
 // One token is bound by the state's traffic, 128 KB per unit against 128 x 128
 // fused multiply-adds (256 sequences x 48 heads: 233 us, 6.9 TB/s; 1 x 16 heads:
-// 2.6 us); a few tokens by that and by instruction issue (64 x 48 heads, 4
-// tokens: 74 us, 5.5 TB/s); long runs by the latency of a token's sums (2 x 1001
-// tokens, 8 heads, fp32: 120 us, 0.12 us per token).
+// 2.5 us); a few tokens by that and by instruction issue (64 x 48 heads, 4
+// tokens: 71 us, 5.8 TB/s); long runs by a token's loads from shared memory, its
+// arithmetic and its sums in turn (2 x 1001 tokens, 8 heads, fp32: 102 us, 0.10 us
+// per token).
 #include <type_traits>
 
 #include "gdn_device.cuh"
@@ -22,8 +23,6 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kTB = 8;    // tokens per block
 constexpr int kRing = 4;  // blocks in the ring
 
@@ -63,8 +62,9 @@ __device__ __forceinline__ float4 decayed(float4 s, Decay a, float v, float4 k) 
 }
 
 // kGroup: tokens whose sums are reduced together.
-template <typename IO, int kRows, int kGroup>
-__global__ void __launch_bounds__(kThreads) linattn_recurrent_kernel(LinAttnArgs a) {
+template <typename IO, int kRows, int kGroup, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32) linattn_recurrent_kernel(LinAttnArgs a) {
+  constexpr int kThreads = kWarps * 32;
   constexpr int kSplit = kD / (kWarps * kRows);  // CTAs per unit
   constexpr int kCtaRows = kWarps * kRows;
   __shared__ __align__(16) IO s_q[kRing][kTB][kD], s_k[kRing][kTB][kD], s_v[kRing][kTB][kCtaRows];
@@ -96,16 +96,19 @@ __global__ void __launch_bounds__(kThreads) linattn_recurrent_kernel(LinAttnArgs
   auto fetch = [&](int block) {  // copies block `block` into its place in the ring
     const int t0 = block * kTB, slot = block % kRing;
     constexpr int kWide = kD / kPiece, kNarrow = kCtaRows / kPiece;  // copies per row of q, k; of v
-    const int t = tid / kWide, c = tid % kWide * kPiece;
-    if (t < kTB && t0 + t < T) {
-      copy16(&s_q[slot][t][c], q + (t0 + t) * a.ldq + c);
-      copy16(&s_k[slot][t][c], k + (t0 + t) * a.ldk + c);
+#pragma unroll
+    for (int i = 0; i < kTB * kWide; i += kThreads) {
+      const int t = (tid + i) / kWide, c = tid % kWide * kPiece;
+      if (t < kTB && t0 + t < T) {
+        copy16(&s_q[slot][t][c], q + (t0 + t) * a.ldq + c);
+        copy16(&s_k[slot][t][c], k + (t0 + t) * a.ldk + c);
+      }
     }
     const int tv = tid / kNarrow, cv = tid % kNarrow * kPiece;
     if (tv < kTB && t0 + tv < T) copy16(&s_v[slot][tv][cv], v + (t0 + tv) * a.ldv + cv);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  static_assert(kTB * kD / kPiece <= kThreads, "one copy of q and of k per thread");
+  static_assert(kThreads % (kD / kPiece) == 0 && kTB * kCtaRows / kPiece <= kThreads, "copies");
   auto decay = [&](int t) { return a.g ? a.g[(row0 + t) * a.Hv + h] : a.log_decay[h]; };
   for (int b = 0; b < kRing - 1; ++b) fetch(b);
   if (tid < kTB * (kRing - 1) && tid < T) s_a[tid / kTB][tid % kTB] = Decay::of(decay(tid));
@@ -129,8 +132,8 @@ __global__ void __launch_bounds__(kThreads) linattn_recurrent_kernel(LinAttnArgs
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
         S[r] = decayed(S[r], al, ld_io(&s_v[buf][t + i][warp * kRows + r]), kv);
-        // Groups of bf16 tokens: in packed pairs (64 x 48 heads, 4 tokens: 74 us, 80
-        // without; groups of fp32 tokens and single ones are slower with them).
+        // Groups of bf16 tokens: in packed pairs (64 x 48 heads, 4 tokens, CTAs of 8
+        // warps of 4 rows: 74 us, 80 without; groups of fp32 tokens and single ones are slower with them).
         if (kGroup > 1 && sizeof(IO) == 2) {
           const float2 pq = __ffma2_rn(make_float2(S[r].x, S[r].y), make_float2(qv.x, qv.y),
                                        __fmul2_rn(make_float2(S[r].z, S[r].w), make_float2(qv.z, qv.w)));
@@ -157,6 +160,8 @@ __global__ void __launch_bounds__(kThreads) linattn_recurrent_kernel(LinAttnArgs
     int t = 0;
     if (kGroup > 1)
       for (; t + kGroup <= n; t += kGroup) tokens(std::integral_constant<int, kGroup>(), buf, t0, t);
+    if (kGroup > 4)
+      for (; t + 4 <= n; t += 4) tokens(std::integral_constant<int, 4>(), buf, t0, t);
     for (; t < n; ++t) tokens(std::integral_constant<int, 1>(), buf, t0, t);
     if (tid < kTB && next < T) s_a[(block + kRing - 1) % kRing][tid] = Decay::of(na);
   }
@@ -166,36 +171,49 @@ __global__ void __launch_bounds__(kThreads) linattn_recurrent_kernel(LinAttnArgs
     if (in_bounds(s_at + r * kD + 4, s_size, a.err)) st_stream(a.S_T + s_at + r * kD, S[r]);
 }
 
-template <typename IO, int kRows>
+template <typename IO, int kRows, int kGroup, int kWarps>
 void launch(const LinAttnArgs &a, cudaStream_t s) {
   const unsigned grid = (unsigned)((long long)a.B * a.Hv * (kD / (kWarps * kRows)));
-  // Up to three tokens are bound by the state's traffic: no groups, and the
-  // registers of more CTAs per SM instead (64 x 48 heads, 3 tokens: 72 us, in
-  // groups 75).
-  if (a.T < 4)
-    linattn_recurrent_kernel<IO, kRows, 1><<<grid, kThreads, 0, s>>>(a);
-  else
-    linattn_recurrent_kernel<IO, kRows, 4><<<grid, kThreads, 0, s>>>(a);
+  linattn_recurrent_kernel<IO, kRows, kGroup, kWarps><<<grid, kWarps * 32, 0, s>>>(a);
 }
 
 template <typename IO>
-void launch_rows(const LinAttnArgs &a, int num_sms, cudaStream_t s) {
-  // Few units: the rows of a unit over more CTAs.  (1 x 16 heads, one token: 2.5
-  // us with 2 rows per warp, 2.8 with 4, 3.0 with 8; 64 x 48 heads: 71, 60, 61 us.)
+void launch_form(const LinAttnArgs &a, int num_sms, cudaStream_t s) {
   const long long units = (long long)a.B * a.Hv;
+  const long long tokens = a.cu_seqlens ? a.T / a.B : a.T;  // of a sequence (packed: on average)
+  // From four tokens on: CTAs of 4 warps, which drift apart, so that one's loads
+  // from shared memory run beside another's arithmetic and sums; 8 rows per warp
+  // where the units fill the SMs, else 4 rows and the sums of 8 tokens together.
+  // (fp32, 2 x 1001 tokens, 8 heads: 102 us, with CTAs of 8 warps of 2 rows and
+  // groups of 4 121; 4 x 1001, 12 heads: 186, with 8 warps of 4 rows 257, 4 warps of
+  // 8 236; 16 x 256, 32 heads: 360 with 8 rows in groups of 4, 377 with 4 rows in
+  // groups of 8, 407 with 8 warps of 4 rows; 64 x 48 heads, 4 tokens: 71, 74 with 8
+  // warps of 4 rows.)
+  if (tokens >= 4) {
+    if (units < num_sms)
+      launch<IO, 4, 8, 4>(a, s);
+    else
+      launch<IO, 8, 4, 4>(a, s);
+    return;
+  }
+  // Up to three tokens are bound by the state's traffic: no groups, and the
+  // registers of more CTAs per SM instead (64 x 48 heads, 3 tokens: 72 us, in
+  // groups 75).  Few units: the rows of a unit over more CTAs (1 x 16 heads, one
+  // token: 2.5 us with 2 rows per warp, 2.8 with 4, 3.0 with 8; 64 x 48 heads: 71,
+  // 60, 61 us.)
   if (units * 4 <= num_sms)
-    launch<IO, 2>(a, s);
+    launch<IO, 2, 1, 8>(a, s);
   else
-    launch<IO, 4>(a, s);
+    launch<IO, 4, 1, 8>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_linattn_recurrent(const LinAttnArgs &a, bool bf16, int num_sms, cudaStream_t s) {
   if (bf16)
-    launch_rows<__nv_bfloat16>(a, num_sms, s);
+    launch_form<__nv_bfloat16>(a, num_sms, s);
   else
-    launch_rows<float>(a, num_sms, s);
+    launch_form<float>(a, num_sms, s);
   return cudaGetLastError();
 }
 
