@@ -19,6 +19,7 @@
 //                     sums through distributed shared memory and add them in a
 //                     fixed order: no workspace, no second launch, the same
 //                     result every time.
+#include <atomic>
 #include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -563,7 +564,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 // =============================================================================
 // lin_skinny_kernel
 // =============================================================================
-constexpr int kRowsW = 128;  // rows of w per tile (gated: 64 gate, 64 up)
+constexpr int kRowsW = 128;  // rows of w per tile at most (gated: half of them gate rows, half up rows)
 constexpr int kSkinnyThreads = 192;
 
 template <int NT>
@@ -658,18 +659,19 @@ __device__ __forceinline__ void finish(const LinCol &c, long long row0, int step
 
 template <int NT, bool kGated>
 __global__ void __launch_bounds__(kSkinnyThreads, 1)
-    lin_skinny_kernel(const LinArgs g, int split, const __grid_constant__ CUtensorMap tm_x,
+    lin_skinny_kernel(const LinArgs g, int split, int rows_w, const __grid_constant__ CUtensorMap tm_x,
                       const __grid_constant__ CUtensorMap tm_w) {
   using L = Skinny<NT>;
   static_assert(L::kRing <= 12, "barriers");
-  constexpr int kOut = kGated ? kRowsW / 2 : kRowsW;  // output columns of a tile
+  constexpr int kOut = kGated ? kRowsW / 2 : kRowsW;  // output columns of a tile at most
+  const int out = kGated ? rows_w / 2 : rows_w;       // and of this call's
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   SkinnyBars &B = *reinterpret_cast<SkinnyBars *>(sm + L::kBars);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rank = blockIdx.x % split, tile = blockIdx.x / split;
-  const int tiles_n = (g.N + kOut - 1) / kOut;
-  const int n0 = (tile % tiles_n) * kOut, m0 = (tile / tiles_n) * NT;
+  const int tiles_n = (g.N + out - 1) / out;
+  const int n0 = (tile % tiles_n) * out, m0 = (tile / tiles_n) * NT;
   const int nk = (g.K + BK - 1) / BK;
   const int kb0 = (int)((long long)nk * rank / split), kb1 = (int)((long long)nk * (rank + 1) / split);
   const uint32_t sbase = smem_u32(sm);
@@ -697,12 +699,13 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
       ok = __all_sync(0xffffffffu, bar_wait(&B.empty[s], ((it / L::kRing) & 1) ^ 1));
       if (!ok) break;
       const int n = min(L::kSteps, kb1 - kb0 - it * L::kSteps);
-      bar_expect_tx_w(&B.full[s], n * L::kBlock);
+      bar_expect_tx_w(&B.full[s], n * (rows_w * BK * 2 + L::kB));
       for (int i = 0; i < n; ++i) {
         const uint32_t dst = sbase + s * L::kStage + i * L::kBlock;
         const int k = (kb0 + it * L::kSteps + i) * BK;
+        // One copy for all rows of w, gate and up: the rows past rows_w, if any, stay
+        // what they are and so does what the MMAs make of them, which nothing reads.
         tma_load_3d_w(dst, &tm_w, k, n0, 0, &B.full[s]);
-        tma_load_3d_w(dst + L::kA / 2, &tm_w, k, kGated ? g.N + n0 : n0 + kRowsW / 2, 0, &B.full[s]);
         tma_load_3d_w(dst + L::kA, &tm_x, k, m0, 0, &B.full[s]);
       }
     }
@@ -745,8 +748,8 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
     LinCol c{};
     float b = 0.f;
     if (direct) {
-      c = column(g, n0 + n);
-      if (bias && n0 + n < g.N) b = __bfloat162float(bias[n0 + n]);
+      if (n < out) c = column(g, n0 + n);
+      if (bias && c.y) b = __bfloat162float(bias[n0 + n]);
     }
     uint32_t to = 0, at = sbase + (uint32_t)(rank * per * kRowsW + n) * 4;
 #pragma unroll 1
@@ -785,7 +788,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
   const int n = tid % kOut;
   constexpr int kShare = kSkinnyThreads / kOut;  // 1 or 3 threads per column
   constexpr int kRun = NT <= 32 ? 4 : 8;         // tokens finished side by side
-  const LinCol c = tid < kShare * kOut ? column(g, n0 + n) : LinCol{};
+  const LinCol c = tid < kShare * kOut && n < out ? column(g, n0 + n) : LinCol{};
   const long long row0 = (long long)m0 + rank;
   bf16 ahead[kRun];
   int t = kRun * (tid / kOut);
@@ -812,21 +815,22 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
       for (int e = 0; e < kRun; ++e)
         if (t + e < mine) {
           p[e] += src[e * kRowsW];
-          if (kGated) u[e] += src[e * kRowsW + kOut];
+          if (kGated) u[e] += src[e * kRowsW + out];
         }
     }
     finish<kGated>(c, row0 + (long long)t * split, split, mine - t, p, u, res);
   }
 }
 
-// A row-major [rows][K] bf16 matrix as a 3-d map (third extent 1) with
-// 128-byte-swizzled boxes of 64 columns x box_rows rows.
-bool encode_kmajor(CUtensorMap *m, const void *base, long long rows, long long K, long long ld, int box_rows) {
+// A row-major [rows][K] bf16 matrix, or `parts` of them one after the other, as a
+// 3-d map with 128-byte-swizzled boxes of 64 columns x box_rows rows of each part.
+bool encode_kmajor(CUtensorMap *m, const void *base, long long rows, long long K, long long ld, int box_rows,
+                   int parts = 1) {
   EncodeTiled enc = encoder();
   if (!enc) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)rows, 1};
+  const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)rows, (cuuint64_t)parts};
   const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)rows};
-  const cuuint32_t box[3] = {(cuuint32_t)BK, (cuuint32_t)box_rows, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)BK, (cuuint32_t)box_rows, (cuuint32_t)parts};
   const cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -882,26 +886,86 @@ cudaError_t launch_tile(const LinArgs &a, int num_sms, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// How many clusters of `size` CTAs of the skinny kernel run at once: fewer than
+// the SMs would take, since a cluster stays within one group of SMs (152 SMs: 46
+// of 3, 36 of 4, 28 of 5, 23 of 6, 15 of 7 or 8).  Asked once per device.
+template <int NT, bool kGated>
+cudaError_t cluster_caps(int num_sms, int (&cap)[9]) {
+  using L = Skinny<NT>;
+  static std::atomic<uint64_t> known[64];  // a byte per size
+  auto *kernel = lin_skinny_kernel<NT, kGated>;
+  cudaError_t e = allow_smem<SkinnyTag<NT, kGated>>(kernel, L::kSmem);
+  int dev = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  uint64_t bytes = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (bytes == 0) {
+    for (int size = 2; size <= 8; ++size) {
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3((unsigned)(size * num_sms));
+      cfg.blockDim = dim3(kSkinnyThreads);
+      cfg.dynamicSmemBytes = L::kSmem;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = (unsigned)size;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int n = 0;
+      e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      bytes |= (uint64_t)(n < 255 ? n : 255) << (8 * (size - 1));
+    }
+    bytes |= 1;  // asked
+    if (dev < 64) known[dev].store(bytes, std::memory_order_relaxed);
+  }
+  cap[0] = 0, cap[1] = num_sms;
+  for (int size = 2; size <= 8; ++size) cap[size] = (int)(bytes >> (8 * (size - 1)) & 255);
+  return cudaSuccess;
+}
+
+// The widest split of `tiles` whose CTAs all run at once, each with some k steps
+// and (the partial sums' space) whole tokens; 1 where they do not.  A wider one
+// costs a second wave (16 tokens, 4096 -> 2560: 6.6 us with 6 CTAs per cluster,
+// 11.8 with 7, whose 20 clusters do not fit).
+template <int NT>
+int skinny_split(long long tiles, int nk, const int (&cap)[9]) {
+  int split = nk / 2 < 8 ? nk / 2 : 8;
+  while (split > 1 && (tiles > cap[split] || split * ((NT + split - 1) / split) * kRowsW * 4 > (int)Skinny<NT>::kBars)) --split;
+  return split < 1 ? 1 : split;
+}
+
 template <int NT, bool kGated>
 cudaError_t launch_skinny(const LinArgs &a, int num_sms, cudaStream_t s) {
   using L = Skinny<NT>;
+  int cap[9];
+  cudaError_t e = cluster_caps<NT, kGated>(num_sms, cap);
+  if (e != cudaSuccess) return e;
+  const int nk = (a.K + BK - 1) / BK;
+  // Rows of w per tile: all 128, or fewer where the tiles come in several waves
+  // and smaller ones fill the last better.  Microseconds of a wave: its rows of w at
+  // 6.5 TB/s, or a CTA's k steps at 0.15 (8 tokens, 5120 -> 24576: 43.9 us with 96
+  // rows, 45.7 with 128).  From 128 tokens on the loads of x count as much.
+  int rows_w = kRowsW, split = 1;
+  long long tiles = 0;
+  float least = 0.f;
+  for (int rows = kRowsW; rows >= (NT <= 64 ? 80 : kRowsW); rows -= 16) {
+    const int out = kGated ? rows / 2 : rows;
+    const long long n = (long long)((a.N + out - 1) / out) * ((a.M + NT - 1) / NT);
+    const int sp = skinny_split<NT>(n, nk, cap);
+    const float cta = rows * 2e-6f * a.K / sp / 6.5f, steps = 0.15f * nk / sp;
+    auto wave = [&](long long clusters) {
+      const float all = cta * (clusters * sp);
+      return all > steps ? all : steps;
+    };
+    const long long waves = n / cap[sp], rest = n % cap[sp];
+    const float cost = 3.f + waves * wave(cap[sp]) + (rest ? wave(rest) : 0.f);
+    if (rows == kRowsW || cost < 0.97f * least) least = cost, rows_w = rows, split = sp, tiles = n;
+  }
   CUtensorMap tm_x, tm_w;
   if (!encode_kmajor(&tm_x, a.x, a.M, a.K, a.ldx, NT) ||
-      !encode_kmajor(&tm_w, a.w, (long long)a.N * (kGated ? 2 : 1), a.K, a.ldw, kRowsW / 2))
+      !encode_kmajor(&tm_w, a.w, a.N, a.K, a.ldw, kGated ? rows_w / 2 : rows_w, kGated ? 2 : 1))
     return cudaErrorInvalidValue;
-  auto *kernel = lin_skinny_kernel<NT, kGated>;
-  cudaError_t e = allow_smem<SkinnyTag<NT, kGated>>(kernel, L::kSmem);
-  if (e != cudaSuccess) return e;
-  constexpr int kOut = kGated ? kRowsW / 2 : kRowsW;
-  const long long tiles = (long long)((a.N + kOut - 1) / kOut) * ((a.M + NT - 1) / NT);
-  const int nk = (a.K + BK - 1) / BK;
-  // The widest split whose CTAs are all resident at once, each with some k steps
-  // and (the partial sums' space) whole tokens.
-  long long split = (long long)num_sms / tiles;
-  if (split > nk / 2) split = nk / 2;
-  if (split > 8) split = 8;
-  if (split < 1) split = 1;
-  while (split > 1 && (long long)split * ((NT + split - 1) / split) * kRowsW * 4 > L::kBars) --split;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * split));
   cfg.blockDim = dim3(kSkinnyThreads);
@@ -913,7 +977,7 @@ cudaError_t launch_skinny(const LinArgs &a, int num_sms, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, (int)split, tm_x, tm_w);
+  return cudaLaunchKernelEx(&cfg, lin_skinny_kernel<NT, kGated>, a, split, rows_w, tm_x, tm_w);
 }
 
 // Microseconds of the tile kernel with tiles of BN w rows: a wave's k steps or
@@ -935,10 +999,14 @@ cudaError_t launch(const LinArgs &a, int num_sms, cudaStream_t s) {
   // tiles, and 8 us for the meeting in the cluster (14 with a residual).
   if (a.M > 128) {
     const int nk = (a.K + BK - 1) / BK, out = kGated ? kRowsW / 2 : kRowsW;
-    const long long tiles2 = (long long)((a.N + out - 1) / out) * ((a.M + 255) / 256), split = num_sms / tiles2;
+    const long long tiles2 = (long long)((a.N + out - 1) / out) * ((a.M + 255) / 256);
+    int cap[9];
+    const cudaError_t e = cluster_caps<256, kGated>(num_sms, cap);
+    if (e != cudaSuccess) return e;
+    const int split = skinny_split<256>(tiles2, nk, cap);
     bool residual = false;
     for (int o = 0; o < a.n_out; ++o) residual |= a.out[o].res != nullptr;
-    const float skinny = split < 2 ? 1e30f : 0.6f * nk / (split > 8 ? 8 : split) + (residual ? 14.f : 8.f);
+    const float skinny = split < 2 ? 1e30f : 0.6f * nk / split + (residual ? 14.f : 8.f);
     const float t256 = tile_cost<kGated>(a, 256, num_sms), t128 = tile_cost<kGated>(a, 128, num_sms);
     const float t64 = kGated ? 1e30f : tile_cost<kGated>(a, 64, num_sms);
     // Pairs: 0.37 us per k step of a wave of their 256 x 256 tiles.
