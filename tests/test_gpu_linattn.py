@@ -290,3 +290,18 @@ def test_very_slow_constant_decay(io, T):
         torch.cuda.synchronize()
         ratio = (S.double() / S0.double()) / math.exp(T * float(torch.tensor(g)))
         assert (ratio - 1).abs().max().item() < 2 * T * 2.0 ** -24
+
+
+# Units below and above the number of SMs, tokens short of, at and past the groups' and blocks' ends.
+@pytest.mark.parametrize("B,Hk,Hv", [(3, 1, 2), (40, 2, 4)])
+@pytest.mark.parametrize("T", [3, 4, 5, 8, 12, 23])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_decode_several_tokens(B, Hk, Hv, T, io):
+    c = Case([T] * B, Hk, Hv, io, seed=90 + T)
+    c.check(*decode(c, pad=8), decode=True)
+
+
+@pytest.mark.parametrize("lens", [[1, 0, 2, 1, 1], [0, 37, 3, 4, 12, 1], [2] * 40 + [9, 0, 30] + [5] * 40])
+def test_prefill_fp32_packed(lens):
+    c = Case(lens, 1, 2, "f32", seed=120 + len(lens))
+    c.check(*prefill(c, packed=True))

@@ -145,3 +145,12 @@ def test_repeats_bit_for_bit_on_a_side_stream_and_in_a_graph():
 def test_pairs_of_ctas(M, N, K):
     check(M, N, K, seed=20, residual=True)
     check(M, N, K, gated=True, seed=21, bias=K != 64)
+
+
+@pytest.mark.parametrize("M", [3, 30, 64])
+def test_few_tokens_in_several_waves_of_smaller_tiles(M):
+    check(M, 24600, 1024, seed=M, pad=8)
+    check(M, 24599, 1000, seed=M + 1, odd=3, residual=True,
+          ranges=[(0, 8200, "silu"), (8200, 16001, "none"), (16001, 24599, "sigmoid")])
+    check(M, 12300, 1024, gated=True, seed=M + 2, residual=M > 3)
+    check(M, 12299, 1000, gated=True, seed=M + 3, bias=False, odd=1)
