@@ -20,6 +20,7 @@
 //                     fixed order: no workspace, no second launch, the same
 //                     result every time.
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -935,49 +936,66 @@ int skinny_split(long long tiles, int nk, const int (&cap)[9]) {
   return split < 1 ? 1 : split;
 }
 
+// The skinny kernel's tiles: NT tokens by rows_w rows of w, over clusters of
+// `split`.  Microseconds, measured: a wave's loads (w and x) at 11.5 TB/s from
+// L2, w at 6.5 from memory, or a CTA's k steps at 0.15; per wave a start, the
+// partial sums' exchange by the tokens, and the finishing by a CTA's share of them.
+struct SkinnyPlan {
+  int rows_w, split;
+  long long tiles;
+  float cost;
+};
 template <int NT, bool kGated>
-cudaError_t launch_skinny(const LinArgs &a, int num_sms, cudaStream_t s) {
-  using L = Skinny<NT>;
+cudaError_t skinny_plan(const LinArgs &a, int num_sms, bool residual, SkinnyPlan &plan) {
   int cap[9];
-  cudaError_t e = cluster_caps<NT, kGated>(num_sms, cap);
+  const cudaError_t e = cluster_caps<NT, kGated>(num_sms, cap);
   if (e != cudaSuccess) return e;
   const int nk = (a.K + BK - 1) / BK;
-  // Rows of w per tile: all 128, or fewer where the tiles come in several waves
-  // and smaller ones fill the last better.  Microseconds of a wave: its rows of w at
-  // 6.5 TB/s, or a CTA's k steps at 0.15 (8 tokens, 5120 -> 24576: 43.9 us with 96
-  // rows, 45.7 with 128).  From 128 tokens on the loads of x count as much.
-  int rows_w = kRowsW, split = 1;
-  long long tiles = 0;
-  float least = 0.f;
+  const long long tiles_m = (a.M + NT - 1) / NT;
+  const float tokens = (float)(a.M < NT ? a.M : NT);
+  // All 128 rows of w, or fewer where the tiles come in several waves and smaller
+  // ones fill the last better (8 tokens, 5120 -> 24576: 43.9 us with 96 rows, 45.7
+  // with 128).  From 128 tokens on the loads of x count as much.
   for (int rows = kRowsW; rows >= (NT <= 64 ? 80 : kRowsW); rows -= 16) {
     const int out = kGated ? rows / 2 : rows;
-    const long long n = (long long)((a.N + out - 1) / out) * ((a.M + NT - 1) / NT);
-    const int sp = skinny_split<NT>(n, nk, cap);
-    const float cta = rows * 2e-6f * a.K / sp / 6.5f, steps = 0.15f * nk / sp;
+    const long long n = (a.N + out - 1) / out * tiles_m;
+    const int split = skinny_split<NT>(n, nk, cap);
+    const float steps = (float)nk / split;
+    const float cta = steps * BK * 2e-6f;  // MB per row
+    const float load = cta * (rows + NT) / 11.5f, mem = cta * rows / 6.5f / tiles_m;
+    const bool direct = split == 1 && !kGated;
+    const float rest = 4.3f + (direct ? 0.03f : 0.016f + 0.06f / split) * tokens +
+                       (!residual ? 0.f : direct ? 0.03f * tokens : 0.5f + 0.01f * tokens);
     auto wave = [&](long long clusters) {
-      const float all = cta * (clusters * sp);
-      return all > steps ? all : steps;
+      const float all = (load > mem ? load : mem) * (clusters * split), one = 0.15f * steps;
+      return (all > one ? all : one) + rest;
     };
-    const long long waves = n / cap[sp], rest = n % cap[sp];
-    const float cost = 3.f + waves * wave(cap[sp]) + (rest ? wave(rest) : 0.f);
-    if (rows == kRowsW || cost < 0.97f * least) least = cost, rows_w = rows, split = sp, tiles = n;
+    const long long waves = n / cap[split], left = n % cap[split];
+    // Part of a start runs beside the wave before it.
+    const float cost = waves * wave(cap[split]) + (left ? wave(left) : 0.f) - 2.3f * (waves - (left ? 0 : 1));
+    if (rows == kRowsW || cost < 0.97f * plan.cost) plan = SkinnyPlan{rows, split, n, cost};
   }
+  return cudaSuccess;
+}
+
+template <int NT, bool kGated>
+cudaError_t launch_skinny(const LinArgs &a, const SkinnyPlan &plan, cudaStream_t s) {
   CUtensorMap tm_x, tm_w;
   if (!encode_kmajor(&tm_x, a.x, a.M, a.K, a.ldx, NT) ||
-      !encode_kmajor(&tm_w, a.w, a.N, a.K, a.ldw, kGated ? rows_w / 2 : rows_w, kGated ? 2 : 1))
+      !encode_kmajor(&tm_w, a.w, a.N, a.K, a.ldw, kGated ? plan.rows_w / 2 : plan.rows_w, kGated ? 2 : 1))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.gridDim = dim3((unsigned)(plan.tiles * plan.split));
   cfg.blockDim = dim3(kSkinnyThreads);
-  cfg.dynamicSmemBytes = L::kSmem;
+  cfg.dynamicSmemBytes = Skinny<NT>::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)split;
+  at[0].val.clusterDim.x = (unsigned)plan.split;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, lin_skinny_kernel<NT, kGated>, a, split, rows_w, tm_x, tm_w);
+  return cudaLaunchKernelEx(&cfg, lin_skinny_kernel<NT, kGated>, a, plan.split, plan.rows_w, tm_x, tm_w);
 }
 
 // Microseconds of the tile kernel with tiles of BN w rows: a wave's k steps or
@@ -994,38 +1012,55 @@ float tile_cost(const LinArgs &a, int BN, int num_sms) {
 
 template <bool kGated>
 cudaError_t launch(const LinArgs &a, int num_sms, cudaStream_t s) {
-  // Up to 128 tokens w is read once either way.  Above, the tile kernel against
-  // the split form, where a wave of it fits: 0.6 us per k step of its 128 x 256
-  // tiles, and 8 us for the meeting in the cluster (14 with a residual).
-  if (a.M > 128) {
-    const int nk = (a.K + BK - 1) / BK, out = kGated ? kRowsW / 2 : kRowsW;
-    const long long tiles2 = (long long)((a.N + out - 1) / out) * ((a.M + 255) / 256);
-    int cap[9];
-    const cudaError_t e = cluster_caps<256, kGated>(num_sms, cap);
+  const int nk = (a.K + BK - 1) / BK;
+  bool residual = false;
+  for (int o = 0; o < a.n_out; ++o) residual |= a.out[o].res != nullptr;
+  // Few tokens or few columns: tiles of 16 to 256 tokens, fewer than there are
+  // where that fills the SMs (219 tokens, 3640 -> 421: 8.2 us in tiles of 32, 15.3
+  // in one of 256, 19.5 by the tile kernel; 128 tokens, 6144 -> 5120: 20.2 in one
+  // of 128, 38.7 in tiles of 32).
+  constexpr int kMostTokens = 2048;  // beyond, other forms have the tiles
+  SkinnyPlan best{0, 0, 0, 1e30f};
+  int nt = 0;
+  cudaError_t e = cudaSuccess;
+  auto consider = [&](auto tokens) {
+    constexpr int NT = decltype(tokens)::value;
+    if (e != cudaSuccess || (NT > 16 && a.M <= NT / 2)) return;
+    SkinnyPlan p{0, 0, 0, 1e30f};
+    e = skinny_plan<NT, kGated>(a, num_sms, residual, p);
+    if (p.cost < best.cost) best = p, nt = NT;
+  };
+  if (a.M <= kMostTokens) {
+    consider(std::integral_constant<int, 16>());
+    consider(std::integral_constant<int, 32>());
+    consider(std::integral_constant<int, 64>());
+    consider(std::integral_constant<int, 128>());
+    consider(std::integral_constant<int, 256>());
     if (e != cudaSuccess) return e;
-    const int split = skinny_split<256>(tiles2, nk, cap);
-    bool residual = false;
-    for (int o = 0; o < a.n_out; ++o) residual |= a.out[o].res != nullptr;
-    const float skinny = split < 2 ? 1e30f : 0.6f * nk / split + (residual ? 14.f : 8.f);
-    const float t256 = tile_cost<kGated>(a, 256, num_sms), t128 = tile_cost<kGated>(a, 128, num_sms);
-    const float t64 = kGated ? 1e30f : tile_cost<kGated>(a, 64, num_sms);
-    // Pairs: 0.37 us per k step of a wave of their 256 x 256 tiles.
-    const int cols = kGated ? 128 : 256;
-    const long long tiles = (long long)((a.M + 255) / 256) * ((a.N + cols - 1) / cols);
-    const float loop = 0.37f * nk, epi = 1.5f * cols / 64;
-    const float pair = (float)((tiles + num_sms / 2 - 1) / (num_sms / 2)) * (loop > epi ? loop : epi) + epi;
-    if (pair <= t256 && pair <= t128 && pair <= t64 && pair <= skinny) return launch_pair<kGated>(a, num_sms, s);
-    if (skinny > t256 || skinny > t128 || skinny > t64) {
-      if (t256 <= t128 && t256 <= t64) return launch_tile<256, kGated>(a, num_sms, s);
-      if (t128 <= t64) return launch_tile<128, kGated>(a, num_sms, s);
-      return launch_tile<kGated ? 128 : 64, kGated>(a, num_sms, s);
-    }
   }
-  if (a.M <= 16) return launch_skinny<16, kGated>(a, num_sms, s);
-  if (a.M <= 32) return launch_skinny<32, kGated>(a, num_sms, s);
-  if (a.M <= 64) return launch_skinny<64, kGated>(a, num_sms, s);
-  if (a.M <= 128) return launch_skinny<128, kGated>(a, num_sms, s);
-  return launch_skinny<256, kGated>(a, num_sms, s);
+  // Against the tile kernel and the pairs, whose costs are without the launch.
+  const float t256 = tile_cost<kGated>(a, 256, num_sms), t128 = tile_cost<kGated>(a, 128, num_sms);
+  const float t64 = kGated ? 1e30f : tile_cost<kGated>(a, 64, num_sms);
+  // Pairs: 0.37 us per k step of a wave of their 256 x 256 tiles.
+  const int cols = kGated ? 128 : 256;
+  const long long tiles = (long long)((a.M + 255) / 256) * ((a.N + cols - 1) / cols);
+  const float loop = 0.37f * nk, epi = 1.5f * cols / 64;
+  const float pair = (float)((tiles + num_sms / 2 - 1) / (num_sms / 2)) * (loop > epi ? loop : epi) + epi;
+  const float mem = (kGated ? 4e-6f : 2e-6f) * a.N / 6.5f * a.K;  // w, once
+  const float least = fmaxf(fminf(fminf(t256, t128), fminf(t64, pair)), mem) + (residual ? 6.f : 4.5f);
+  // Up to 128 tokens they read w once as well, but in fewer pieces: a clear gain only
+  // (107 tokens, 920 -> 6856 with a residual: 8.9 us by tiles, 11.9 so).
+  if (best.cost < least * (a.M <= 128 ? 1.1f : 0.9f)) switch (nt) {
+      case 16: return launch_skinny<16, kGated>(a, best, s);
+      case 32: return launch_skinny<32, kGated>(a, best, s);
+      case 64: return launch_skinny<64, kGated>(a, best, s);
+      case 128: return launch_skinny<128, kGated>(a, best, s);
+      default: return launch_skinny<256, kGated>(a, best, s);
+    }
+  if (pair <= t256 && pair <= t128 && pair <= t64) return launch_pair<kGated>(a, num_sms, s);
+  if (t256 <= t128 && t256 <= t64) return launch_tile<256, kGated>(a, num_sms, s);
+  if (t128 <= t64) return launch_tile<128, kGated>(a, num_sms, s);
+  return launch_tile<kGated ? 128 : 64, kGated>(a, num_sms, s);
 }
 
 }  // namespace

@@ -154,3 +154,9 @@ def test_few_tokens_in_several_waves_of_smaller_tiles(M):
           ranges=[(0, 8200, "silu"), (8200, 16001, "none"), (16001, 24599, "sigmoid")])
     check(M, 12300, 1024, gated=True, seed=M + 2, residual=M > 3)
     check(M, 12299, 1000, gated=True, seed=M + 3, bias=False, odd=1)
+
+
+@pytest.mark.parametrize("M,N,K", [(219, 421, 1640), (526, 62, 1136), (130, 129, 2048), (1100, 40, 520)])
+def test_few_columns_in_several_tiles_of_tokens(M, N, K):
+    check(M, N, K, seed=M, residual=True, odd=1)
+    check(M, N, K, seed=M + 1, gated=True, ranges=[(0, 33, "silu"), (33, N, "sigmoid")])
