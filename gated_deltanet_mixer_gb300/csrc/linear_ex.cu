@@ -269,7 +269,8 @@ __device__ __forceinline__ bool tile_epilogue(const LinArgs &g, float *run, int 
     const int col0 = tile0 + c;
     if (c + 32 < first + kCols / 2) loaded = prefetch_residual(g, row0, lane, col0 + 32, ahead);
     float v[32], u[32];
-    tmem_ld32(taddr + c, v);  // every lane of the warp takes part
+    __syncwarp();  // lanes parted on their rows and columns: the TMEM loads take the whole warp together
+    tmem_ld32(taddr + c, v);
     if (kGated) tmem_ld32(taddr + kCols + c, u);
     if (row0 >= g.M || col0 >= g.N) continue;
     if (bias) {
@@ -756,6 +757,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
 #pragma unroll 1
     for (int t0 = 0; t0 < rows; t0 += 8) {
       float v[8];
+      __syncwarp();  // lanes without a column skipped the stores
       tmem_ld8(taddr + t0, v);
       if (direct) {
 #pragma unroll
@@ -794,6 +796,7 @@ __global__ void __launch_bounds__(kSkinnyThreads, 1)
   bf16 ahead[kRun];
   int t = kRun * (tid / kOut);
   if (c.y) load_rows(c, row0 + (long long)t * split, split, mine - t, ahead);
+  __syncwarp();  // the barrier takes whole warps
   if (split > 1) cluster_sync();
   if (!c.y) return;
   float b = 0.f, bu = 0.f;
