@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4 *>(sm + s * kStageBytes + 2 * kTile + jrow + 16 * c) = make_uint4(0, 0, 0, 0);
         }
       }
+      __syncwarp();  // the transposing loads and TMEM stores take the whole warp together
       const uint32_t vbase = sbase + s * kStageBytes + 2 * kTile + vrow;
       // Two pieces at a time, the small ones first: the last update has read those.
 #pragma unroll 1
@@ -657,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!kStateOnly) {
         if (n > 0) ok = warp_wait(&B.o_done, par ^ 1);  // the last output has read its state
         if (!ok) break;
+        __syncwarp();
         tmem_st32w_nw(tl + kTSh + 32 * half, hi);
         tmem_st32w_nw(tl + kTSl + 32 * half, lo);
         tmem_wait_st();
@@ -700,6 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         buf[row_ * 32 + ((piece + i) ^ l)] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+      __syncwarp();
       asm volatile("bar.sync 1, 256;" ::: "memory");
       float *dst = kStateOnly ? a.ws + (seg_ + 1) * units * kState : a.S_T;
 #pragma unroll 1
@@ -732,6 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
           uint32_t r[16];
+          __syncwarp();  // lanes past the sequence's end skipped the stores
           tmem_ld16_nw(tl + kTO + 16 * i, r);
           tmem_wait_ld();
           if (i == 3) {
