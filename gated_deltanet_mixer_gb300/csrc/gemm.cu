@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < BN; c += 32) {
         float v[32];
+        __syncwarp();  // lanes past the last row skipped the stores
         tmem_ld32(taddr + c, v);  // every lane of the warp takes part
         const int col0 = nt * BN + c;
         if (row >= g.M || col0 >= g.N) continue;

@@ -81,7 +81,7 @@ def unsafe(lines):
     return bad
 
 
-@pytest.mark.parametrize("name", ["linear_ex.cu", "linattn_chunked.cu"])
+@pytest.mark.parametrize("name", ["linear_ex.cu", "linattn_chunked.cu", "gemm.cu"])
 def test_aligned_instructions_follow_a_meeting_point(name):
     assert unsafe(code(os.path.join(CSRC, name))) == []
 
