@@ -248,8 +248,9 @@ __device__ __forceinline__ void chunk_vec(ChunkVec &cv, float g0, float g1, floa
   cv.G[lane + 32] = p1 * kLog2e;
   cv.over[lane] = fminf(p0 - kFloor, 0.f) * kLog2e;
   cv.over[lane + 32] = fminf(p1 - kFloor, 0.f) * kLog2e;
-  cv.eF[lane] = scale * expf(fmaxf(p0, kFloor));
-  cv.eF[lane + 32] = scale * expf(fmaxf(p1, kFloor));
+  // A NaN, and with it every sum from its token on, gets into the outputs here.
+  cv.eF[lane] = scale * expf(p0 < kFloor ? kFloor : p0);
+  cv.eF[lane + 32] = scale * expf(p1 < kFloor ? kFloor : p1);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = lane + 32 * i;
@@ -322,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t < T) g0 = gh;
       if (t + 32 < T) g1 = gh;
     }
-    g0 = fmaxf(g0, kMinLogDecay);
-    g1 = fmaxf(g1, kMinLogDecay);
+    if (g0 < kMinLogDecay) g0 = kMinLogDecay;  // a NaN stays one
+    if (g1 < kMinLogDecay) g1 = kMinLogDecay;
   };
   float g0 = 0.f, g1 = 0.f;
   if (warp == 20 && n_chunks > 0) load_g(c0, g0, g1);

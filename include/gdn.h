@@ -382,7 +382,9 @@ gdn_status gdn_linear_ex(int M, int N, int K, int gated, const void *x, long lon
  * state, 16 bits of what feeds o only), the state itself is summed in fp32.
  * Log decays below -80 act as -80 there.  q, k and v are finite: a NaN or
  * infinity spreads over its chunk and into the state (never into another
- * sequence).  fp32 io runs token by token in fp32.
+ * sequence).  A NaN log decay makes the outputs of its head from its token on
+ * and the head's state NaN, whichever way the call runs.  fp32 io runs token
+ * by token in fp32.
  */
 typedef struct {
   const void *q, *k, *v;

@@ -1,0 +1,63 @@
+"""Linear attention at unusual decays.  Tolerances as in test_gpu_linattn.py."""
+import math
+
+import pytest
+import torch
+
+from gated_deltanet_mixer_gb300 import gdn
+from test_gpu_linattn import Case, decode, prefill
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from gated_deltanet_mixer_gb300 import build
+    build.build()
+    gdn.lib()
+    assert gdn.gdn_device_status(reset=True) == 0
+
+
+def check_with_nan(c, o, S, token_loop):
+    """NaN exactly where the 64-bit loop has it, the rest within the tolerances."""
+    o, S = o.cpu().double().view(-1, c.Hv, D), S.cpu().double()
+    for b, n in enumerate(c.lens):
+        at = sum(c.lens[:b])
+        ro, rS, Ao, AS = c.reference(b)
+        e = (2 * n + 160) * 2.0 ** -24
+        half = 2.0 ** -8 if c.dt == torch.bfloat16 else 2.0 ** -24
+        for got, ref, bound in ((S[b], rS, (e if token_loop else 2.0 ** -18) * AS),
+                                (o[at:at + n], ro, (e if token_loop else 2.0 ** -14) * Ao + half * ro.abs())):
+            assert torch.equal(got.isnan(), ref.isnan())
+            ok = ~ref.isnan()
+            assert bool(((got - ref).abs()[ok] <= bound[ok] + 1e-30).all())
+
+
+@pytest.mark.parametrize("io,T", [("bf16", 20), ("bf16", 200), ("bf16", 2000), ("f32", 70)])
+@pytest.mark.parametrize("where", [0, 17, -1])
+def test_nan_decay_reaches_everything_behind_it(io, T, where):
+    """From its token on, in its head: outputs and the state; nothing else.  20 tokens run token
+    by token, 200 in chunks, 2000 in segments."""
+    def edit(c):
+        c.g[where, 0] = math.nan
+    c = Case([T], 1, 2, io, seed=200 + T, edit=edit)
+    check_with_nan(c, *prefill(c), io == "f32" or T == 20)
+
+
+def test_nan_decay_of_a_token_from_the_cache_and_of_a_head():
+    def edit(c):
+        c.g[1, 1] = math.nan
+    c = Case([3], 1, 2, "bf16", seed=210, edit=edit)
+    check_with_nan(c, *decode(c), True)
+
+    def head(c):
+        c.ld[0] = math.nan
+    c = Case([150], 1, 2, "bf16", "head", seed=211, edit=head)
+    check_with_nan(c, *prefill(c), False)
+
+
+def test_nan_decay_stays_in_its_sequence():
+    def edit(c):
+        c.g[100, 0] = math.nan
+    c = Case([70, 40, 129], 1, 2, "bf16", seed=212, edit=edit)
+    check_with_nan(c, *prefill(c, packed=True), False)
