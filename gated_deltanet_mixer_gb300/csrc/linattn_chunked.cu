@@ -6,15 +6,16 @@
 // value-major (S[v][k]) and with tokens along the columns,
 //   O^T = e^{F_i} (S Q^T + V^T P^T),  P_ij = e^{G_i - F_i - G_j} q_i . k_j (j <= i),
 //   S'  = e^{G_last} S + (Gamma V)^T K,  Gamma_j = e^{G_last - G_j},
-// with F_i = max(G_i, -40), so that one accumulator takes both products of an
-// output: P grows to e^40 at most, and an output of a token 40 below the chunk's
-// start in log decay sees e^-40 of the state where it should see less.  Only S Q^T
+// with F_i = max(G_i, -58 ln 2), so that one accumulator takes both products of an
+// output: P grows to 2^58 at most, and an output of a token further below the chunk's
+// start sees 2^-58 of the state where it should see less.  Only S Q^T
 // and the sum of S' carry the state: the products P, V^T P^T and (Gamma V)^T K of a
 // chunk do not wait for it.
 //
 // One CTA walks the chunks of one (sequence, value head, segment):
-//   warp 20      TMA: q, k, v tiles into a 4-stage ring; the chunk's decays
+//   warp 20      TMA: q, k, v tiles into a 4-stage ring
 //   warp 21      issues the MMAs
+//   warp 22      the chunk's decays
 //   warps 16-19  (Gamma V)^T from shared memory into TMEM (a transposing load
 //                hands each thread the words that its TMEM lanes hold)
 //   warps 8-11   P from TMEM into shared memory
@@ -62,7 +63,7 @@ using namespace umma;
 constexpr int kC = 64;  // tokens per chunk
 constexpr int kStages = 4;
 constexpr int kVecs = 8;  // chunk vectors in flight (the output warps lag the loads by less)
-constexpr float kFloor = -40.f;  // of the sum of a chunk's log decays in front of an output (below)
+constexpr int kFloor = -58;  // of the sum of a chunk's log2 decays in front of an output (above)
 constexpr float kMinLogDecay = -80.f;  // a decay below e^-80 acts as e^-80: sums of it stay finite
 
 constexpr uint32_t kTile = kC * kD * 2;             // 16 KB: 64 tokens x 128
@@ -72,9 +73,12 @@ constexpr uint32_t kPTile = kC * kC * 2;
 constexpr uint32_t kShared = kP + 2 * kPTile;
 
 struct ChunkVec {
-  float G[kC];   // sums of the log2 decays from the chunk's first token
-  float over[kC];  // G - F where G is below it, else 0 (log2)
-  float eF[kC];  // scale e^F, F = max(natural G, kFloor)
+  // Sums of the log2 decays from the chunk's first token, G = n + f with n whole
+  // and 0 <= f <= 1: (-n, -n, -f, -f) of the tokens 2 i, 2 i + 1.  The ratio of two
+  // decays is 2 to a difference of sums that may be thousands: in one fp32 number
+  // each, 40 decays of e^-80 would leave the ratio of those behind them 10 bits.
+  float4 G[kC / 2];
+  float eF[kC];  // scale 2^F, F = max(G, kFloor)
   // e^{G_last - G} of the tokens 2 i, 2 i + 1 as bf16 pairs (c0, 0) and (c1, c2)
   // with c0 + c1 + c2 = it to 24 bits; 0 past the sequence's end
   uint2 gam[2][kC / 2];
@@ -92,11 +96,12 @@ struct Shared {
 constexpr uint32_t kSmem = kShared + ((sizeof(Shared) + 127) / 128) * 128 + 1024;
 static_assert(kSmem <= 232448, "shared memory per CTA");
 
-// Six warpgroups; the last one's warps 22 and 23 only take part in barriers.
+// Six warpgroups; warp 23 only takes part in barriers.
 // Registers per thread: launched with 80, then split by what a group holds
-// (256 x 136 + 128 x (56 + 56 + 56 + 40) = 768 x 80).
+// (256 x 136 + 128 x (64 + 56 + 56 + 32) = 768 x 80; P with 56 and the last
+// group with 40: 4 x 8192 tokens take 258 us, so 256).
 constexpr int kThreads = 24 * 32;
-constexpr int kRegsState = 136, kRegsP = 56, kRegsOut = 56, kRegsGv = 56, kRegsIssue = 40;
+constexpr int kRegsState = 136, kRegsP = 64, kRegsOut = 56, kRegsGv = 56, kRegsIssue = 32;
 static_assert(256 * kRegsState + 128 * (kRegsP + kRegsOut + kRegsGv + kRegsIssue) <= kThreads * 80, "register split");
 // TMEM columns (fp32, or bf16 pairs for the operands): all 512 are used.  The
 // state-only form double-buffers both the update and Gamma V.
@@ -228,33 +233,35 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
 
 // The decays of a chunk, by one warp: lane L holds tokens L and L + 32.
 __device__ __forceinline__ void chunk_vec(ChunkVec &cv, float g0, float g1, float scale, int len, int lane) {
-  float p0 = g0, p1 = g1;  // inclusive sums from the front
-  float s0 = g0, s1 = g1;  // and from the back: no cancellation in e^{G_last - G_j}
+  // Sums from the front, of log2 decays in units of 2^-48 (64 of them take 62 bits):
+  // exact, so that those to the chunk's end, their differences, are as well.
+  constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+  using Fixed = unsigned long long;
+  Fixed p0 = (Fixed)__float2ll_rn(g0 * kLog2e * 0x1p48f), p1 = (Fixed)__float2ll_rn(g1 * kLog2e * 0x1p48f);
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const float a = __shfl_up_sync(0xffffffffu, p0, off), b = __shfl_up_sync(0xffffffffu, p1, off);
-    const float c = __shfl_down_sync(0xffffffffu, s0, off), d = __shfl_down_sync(0xffffffffu, s1, off);
+    const Fixed a = __shfl_up_sync(0xffffffffu, p0, off), b = __shfl_up_sync(0xffffffffu, p1, off);
     if (lane >= off) p0 += a, p1 += b;
-    if (lane + off < 32) s0 += c, s1 += d;
   }
   p1 += __shfl_sync(0xffffffffu, p0, 31);
-  s0 += __shfl_sync(0xffffffffu, s1, 0);
-  // sums over the tokens behind: shift the inclusive sums by one token
-  float e0 = __shfl_down_sync(0xffffffffu, s0, 1), e1 = __shfl_down_sync(0xffffffffu, s1, 1);
-  const float first1 = __shfl_sync(0xffffffffu, s1, 0);
-  if (lane == 31) e0 = first1, e1 = 0.f;
-  constexpr float kLog2e = 1.44269504088896341f;
-  cv.G[lane] = p0 * kLog2e;
-  cv.G[lane + 32] = p1 * kLog2e;
-  cv.over[lane] = fminf(p0 - kFloor, 0.f) * kLog2e;
-  cv.over[lane + 32] = fminf(p1 - kFloor, 0.f) * kLog2e;
-  // A NaN, and with it every sum from its token on, gets into the outputs here.
-  cv.eF[lane] = scale * expf(p0 < kFloor ? kFloor : p0);
-  cv.eF[lane + 32] = scale * expf(p1 < kFloor ? kFloor : p1);
+  const Fixed last = __shfl_sync(0xffffffffu, p1, 31);
+  // A NaN, which whole numbers do not hold, gets into the outputs from its token on by eF, into the state by d.
+  const unsigned nan0 = __ballot_sync(0xffffffffu, g0 != g0), nan1 = __ballot_sync(0xffffffffu, g1 != g1);
+  const unsigned upto = 0xffffffffu >> (31 - lane);
+  const float nan = __int_as_float(0x7fc00000);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int t = lane + 32 * i;
-    const float x = t < len ? expf(i ? e1 : e0) : 0.f;
+    const Fixed p = i ? p1 : p0;
+    const int n = (int)((long long)p >> 48);
+    const float f = (float)(unsigned)(p >> 16) * 0x1p-32f;
+    float *G = reinterpret_cast<float *>(&cv.G[t >> 1]) + (t & 1);
+    G[0] = (float)-n;
+    G[2] = -f;
+    const bool bad = i ? nan0 || (nan1 & upto) : nan0 & upto;
+    const float eF = n < kFloor ? scale * 0x1p-58f : scale * ex2(f) * __int_as_float((min(n, 128) + 127) << 23);
+    cv.eF[t] = bad ? nan : eF;
+    const float x = t < len ? expf((float)(long long)(last - p) * (kLn2 * 0x1p-48f)) : 0.f;
     const __nv_bfloat16 g0 = __float2bfloat16_rn(x);
     const __nv_bfloat16 g1 = __float2bfloat16_rn(x - __bfloat162float(g0));
     const __nv_bfloat16 g2 = __float2bfloat16_rn(x - __bfloat162float(g0) - __bfloat162float(g1));
@@ -265,8 +272,8 @@ __device__ __forceinline__ void chunk_vec(ChunkVec &cv, float g0, float g1, floa
     to[4 * (kC / 2) + 2] = g2;
   }
   if (lane == 0) {
-    cv.d = Decay::of(s0);
-    cv.total = s0;
+    cv.total = nan0 | nan1 ? nan : (float)(long long)last * (kLn2 * 0x1p-48f);
+    cv.d = Decay::of(cv.total);
   }
 }
 
@@ -327,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (g1 < kMinLogDecay) g1 = kMinLogDecay;
   };
   float g0 = 0.f, g1 = 0.f;
-  if (warp == 20 && n_chunks > 0) load_g(c0, g0, g1);
+  if (warp == 22 && n_chunks > 0) load_g(c0, g0, g1);
 
   if (tid == 0) {
     auto bar_init = [](uint64_t *bar, uint32_t count) {
@@ -451,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 20) {
     regs_dec<kRegsIssue>();
     if (warp == 20) {
-      // ---- TMA producer and the chunk vectors
+      // ---- TMA producer
       int n = 0;
       for (; n < n_chunks; ++n) {
         const int s = n % kStages;
@@ -470,10 +477,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(dst + 2 * kTile + x * (kTile / 2), &tm_v, h * kD + 64 * x, row, 0, &B.full[s]);
           }
         }
-        chunk_vec(B.vec[n % kVecs], g0, g1, a.scale, T - c * kC, lane);
-        __syncwarp();
-        if (lane == 0) arrive(&B.full[s]);
-        if (n + 1 < n_chunks) load_g(c + 1, g0, g1);
       }
       // Leave only when every tile issued has been consumed (bounded).
       for (int j = max(0, n - kStages); ok && j < n; ++j)
@@ -559,6 +562,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       commit_w(&B.end);  // every MMA issued is complete before TMEM is freed
       if (!warp_wait(&B.end, 0)) ok = false;
+    } else if (warp == 22) {
+      // ---- the chunk vectors, each with its stage (a warp of their own on another
+      // scheduler: with the TMA's warp 4 x 8192 tokens take 4 us more)
+      for (int n = 0; n < n_chunks; ++n) {
+        const int s = n % kStages, c = c0 + n;
+        ok = warp_wait(&B.empty[s], ((n / kStages) & 1) ^ 1);
+        if (!ok) break;
+        chunk_vec(B.vec[n % kVecs], g0, g1, a.scale, T - c * kC, lane);
+        warp_arrive(&B.full[s]);
+        if (n + 1 < n_chunks) load_g(c + 1, g0, g1);
+      }
     }
   } else if (warp >= 16) {
     regs_dec<kRegsGv>();
@@ -581,18 +595,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16x64(tmem + ((uint32_t)(32 * w) << 16) + kTP, r);
         fence_before();
         warp_arrive(&B.p_loaded);
-        const float ga = cv.over[i0], gb = cv.over[i0 + 8];
+        // G - F of this thread's rows: 0 down to the floor, below it what is missing.
+        float2 over[2];  // (whole part, fraction)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float *G = reinterpret_cast<const float *>(&cv.G[(i0 + 8 * q) >> 1]) + (i0 & 1);
+          const bool below = -G[0] < (float)kFloor;
+          over[q] = below ? make_float2(-G[0] - (float)kFloor, -G[2]) : make_float2(0.f, 0.f);
+        }
         // r becomes the pieces: register 4 b + 2 q the first of row i0 + 8 q, the next one the second.
 #pragma unroll
         for (int blk = 0; blk < 8; ++blk) {
           const int jc = 8 * blk + cc;
-          const float2 gj = *reinterpret_cast<const float2 *>(&cv.G[jc]);
+          const float4 gj = cv.G[jc >> 1];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const float gi = q ? gb : ga;
             const int i = i0 + 8 * q;
+            const float2 e = __fadd2_rn(__fadd2_rn(make_float2(over[q].x, over[q].x), make_float2(gj.x, gj.y)),
+                                        __fadd2_rn(make_float2(over[q].y, over[q].y), make_float2(gj.z, gj.w)));
             float2 x = __fmul2_rn(make_float2(__uint_as_float(r[4 * blk + 2 * q]), __uint_as_float(r[4 * blk + 2 * q + 1])),
-                                  make_float2(ex2(gi - gj.x), ex2(gi - gj.y)));
+                                  make_float2(ex2(e.x), ex2(e.y)));
             if (jc > i) x.x = 0.f;
             if (jc + 1 > i) x.y = 0.f;
             r[4 * blk + 2 * q] = take_bf16(x);

@@ -1,10 +1,12 @@
-"""Linear attention at unusual decays.  Tolerances as in test_gpu_linattn.py."""
+"""Linear attention at unusual decays: NaN, strong ones in front of slow ones.
+Tolerances as in test_gpu_linattn.py."""
 import math
 
 import pytest
 import torch
 
 from gated_deltanet_mixer_gb300 import gdn
+from linattn_reference import D
 from test_gpu_linattn import Case, decode, prefill
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +63,20 @@ def test_nan_decay_stays_in_its_sequence():
         c.g[100, 0] = math.nan
     c = Case([70, 40, 129], 1, 2, "bf16", seed=212, edit=edit)
     check_with_nan(c, *prefill(c, packed=True), False)
+
+
+@pytest.mark.parametrize("strong", [-1.0, -5.0, -10.0, -20.0, -40.0, -80.0, -math.inf])
+@pytest.mark.parametrize("first", [0, 20])
+def test_slow_decays_behind_strong_ones(strong, first):
+    """40 strong decays, then pairs of tokens that cancel: v of the second is minus the first's after its
+    decay, so that o is what the rounding of v leaves and an error of the ratio of their decays shows."""
+    def edit(c):
+        c.g[:] = -0.3 * torch.rand(c.g.shape, generator=torch.Generator().manual_seed(1))
+        c.g[first:first + 40] = strong
+        for t in range(first + 40, 128, 2):
+            c.k[t + 1] = c.k[t]
+            for h in range(c.Hv):
+                cols = slice(h * D, (h + 1) * D)
+                c.v[t + 1, cols] = -(c.v[t, cols].double() * math.exp(c.g[t + 1, h])).to(c.dt)
+    c = Case([128], 1, 2, "bf16", seed=220, edit=edit)
+    c.check(*prefill(c))
