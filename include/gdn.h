@@ -338,7 +338,7 @@ gdn_status gdn_linear(int M, int N, int K, const void *x, long long ldx, const v
 typedef enum {
   GDN_ACT_NONE = 0,
   GDN_ACT_SILU = 1,    /* x sigmoid(x) */
-  GDN_ACT_GELU = 2,    /* x Phi(x), Phi by erf */
+  GDN_ACT_GELU = 2,    /* x Phi(x), in the tails to 2^-16 of itself */
   GDN_ACT_SIGMOID = 3
 } gdn_activation;
 
