@@ -329,6 +329,12 @@ bool column_blocks(const void *a, size_t wa, const void *b, size_t wb, size_t pi
   return d >= wa && d + wb <= pitch;
 }
 
+// The kernels of gdn_linear_ex count their tiles (128 x 64 the smallest) in 31 bits.
+bool linear_ex_sizes(int M, int N, int K) {
+  return M <= (1 << 30) && N <= (1 << 29) && K <= (1 << 30) &&
+         ((M + 127LL) / 128) * ((N + 63LL) / 64) < (1LL << 31);
+}
+
 gdn_status linattn_impl(const gdn_shape *shape, const gdn_linattn_io *io, bool decode, void *stream) {
   if (!shape || !io) return GDN_ERR_INVALID_ARG;
   if (shape->B < 1 || shape->T < 1) return GDN_ERR_INVALID_ARG;
@@ -530,10 +536,7 @@ gdn_status gdn_linear_ex(int M, int N, int K, int gated, const void *x, long lon
   if (M < 1 || N < 1 || K < 1 || !x || !w || !out || n_out < 1 || n_out > gdn::kGemmMaxOut)
     return GDN_ERR_INVALID_ARG;
   if (ldx < K || ldw < K) return GDN_ERR_INVALID_ARG;
-  if (M > (1 << 30) || N > (1 << 29) || K > (1 << 30) || ldx > (1LL << 32) || ldw > (1LL << 32))
-    return GDN_ERR_UNSUPPORTED_SHAPE;
-  // The kernels count their tiles (128 x 64 the smallest) in 31 bits.
-  if (((M + 127LL) / 128) * ((N + 63LL) / 64) >= (1LL << 31)) return GDN_ERR_UNSUPPORTED_SHAPE;
+  if (!linear_ex_sizes(M, N, K) || ldx > (1LL << 32) || ldw > (1LL << 32)) return GDN_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(x) || !aligned16(w) || !aligned16(bias) || (ldx % 8) != 0 || (ldw % 8) != 0) return GDN_ERR_ALIGNMENT;
   gdn::LinArgs a{};
   a.M = M;
@@ -586,6 +589,25 @@ gdn_status gdn_linear_ex(int M, int N, int K, int gated, const void *x, long lon
   if (st != GDN_OK) return st;
   a.err = dev.err;
   return gdn::launch_linear_ex(a, dev.sms, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_selftest_linear_ex_form(int M, int N, int K, int gated, int residual, gdn_linear_ex_form *form) {
+  if (M < 1 || N < 1 || K < 1 || !form) return GDN_ERR_INVALID_ARG;
+  if (!linear_ex_sizes(M, N, K)) return GDN_ERR_UNSUPPORTED_SHAPE;
+  DeviceInfo dev;
+  const gdn_status st = device_info(&dev);
+  if (st != GDN_OK) return st;
+  gdn::LinArgs a{};
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.gated = gated != 0;
+  a.n_out = 1;
+  a.out[0].res = residual ? &a : nullptr;  // only whether there is one
+  gdn::LinForm f;
+  if (gdn::linear_ex_form(a, dev.sms, &f) != cudaSuccess) return GDN_ERR_CUDA;
+  *form = gdn_linear_ex_form{f.kernel, f.tile, f.tiles, f.rows_w, f.split};
+  return GDN_OK;
 }
 
 gdn_status gdn_linattn_prefill(const gdn_shape *shape, const gdn_linattn_io *io, void *stream) {

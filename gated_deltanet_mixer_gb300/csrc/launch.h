@@ -99,6 +99,14 @@ struct LinArgs {
   unsigned int *err;
 };
 
+// The kernel that a call takes: gdn_linear_ex_kernel; its tiles' columns (few:
+// tokens), their number, and (few) their rows of w and the CTAs of a cluster.
+struct LinForm {
+  int kernel, tile;
+  long long tiles;
+  int rows_w, split;
+};
+
 // Linear attention with a log decay per value head: S <- e^g S + v k^T,
 // o = scale S q.  Token rows of q, k, v, o are ld* elements apart; sequence b
 // owns rows b*T .. b*T+T-1, or cu_seqlens[b] .. cu_seqlens[b+1]-1 (packed, T
@@ -134,6 +142,7 @@ inline size_t linattn_ws_bytes(int B, int Hv, LinAttnCut c) {
 
 // Each returns the cudaGetLastError() of its launch.
 cudaError_t launch_linear_ex(const LinArgs &a, int num_sms, cudaStream_t s);
+cudaError_t linear_ex_form(const LinArgs &a, int num_sms, LinForm *form);
 cudaError_t launch_linattn_recurrent(const LinAttnArgs &a, bool bf16, int num_sms, cudaStream_t s);
 cudaError_t launch_linattn_chunked(const LinAttnArgs &a, cudaStream_t s);  // bf16 io
 cudaError_t launch_decode(const DecodeArgs &a, bool bf16, cudaStream_t s);

@@ -1006,7 +1006,7 @@ cudaError_t skinny_plan(const LinArgs &a, int num_sms, bool residual, SkinnyPlan
 }
 
 template <int NT, bool kGated>
-cudaError_t launch_skinny(const LinArgs &a, const SkinnyPlan &plan, cudaStream_t s) {
+cudaError_t launch_skinny(const LinArgs &a, const LinForm &plan, cudaStream_t s) {
   CUtensorMap tm_x, tm_w;
   if (!encode_kmajor(&tm_x, a.x, a.M, a.K, a.ldx, NT) ||
       !encode_kmajor(&tm_w, a.w, a.N, a.K, a.ldw, kGated ? plan.rows_w / 2 : plan.rows_w, kGated ? 2 : 1))
@@ -1037,8 +1037,9 @@ float tile_cost(const LinArgs &a, int BN, int num_sms) {
   return (float)((tiles + num_sms - 1) / num_sms) * (loop > epi ? loop : epi) + epi;
 }
 
+// The form with the least cost.
 template <bool kGated>
-cudaError_t launch(const LinArgs &a, int num_sms, cudaStream_t s) {
+cudaError_t choose(const LinArgs &a, int num_sms, LinForm *form) {
   const int nk = (a.K + BK - 1) / BK;
   bool residual = false;
   for (int o = 0; o < a.n_out; ++o) residual |= a.out[o].res != nullptr;
@@ -1077,23 +1078,46 @@ cudaError_t launch(const LinArgs &a, int num_sms, cudaStream_t s) {
   const float least = fmaxf(fminf(fminf(t256, t128), fminf(t64, pair)), mem) + (residual ? 6.f : 4.5f);
   // Up to 128 tokens they read w once as well, but in fewer pieces: a clear gain only
   // (107 tokens, 920 -> 6856 with a residual: 8.9 us by tiles, 11.9 so).
-  if (best.cost < least * (a.M <= 128 ? 1.1f : 0.9f)) switch (nt) {
-      case 16: return launch_skinny<16, kGated>(a, best, s);
-      case 32: return launch_skinny<32, kGated>(a, best, s);
-      case 64: return launch_skinny<64, kGated>(a, best, s);
-      case 128: return launch_skinny<128, kGated>(a, best, s);
-      default: return launch_skinny<256, kGated>(a, best, s);
-    }
-  if (pair <= t256 && pair <= t128 && pair <= t64) return launch_pair<kGated>(a, num_sms, s);
-  if (t256 <= t128 && t256 <= t64) return launch_tile<256, kGated>(a, num_sms, s);
-  if (t128 <= t64) return launch_tile<128, kGated>(a, num_sms, s);
-  return launch_tile<kGated ? 128 : 64, kGated>(a, num_sms, s);
+  if (best.cost < least * (a.M <= 128 ? 1.1f : 0.9f)) {
+    *form = LinForm{GDN_LINEAR_EX_FEW, nt, best.tiles, best.rows_w, best.split};
+    return cudaSuccess;
+  }
+  if (pair <= t256 && pair <= t128 && pair <= t64) {
+    *form = LinForm{GDN_LINEAR_EX_PAIR, cols, tiles, 0, 0};
+    return cudaSuccess;
+  }
+  const int BN = t256 <= t128 && t256 <= t64 ? 256 : t128 <= t64 ? 128 : 64, out = kGated ? BN / 2 : BN;
+  *form = LinForm{GDN_LINEAR_EX_TILE, out, (long long)((a.M + BM - 1) / BM) * ((a.N + out - 1) / out), 0, 0};
+  return cudaSuccess;
+}
+
+template <bool kGated>
+cudaError_t launch(const LinArgs &a, int num_sms, cudaStream_t s) {
+  LinForm form;
+  const cudaError_t e = choose<kGated>(a, num_sms, &form);
+  if (e != cudaSuccess) return e;
+  if (form.kernel == GDN_LINEAR_EX_PAIR) return launch_pair<kGated>(a, num_sms, s);
+  if (form.kernel == GDN_LINEAR_EX_TILE) {
+    if (form.tile == (kGated ? 128 : 256)) return launch_tile<256, kGated>(a, num_sms, s);
+    if (form.tile == (kGated ? 64 : 128)) return launch_tile<128, kGated>(a, num_sms, s);
+    return launch_tile<kGated ? 128 : 64, kGated>(a, num_sms, s);
+  }
+  switch (form.tile) {
+    case 16: return launch_skinny<16, kGated>(a, form, s);
+    case 32: return launch_skinny<32, kGated>(a, form, s);
+    case 64: return launch_skinny<64, kGated>(a, form, s);
+    case 128: return launch_skinny<128, kGated>(a, form, s);
+    default: return launch_skinny<256, kGated>(a, form, s);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_linear_ex(const LinArgs &a, int num_sms, cudaStream_t s) {
   return a.gated ? launch<true>(a, num_sms, s) : launch<false>(a, num_sms, s);
+}
+cudaError_t linear_ex_form(const LinArgs &a, int num_sms, LinForm *form) {
+  return a.gated ? choose<true>(a, num_sms, form) : choose<false>(a, num_sms, form);
 }
 
 }  // namespace gdn

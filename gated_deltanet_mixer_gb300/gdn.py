@@ -67,6 +67,11 @@ class gdn_linear_ex_out(ctypes.Structure):
                 ("act", ctypes.c_int), ("residual", vp), ("ldr", ctypes.c_longlong)]
 
 
+class gdn_linear_ex_form(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int), ("tile", ctypes.c_int), ("tiles", ctypes.c_longlong), ("rows_w", ctypes.c_int),
+                ("split", ctypes.c_int)]
+
+
 class gdn_linattn_io(ctypes.Structure):
     _fields_ = [(n, vp) for n in ("q", "k", "v")] + \
                [(n, ctypes.c_longlong) for n in ("ldq", "ldk", "ldv", "ldo")] + \
@@ -107,6 +112,8 @@ def lib():
                                                       ctypes.POINTER(gdn_linear_out), vp]
         L.gdn_linear_ex.restype = ctypes.c_int
         L.gdn_linear_ex.argtypes = [ctypes.c_int] * 4 + [vp, ctypes.c_longlong, vp, ctypes.c_longlong, vp, ctypes.c_int, vp, vp]
+        L.gdn_selftest_linear_ex_form.restype = ctypes.c_int
+        L.gdn_selftest_linear_ex_form.argtypes = [ctypes.c_int] * 5 + [ctypes.POINTER(gdn_linear_ex_form)]
         for name in ("gdn_linattn_prefill", "gdn_linattn_decode"):
             getattr(L, name).restype = ctypes.c_int
             getattr(L, name).argtypes = [vp, vp, vp]  # structures by reference, or packed bytes
@@ -319,6 +326,15 @@ def gdn_linear_ex(x, w, outs, *, bias=None, gated=False, stream=None):
                                        b"".join(packed), _raw_stream(stream, x))
     if st != GDN_OK:
         raise GdnError(st, "gdn_linear_ex")
+
+
+def gdn_selftest_linear_ex_form(M, N, K, gated=False, residual=False):
+    """The kernel that gdn_linear_ex takes for these sizes (gdn_selftest_linear_ex_form)."""
+    f = gdn_linear_ex_form()
+    st = lib().gdn_selftest_linear_ex_form(M, N, K, int(gated), int(residual), ctypes.byref(f))
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_selftest_linear_ex_form")
+    return f
 
 
 _BF16 = torch.bfloat16

@@ -69,7 +69,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 5
+#define GDN_ABI_VERSION 6
 
 typedef enum {
   GDN_OK = 0,
@@ -353,6 +353,24 @@ typedef struct {
 
 gdn_status gdn_linear_ex(int M, int N, int K, int gated, const void *x, long long ldx, const void *w,
                          long long ldw, const void *bias, int n_out, const gdn_linear_ex_out *out, void *stream);
+
+/* Which of its kernels gdn_linear_ex takes for these sizes on the current
+ * device (residual != 0: some range has one), for tests that mean one. */
+typedef enum {
+  GDN_LINEAR_EX_PAIR = 0, /* tiles by pairs of CTAs */
+  GDN_LINEAR_EX_TILE = 1, /* tiles of one CTA */
+  GDN_LINEAR_EX_FEW = 2   /* few tokens or columns: the contraction over a cluster */
+} gdn_linear_ex_kernel;
+
+typedef struct {
+  int kernel;      /* gdn_linear_ex_kernel */
+  int tile;        /* output columns of a tile; FEW: tokens */
+  long long tiles;
+  int rows_w;      /* FEW: rows of w per tile, else 0 */
+  int split;       /* FEW: CTAs of a cluster, else 0 */
+} gdn_linear_ex_form;
+
+gdn_status gdn_selftest_linear_ex_form(int M, int N, int K, int gated, int residual, gdn_linear_ex_form *form);
 
 /*
  * Linear attention with a decay for each head ("How Qwen3.5 works" section
