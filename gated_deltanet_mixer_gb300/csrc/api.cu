@@ -335,6 +335,21 @@ bool linear_ex_sizes(int M, int N, int K) {
          ((M + 127LL) / 128) * ((N + 63LL) / 64) < (1LL << 31);
 }
 
+// How a prefill runs.  bf16 prompts go in chunks on the tensor cores; the
+// shortest ones and fp32 io (fp32 arithmetic throughout) token by token.  The
+// host does not know the lengths of packed sequences: any of them may be as
+// long as the batch, and the token loop is the slower one by far on a long one
+// where chunks lose a few microseconds on short ones.
+struct LinAttnPlan {
+  bool chunked;
+  gdn::LinAttnCut cut;
+};
+LinAttnPlan linattn_plan(const gdn_shape *shape, long long tokens, bool packed, bool workspace, int sms) {
+  LinAttnPlan p{shape->io_dtype == GDN_BF16 && !gdn::linattn_recurrent_pays(shape->B, shape->Hv, shape->T, sms), {1, 1}};
+  if (p.chunked && workspace) p.cut = gdn::linattn_cut(shape->B, shape->Hv, tokens, packed, sms);
+  return p;
+}
+
 gdn_status linattn_impl(const gdn_shape *shape, const gdn_linattn_io *io, bool decode, void *stream) {
   if (!shape || !io) return GDN_ERR_INVALID_ARG;
   if (shape->B < 1 || shape->T < 1) return GDN_ERR_INVALID_ARG;
@@ -373,9 +388,6 @@ gdn_status linattn_impl(const gdn_shape *shape, const gdn_linattn_io *io, bool d
     if (!(i == n - 1 && in_place) && overlap(rs, in[i])) return GDN_ERR_ALIAS;
   }
   if (overlap(ro, rs)) return GDN_ERR_ALIAS;
-  // bf16 prompts run in chunks on the tensor cores; the shortest ones, tokens
-  // from the cache and fp32 io (fp32 arithmetic throughout) token by token.
-  const bool bf16 = shape->io_dtype == GDN_BF16;
   if (io->workspace && (reinterpret_cast<uintptr_t>(io->workspace) & 255u) != 0) return GDN_ERR_ALIGNMENT;
   const Range rw = range_of(io->workspace, io->workspace_bytes);
   for (int i = 0; i < n; ++i)
@@ -384,18 +396,17 @@ gdn_status linattn_impl(const gdn_shape *shape, const gdn_linattn_io *io, bool d
   DeviceInfo dev;
   st = device_info(&dev);
   if (st != GDN_OK) return st;
-  const bool chunked = bf16 && !decode && !gdn::linattn_recurrent_pays(shape->B, shape->Hv, shape->T, dev.sms);
-  gdn::LinAttnCut cut{1, 1};
-  if (chunked && io->workspace) {
-    cut = gdn::linattn_cut(shape->B, shape->Hv, tokens, packed, dev.sms);
-    if (io->workspace_bytes < gdn::linattn_ws_bytes(shape->B, shape->Hv, cut)) return GDN_ERR_INVALID_ARG;
-  }
+  LinAttnPlan plan{false, {1, 1}};
+  if (!decode) plan = linattn_plan(shape, tokens, packed, io->workspace != nullptr, dev.sms);
+  const gdn::LinAttnCut cut = plan.cut;
+  if (io->workspace && io->workspace_bytes < gdn::linattn_ws_bytes(shape->B, shape->Hv, cut)) return GDN_ERR_INVALID_ARG;
   gdn::LinAttnArgs a{shape->B, shape->T,  shape->Hk, shape->Hv, d.q_scale, io->q,
                      io->k,    io->v,     io->o,     io->ldq,   io->ldk,   io->ldv,
                      io->ldo,  io->g,     io->log_decay, decode ? io->S_T : io->S0, io->S_T, io->cu_seqlens,
                      cut.nseg > 1 ? static_cast<float *>(io->workspace) : nullptr, cut.nseg, cut.sub, dev.err};
-  const cudaError_t e = chunked ? gdn::launch_linattn_chunked(a, (cudaStream_t)stream)
-                                : gdn::launch_linattn_recurrent(a, bf16, dev.sms, (cudaStream_t)stream);
+  const cudaError_t e = plan.chunked ? gdn::launch_linattn_chunked(a, (cudaStream_t)stream)
+                                     : gdn::launch_linattn_recurrent(a, shape->io_dtype == GDN_BF16, dev.sms,
+                                                                     (cudaStream_t)stream);
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -616,6 +627,20 @@ gdn_status gdn_linattn_prefill(const gdn_shape *shape, const gdn_linattn_io *io,
 
 gdn_status gdn_linattn_decode(const gdn_shape *shape, const gdn_linattn_io *io, void *stream) {
   return linattn_impl(shape, io, true, stream);
+}
+
+gdn_status gdn_selftest_linattn_form(const gdn_shape *shape, int packed, int workspace, gdn_linattn_form *form) {
+  if (!shape || !form || shape->B < 1 || shape->T < 1) return GDN_ERR_INVALID_ARG;
+  const long long tokens = packed ? (long long)shape->T : (long long)shape->B * shape->T;
+  gdn::Dims d;
+  Sizes sz;
+  DeviceInfo dev;
+  gdn_status st = check_shape(shape, tokens, &d, &sz);
+  if (st == GDN_OK) st = device_info(&dev);
+  if (st != GDN_OK) return st;
+  const LinAttnPlan p = linattn_plan(shape, tokens, packed != 0, workspace != 0, dev.sms);
+  *form = gdn_linattn_form{p.chunked ? 1 : 0, p.cut.nseg, p.cut.sub};
+  return GDN_OK;
 }
 
 size_t gdn_linattn_workspace_bytes(const gdn_shape *shape, int packed) {

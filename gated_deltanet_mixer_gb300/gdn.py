@@ -72,6 +72,10 @@ class gdn_linear_ex_form(ctypes.Structure):
                 ("split", ctypes.c_int)]
 
 
+class gdn_linattn_form(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("chunked", "segments", "parts")]
+
+
 class gdn_linattn_io(ctypes.Structure):
     _fields_ = [(n, vp) for n in ("q", "k", "v")] + \
                [(n, ctypes.c_longlong) for n in ("ldq", "ldk", "ldv", "ldo")] + \
@@ -117,6 +121,9 @@ def lib():
         for name in ("gdn_linattn_prefill", "gdn_linattn_decode"):
             getattr(L, name).restype = ctypes.c_int
             getattr(L, name).argtypes = [vp, vp, vp]  # structures by reference, or packed bytes
+        L.gdn_selftest_linattn_form.restype = ctypes.c_int
+        L.gdn_selftest_linattn_form.argtypes = [ctypes.POINTER(gdn_shape), ctypes.c_int, ctypes.c_int,
+                                                ctypes.POINTER(gdn_linattn_form)]
         L.gdn_linattn_workspace_bytes.restype = ctypes.c_size_t
         L.gdn_linattn_workspace_bytes.argtypes = [ctypes.POINTER(gdn_shape), ctypes.c_int]
         L.gdn_selftest_wait_timeout.restype = ctypes.c_int
@@ -456,6 +463,15 @@ def gdn_linattn_workspace_bytes(B, T, Hk, Hv, packed=False, D=128, io_dtype=None
     """Workspace bytes of gdn_linattn_prefill (packed: T is the total token count)."""
     sh = make_shape(B, T, Hk, Hv, D, GDN_BF16 if io_dtype is None else io_dtype)
     return lib().gdn_linattn_workspace_bytes(ctypes.byref(sh), 1 if packed else 0)
+
+
+def gdn_selftest_linattn_form(B, T, Hk, Hv, packed=False, workspace=True, D=128, io_dtype=None):
+    """How gdn_linattn_prefill runs this shape (gdn_selftest_linattn_form)."""
+    sh, f = make_shape(B, T, Hk, Hv, D, GDN_BF16 if io_dtype is None else io_dtype), gdn_linattn_form()
+    st = lib().gdn_selftest_linattn_form(ctypes.byref(sh), int(packed), int(workspace), ctypes.byref(f))
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_selftest_linattn_form")
+    return f
 
 
 def gdn_device_status(stream=None, reset=False):

@@ -428,6 +428,17 @@ size_t gdn_linattn_workspace_bytes(const gdn_shape *shape, int packed);
  * are NULL.  The state is read and written once, whatever T is. */
 gdn_status gdn_linattn_decode(const gdn_shape *shape, const gdn_linattn_io *io, void *stream);
 
+/* How gdn_linattn_prefill runs a shape on the current device (packed as for
+ * gdn_linattn_workspace_bytes; workspace != 0: the call has one), for tests
+ * that mean one form. */
+typedef struct {
+  int chunked;  /* 1: in chunks on the tensor cores, 0: token by token */
+  int segments; /* of a sequence, side by side */
+  int parts;    /* of a segment, in the launch that forms the states between them */
+} gdn_linattn_form;
+
+gdn_status gdn_selftest_linattn_form(const gdn_shape *shape, int packed, int workspace, gdn_linattn_form *form);
+
 /*
  * Synchronise `stream` and report device-side failures recorded since the
  * last reset: GDN_ERR_TIMEOUT if a kernel's bounded wait gave up (the kernel
