@@ -571,6 +571,8 @@ gdn_status gdn_linear_ex(int M, int N, int K, int gated, const void *x, long lon
       return GDN_ERR_INVALID_ARG;
     for (int p = 0; p < o; ++p)
       if (q.col_begin < out[p].col_end && out[p].col_begin < q.col_end) return GDN_ERR_INVALID_ARG;
+    // As for x and w: the extents below stay within 64 bits.
+    if (q.ld > (1LL << 32) || (q.residual && q.ldr > (1LL << 32))) return GDN_ERR_UNSUPPORTED_SHAPE;
     if (((reinterpret_cast<uintptr_t>(q.ptr) | reinterpret_cast<uintptr_t>(q.residual)) & 1u) != 0)
       return GDN_ERR_ALIGNMENT;
     const long long cols = q.col_end - q.col_begin;
