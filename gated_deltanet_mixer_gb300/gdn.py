@@ -449,7 +449,9 @@ def gdn_linattn_prefill(q, k, v, S0, o, S_T, *, Hk, Hv, g=None, log_decay=None, 
     """Linear attention with decay over prompts (gdn_linattn_prefill): q, k
     [B, T, Hk*D], v and o [B, T, Hv*D] (packed: [tokens, ..] with cu_seqlens
     int32 [B+1]), rows possibly strided; g [.., Hv] or log_decay [Hv]; S0 (or
-    None) and S_T [B, Hv, D, D]; a workspace of gdn_linattn_workspace_bytes()."""
+    None) and S_T [B, Hv, D, D]; a workspace of gdn_linattn_workspace_bytes().
+    bf16 prompts run in chunks of 64 tokens, where a log decay acts as -80 at
+    least and an output sees at least 2^-58 of the state at its chunk's start."""
     _linattn("gdn_linattn_prefill", q, k, v, o, S0, S_T, Hk, Hv, g, log_decay, cu_seqlens, workspace, scale, stream)
 
 

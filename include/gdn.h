@@ -385,7 +385,8 @@ gdn_status gdn_selftest_linear_ex_form(int M, int N, int K, int gated, int resid
  *        buffer): ld >= heads * 128 elements, rows 16-byte aligned.
  *   g         [tokens][Hv] fp32 log decay per token, or NULL
  *   log_decay [Hv] fp32 constant log decay of a head, or NULL; exactly one of
- *        the two.  Values are <= 0 (-inf resets the state).
+ *        the two.  Values are <= 0; -inf resets the state (in chunks to
+ *        within the bounds below).
  *   S0, S_T, cu_seqlens as for gdn_prefill_ex: S_T may be exactly S0; packed
  *        sequences of any length from 0; o must not overlap any other tensor.
  *   workspace 256-byte aligned scratch of at least
@@ -398,7 +399,12 @@ gdn_status gdn_selftest_linear_ex_form(int M, int N, int K, int gated, int resid
  * prompts, up to about a hundred tokens, token by token as fp32 io does): operands that are
  * not bf16 already enter as sums of bf16 pieces (24 bits of what feeds the
  * state, 16 bits of what feeds o only), the state itself is summed in fp32.
- * Log decays below -80 act as -80 there.  q, k and v are finite: a NaN or
+ * Log decays below -80 act as -80 there: of a state that a reset should have
+ * emptied e^-80 is left.  An output sees at least 2^-58 of the state at the
+ * start of its chunk, also behind decays or a reset that should leave less of
+ * it.  An output's sums carry the inverse of what has decayed since the start
+ * of the chunk, 2^58 at most: where it is that, o / scale must stay below 2^69
+ * in size.  None of this holds for the token loop.  q, k and v are finite: a NaN or
  * infinity spreads over its chunk and into the state (never into another
  * sequence).  A NaN log decay makes the outputs of its head from its token on
  * and the head's state NaN, whichever way the call runs.  fp32 io runs token

@@ -1,5 +1,5 @@
-"""Linear attention at unusual decays: NaN, strong ones in front of slow ones.
-Tolerances as in test_gpu_linattn.py."""
+"""Linear attention at unusual decays: NaN, strong ones in front of slow ones,
+resets of a large state.  Tolerances as in test_gpu_linattn.py."""
 import math
 
 import pytest
@@ -79,4 +79,30 @@ def test_slow_decays_behind_strong_ones(strong, first):
                 cols = slice(h * D, (h + 1) * D)
                 c.v[t + 1, cols] = -(c.v[t, cols].double() * math.exp(c.g[t + 1, h])).to(c.dt)
     c = Case([128], 1, 2, "bf16", seed=220, edit=edit)
+    c.check(*prefill(c))
+
+
+def test_reset_of_a_large_state():
+    """Behind a reset inside a chunk an output still sees 2^-58 of the state at the chunk's start, and
+    the state e^-80 of what it was; both count in the bound, nothing else does."""
+    def edit(c):
+        c.S0 *= 1e9
+        c.g[[5, 90]] = -math.inf
+    c = Case([130], 1, 2, "bf16", seed=230, edit=edit)
+    o, S = (x.cpu().double() for x in prefill(c))
+    ro, rS, Ao, AS = c.reference(0)
+    q = c.q.double().abs().view(-1, 1, 1, D)
+    left = 2.0 ** -58 / math.sqrt(D) * (c.S0[0].double().abs() * q).sum(-1)  # [T, Hv, D]
+    bound = 2.0 ** -14 * Ao + 2.0 ** -8 * ro.abs() + 1.01 * left
+    assert bool(((o.view(-1, 2, D) - ro).abs() <= bound).all())
+    assert bool(((S[0] - rS).abs() <= 2.0 ** -18 * AS + math.exp(-80) * c.S0[0].double().abs()).all())
+
+
+def test_large_outputs_behind_a_reset():
+    """Sums behind strong decays carry a factor of 2^58: outputs around 2^52 come out whole."""
+    def edit(c):
+        c.g[10] = -math.inf
+        c.v[:] = (c.v.float() * 2.0 ** 50).bfloat16()
+        c.S0 *= 2.0 ** 50
+    c = Case([130], 1, 2, "bf16", seed=231, edit=edit)
     c.check(*prefill(c))
