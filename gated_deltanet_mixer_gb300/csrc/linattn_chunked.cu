@@ -36,17 +36,17 @@
 // parts from zero, a small one turns those into the state before every segment,
 // and a third starts every segment from its own.  Cost: k and v are read twice.
 //
-// Bound: a chunk of 64 tokens takes about 3,600 cycles of its SM, of which the
-// tensor pipe works 1,900 (52 %) and instruction issue 54 %; what paces it is the
-// chain update -> P and Gamma V -> next update and the MMAs in their order, whose
-// products of 64 columns take about 57 cycles each where the pipe works 32, not
-// memory (4 x 8192 tokens, 16/32 heads: 240 us, 3.4 TB/s of the 0.81 GB that the
-// call cannot do without, where a copy runs at 6.8; 65536 tokens, 16/48 heads: 918
-// us).  Measured and not taken: two issuing warps (256 us), all of an iteration's
-// waits before its first MMA (251), Q K^T after the output's products (271) or
-// between them (246).  The loops of the roles
-// share one instruction cache: a form with 82 KB of code instead of 58 waited for
-// instructions in a third of its samples and took 1.4 times as long.
+// Bound: a chunk of 64 tokens takes about 3,400 cycles of its SM, of which the
+// tensor pipe works 51 % and instruction issue 54 %; what paces it is the chain
+// update -> P and Gamma V -> next update and the MMAs in their order, not memory
+// (calls of 4 x 8192 tokens, 16/32 heads: 256 us, 3.2 TB/s of the 0.82 GB that they
+// cannot do without, where a copy runs at 6.8; of 65536 tokens, 16/48 heads: 940).
+// The state-only form is paced by Gamma V and by adding the update (tensor pipe
+// 32 %, issue 30 %).  Measured and not taken, against 240 us of an earlier form: two
+// issuing warps (256 us), all of an iteration's waits before its first MMA (251),
+// Q K^T after the output's products (271) or between them (246).  The loops of the
+// roles share one instruction cache: a form with 82 KB of code instead of 58 (61
+// now) waited for instructions in a third of its samples and took 1.4 times as long.
 #include <cuda.h>
 #include <cuda_bf16.h>
 

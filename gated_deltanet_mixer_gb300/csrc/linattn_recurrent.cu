@@ -10,11 +10,14 @@
 // shared memory, three blocks ahead of the one worked on.
 //
 // One token is bound by the state's traffic, 128 KB per unit against 128 x 128
-// fused multiply-adds (256 sequences x 48 heads: 233 us, 6.9 TB/s; 1 x 16 heads:
-// 2.5 us); a few tokens by that and by instruction issue (64 x 48 heads, 4
-// tokens: 71 us, 5.8 TB/s); long runs by a token's loads from shared memory, its
-// arithmetic and its sums in turn (2 x 1001 tokens, 8 heads, fp32: 102 us, 0.10 us
-// per token).
+// fused multiply-adds (calls of 256 sequences x 48 heads on states in turn: 243 us,
+// 6.65 TB/s, a copy's rate; 1 x 16 heads: 2.3 us on the device, 7.2 a call); a few
+// tokens by that and by instruction issue (64 x 48 heads, 4 tokens: 76 us, 5.4
+// TB/s); long runs of few units by a token's loads from shared memory, its
+// arithmetic and its sums in turn: one warp per scheduler, which issues in 24 % of
+// its cycles (2 x 1001 tokens, 8 heads, fp32: 111 us, 0.11 us per token).
+//
+// Figures with two forms below: launches in a graph, both on one box.
 #include <type_traits>
 
 #include "gdn_device.cuh"

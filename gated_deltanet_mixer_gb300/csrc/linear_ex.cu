@@ -7,9 +7,10 @@
 //
 // Three kernels:
 //   lin_pair_kernel   256 x 256 tiles by pairs of CTAs: bound by the tensor pipe,
-//                     92 % active (8192 tokens 5120 -> 16480: 817 us, 1692
-//                     TFLOP/s; the tile kernel below: 912 us).  Persistent, the
-//                     epilogue of a tile under the next tile's MMAs.
+//                     92 % active (calls of 8192 tokens 5120 -> 16480 in three
+//                     ranges: 840 to 870 us by the power there is, 1.6 PFLOP/s;
+//                     the tile kernel below: 1.1 times as long).  Persistent,
+//                     the epilogue of a tile under the next tile's MMAs.
 //   lin_tile_kernel   128 x 64 .. 256 tiles of one CTA, where pairs' tiles are too
 //                     few for the SMs (1024 x 2048 x 2048: 12 us).
 //   lin_skinny_kernel fewer tiles (few tokens, or few columns): bound by
@@ -18,7 +19,9 @@
 //                     a cluster of CTAs, which hand each other their partial
 //                     sums through distributed shared memory and add them in a
 //                     fixed order: no workspace, no second launch, the same
-//                     result every time.
+//                     result every time (64 tokens 6144 -> 5120 with a residual:
+//                     18.7 us, 3.4 TB/s).
+// Figures below are of launches in a graph; calls in a row take 2 us more each.
 #include <atomic>
 #include <cmath>
 #include <type_traits>
@@ -51,7 +54,8 @@ constexpr uint32_t idesc_bf16(int M, int N) {
 // 2^-21; with the roundings Phi(-a) is good to 2^-19 up to a = 3 and to 2^-16 at 12,
 // where a^2 has lost bits.  erfcf would do, but 32 of them side by side are more
 // code than the instruction cache takes beside the epilogue's loop, whichever
-// activation runs (4096 x 6552 x 144 with none: 34 us so, 41 with erff, 72 with erfcf).
+// activation runs (calls of 4096 x 6552 x 144 with none: 34 us so, 41 with erff, 72
+// with erfcf).
 __device__ __forceinline__ float gelu(float x) {
   const float a = fabsf(x), t = __fdividef(1.0f, fmaf(0.33f, a, 1.0f));
   float p = -0.27709153f;
@@ -205,9 +209,10 @@ __device__ __forceinline__ int prefetch_residual(const LinArgs &g, long long row
 // `loaded`.  Whole aligned runs are stored 16 bytes per lane.  Others go through
 // shared memory, so that a warp stores 32 neighbouring columns of one row at a
 // time: a lane storing its own row would touch 32 rows with every 2-byte store
-// (4069 x 6549 x 144 with a residual: 601 us so, 67 this way).  What bounds these
-// loops is instructions: with the fields of a range read from the parameters at
-// each use, and every row tested against the last one, the same call took 121 us.
+// (4069 x 6549 x 144 with a residual: ten times as long so; 53 us this way).  What
+// bounds these loops is instructions: with the fields of a range read from the
+// parameters at each use, and every row tested against the last one, it took 1.8
+// times as long.
 template <bool kGated>
 __device__ __forceinline__ void store_run(const LinArgs &g, long long row0, int lane, int col0, const float (&v)[32],
                                           const float (&u)[32], float *run, int loaded, uint32_t (&x)[16]) {
@@ -596,7 +601,7 @@ constexpr int kSkinnyThreads = 192;
 template <int NT>
 struct Skinny {
   // 64-wide k blocks per stage: two for the smallest, whose blocks are short
-  // against a wait (16 tokens, 6144 -> 5120: 14.4 us against 15.0 with one).
+  // against a wait (16 tokens, 6144 -> 5120: 15.0 us, 4 % more with one).
   static constexpr int kSteps = NT <= 16 ? 2 : 1;
   static constexpr uint32_t kA = kRowsW * BK * 2, kB = NT * BK * 2;
   static constexpr uint32_t kBlock = kA + kB;
@@ -954,8 +959,8 @@ cudaError_t cluster_caps(int num_sms, int (&cap)[9]) {
 
 // The widest split of `tiles` whose CTAs all run at once, each with some k steps
 // and (the partial sums' space) whole tokens; 1 where they do not.  A wider one
-// costs a second wave (16 tokens, 4096 -> 2560: 6.6 us with 6 CTAs per cluster,
-// 11.8 with 7, whose 20 clusters do not fit).
+// costs a second wave (16 tokens, 4096 -> 2560, w in L2: 6.6 us with 6 CTAs per
+// cluster, 11.8 with 7, whose 20 clusters do not fit).
 template <int NT>
 int skinny_split(long long tiles, int nk, const int (&cap)[9]) {
   int split = nk / 2 < 8 ? nk / 2 : 8;
@@ -981,7 +986,7 @@ cudaError_t skinny_plan(const LinArgs &a, int num_sms, bool residual, SkinnyPlan
   const long long tiles_m = (a.M + NT - 1) / NT;
   const float tokens = (float)(a.M < NT ? a.M : NT);
   // All 128 rows of w, or fewer where the tiles come in several waves and smaller
-  // ones fill the last better (8 tokens, 5120 -> 24576: 43.9 us with 96 rows, 45.7
+  // ones fill the last better (8 tokens, 5120 -> 24576: 43.9 us with 112 rows, 45.7
   // with 128).  From 128 tokens on the loads of x count as much.
   for (int rows = kRowsW; rows >= (NT <= 64 ? 80 : kRowsW); rows -= 16) {
     const int out = kGated ? rows / 2 : rows;
@@ -1044,9 +1049,9 @@ cudaError_t choose(const LinArgs &a, int num_sms, LinForm *form) {
   bool residual = false;
   for (int o = 0; o < a.n_out; ++o) residual |= a.out[o].res != nullptr;
   // Few tokens or few columns: tiles of 16 to 256 tokens, fewer than there are
-  // where that fills the SMs (219 tokens, 3640 -> 421: 8.2 us in tiles of 32, 15.3
-  // in one of 256, 19.5 by the tile kernel; 128 tokens, 6144 -> 5120: 20.2 in one
-  // of 128, 38.7 in tiles of 32).
+  // where that fills the SMs (219 tokens, 3640 -> 421: 7.8 us in tiles of 32, 15.3
+  // in one of 256, 19.5 by the tile kernel; 128 tokens, 6144 -> 5120: 21 in one of
+  // 128, 38.7 in tiles of 32).
   constexpr int kMostTokens = 2048;  // beyond, other forms have the tiles
   SkinnyPlan best{0, 0, 0, 1e30f};
   int nt = 0;
@@ -1077,7 +1082,7 @@ cudaError_t choose(const LinArgs &a, int num_sms, LinForm *form) {
   const float mem = (kGated ? 4e-6f : 2e-6f) * a.N / 6.5f * a.K;  // w, once
   const float least = fmaxf(fminf(fminf(t256, t128), fminf(t64, pair)), mem) + (residual ? 6.f : 4.5f);
   // Up to 128 tokens they read w once as well, but in fewer pieces: a clear gain only
-  // (107 tokens, 920 -> 6856 with a residual: 8.9 us by tiles, 11.9 so).
+  // (107 tokens, 920 -> 6856 with a residual: 9.6 us by tiles, 11.9 so).
   if (best.cost < least * (a.M <= 128 ? 1.1f : 0.9f)) {
     *form = LinForm{GDN_LINEAR_EX_FEW, nt, best.tiles, best.rows_w, best.split};
     return cudaSuccess;

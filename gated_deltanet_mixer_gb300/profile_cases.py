@@ -6,7 +6,7 @@
     python -m gated_deltanet_mixer_gb300.profile_cases linear --T 2048 --K 5120 --N 16480 --calls 2
     python -m gated_deltanet_mixer_gb300.profile_cases decode_multi --B 64 --T 4 --calls 2 [--snap]
     python -m gated_deltanet_mixer_gb300.profile_cases serial --B 4 --T 1024 --Hv 32 --calls 2
-    python -m gated_deltanet_mixer_gb300.profile_cases linattn --B 4 --T 2048 --calls 2
+    python -m gated_deltanet_mixer_gb300.profile_cases linattn --B 4 --T 2048 --calls 2 [--io f32]
     python -m gated_deltanet_mixer_gb300.profile_cases linattn_decode --B 48 --T 1 --calls 2
     python -m gated_deltanet_mixer_gb300.profile_cases linear_ex --T 64 --K 6144 --N 5120 --calls 2 [--gated]
 
@@ -93,14 +93,13 @@ def linear(T, K, N, calls):
         gdn.gdn_linear(x, w, [(0, N, y)])
 
 
-def linattn(B, T, Hk, Hv, calls):
-    """Linear attention with decay over prompts (the chunked kernel)."""
-    t = torch.bfloat16
+def linattn(B, T, Hk, Hv, calls, t):
+    """Linear attention with decay over prompts (bf16: the chunked kernel; fp32: the token loop)."""
     q, k = (torch.randn(B, T, Hk * 128, device="cuda", dtype=t) for _ in range(2))
     v = torch.randn(B, T, Hv * 128, device="cuda", dtype=t)
     g = -torch.nn.functional.softplus(-(3.0 + torch.randn(B, T, Hv, device="cuda")))
     o, S_T = torch.empty_like(v), torch.empty(B, Hv, 128, 128, device="cuda")
-    ws = torch.empty(gdn.gdn_linattn_workspace_bytes(B, T, Hk, Hv), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(gdn.gdn_linattn_workspace_bytes(B, T, Hk, Hv, io_dtype=gdn._IO_CODES[t]), dtype=torch.uint8, device="cuda")
     for _ in range(calls):
         gdn.gdn_linattn_prefill(q, k, v, None, o, S_T, Hk=Hk, Hv=Hv, g=g, workspace=ws)
 
@@ -137,6 +136,7 @@ def main():
     ap.add_argument("--form", choices=["fused", "staged", "split"], default="fused",
                     help="prefill: no workspace, the staged q^/k^ workspace, or the chunk-parallel workspace")
     ap.add_argument("--g-mu", type=float, default=3.0, help="prefill: mean of the log-decay logits")
+    ap.add_argument("--io", choices=["bf16", "f32"], default="bf16", help="linattn: the tensors' type")
     ap.add_argument("--gated", action="store_true", help="linear_ex: the gated form")
     ap.add_argument("--snap", action="store_true", help="decode_multi: a state snapshot after every token")
     a = ap.parse_args()
@@ -148,7 +148,7 @@ def main():
     elif a.kernel == "decode_multi":
         decode_multi(a.B or 64, a.T, a.Hk, a.Hv or 48, a.calls, a.snap)
     elif a.kernel == "linattn":
-        linattn(a.B or 4, a.T, a.Hk, a.Hv or 32, a.calls)
+        linattn(a.B or 4, a.T, a.Hk, a.Hv or 32, a.calls, torch.float32 if a.io == "f32" else torch.bfloat16)
     elif a.kernel == "linattn_decode":
         linattn_decode(a.B or 48, a.T, a.Hk, a.Hv or 48, a.calls)
     elif a.kernel == "linear_ex":
