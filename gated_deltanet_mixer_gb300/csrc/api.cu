@@ -6,25 +6,22 @@
 #include <mutex>
 
 #include "gdn.h"
+#include "host_checks.h"
 #include "launch.h"
 
 namespace {
 
+using gdn::aligned16;
+using gdn::column_blocks;
+using gdn::device_info;
+using gdn::DeviceInfo;
+using gdn::overlap;
+using gdn::Range;
+using gdn::range_of;
+using gdn::rows_bytes;
+
 // One error word per device that loads the library: kernels OR bits into it.
 __device__ unsigned int g_err_word;
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi); empty when lo == hi
-};
-
-Range range_of(const void *p, size_t bytes) {
-  uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Range{a, a + (p ? bytes : 0)};
-}
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct Sizes {
   size_t io;                                                     // bytes per io element
@@ -288,12 +285,9 @@ gdn_status decode_impl(const gdn_shape *shape, const gdn_decode_io *io, void *st
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-// What check_device finds, and the SM count, looked up once per device: the
-// smallest calls take a few microseconds, of which the look-up would be one.
-struct DeviceInfo {
-  unsigned int *err;
-  int sms;
-};
+}  // namespace
+
+namespace gdn {
 gdn_status device_info(DeviceInfo *out) {
   constexpr int kMax = 64;
   static std::mutex mu;
@@ -316,18 +310,9 @@ gdn_status device_info(DeviceInfo *out) {
   return GDN_OK;
 }
 
-// Bytes from the first row's first element to the last row's last.
-size_t rows_bytes(long long rows, long long ld, long long cols, size_t el) {
-  return ((size_t)(rows - 1) * (size_t)ld + (size_t)cols) * el;
-}
+}  // namespace gdn
 
-// Whether rows of wa bytes at a and of wb bytes at b, both `pitch` bytes apart,
-// are disjoint column blocks of one buffer.
-bool column_blocks(const void *a, size_t wa, const void *b, size_t wb, size_t pitch) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  const size_t d = x <= y ? (y - x) % pitch : (pitch - (x - y) % pitch) % pitch;  // b's column, from a's
-  return d >= wa && d + wb <= pitch;
-}
+namespace {
 
 // The kernels of gdn_linear_ex count their tiles (128 x 64 the smallest) in 31 bits.
 bool linear_ex_sizes(int M, int N, int K) {

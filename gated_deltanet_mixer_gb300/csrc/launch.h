@@ -183,9 +183,75 @@ cudaError_t static_scratch(void **ptr);
 cudaError_t launch_gemm(const GemmArgs &a, int num_sms, cudaStream_t s);
 cudaError_t launch_wait_selftest(unsigned int *err, unsigned long long limit_ns, cudaStream_t s);
 
+// The sequences of a call on the paged cache: sequence b owns token rows b*T ..
+// b*T + T - 1, or (cu != nullptr) cu[b] .. cu[b+1]-1 of T rows; they are the
+// last of its kv_lens[b] tokens.
+struct SeqArgs {
+  int B, T;
+  int max_new, max_kv;
+  const int *cu, *kv_lens;
+  unsigned int *err;
+};
+// Pages of [Hk][1 << page_shift][D] e4m3 bytes with a scale per page and head.
+struct CacheArgs {
+  uint8_t *k, *v;
+  float *ks, *vs;
+  int n_pages, page_shift, Hk, D;
+  const int *table;
+  long long table_ld;
+  int max_blocks;
+};
+struct AppendArgs {
+  SeqArgs seq;
+  CacheArgs cache;
+  const void *k, *v;
+  long long ldk, ldv;
+};
+struct AttnArgs {
+  SeqArgs seq;
+  CacheArgs cache;
+  int Hq, r;  // r = Hq / Hk
+  const void *q;
+  void *o;
+  long long ldq, ldo;
+  int causal;
+  float scale;
+  void *ws;  // may be null
+  int splits;  // ranges of the tokens side by side, with ws
+};
+struct RopeX {
+  const void *x;
+  void *y;
+  long long ldx, ldy;
+  int heads;
+};
+constexpr int kRopeMaxX = 4, kRopeMaxPairs = 128;
+struct RopeArgs {
+  int tokens, D, rot, interleaved, n_x, heads;  // heads: of all x
+  int vec;                                      // 16-byte accesses allowed
+  float m, sign;
+  const int *positions;
+  RopeX x[kRopeMaxX];
+  unsigned long long turns[kRopeMaxPairs];
+};
+struct PagesArgs {
+  int B, page_shift, max_blocks, n_free;
+  long long table_ld, max_tokens;
+  const int *kv_lens, *new_tokens, *free_pages, *free_used;
+  int *table, *kv_lens_out, *free_used_out, *cu;
+  long long *slots;
+  int *positions;
+  unsigned int *err;
+};
+constexpr int kPagesMaxB = 16384;
+cudaError_t launch_kv_pages(const PagesArgs &a, cudaStream_t s);
+cudaError_t launch_rope(const RopeArgs &a, bool bf16, cudaStream_t s);
+cudaError_t launch_kv_append(const AppendArgs &a, bool bf16, cudaStream_t s);
+cudaError_t launch_attn_rows(const AttnArgs &a, bool bf16, cudaStream_t s);
+
 // Device error bits (the error word is OR-ed).
 constexpr unsigned int kErrTimeout = 1u;  // a bounded wait gave up
-constexpr unsigned int kErrSeqlens = 2u;  // packed-sequence offsets out of order or range
+constexpr unsigned int kErrSeqlens = 2u;  // packed-sequence offsets, lengths or pages out of order or range
 constexpr unsigned int kErrBounds = 4u;   // a GDN_CHECKS bounds check failed
 
 // GDN_CHECKS builds check every thread-issued global store of the prefill

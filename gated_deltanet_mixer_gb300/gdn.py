@@ -83,6 +83,49 @@ class gdn_linattn_io(ctypes.Structure):
                [("workspace_bytes", ctypes.c_size_t)]
 
 
+class gdn_attn_shape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "Hq", "Hk", "D", "io_dtype", "max_new", "max_kv")]
+
+
+class gdn_kv_cache(ctypes.Structure):
+    _fields_ = [(n, vp) for n in ("k", "v", "k_scale", "v_scale")] + \
+               [("n_pages", ctypes.c_int), ("page", ctypes.c_int), ("block_table", vp), ("table_ld", ctypes.c_longlong),
+                ("max_blocks", ctypes.c_int), ("kv_lens", vp)]
+
+
+class gdn_kv_append_io(ctypes.Structure):
+    _fields_ = [("k", vp), ("v", vp), ("ldk", ctypes.c_longlong), ("ldv", ctypes.c_longlong), ("cu_seqlens", vp),
+                ("cache", gdn_kv_cache)]
+
+
+class gdn_attn_io(ctypes.Structure):
+    _fields_ = [("q", vp), ("o", vp), ("ldq", ctypes.c_longlong), ("ldo", ctypes.c_longlong), ("cu_seqlens", vp),
+                ("cache", gdn_kv_cache), ("causal", ctypes.c_int), ("scale", ctypes.c_float), ("workspace", vp),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class gdn_rope_plan_t(ctypes.Structure):  # gdn_rope_plan of the header
+    _fields_ = [("rot", ctypes.c_int), ("layout", ctypes.c_int), ("m", ctypes.c_float), ("turns", ctypes.c_ulonglong * 128)]
+
+
+class gdn_rope_spec(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("rot", "layout", "scaling")] + \
+               [(n, ctypes.c_double) for n in ("base", "factor", "original", "fast", "slow")]
+
+
+class gdn_rope_x(ctypes.Structure):
+    _fields_ = [("x", vp), ("y", vp), ("ldx", ctypes.c_longlong), ("ldy", ctypes.c_longlong), ("heads", ctypes.c_int)]
+
+
+class gdn_kv_pages_io(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "page", "max_blocks", "n_free")] + \
+               [("table_ld", ctypes.c_longlong), ("max_tokens", ctypes.c_longlong)] + \
+               [(n, vp) for n in ("kv_lens", "new_tokens", "free_pages", "free_used", "block_table", "kv_lens_out",
+                                  "free_used_out", "cu_seqlens", "slots", "positions")]
+
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"linear": 1, "ntk": 2, "parts": 3}
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "sigmoid": 3}
 
 _lib = None
@@ -128,6 +171,17 @@ def lib():
         L.gdn_linattn_workspace_bytes.argtypes = [ctypes.POINTER(gdn_shape), ctypes.c_int]
         L.gdn_selftest_wait_timeout.restype = ctypes.c_int
         L.gdn_selftest_wait_timeout.argtypes = [ctypes.c_int, vp]
+        for name in ("gdn_kv_append", "gdn_attn"):
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name).argtypes = [vp, vp, vp]  # structures by reference, or packed bytes
+        L.gdn_attn_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_attn_workspace_bytes.argtypes = [ctypes.POINTER(gdn_attn_shape), ctypes.c_int]
+        L.gdn_rope_plan_init.restype = ctypes.c_int
+        L.gdn_rope_plan_init.argtypes = [ctypes.POINTER(gdn_rope_spec), ctypes.POINTER(gdn_rope_plan_t)]
+        L.gdn_rope.restype = ctypes.c_int
+        L.gdn_rope.argtypes = [ctypes.c_int] * 3 + [ctypes.POINTER(gdn_rope_plan_t), vp, ctypes.c_int, vp, ctypes.c_int, vp]
+        L.gdn_kv_pages.restype = ctypes.c_int
+        L.gdn_kv_pages.argtypes = [vp, vp]
         L.gdn_prefill_static.restype = ctypes.c_int
         L.gdn_prefill_static.argtypes = [ctypes.POINTER(gdn_shape), ctypes.POINTER(gdn_prefill_io), vp]
         L.gdn_prefill_workspace_bytes.restype = ctypes.c_size_t
@@ -474,6 +528,174 @@ def gdn_selftest_linattn_form(B, T, Hk, Hv, packed=False, workspace=True, D=128,
     if st != GDN_OK:
         raise GdnError(st, "gdn_selftest_linattn_form")
     return f
+
+
+_PACK_ATTN_SHAPE = struct.Struct("=8i")
+_PACK_CACHE = struct.Struct("=4Q2iQqi4xQ")
+_PACK_APPEND = struct.Struct("=2Q2qQ")
+_PACK_ATTN = struct.Struct("=2Q2qQ")
+_PACK_ATTN_END = struct.Struct("=if2Q")
+_PACK_ROPE_X = struct.Struct("=2Q2qi4x")
+_PACK_PAGES = struct.Struct("=4i2q10Q")
+_CACHE_BYTES = (torch.float8_e4m3fn, torch.uint8)
+_I32 = torch.int32
+
+
+def _int32(t, n, what):
+    if t.dtype != _I32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s: %d contiguous int32 values are wanted" % (what, n))
+    return t.data_ptr()
+
+
+def _table(t, B):
+    """(pointer, elements between rows, blocks of a row) of a block table [B, blocks]."""
+    if t.dtype != _I32 or t.dim() != 2 or t.shape[0] != B or t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("block_table is int32 [B, blocks]")
+    return t.data_ptr(), t.stride(0) if B > 1 else max(t.stride(0), t.shape[1]), t.shape[1]
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens):
+    """(packed gdn_kv_cache, B, Hk, D)."""
+    P, Hk, page, D = k_cache.shape
+    for t in (k_cache, v_cache):
+        if t.dtype not in _CACHE_BYTES or t.shape != k_cache.shape or not t.is_contiguous():
+            raise ValueError("k_cache and v_cache are contiguous [pages, Hk, page, D] of float8_e4m3fn or uint8")
+    _fp32(k_scale, P * Hk, "k_scale")
+    _fp32(v_scale, P * Hk, "v_scale")
+    B = kv_lens.numel()
+    table, ld, blocks = _table(block_table, B)
+    return _PACK_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, page, table,
+                            ld, blocks, _int32(kv_lens, B, "kv_lens")), B, Hk, D
+
+
+def _new_rows(t, B, cu_seqlens, what):
+    """(rows of a sequence or in all, width, stride) of the new tokens' tensor."""
+    Bt, T, C, ld = _token_rows(t, what)
+    if (cu_seqlens is None) != (t.dim() == 3) or (Bt and Bt != B):
+        raise ValueError("%s is [B, T, heads * D], or packed [tokens, heads * D] with cu_seqlens" % what)
+    return T, C, ld
+
+
+def gdn_kv_append(k, v, kv_lens, block_table, k_cache, v_cache, k_scale, v_scale, *, cu_seqlens=None, max_new=0, max_kv=0,
+                  stream=None):
+    """New keys and values k, v [B, T, Hk*D] (packed: [tokens, Hk*D] with
+    cu_seqlens int32 [B+1]), rows possibly strided, into the paged cache
+    k_cache, v_cache [pages, Hk, page, D] with k_scale, v_scale [pages, Hk]
+    (gdn_kv_append).  kv_lens [B] counts the new tokens, the last ones, in."""
+    cache, B, Hk, D = _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens)
+    T, C, ldk = _new_rows(k, B, cu_seqlens, "k")
+    Tv, Cv, ldv = _new_rows(v, B, cu_seqlens, "v")
+    if T != Tv or C != Cv or C != Hk * D:
+        raise ValueError("k and v are [.., Hk * D] over the same tokens")
+    if k.dtype != v.dtype or k.dtype not in _IO_CODES:
+        raise TypeError("k and v have one dtype, bfloat16 or float32")
+    st = (_lib or lib()).gdn_kv_append(
+        _PACK_ATTN_SHAPE.pack(B, T, 0, Hk, D, _IO_CODES[k.dtype], max_new, max_kv),
+        _PACK_APPEND.pack(k.data_ptr(), v.data_ptr(), ldk, ldv,
+                          0 if cu_seqlens is None else _int32(cu_seqlens, B + 1, "cu_seqlens")) + cache,
+        _raw_stream(stream, k))
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_kv_append")
+
+
+def gdn_attn(q, o, kv_lens, block_table, k_cache, v_cache, k_scale, v_scale, *, Hq, cu_seqlens=None, max_new=0, max_kv=0,
+             causal=True, scale=0.0, workspace=None, stream=None):
+    """Attention of the new tokens q [B, T, Hq*D] (packed: [tokens, Hq*D] with
+    cu_seqlens) over the paged cache into o (gdn_attn).  Of a sequence's
+    kv_lens[b] tokens the new ones are the last; causal: each sees those up to
+    itself.  max_new, max_kv: bounds of the new and of all tokens of a sequence,
+    as the caller knows them (0: what the tensors allow); workspace: any tensor
+    of gdn_attn_workspace_bytes() bytes."""
+    cache, B, Hk, D = _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens)
+    T, C, ldq = _new_rows(q, B, cu_seqlens, "q")
+    To, Co, ldo = _new_rows(o, B, cu_seqlens, "o")
+    if T != To or C != Co or C != Hq * D:
+        raise ValueError("q and o are [.., Hq * D] over the same tokens")
+    if q.dtype != o.dtype or q.dtype not in _IO_CODES:
+        raise TypeError("q and o have one dtype, bfloat16 or float32")
+    ws = ws_bytes = 0
+    if workspace is not None and workspace.numel():
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = (_lib or lib()).gdn_attn(
+        _PACK_ATTN_SHAPE.pack(B, T, Hq, Hk, D, _IO_CODES[q.dtype], max_new, max_kv),
+        _PACK_ATTN.pack(q.data_ptr(), o.data_ptr(), ldq, ldo,
+                        0 if cu_seqlens is None else _int32(cu_seqlens, B + 1, "cu_seqlens")) + cache +
+        _PACK_ATTN_END.pack(1 if causal else 0, scale, ws, ws_bytes),
+        _raw_stream(stream, q))
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_attn")
+
+
+def gdn_attn_workspace_bytes(B, T, Hq, Hk, D, *, max_new=0, max_kv=0, packed=True, io_dtype=None):
+    """Workspace bytes of gdn_attn (packed: T is the total token count)."""
+    sh = gdn_attn_shape(B, T, Hq, Hk, D, GDN_BF16 if io_dtype is None else io_dtype, max_new, max_kv)
+    return lib().gdn_attn_workspace_bytes(ctypes.byref(sh), 1 if packed else 0)
+
+
+def gdn_rope_plan(rot, *, base=10000.0, layout="half", scaling=None):
+    """The frequencies of gdn_rope, made once on the host (gdn_rope_plan_init):
+    layout "half" or "interleaved"; scaling None or dict(kind="linear" or "ntk",
+    factor=..) or dict(kind="parts", factor=.., original=.., fast=32, slow=1)."""
+    s = dict(scaling) if scaling else {}
+    kind = ROPE_SCALINGS[s.pop("kind")] if scaling else 0
+    spec = gdn_rope_spec(rot, ROPE_LAYOUTS[layout], kind, base, s.pop("factor", 1.0), s.pop("original", 0.0),
+                         s.pop("fast", 32.0), s.pop("slow", 1.0))
+    if s:
+        raise ValueError("scaling: %s" % ", ".join(s))
+    plan = gdn_rope_plan_t()
+    st = lib().gdn_rope_plan_init(ctypes.byref(spec), ctypes.byref(plan))
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_rope_plan_init")
+    return plan
+
+
+def gdn_rope(plan, positions, tensors, *, D, inverse=False, stream=None):
+    """Rotary positions on the first plan.rot of each head's D elements
+    (gdn_rope): positions int32 [tokens]; ``tensors`` lists (x, y) pairs of one
+    dtype, [.., heads * D] over the tokens, rows possibly strided, y the output
+    (x itself: in place).  inverse: turned back, the forward call's gradient."""
+    tokens = positions.numel()
+    dtype = tensors[0][0].dtype
+    if dtype not in _IO_CODES:
+        raise TypeError("tensors must be bfloat16 or float32")
+    packed = []
+    for x, y in tensors:
+        B, T, C, ldx = _token_rows(x, "x")
+        By, Ty, Cy, ldy = _token_rows(y, "y")
+        if x.dtype != dtype or y.dtype != dtype:
+            raise TypeError("the tensors have one dtype")
+        if (B or 1) * T != tokens or (By or 1) * Ty != tokens or C != Cy or C % D:
+            raise ValueError("x and y are [.., heads * D] over the tokens of positions")
+        packed.append(_PACK_ROPE_X.pack(x.data_ptr(), y.data_ptr(), ldx, ldy, C // D))
+    st = (_lib or lib()).gdn_rope(tokens, D, _IO_CODES[dtype], ctypes.byref(plan), _int32(positions, tokens, "positions"),
+                                  len(packed), b"".join(packed), 1 if inverse else 0, _raw_stream(stream, positions))
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_rope")
+
+
+def gdn_kv_pages(kv_lens, new_tokens, free_pages, free_used, block_table, kv_lens_out, free_used_out, cu_seqlens, slots=None,
+                 positions=None, *, page, max_tokens=None, stream=None):
+    """Pages for new_tokens [B] more tokens of requests with kv_lens [B] cached
+    ones, from free_pages behind the first free_used [1] (gdn_kv_pages): fills
+    block_table [B, blocks], kv_lens_out and free_used_out (may be the inputs),
+    cu_seqlens [B+1], slots int64 and positions int32 [max_tokens]."""
+    B = kv_lens.numel()
+    table, ld, blocks = _table(block_table, B)
+    sizes = [t.numel() for t in (slots, positions) if t is not None] + ([] if max_tokens is None else [max_tokens])
+    if not sizes or min(sizes) != max(sizes):
+        raise ValueError("slots, positions and max_tokens say how many tokens there may be")
+    if slots is not None and (slots.dtype != torch.int64 or not slots.is_contiguous()):
+        raise ValueError("slots: contiguous int64 values are wanted")
+    st = (_lib or lib()).gdn_kv_pages(
+        _PACK_PAGES.pack(B, page, blocks, free_pages.numel(), ld, sizes[0], _int32(kv_lens, B, "kv_lens"),
+                         _int32(new_tokens, B, "new_tokens"), _int32(free_pages, free_pages.numel(), "free_pages"),
+                         _int32(free_used, 1, "free_used"), table, _int32(kv_lens_out, B, "kv_lens_out"),
+                         _int32(free_used_out, 1, "free_used_out"), _int32(cu_seqlens, B + 1, "cu_seqlens"),
+                         0 if slots is None else slots.data_ptr(),
+                         0 if positions is None else _int32(positions, sizes[0], "positions")),
+        _raw_stream(stream, kv_lens))
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_kv_pages")
 
 
 def gdn_device_status(stream=None, reset=False):

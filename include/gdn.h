@@ -69,7 +69,7 @@
 extern "C" {
 #endif
 
-#define GDN_ABI_VERSION 6
+#define GDN_ABI_VERSION 7
 
 typedef enum {
   GDN_OK = 0,
@@ -444,6 +444,211 @@ typedef struct {
 } gdn_linattn_form;
 
 gdn_status gdn_selftest_linattn_form(const gdn_shape *shape, int packed, int workspace, gdn_linattn_form *form);
+
+/*
+ * Softmax attention over a paged cache in 8 bits: the layer of the hybrid
+ * decoders that stands between the linear ones (node kv of "Qwen3.8-27B", page
+ * size 16; "How Qwen3.5 works" sections 10 and 13), from the output of its
+ * in-projection to the input of its out-projection.
+ *
+ * The cache of a layer: n_pages pages of `page` tokens (16, 32, 64 or 128)
+ *   k, v       [n_pages][Hk][page][D] e4m3 (1 sign, 4 exponent and 3 fraction
+ *              bits, bias 7): the value byte * scale
+ *   k_scale, v_scale [n_pages][Hk] fp32: the scale of a page and head
+ * and where the sequences lie in it
+ *   block_table [B][table_ld] int32: token t of sequence b is row t % page of
+ *              page block_table[b][t / page]; max_blocks entries of a row count
+ *   kv_lens    [B] int32: the tokens of each sequence, those of the call included
+ * D is 64, 128 or 256.  Pages may be shared by sequences that only read them.
+ *
+ * The new tokens of a call: fixed length, sequence b owns token rows b*T ..
+ * b*T+T-1 and T tokens are new; packed, rows cu_seqlens[b] .. cu_seqlens[b+1]-1
+ * of T rows (rows behind cu_seqlens[B] are neither read nor written).  They are
+ * the last of the sequence: row i of n is at position kv_lens[b] - n + i.
+ *   max_new   packed: no sequence has more new tokens (0: T)
+ *   max_kv    no sequence has more tokens in all (0: max_blocks * page)
+ * Lengths and tables are read on the device.  A sequence with offsets out of
+ * order or range, or with more tokens than max_new, max_kv or its table allow,
+ * is skipped (its outputs stay untouched); an entry of the table that is used
+ * and is not a page of the cache is left out.  Both record GDN_ERR_INVALID_ARG
+ * for gdn_device_status.
+ */
+typedef struct {
+  int B, T;
+  int Hq, Hk;     /* query heads, key heads; Hq % Hk == 0, at most 64 query heads to a key head */
+  int D;
+  int io_dtype;   /* gdn_dtype of q, k, v and o */
+  int max_new, max_kv;
+} gdn_attn_shape;
+
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int n_pages, page;
+  const int *block_table;
+  long long table_ld;
+  int max_blocks;
+  const int *kv_lens;
+} gdn_kv_cache;
+
+/*
+ * New keys and values into the cache: k, v [rows][ldk], [rows][ldv], Hk heads
+ * of D, rows 16-byte aligned.  Hq is not used.
+ *   The scale of a page and head is the smallest power of two s with |x| <= 448 s
+ *   for the page's new tokens, at least 2^-120 and at most 2^7 (larger values
+ *   are stored as +-57344), and never below the one it has where the page holds
+ *   older tokens of the sequence; where it grows, those are rounded anew.  A
+ *   byte is x / s rounded to nearest, ties to even.
+ *   A NaN or infinity among a page's new tokens makes the scale of that page
+ *   and head NaN (the new bytes are 0).
+ *   Rows of a page behind the sequence's end keep what they hold.
+ *   A page that is written belongs to one sequence: where the table gives it to
+ *   two, what the two write there is not specified.
+ */
+typedef struct {
+  const void *k, *v;
+  long long ldk, ldv;
+  const int *cu_seqlens; /* or NULL: fixed length */
+  gdn_kv_cache cache;
+} gdn_kv_append_io;
+
+gdn_status gdn_kv_append(const gdn_attn_shape *shape, const gdn_kv_append_io *io, void *stream);
+
+/*
+ * Attention of the new tokens over the cache (which holds their keys and values
+ * already):  o_i = sum_j p_ij v_j,  p_ij = softmax over j of scale q_i . k_j,
+ * query head h with key head h / (Hq / Hk).
+ *   q, o [rows][ldq], [rows][ldo]   Hq heads of D, io dtype, 16-byte rows
+ *   causal != 0: row i at position p sees tokens 0 .. p; 0: it sees all
+ *     kv_lens[b] (an encoder's states, say).  A row that sees none gives 0.
+ *   scale   0 means 1/sqrt(D)
+ *   workspace 256-byte aligned scratch of gdn_attn_workspace_bytes(), or NULL;
+ *     with it the tokens of long sequences are spread over the GPU where there
+ *     are few rows.  Undefined after the call; not to be shared by calls that
+ *     may overlap in time.
+ * What the cache holds behind a row's last token does not reach it, whatever it
+ * is, but for its page's scales: a row that sees a token of a page whose k or
+ * v scale is NaN gives NaN.  Scales are 0 <= s <= 2^7.  In the bytes there is no
+ * NaN (0x7f, 0xff; gdn_kv_append writes none): where there is one among the
+ * tokens seen, what it is taken for is not specified.
+ * bf16 io: products of exact 16-bit operands on the tensor cores, p rounded to
+ * 16 bits, sums and softmax in fp32.  fp32 io: fp32 throughout.
+ */
+typedef struct {
+  const void *q;
+  void *o;
+  long long ldq, ldo;
+  const int *cu_seqlens; /* or NULL: fixed length */
+  gdn_kv_cache cache;
+  int causal;
+  float scale;
+  void *workspace;
+  size_t workspace_bytes;
+} gdn_attn_io;
+
+gdn_status gdn_attn(const gdn_attn_shape *shape, const gdn_attn_io *io, void *stream);
+
+/* Bytes of workspace of gdn_attn for this shape on the current device (packed as
+ * for gdn_linattn_workspace_bytes); 0 where the call uses none or the shape is
+ * invalid. */
+size_t gdn_attn_workspace_bytes(const gdn_attn_shape *shape, int packed);
+
+/*
+ * Rotary positions on the first `rot` elements of every head ("How Qwen3.5
+ * works" section 10: 64 of 256).  The pair (a, b) of index i at position p
+ * becomes m (a cos x - b sin x, b cos x + a sin x), x = p f_i.
+ *   GDN_ROPE_HALF         the pair is elements i and i + rot/2
+ *   GDN_ROPE_INTERLEAVED  elements 2i and 2i + 1
+ * gdn_rope_plan_init fills a plan on the host (no GPU is needed):
+ *   GDN_ROPE_PLAIN   f_i = base^(-2i/rot), m = 1
+ *   GDN_ROPE_LINEAR  f_i / factor
+ *   GDN_ROPE_NTK     base * factor^(rot/(rot-2)) in the place of base (rot > 2)
+ *   GDN_ROPE_PARTS   pairs that turn more than `fast` times over the `original`
+ *                    context keep f_i, those that turn less than `slow` times
+ *                    take f_i / factor, a ramp over the pairs between lies
+ *                    between the two: with c(n) = rot ln(original / (2 pi n)) /
+ *                    (2 ln base) it goes from max(floor(c(fast)), 0) to
+ *                    min(ceil(c(slow)), rot - 1), and m = 0.1 ln(factor) + 1.
+ *                    (Peng et al., arXiv 2309.00071, sections 3.2 and 3.4)
+ * Other frequencies: write turns and m into the plan.  turns[i] is f_i / (2 pi),
+ * modulo 1, times 2^64: the angle of any 32-bit position is p * turns[i] modulo
+ * 2^64, which no distance makes less exact.
+ */
+typedef enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout;
+typedef enum { GDN_ROPE_PLAIN = 0, GDN_ROPE_LINEAR = 1, GDN_ROPE_NTK = 2, GDN_ROPE_PARTS = 3 } gdn_rope_scaling;
+
+#define GDN_ROPE_MAX_PAIRS 128
+typedef struct {
+  int rot;     /* even, 2 .. 256 */
+  int layout;  /* gdn_rope_layout */
+  float m;
+  unsigned long long turns[GDN_ROPE_MAX_PAIRS];
+} gdn_rope_plan;
+
+typedef struct {
+  int rot, layout, scaling;  /* scaling: gdn_rope_scaling */
+  double base, factor;       /* base > 1, factor >= 1 */
+  double original, fast, slow; /* GDN_ROPE_PARTS only: original > 0, fast > slow > 0 */
+} gdn_rope_spec;
+
+gdn_status gdn_rope_plan_init(const gdn_rope_spec *spec, gdn_rope_plan *plan);
+
+/*
+ *   positions  [tokens] int32, any values
+ *   x[0 .. n_x-1], 1 <= n_x <= 4: q, k and the like, [tokens] rows of `heads`
+ *     heads of D elements, ld* elements apart, io dtype.  y may be exactly x
+ *     (the same pointer and stride: turned in place, the other D - rot elements
+ *     of a head are not touched); otherwise it must not overlap any x or y
+ *     (but as disjoint column blocks of one buffer: the same stride) and takes
+ *     whole heads.
+ *   D: rot .. 1024.  Elements are aligned to their own size only; heads of
+ *     16-byte alignment run faster.
+ *   inverse != 0: turns back (by -x), times m all the same: the gradient of
+ *     the forward call.
+ */
+typedef struct {
+  const void *x;
+  void *y;
+  long long ldx, ldy;
+  int heads;
+} gdn_rope_x;
+
+gdn_status gdn_rope(int tokens, int D, int io_dtype, const gdn_rope_plan *plan, const int *positions, int n_x,
+                    const gdn_rope_x *x, int inverse, void *stream);
+
+/*
+ * Block tables and slot maps, on the GPU: pages for the new tokens of B requests.
+ *   kv_lens     [B] int32: tokens cached so far
+ *   new_tokens  [B] int32: tokens to come, 0 or more
+ *   free_pages  [n_free] int32: pages to hand out, the first free_used[0] are gone
+ *   block_table [B][table_ld] int32, max_blocks entries of a row: of request b the
+ *               entries from ceil(kv / page) to ceil((kv + new) / page) - 1 get
+ *               the next free pages (in order: requests, then blocks); the others
+ *               are not written
+ *   kv_lens_out [B], free_used_out [1]: kv + new, and the count moved on; each may
+ *               be exactly the buffer it comes from
+ *   cu_seqlens  [B + 1]: out: the offsets of the requests' new tokens
+ *   slots       [max_tokens] int64 or NULL: page * page size + row of each new
+ *               token; -1 behind the last one
+ *   positions   [max_tokens] int32 or NULL: its position; 0 behind the last one
+ * All or nothing: where a count is negative, a request would need more than
+ * max_blocks, the pages do not suffice or there are more than max_tokens new
+ * tokens, the call records GDN_ERR_INVALID_ARG for gdn_device_status, hands out
+ * nothing, and leaves cu_seqlens all 0, every slot -1, kv_lens_out and
+ * free_used_out as if no token were new (the other calls then have nothing to do).
+ * An entry of the table that is already there is not checked.
+ * page: 16, 32, 64 or 128; n_free may be 0; B <= 65536.
+ */
+typedef struct {
+  int B, page, max_blocks, n_free;
+  long long table_ld, max_tokens;
+  const int *kv_lens, *new_tokens, *free_pages, *free_used;
+  int *block_table, *kv_lens_out, *free_used_out, *cu_seqlens;
+  long long *slots;
+  int *positions;
+} gdn_kv_pages_io;
+
+gdn_status gdn_kv_pages(const gdn_kv_pages_io *io, void *stream);
 
 /*
  * Synchronise `stream` and report device-side failures recorded since the
