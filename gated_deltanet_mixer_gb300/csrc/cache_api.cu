@@ -58,10 +58,11 @@ gdn_status check_cache(const gdn_attn_shape *s, const gdn_kv_cache *c, gdn::Cach
                       s->Hk, s->D, c->block_table, c->table_ld, c->max_blocks};
   return GDN_OK;
 }
-gdn::SeqArgs seq_args(const gdn_attn_shape *s, const int *cu, const gdn_kv_cache *c) {
-  const int cap = c->max_blocks * c->page;
-  const int max_new = cu && s->max_new ? std::min(s->max_new, s->T) : s->T;
-  return gdn::SeqArgs{s->B, s->T, max_new, s->max_kv ? std::min(s->max_kv, cap) : cap, cu, c->kv_lens, nullptr};
+// The bounds on a sequence's new and cached tokens.
+int bound_new(const gdn_attn_shape *s, bool packed) { return packed && s->max_new ? std::min(s->max_new, s->T) : s->T; }
+int bound_kv(const gdn_attn_shape *s, int cap) { return s->max_kv ? std::min(s->max_kv, cap) : cap; }
+gdn::SeqArgs seq_args(const gdn_attn_shape *s, const int *cu, const gdn_kv_cache *c, unsigned int *err) {
+  return gdn::SeqArgs{s->B, s->T, bound_new(s, cu != nullptr), bound_kv(s, c->max_blocks * c->page), cu, c->kv_lens, err};
 }
 
 gdn_status check_rows(const void *p, long long ld, long long width, size_t el) {
@@ -70,14 +71,25 @@ gdn_status check_rows(const void *p, long long ld, long long width, size_t el) {
   return aligned16(p) && ld * el % 16 == 0 ? GDN_OK : GDN_ERR_ALIGNMENT;
 }
 
-// Ranges of the tokens side by side: enough blocks to fill the GPU twice, none with less than 64 tokens.
-int rows_splits(const gdn_attn_shape *s, bool packed, int max_kv, int sms) {
+// How a call of gdn_attn runs, and the workspace it makes use of.
+struct AttnPlan {
+  int few_rows;  // rows of a tile of attn_few.cu; 0: attn_rows.cu
+  int splits;    // attn_rows.cu: ranges of the tokens side by side
+  size_t bytes;
+};
+AttnPlan attn_plan(const gdn_attn_shape *s, bool packed, long long rows, int max_kv, int sms) {
   const int r = s->Hq / s->Hk;
-  const gdn::SeqArgs q{s->B, s->T, 0, 0, packed ? &s->B : nullptr, nullptr, nullptr};
-  const long long rows = packed ? (long long)s->T * r / 16 + s->B : ((long long)s->T * r / 16 + 1) * s->B;
-  (void)q;
-  const long long blocks = rows * s->Hk;
-  return (int)std::max(1LL, std::min({(2LL * sms + blocks - 1) / blocks, (max_kv + 63LL) / 64, 64LL}));
+  AttnPlan p{0, 1, 0};
+  if (s->io_dtype == GDN_BF16) p.few_rows = gdn::attn_few_rows(s->D, (long long)bound_new(s, packed) * r);
+  if (p.few_rows) {
+    p.bytes = gdn::attn_few_ws_bytes(s->D, p.few_rows, sms);
+    return p;
+  }
+  // enough blocks to fill the GPU twice, none with less than 64 tokens
+  const long long blocks = (packed ? rows * r / 16 + s->B : ((long long)s->T * r / 16 + 1) * s->B) * s->Hk;
+  p.splits = (int)std::max(1LL, std::min({(2LL * sms + blocks - 1) / blocks, (max_kv + 63LL) / 64, 64LL}));
+  if (p.splits > 1) p.bytes = (size_t)p.splits * rows * s->Hq * (s->D + 2) * sizeof(float);
+  return p;
 }
 
 }  // namespace
@@ -107,8 +119,7 @@ gdn_status gdn_kv_append(const gdn_attn_shape *shape, const gdn_kv_append_io *io
   }
   DeviceInfo dev;
   if ((st = device_info(&dev)) != GDN_OK) return st;
-  a.seq = seq_args(shape, io->cu_seqlens, &io->cache);
-  a.seq.err = dev.err;
+  a.seq = seq_args(shape, io->cu_seqlens, &io->cache, dev.err);
   a.k = io->k;
   a.v = io->v;
   a.ldk = io->ldk;
@@ -121,8 +132,7 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_shape *shape, int packed) {
   DeviceInfo dev;
   if (!shape || check_attn_shape(shape, packed != 0, &rows) != GDN_OK || check_heads(shape) != GDN_OK || device_info(&dev) != GDN_OK)
     return 0;
-  const int splits = rows_splits(shape, packed != 0, shape->max_kv ? shape->max_kv : 1 << 30, dev.sms);
-  return splits < 2 ? 0 : (size_t)splits * rows * shape->Hq * (shape->D + 2) * sizeof(float);
+  return attn_plan(shape, packed != 0, rows, bound_kv(shape, 1 << 30), dev.sms).bytes;
 }
 
 gdn_status gdn_attn(const gdn_attn_shape *shape, const gdn_attn_io *io, void *stream) {
@@ -148,8 +158,7 @@ gdn_status gdn_attn(const gdn_attn_shape *shape, const gdn_attn_io *io, void *st
   if (overlap(ro, rw)) return GDN_ERR_ALIAS;
   DeviceInfo dev;
   if ((st = device_info(&dev)) != GDN_OK) return st;
-  a.seq = seq_args(shape, io->cu_seqlens, &io->cache);
-  a.seq.err = dev.err;
+  a.seq = seq_args(shape, io->cu_seqlens, &io->cache, dev.err);
   a.Hq = shape->Hq;
   a.r = shape->Hq / shape->Hk;
   a.q = io->q;
@@ -158,13 +167,15 @@ gdn_status gdn_attn(const gdn_attn_shape *shape, const gdn_attn_io *io, void *st
   a.ldo = io->ldo;
   a.causal = io->causal != 0;
   a.scale = io->scale != 0.f ? io->scale : 1.0f / std::sqrt((float)shape->D);
-  a.splits = 1;
-  if (io->workspace) {
-    if (io->workspace_bytes < gdn_attn_workspace_bytes(shape, packed)) return GDN_ERR_INVALID_ARG;
-    a.splits = rows_splits(shape, packed, a.seq.max_kv, dev.sms);
-    if (a.splits > 1) a.ws = io->workspace;
+  const AttnPlan plan = attn_plan(shape, packed, rows, a.seq.max_kv, dev.sms);
+  if (io->workspace && plan.bytes) {
+    if (io->workspace_bytes < plan.bytes) return GDN_ERR_INVALID_ARG;
+    a.ws = io->workspace;
   }
-  return gdn::launch_attn_rows(a, shape->io_dtype == GDN_BF16, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  a.splits = plan.splits;
+  const cudaError_t e = plan.few_rows ? gdn::launch_attn_few(a, plan.few_rows, dev.sms, (cudaStream_t)stream)
+                                      : gdn::launch_attn_rows(a, shape->io_dtype == GDN_BF16, (cudaStream_t)stream);
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 gdn_status gdn_rope_plan_init(const gdn_rope_spec *spec, gdn_rope_plan *plan) {

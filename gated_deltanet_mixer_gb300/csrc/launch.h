@@ -248,6 +248,11 @@ cudaError_t launch_kv_pages(const PagesArgs &a, cudaStream_t s);
 cudaError_t launch_rope(const RopeArgs &a, bool bf16, cudaStream_t s);
 cudaError_t launch_kv_append(const AppendArgs &a, bool bf16, cudaStream_t s);
 cudaError_t launch_attn_rows(const AttnArgs &a, bool bf16, cudaStream_t s);
+// bf16 io, few rows: the rows of a tile that hold `rows` rows of a sequence and
+// key head (0: too many), the partial results' bytes, the launches.
+int attn_few_rows(int D, long long rows);
+size_t attn_few_ws_bytes(int D, int rows_tile, int num_sms);
+cudaError_t launch_attn_few(const AttnArgs &a, int rows_tile, int num_sms, cudaStream_t s);
 
 // Device error bits (the error word is OR-ed).
 constexpr unsigned int kErrTimeout = 1u;  // a bounded wait gave up

@@ -70,10 +70,11 @@ def check_rows(got, q, cache, b, n, kv, Hq, causal, scale, dt, k=None, v=None):
     assert bool((err <= tol + 1e-37).all()), "off by %.3g of the tolerance" % float((err / (tol + 1e-37)).max())
 
 
-def attend(cache, new, Hq, dt, causal=True, scale=0.0, seed=3, ws=True, pad=8, q=None, max_new=0, max_kv=0):
-    """A packed call; o [tokens, Hq * D], NaN where nothing was written."""
+def attend(cache, new, Hq, dt, causal=True, scale=0.0, seed=3, ws=True, pad=8, q=None, max_new=None, max_kv=0):
+    """A packed call, max_new as the lengths have it; o [tokens, Hq * D], NaN where nothing was written."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     T, width = max(1, sum(new)), Hq * cache.D
+    max_new = max(new) if max_new is None else max_new
     if q is None:
         q = rows(T, width, dt, g, pad)
     buf = torch.full((T, width + 2 * pad), math.nan, device="cuda", dtype=dt)
@@ -101,10 +102,12 @@ def check(cache, new, Hq, dt, causal=True, scale=0.0, **kw):
 @pytest.mark.parametrize("D,Hk,r,page", [(64, 2, 1, 16), (128, 1, 3, 32), (256, 2, 6, 16), (128, 2, 8, 64), (256, 1, 2, 128),
                                          (64, 3, 16, 16), (256, 1, 12, 16), (128, 1, 64, 16)])
 @pytest.mark.parametrize("ws", [True, False])
-def test_single_tokens(dt, D, Hk, r, page, ws):
+@pytest.mark.parametrize("said", [True, False])
+def test_single_tokens(dt, D, Hk, r, page, ws, said):
     """Decoding: one token each, lengths around tile and page borders, from one on."""
     lens = [1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 129, 300, 1000]
-    check(R.Cache(lens, Hk, D, page, device="cuda").fill(), [1] * len(lens), Hk * r, dt, ws=ws)
+    check(R.Cache(lens, Hk, D, page, device="cuda").fill(), [1] * len(lens), Hk * r, dt, ws=ws,
+          max_new=None if said else 0)
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
