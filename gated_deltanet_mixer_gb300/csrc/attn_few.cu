@@ -30,33 +30,34 @@ namespace {
 
 using namespace umma;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kSlab = 16;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kBlocksSM = 2;
+constexpr float kNone = -1.7e38f;  // the running maximum of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kPScale = 32768.f;  // on p, in fp16: p <= 1 stays finite, p >= 2^-29 normal
+// The reference of a row's exponents is its running maximum, moved only when a
+// score passes it by kSlack (in powers of 2): p stays below 2^kSlack, and in
+// fp16 times kPScale finite, and normal from 2^-25 on.
+constexpr float kSlack = 4.f;
+constexpr float kPScale = 2048.f;
 
-template <int D>
-struct Geo {
-  static constexpr int kGroup = 4 * D + 32;       // bytes of 4 tokens, and the distance that spreads the banks
-  static constexpr int kHalfSlab = 4 * kGroup;    // k, then v
-  static constexpr int kSlabBytes = 2 * kHalfSlab;
-  static constexpr int kDepth = D == 256 ? 3 : 6;
-  static constexpr int kRing = kWarps * kDepth * kSlabBytes;
-};
+// A slab's copies: kSub times 16 tokens, of a page each, in a ring of kDepth slabs per warp.  More tokens at a
+// time spread what a slab costs whatever its width (waits, votes, copies; some 250 instructions of a warp with
+// 16 tokens); wide heads have no room for them.
 template <int D, int NT>
-struct Smem {
+struct Geo {
   static constexpr int kRows = 8 * NT;
-  static constexpr int kMerge = kWarps * kRows * D * 4;  // takes the ring's place when a piece ends
-  static constexpr int kBig = Geo<D>::kRing > kMerge ? Geo<D>::kRing : kMerge;
+  static constexpr int kSub = D == 256 ? 1 : D == 128 ? (NT <= 2 ? 2 : 1) : NT == 1 ? 4 : 2;
+  static constexpr int kSlab = 16 * kSub;
+  static constexpr int kGroup = 4 * D + 32;         // bytes of 4 tokens, and the distance that spreads the banks
+  static constexpr int kK = 4 * kGroup;             // of 16 tokens' keys; their values follow
+  static constexpr int kSlabBytes = 2 * kK * kSub;
+  static constexpr int kDepth = D == 256 ? 3 : kSub == 1 ? 5 : D == 64 && kSub == 2 ? 5 : 3;
+  static constexpr int kRing = kWarps * kDepth * kSlabBytes;
+  static constexpr int kPitch = D + 4;                        // of a row of the merge, in floats
+  static constexpr int kMerge = kWarps * kRows * kPitch * 4;  // takes the ring's place when a piece ends
+  static constexpr int kBig = kRing > kMerge ? kRing : kMerge;
   static constexpr int kQ = (D / 16) * NT * 256;
   static constexpr int kBytes = kBig + kQ;
-};
-
-// Positions of a call's work: slabs of all units in a row.
-struct Place {
-  Seq s;
-  int hk, tile, slabs;  // of every unit of the sequence
-  int slab;             // in the unit
 };
 
 struct SeqLen {
@@ -64,19 +65,24 @@ struct SeqLen {
   int slabs, tiles;
   long long len;  // of the sequence's units together
 };
-__device__ __forceinline__ SeqLen seq_len(const AttnArgs &a, int b, int rows_tile) {
+__device__ __forceinline__ SeqLen seq_len(const AttnArgs &a, int b, int rows_tile, int slab) {
   SeqLen x{};
   const int lo = a.seq.cu ? a.seq.cu[b] : b * a.seq.T, n = a.seq.cu ? a.seq.cu[b + 1] - lo : a.seq.T;
   x.s = Seq{-1, lo, n, 0};
   if (lo < 0 || n < 0 || (a.seq.cu && (long long)lo + n > a.seq.T)) return x;  // recorded by the scan
   x.s = load_seq(a.seq, b, lo, n);
   if (x.s.b < 0 || n == 0) return x;
-  x.slabs = max(1, (x.s.kv + kSlab - 1) / kSlab);
+  x.slabs = max(1, (x.s.kv + slab - 1) / slab);
   x.tiles = (n * a.r + rows_tile - 1) / rows_tile;
   x.len = (long long)x.slabs * x.tiles * a.cache.Hk;
   return x;
 }
 
+// a / b rounded up; a 64-bit division takes some hundred instructions
+__device__ __forceinline__ long long div_up(long long a, int b) {
+  return a < 0x40000000 ? ((int)a + b - 1) / b : (a + b - 1) / b;
+}
+__device__ __forceinline__ int quotient(long long a, int b) { return a < 0x7fffffff ? (int)a / b : (int)(a / b); }
 __device__ __forceinline__ long long warp_sum_incl(long long v, int lane) {
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -94,7 +100,7 @@ struct Located {
   int b;              // sequence at pos, -1: none
   long long in_seq;   // position there
 };
-__device__ Located locate(const AttnArgs &a, int rows_tile, int index, int parts, int least, bool whole) {
+__device__ Located locate(const AttnArgs &a, int rows_tile, int slab, int index, int parts, int least, bool whole) {
   __shared__ long long sums[kWarps], base;
   __shared__ int bad, at_b;
   __shared__ long long at_in;
@@ -114,7 +120,7 @@ __device__ Located locate(const AttnArgs &a, int rows_tile, int index, int parts
         return 0;
       }
     }
-    const SeqLen x = seq_len(a, b, rows_tile);
+    const SeqLen x = seq_len(a, b, rows_tile, slab);
     return whole ? (long long)x.tiles * a.cache.Hk : x.len;
   };
   Located r{};
@@ -136,7 +142,7 @@ __device__ Located locate(const AttnArgs &a, int rows_tile, int index, int parts
     r.total = 0;
     return r;
   }
-  r.share = max((r.total + parts - 1) / parts, (long long)least);
+  r.share = max(div_up(r.total, parts), (long long)least);
   const long long pos = r.share * index;
   if (pos >= r.total) return r;
   if (one) {
@@ -189,7 +195,7 @@ __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w, int high) {
   return o;
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -197,7 +203,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 // The transpose of an 8 x 8 matrix of 16-bit values over the warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -211,17 +222,27 @@ __device__ __forceinline__ void bar_arrive(uint64_t *bar) {
 // Bytes 4w .. 4w+3 of a 16-byte word.
 __device__ __forceinline__ uint32_t word(const uint4 &v, int w) { return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w; }
 
+// Where a row of the merge has the two dimensions of product row i of lane group g: dimension 16 g + 2 i (and 128 on
+// from i = 8; D = 64: 8 g + 2 i), the pairs of 16 in an order that spreads the groups over the banks.
+template <int D>
+__device__ __forceinline__ int merge_at(int g, int i) {
+  return D >= 128 ? 128 * (i >> 3) + 16 * g + 2 * ((i & 7) ^ (g >> 1)) : 8 * g + 2 * i;
+}
+// Token row and query head of a row of the tile.
+struct RowAt {
+  long long token;
+  int head;
+};
+
 // q of a row tile as mma operands: element (row n, dim 64 c + 16 t + 4 s + e) is in k step 4 c + s, lane 4 (n % 8) + t,
 // times a power of two that brings the row's largest into [2^14, 2^15).
 template <int D, int NT>
-__device__ __forceinline__ void load_q(const AttnArgs &a, const Seq &s, int hk, int first, uint8_t *sq, float *qscale) {
+__device__ __forceinline__ void load_q(const AttnArgs &a, int count, const RowAt *at_row, uint8_t *sq, float *qscale) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = s.n * a.r;
+#pragma unroll 2
   for (int n = warp; n < 8 * NT; n += kWarps) {
-    const int rr = first + n;
-    const bool real = rr < rows;
-    const __nv_bfloat16 *const src = static_cast<const __nv_bfloat16 *>(a.q) + (long long)(s.row0 + (real ? rr / a.r : 0)) * a.ldq +
-                                     (long long)(hk * a.r + (real ? rr % a.r : 0)) * D;
+    const bool real = n < count;
+    const __nv_bfloat16 *const src = static_cast<const __nv_bfloat16 *>(a.q) + (real ? at_row[n].token * a.ldq + at_row[n].head * D : 0);
     constexpr int G = D / 4;  // groups of 4 elements
     float2 x[(G + 31) / 32][2];
     float top = 0.f;
@@ -258,34 +279,37 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, const Seq &s, int hk, 
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const AttnArgs a, int least) {
-  using G = Geo<D>;
-  using S = Smem<D, NT>;
-  constexpr int RT = 8 * NT, MT = D / 16;
+__global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const AttnArgs a, int least) {
+  using G = Geo<D, NT>;
+  constexpr int RT = 8 * NT, MT = D / 16, SUB = G::kSub;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t *const sq = smem + S::kBig;
+  uint8_t *const sq = smem + G::kBig;
   __shared__ __align__(8) uint64_t bars[kWarps][G::kDepth];
-  __shared__ float qscale[RT], wm[kWarps][RT], wl[kWarps][RT], wref[kWarps], row_m[RT], row_l[RT];
+  __shared__ RowAt at_row[RT];
+  __shared__ float qscale[RT], wm[kWarps][RT], wl[kWarps][RT], row_m[RT], row_l[RT];
+  __shared__ volatile int gave_up;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const CacheArgs &c = a.cache;
   if (tid < kWarps * G::kDepth) bar_init(&bars[tid / G::kDepth][tid % G::kDepth], 1);
+  if (tid == 0) gave_up = 0;
   const bool whole = a.ws == nullptr;
-  const Located loc = locate(a, RT, blockIdx.x, gridDim.x, whole ? 1 : least, whole);
+  const Located loc = locate(a, RT, G::kSlab, blockIdx.x, gridDim.x, whole ? 1 : least, whole);
   if (loc.b < 0) return;
   long long left = min(loc.share, loc.total - loc.share * blockIdx.x);
-  SeqLen q = seq_len(a, loc.b, RT);
-  int unit = (int)(whole ? loc.in_seq : loc.in_seq / q.slabs), slab0 = (int)(whole ? 0 : loc.in_seq % q.slabs);
+  SeqLen q = seq_len(a, loc.b, RT, G::kSlab);
+  int unit = whole ? (int)loc.in_seq : quotient(loc.in_seq, q.slabs);
+  int slab0 = whole ? 0 : (int)(loc.in_seq - (long long)unit * q.slabs);
   uint8_t *const ring = smem + warp * (G::kDepth * G::kSlabBytes);
   uint64_t *const bar = bars[warp];
-  uint32_t uses = 0;  // of the ring so far: slot uses % depth, phase (uses / depth) & 1
-  bool dead = false;
+  uint32_t slot_at = 0, phase_at = 0;  // of the ring, where the next slab goes
   const int page = 1 << c.page_shift;
+  const long long page_bytes = (long long)c.Hk * page * D;
 
   while (left > 0) {
     if (unit >= q.tiles * c.Hk) {  // the next sequence that has rows
       for (int nb = q.s.b + 1;; ++nb) {
         if (nb >= a.seq.B) return;
-        q = seq_len(a, nb, RT);
+        q = seq_len(a, nb, RT, G::kSlab);
         if (q.len > 0) break;
       }
       unit = 0;
@@ -296,32 +320,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const AttnArgs a,
     const int slab1 = whole ? q.slabs : (int)min((long long)q.slabs, slab0 + left);
     const bool starts = slab0 == 0, ends = slab1 == q.slabs;
     const int seen = a.causal ? min(q.s.kv, max(0, q.s.kv - q.s.n + (first + count - 1) / a.r + 1)) : q.s.kv;
-    const int slab_hi = min(slab1, (seen + kSlab - 1) / kSlab);
-    load_q<D, NT>(a, q.s, hk, first, sq, qscale);
-    __syncthreads();  // q is in place; the merge of the piece before is done with the ring
-
-    float acc[MT][NT][4], m[NT][2], l[NT][2], qs[NT][2];
-    int last[NT][2];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int row = 8 * j + 2 * t + u;
-        m[j][u] = -INFINITY;
-        l[j][u] = 0.f;
-        qs[j][u] = qscale[row];
-        last[j][u] = row >= count ? -1 : a.causal ? q.s.kv - q.s.n + (first + row) / a.r : q.s.kv - 1;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i][j][u] = acc[i][j][2 + u] = 0.f;
-      }
-    float ref = 0.f;
-    // this warp's slabs: slab0 + warp + 8 i, i < mine; pages and scales of 32 of them at a time, one per lane
+    const int slab_hi = min(slab1, (seen + G::kSlab - 1) / G::kSlab);
+    // this warp's slabs: slab0 + warp + kWarps i, i < mine; the pages and scales of 32 of their 16 tokens at a
+    // time, one per lane
     const int mine = slab_hi - slab0 > warp ? (slab_hi - slab0 - warp + kWarps - 1) / kWarps : 0;
     const int *const table = c.table + (long long)q.s.b * c.table_ld;
-    auto slab_of = [&](int i) { return slab0 + warp + kWarps * i; };
-    auto load_page = [&](int i) -> int {
-      if (i >= mine) return -1;
-      const int p = table[(slab_of(i) * kSlab) >> c.page_shift];
+    const int tok_first = (slab0 + warp) * G::kSlab;
+    constexpr int kStep = kWarps * G::kSlab;  // tokens from one of them to the next
+    auto load_page = [&](int x) -> int {      // x: 16 tokens, SUB to a slab
+      const int i = x / SUB, tok = tok_first + i * kStep + (x % SUB) * 16;
+      if (i >= mine || tok >= seen) return -1;
+      const int p = table[tok >> c.page_shift];
       if (p >= 0 && p < c.n_pages) return p;
       atomicOr(a.seq.err, kErrSeqlens);
       return -1;
@@ -335,133 +344,232 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const AttnArgs a,
     float2 sc[2];
     pg[0] = load_page(lane);
     pg[1] = load_page(lane + 32);
-    sc[0] = load_scales(pg[0]);
-    sc[1] = load_scales(pg[1]);
-    auto issue = [&](int i, int p) {  // the copies of slab i, whose page is p, into the ring
-      const uint32_t use = uses + i, slot = use % G::kDepth;
+    // Lane 8 sub + 0 .. 3 copies 4 tokens each of 16 tokens' k, 4 .. 7 of their v.  What has no page is copied
+    // from page 0 and not looked at.
+    const uint8_t *const copy_src = (lane & 4 ? c.v : c.k) + ((long long)hk * page + 4 * (lane & 3)) * D;
+    const uint32_t copy_dst = (lane >> 3) * 2 * G::kK + (lane & 7) * G::kGroup;
+    auto issue = [&](int i, int p, uint32_t slot) {  // the copies of slab i into the ring; p: the lane's page
       uint64_t *const b = bar + slot;
-      const uint32_t dst = smem_u32(ring + slot * G::kSlabBytes);
-      if (p < 0) {
-        if (lane == 0) bar_arrive(b);
-      } else {
-        if (lane == 0) bar_expect_tx(b, 8 * 4 * D);
-        __syncwarp();
-        if (lane < 8) {
-          const int tok = (slab_of(i) * kSlab) & (page - 1);
-          const uint8_t *const src = (lane < 4 ? c.k : c.v) + (((long long)p * c.Hk + hk) * page + tok + 4 * (lane & 3)) * D;
-          bulk_load(dst + lane * G::kGroup, src, 4 * D, b);
-        }
+      if (lane == 0) bar_expect_tx(b, SUB * 8 * 4 * D);
+      __syncwarp();
+      if (lane < 8 * SUB) {
+        const int tok = (tok_first + i * kStep + (lane >> 3) * 16) & (page - 1);
+        bulk_load(smem_u32(ring + slot * G::kSlabBytes) + copy_dst, copy_src + max(p, 0) * page_bytes + tok * D, 4 * D, b);
       }
       __syncwarp();
     };
+    uint32_t in_slot = slot_at;
 #pragma unroll 1
-    for (int i = 0; i < min(mine, G::kDepth); ++i) issue(i, __shfl_sync(0xffffffffu, pg[0], i));
+    for (int i = 0; i < min(mine, G::kDepth); ++i) {
+      issue(i, __shfl_sync(0xffffffffu, pg[0], (i * SUB + (lane >> 3)) & 31), in_slot);
+      in_slot = in_slot + 1 == G::kDepth ? 0 : in_slot + 1;
+    }
+    if (tid < RT) {
+      const int rr = first + tid, tok = rr / a.r;
+      at_row[tid] = RowAt{(long long)q.s.row0 + tok, hk * a.r + rr - tok * a.r};
+    }
+    sc[0] = load_scales(pg[0]);
+    sc[1] = load_scales(pg[1]);
+    __syncthreads();
+    load_q<D, NT>(a, count, at_row, sq, qscale);
+    __syncthreads();
 
-#pragma unroll 1
-    for (int i = 0; i < mine; ++i) {
-      const int in = i & 31;
-      if (in == 0 && i > 0) {
-        pg[0] = pg[1];
-        sc[0] = sc[1];
-        pg[1] = load_page(i + 32 + lane);
-      }
-      if (in == 16 && i > 16) sc[1] = load_scales(pg[1]);
-      const int p = __shfl_sync(0xffffffffu, pg[0], in);
-      const float ks = __shfl_sync(0xffffffffu, sc[0].x, in), vs = __shfl_sync(0xffffffffu, sc[0].y, in);
-      const uint32_t use = uses + i, slot = use % G::kDepth, phase = (use / G::kDepth) & 1;
-      if (!dead && !bar_wait(bar + slot, phase)) {
-        dead = true;
-        atomicOr(a.seq.err, kErrTimeout);
-      }
-      dead = __any_sync(0xffffffffu, dead);
-      const uint8_t *const sk = ring + slot * G::kSlabBytes, *const sv = sk + G::kHalfSlab;
-      const int tok0 = slab_of(i) * kSlab;
-      if (p >= 0 && !dead) {
-        // S^T: rows g and g + 8 are the tokens of half 0 and 1
-        float st[NT][4];
+    constexpr bool kQRegs = D * NT <= 256;
+    uint2 qr[kQRegs ? MT : 1][kQRegs ? NT : 1];
+    if constexpr (kQRegs) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) st[j][0] = st[j][1] = st[j][2] = st[j][3] = 0.f;
-        const int tg = g >> 1, bg = g & 1;
-        const int m0 = 2 * bg, gr0 = (tg + 2 * bg) & 3, gr1 = (tg + 2 * bg + 1) & 3;
-        const uint8_t *const k0 = sk + gr0 * G::kGroup + m0 * D + 16 * t, *const k1 = sk + gr1 * G::kGroup + (m0 + 1) * D + 16 * t;
+      for (int k = 0; k < MT; ++k)
 #pragma unroll
-        for (int ch = 0; ch < D / 64; ++ch) {
-          const uint4 w0 = *reinterpret_cast<const uint4 *>(k0 + 64 * ch), w1 = *reinterpret_cast<const uint4 *>(k1 + 64 * ch);
+        for (int j = 0; j < NT; ++j) qr[k][j] = *reinterpret_cast<const uint2 *>(sq + ((k * NT + j) * 32 + lane) * 8);
+    }
+    float acc[MT][NT][4], m[NT][2], l[NT][2], qs[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        m[j][u] = kNone;
+        l[j][u] = 0.f;
+        qs[j][u] = qscale[8 * j + 2 * t + u];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i][j][u] = acc[i][j][2 + u] = 0.f;
+      }
+    auto last_of = [&](int j, int u) {  // the last token that a row sees
+      const int row = 8 * j + 2 * t + u;
+      return row >= count ? -1 : a.causal ? q.s.kv - q.s.n + (int)(at_row[row].token - q.s.row0) : q.s.kv - 1;
+    };
+    // Tokens up to this one are seen by every row (rows that are none may see them too: nothing reads those).
+    const int all_see = a.causal ? q.s.kv - q.s.n + first / a.r : q.s.kv - 1;
+    float ref = 0.f, inv_ref = 0.f;  // the largest value scale so far, kPScale over it
+    // Rows g and g + 8 of S^T are these tokens of 16.
+    const int tg = g >> 1, bg = g & 1, gr0 = (tg + 2 * bg) & 3, gr1 = (tg + 2 * bg + 1) & 3;
+    const int in0 = 4 * gr0 + 2 * bg, in1 = 4 * gr1 + 2 * bg + 1;
+    const uint32_t k_at0 = gr0 * G::kGroup + 2 * bg * D + 16 * t, k_at1 = gr1 * G::kGroup + (2 * bg + 1) * D + 16 * t;
+
+    auto wait = [&](uint32_t slot, uint32_t phase) {
+      if (bar_try_wait(bar + slot, phase)) return;
+      const uint64_t t0 = global_ns();
+      while (!gave_up && !bar_try_wait(bar + slot, phase))
+        if (global_ns() - t0 > 1000000000ull) {
+          gave_up = 1;  // what follows is not right, and stays in its bounds
+          atomicOr(a.seq.err, kErrTimeout);
+        }
+    };
+    // S^T of a slab; 16 tokens alone in two chains of products
+    auto scores = [&](uint32_t slot, float (&st)[SUB][NT][4]) {
+      constexpr int kChains = SUB == 1 ? 2 : 1;
+      float sb[kChains][NT][4];
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) st[u][j][0] = st[u][j][1] = st[u][j][2] = st[u][j][3] = 0.f;
+      if constexpr (kChains == 2)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sb[1][j][0] = sb[1][j][1] = sb[1][j][2] = sb[1][j][3] = 0.f;
+#pragma unroll
+      for (int ch = 0; ch < D / 64; ++ch)
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          const uint8_t *const sk = ring + slot * G::kSlabBytes + u * 2 * G::kK;
+          const uint4 w0 = *reinterpret_cast<const uint4 *>(sk + k_at0 + 64 * ch), w1 = *reinterpret_cast<const uint4 *>(sk + k_at1 + 64 * ch);
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
             const uint32_t x0 = word(w0, s), x1 = word(w1, s);
             const uint32_t a0 = e4m3x2_to_h2(x0, 0), a1 = e4m3x2_to_h2(x1, 0), a2 = e4m3x2_to_h2(x0, 1), a3 = e4m3x2_to_h2(x1, 1);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-              const uint2 bq = *reinterpret_cast<const uint2 *>(sq + (((4 * ch + s) * NT + j) * 32 + lane) * 8);
-              mma16816(st[j], a0, a1, a2, a3, bq.x, bq.y);
+              uint2 bq;
+              if constexpr (kQRegs)
+                bq = qr[4 * ch + s][j];
+              else
+                bq = *reinterpret_cast<const uint2 *>(sq + (((4 * ch + s) * NT + j) * 32 + lane) * 8);
+              if (kChains == 2 && (s & 1))
+                mma16816(sb[kChains - 1][j], a0, a1, a2, a3, bq.x, bq.y);
+              else
+                mma16816(st[u][j], a0, a1, a2, a3, bq.x, bq.y);
             }
           }
         }
-        const int t0 = tok0 + 4 * gr0 + m0, t1 = tok0 + 4 * gr1 + m0 + 1;
-        float x[NT][4];
-        bool rescale = false;
-        float mn[NT][2];
+      if constexpr (kChains == 2)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float f = qs[j][u] * ks;
-            x[j][u] = t0 <= last[j][u] ? st[j][u] * f : -INFINITY;
-            x[j][2 + u] = t1 <= last[j][u] ? st[j][2 + u] * f : -INFINITY;
-            float top = fmaxf(x[j][u], x[j][2 + u]);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            mn[j][u] = fmaxf(m[j][u], top);
-            rescale |= mn[j][u] != m[j][u];
-          }
+          for (int e = 0; e < 4; ++e) st[0][j][e] += sb[1][j][e];
+    };
+
+    float st[SUB][NT][4];
+    uint32_t slot = slot_at, phase = phase_at;
+    if (mine > 0) {
+      wait(slot, phase);
+      scores(slot, st);
+    }
+#pragma unroll 1
+    for (int i = 0; i < mine; ++i) {
+      constexpr int kBatch = 32 / SUB;  // slabs
+      const int in = i & (kBatch - 1);
+      if (in == 0 && i > 0) {
+        pg[0] = pg[1];
+        sc[0] = sc[1];
+        pg[1] = load_page((i + kBatch) * SUB + lane);
+      }
+      if (in == kBatch / 2 && i > kBatch) sc[1] = load_scales(pg[1]);
+      float ks[SUB], vs[SUB], vtop = 0.f;
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        ks[u] = __shfl_sync(0xffffffffu, sc[0].x, in * SUB + u);
+        vs[u] = __shfl_sync(0xffffffffu, sc[0].y, in * SUB + u);
+        vtop = fmaxf(vtop, vs[u]);
+      }
+      const uint32_t next = slot + 1 == G::kDepth ? 0 : slot + 1, next_phase = phase ^ (next == 0 ? 1u : 0u);
+      const int tok0 = tok_first + i * kStep;
+      float y[SUB][NT][4];
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[u][j][e] = st[u][j][e] * (qs[j][e & 1] * ks[u]);
+      // The next slab's scores are on their way while this one's weights are formed.
+      if (i + 1 < mine) {
+        wait(next, next_phase);
+        scores(next, st);
+      }
+      // Tokens that some row does not see, or that have no page.
+      const uint32_t gone = (__ballot_sync(0xffffffffu, pg[0] < 0) >> (in * SUB)) & ((1u << SUB) - 1);  // bit u: no page
+      const bool masked = gone != 0 || tok0 + G::kSlab - 1 > all_see;
+      if (masked) {
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int last = gone >> u & 1 ? -1 : last_of(j, e);
+              if (tok0 + 16 * u + in0 > last) y[u][j][e] = -INFINITY;
+              if (tok0 + 16 * u + in1 > last) y[u][j][2 + e] = -INFINITY;
+            }
+      }
+      float top[NT][2], high = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          top[j][e] = fmaxf(y[0][j][e], y[0][j][2 + e]);
+#pragma unroll
+          for (int u = 1; u < SUB; ++u) top[j][e] = fmaxf(top[j][e], fmaxf(y[u][j][e], y[u][j][2 + e]));
+          high = fmaxf(high, top[j][e] - m[j][e]);
+        }
+      if (__any_sync(0xffffffffu, high > kSlack || vtop > ref)) {
         float shrink = 1.f;  // on the values so far, where a larger value scale sets in
-        if (vs > ref) {
-          shrink = ref / vs;
-          ref = vs;
-          rescale = true;
+        if (vtop > ref) {
+          shrink = ref / vtop;
+          ref = vtop;
+          inv_ref = kPScale / vtop;
         }
-        if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            float al[2];
+        for (int j = 0; j < NT; ++j) {
+          float al[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              al[u] = mn[j][u] == -INFINITY ? 1.f : exp2f(m[j][u] - mn[j][u]);
-              l[j][u] *= al[u];
-              m[j][u] = mn[j][u];
-              al[u] *= shrink;
-            }
+          for (int e = 0; e < 2; ++e) {
+            float x = top[j][e];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            x = fmaxf(x, m[j][e]);
+            al[e] = ex2(m[j][e] - x);
+            l[j][e] *= al[e];
+            m[j][e] = x;
+            al[e] *= shrink;
+          }
 #pragma unroll
-            for (int i2 = 0; i2 < MT; ++i2) {
-              acc[i2][j][0] *= al[0];
-              acc[i2][j][1] *= al[1];
-              acc[i2][j][2] *= al[0];
-              acc[i2][j][3] *= al[1];
-            }
+          for (int i2 = 0; i2 < MT; ++i2) {
+            acc[i2][j][0] *= al[0];
+            acc[i2][j][1] *= al[1];
+            acc[i2][j][2] *= al[0];
+            acc[i2][j][3] *= al[1];
           }
         }
-        const float pv = ref > 0.f ? vs / ref * kPScale : vs * 0.f;  // 0 or NaN where no scale is above 0
+      }
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        const float pv = vs[u] * inv_ref;  // NaN where the scale is, 0 where none is above 0
         uint32_t pb[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           float pp[4];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float base = m[j][u] == -INFINITY ? 0.f : m[j][u];
-            const float p0 = t0 <= last[j][u] ? exp2f(x[j][u] - base) : 0.f, p1 = t1 <= last[j][u] ? exp2f(x[j][2 + u] - base) : 0.f;
-            l[j][u] += p0 + p1;
-            pp[u] = t0 <= last[j][u] ? p0 * pv : 0.f;
-            pp[2 + u] = t1 <= last[j][u] ? p1 * pv : 0.f;
+          for (int e = 0; e < 4; ++e) {
+            const float w = ex2(y[u][j][e] - m[j][e & 1]);
+            l[j][e & 1] += w;
+            pp[e] = w * pv;
+            if (masked && y[u][j][e] == -INFINITY) pp[e] = 0.f;  // whatever the scale is
           }
           pb[j][0] = transpose8(pack2_sat(pp[0], pp[1]));
           pb[j][1] = transpose8(pack2_sat(pp[2], pp[3]));
         }
         // O^T: this lane's tokens are k = 2 t, 2 t + 1 (half 0) and 2 t + 8, 2 t + 9 (half 1)
+        const uint8_t *const sv = ring + slot * G::kSlabBytes + u * 2 * G::kK + G::kK;
         const int ga = t, gb = (t + 2) & 3, gc = (t + 1) & 3, gd = (t + 3) & 3;
         constexpr int W = D >= 128 ? 16 : 8;  // bytes of a lane per token and load
-        const bool tail = tok0 + kSlab > q.s.kv;
 #pragma unroll
         for (int ch = 0; ch < (D >= 128 ? D / 128 : 1); ++ch) {
           uint32_t w[4][W / 4];
@@ -477,11 +585,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const AttnArgs a,
               w[k][0] = v.x, w[k][1] = v.y;
             }
           }
-          if (tail) {  // bytes behind the end may be anything, NaN too
+          if (masked) {  // bytes behind the end, or of no page, may be anything, NaN too
             const int tk[4] = {4 * ga, 4 * gb + 2, 4 * gc + 1, 4 * gd + 3};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (tok0 + tk[k] >= q.s.kv)
+              if (tok0 + 16 * u + tk[k] >= q.s.kv || (gone >> u & 1))
 #pragma unroll
                 for (int e = 0; e < W / 4; ++e) w[k][e] = 0;
           }
@@ -502,11 +610,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const AttnArgs a,
       }
       __syncwarp();
       if (i + G::kDepth < mine) {
-        const int nx = i + G::kDepth, pn = __shfl_sync(0xffffffffu, (nx >> 5) == (i >> 5) ? pg[0] : pg[1], nx & 31);
-        issue(nx, pn);
+        const int x = (i + G::kDepth) * SUB + (lane >> 3), src = x & 31;
+        const int p0 = __shfl_sync(0xffffffffu, pg[0], src), p1 = __shfl_sync(0xffffffffu, pg[1], src);
+        issue(i + G::kDepth, x / 32 == i / kBatch ? p0 : p1, slot);
       }
+      slot = next;
+      phase = next_phase;
     }
-    uses += mine;
+    slot_at = slot;
+    phase_at = phase;
 
     // ---- the warps' results together
 #pragma unroll
@@ -522,17 +634,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const AttnArgs a,
           wl[warp][8 * j + 2 * t + u] = s;
         }
       }
-    if (lane == 0) wref[warp] = ref;
+    asm volatile("griddepcontrol.launch_dependents;");  // the join may come up
     __syncthreads();  // every warp is through with its ring
-    float *const merge = reinterpret_cast<float *>(smem) + warp * RT * D;
+    float *const merge = reinterpret_cast<float *>(smem) + warp * RT * G::kPitch;
     if (tid < RT) {
-      float top = -INFINITY;
+      float top = kNone, sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, wm[w][tid]);
-      float sum = 0.f;
-      const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += exp2f(wm[w][tid] - base) * wl[w][tid];
+      for (int w = 0; w < kWarps; ++w) sum += ex2(wm[w][tid] - top) * wl[w][tid];
       row_m[tid] = top;
       row_l[tid] = sum;
     }
@@ -541,34 +651,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const AttnArgs a,
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int row = 8 * j + 2 * t + u;
-        float top = -INFINITY;
+        float top = kNone;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, wm[w][row]);
-        const float f = exp2f(m[j][u] - (top == -INFINITY ? 0.f : top)) * (ref * (1.f / kPScale));
+        const float f = ex2(m[j][u] - top) * (ref * (1.f / kPScale));
 #pragma unroll
-        for (int i2 = 0; i2 < MT; ++i2) {
-          const int dim = D >= 128 ? 128 * (i2 >> 3) + 16 * g + 2 * (i2 & 7) : 8 * g + 2 * i2;
-          *reinterpret_cast<float2 *>(merge + row * D + dim) = make_float2(acc[i2][j][u] * f, acc[i2][j][2 + u] * f);
-        }
+        for (int i2 = 0; i2 < MT; ++i2)
+          *reinterpret_cast<float2 *>(merge + row * G::kPitch + merge_at<D>(g, i2)) = make_float2(acc[i2][j][u] * f, acc[i2][j][2 + u] * f);
       }
     __syncthreads();
-    const int slot = 2 * blockIdx.x + (starts ? 1 : 0);
-    for (int x = tid * 4; x < count * D; x += kThreads * 4) {
-      const int row = x / D, dim = x % D, rr = first + row;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int part = 2 * blockIdx.x + (starts ? 1 : 0);
+    for (int x = tid; x < count * (D / 2); x += kThreads) {
+      const int row = x / (D / 2), dim = x % (D / 2) * 2;
+      const int at = D >= 128 ? merge_at<D>((dim >> 4) & 7, (dim >> 7) * 8 + ((dim >> 1) & 7)) : dim;
+      float2 o = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem) + w * RT * D + x);
-        o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+        const float2 v = *reinterpret_cast<const float2 *>(reinterpret_cast<const float *>(smem) + (w * RT + row) * G::kPitch + at);
+        o.x += v.x, o.y += v.y;
       }
       if (starts && ends) {
         const float ls = row_l[row], inv = ls == 0.f ? 0.f : 1.f / ls;
-        __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.o) + (long long)(q.s.row0 + rr / a.r) * a.ldo +
-                                   (long long)(hk * a.r + rr % a.r) * D + dim;
-        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.o) + at_row[row].token * a.ldo + at_row[row].head * D + dim;
+        *reinterpret_cast<uint32_t *>(dst) = pack_bf16(o.x * inv, o.y * inv);
       } else {
-        *reinterpret_cast<float4 *>(part_o(a.ws, slot, RT, D) + x) = o;
-        if (dim == 0) part_ml(a.ws, 2 * gridDim.x, slot, RT, D)[row] = make_float2(row_m[row], row_l[row]);
+        *reinterpret_cast<float2 *>(part_o(a.ws, part, RT, D) + row * D + dim) = o;
+        if (dim == 0) part_ml(a.ws, 2 * gridDim.x, part, RT, D)[row] = make_float2(row_m[row], row_l[row]);
       }
     }
     fence_smem_to_async();  // before the next copies into what was written here
@@ -579,76 +687,125 @@ __global__ void __launch_bounds__(kThreads, 1) attn_few_kernel(const AttnArgs a,
   }
 }
 
-// Joins the parts of the unit in which boundary blockIdx.x + 1 between the blocks' ranges is the first:
-// o = sum 2^(m_p - m) o_p / sum 2^(m_p - m) l_p.
+// Joins the parts of the unit in which boundary blockIdx.x + 1 between the blocks' ranges is the first, for
+// row blockIdx.y of its tile:  o = sum 2^(m_p - m) o_p / sum 2^(m_p - m) l_p.  The threads stand side by side
+// over 4 columns each and over the parts.
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads) attn_few_join(const AttnArgs a, int least, int parts) {
-  constexpr int RT = 8 * NT;
-  const int i = blockIdx.x + 1;
-  const Located loc = locate(a, RT, i, parts, least, false);
+  constexpr int RT = 8 * NT, kCols = D / 4, kSide = kThreads / kCols;
+  __shared__ float4 sums[kSide][kCols];
+  __shared__ float side_l[kSide];
+  const int i = blockIdx.x + 1, row = blockIdx.y, col = threadIdx.x % kCols, side = threadIdx.x / kCols;
+  const Located loc = locate(a, RT, Geo<D, NT>::kSlab, i, parts, least, false);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results are written (no block ends before that)
   if (loc.b < 0) return;
-  const SeqLen q = seq_len(a, loc.b, RT);
-  const int unit = (int)(loc.in_seq / q.slabs), slab = (int)(loc.in_seq % q.slabs);
+  const SeqLen q = seq_len(a, loc.b, RT, Geo<D, NT>::kSlab);
+  const int unit = quotient(loc.in_seq, q.slabs), slab = (int)(loc.in_seq - (long long)unit * q.slabs);
   if (slab == 0 || slab > loc.share) return;  // between two units, or not the first boundary inside
   const int c1 = (int)((loc.share * i - slab + q.slabs - 1) / loc.share);
-  const int hk = unit / q.tiles, first = unit % q.tiles * RT, count = min(RT, q.s.n * a.r - first);
-  for (int x = threadIdx.x * 4; x < count * D; x += kThreads * 4) {
-    const int row = x / D, dim = x % D, rr = first + row;
-    float m = -INFINITY;
-    for (int c = i - 1; c <= c1; ++c) m = fmaxf(m, part_ml(a.ws, 2 * parts, 2 * c + (c == i - 1 ? 1 : 0), RT, D)[row].x);
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = i - 1; c <= c1; ++c) {
-      const int slot = 2 * c + (c == i - 1 ? 1 : 0);
-      const float2 ml = part_ml(a.ws, 2 * parts, slot, RT, D)[row];
-      const float4 v = *reinterpret_cast<const float4 *>(part_o(a.ws, slot, RT, D) + x);
-      const float w = exp2f(ml.x - base);
-      l += w * ml.y;
-      o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
+  const int hk = unit / q.tiles, first = unit % q.tiles * RT, rr = first + row;
+  if (rr >= q.s.n * a.r) return;
+  const auto slot_of = [&](int c) { return 2 * c + (c == i - 1 ? 1 : 0); };
+  float m = kNone, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  // Each side with a maximum of its own; 4 parts' loads in flight.
+#pragma unroll 1
+  for (int c = i - 1 + side; c <= c1; c += 4 * kSide) {
+    float2 ml[4];
+    float4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int cu = c + u * kSide;
+      ml[u] = make_float2(kNone, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (cu <= c1) {
+        ml[u] = part_ml(a.ws, 2 * parts, slot_of(cu), RT, D)[row];
+        v[u] = *reinterpret_cast<const float4 *>(part_o(a.ws, slot_of(cu), RT, D) + row * D + 4 * col);
+      }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.o) + (long long)(q.s.row0 + rr / a.r) * a.ldo +
-                               (long long)(hk * a.r + rr % a.r) * D + dim;
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) mn = fmaxf(mn, ml[u].x);
+    const float w0 = ex2(m - mn);
+    l *= w0;
+    o.x *= w0, o.y *= w0, o.z *= w0, o.w *= w0;
+    m = mn;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float w = ex2(ml[u].x - mn);
+      l += w * ml[u].y;
+      o.x += w * v[u].x, o.y += w * v[u].y, o.z += w * v[u].z, o.w += w * v[u].w;
+    }
   }
+  __shared__ float side_m[kSide];
+  if (col == 0) side_m[side] = m;
+  __syncthreads();
+  float top = kNone;
+#pragma unroll
+  for (int u = 0; u < kSide; ++u) top = fmaxf(top, side_m[u]);
+  const float w = ex2(m - top);
+  sums[side][col] = make_float4(o.x * w, o.y * w, o.z * w, o.w * w);
+  if (col == 0) side_l[side] = l * w;
+  __syncthreads();
+  if (side != 0) return;
+  float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
+  float ls = 0.f;
+#pragma unroll
+  for (int u = 0; u < kSide; ++u) {
+    const float4 v = sums[u][col];
+    all.x += v.x, all.y += v.y, all.z += v.z, all.w += v.w;
+    ls += side_l[u];
+  }
+  const float inv = ls == 0.f ? 0.f : 1.f / ls;
+  __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.o) + (long long)(q.s.row0 + rr / a.r) * a.ldo +
+                             (long long)(hk * a.r + rr % a.r) * D + 4 * col;
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(all.x * inv, all.y * inv), pack_bf16(all.z * inv, all.w * inv));
 }
 
 template <int D, int NT>
 struct FewTag {};
 
-constexpr int kLeast = 8;  // slabs of a block's range: one per warp
+constexpr int kLeast = kWarps;  // slabs of a block's range: one per warp
 
 template <int D, int NT>
 cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t s) {
-  cudaError_t e = allow_smem<FewTag<D, NT>>(attn_few_kernel<D, NT>, Smem<D, NT>::kBytes);
+  cudaError_t e = allow_smem<FewTag<D, NT>>(attn_few_kernel<D, NT>, Geo<D, NT>::kBytes);
   if (e != cudaSuccess) return e;
-  attn_few_kernel<D, NT><<<num_sms, kThreads, Smem<D, NT>::kBytes, s>>>(a, kLeast);
+  const int blocks = kBlocksSM * num_sms;
+  attn_few_kernel<D, NT><<<blocks, kThreads, Geo<D, NT>::kBytes, s>>>(a, kLeast);
   e = cudaGetLastError();
-  if (e != cudaSuccess || !a.ws || num_sms < 2) return e;
-  attn_few_join<D, NT><<<num_sms - 1, kThreads, 0, s>>>(a, kLeast, num_sms);
-  return cudaGetLastError();
+  if (e != cudaSuccess || !a.ws) return e;
+  // The join comes up while the last pieces end, and waits for them.
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks - 1, 8 * NT);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attn_few_join<D, NT>, a, kLeast, blocks);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace
 
 int attn_few_rows(int D, long long rows) {
-  const int most = 4096 / D;
+  const int most = D == 256 ? 16 : 32;
   for (int t = 8; t <= most; t *= 2)
     if (rows <= t) return t;
   return 0;
 }
 
-size_t attn_few_ws_bytes(int D, int rows_tile, int num_sms) { return (size_t)2 * num_sms * rows_tile * (D + 2) * sizeof(float); }
+size_t attn_few_ws_bytes(int D, int rows_tile, int num_sms) { return (size_t)2 * kBlocksSM * num_sms * rows_tile * (D + 2) * sizeof(float); }
 
 cudaError_t launch_attn_few(const AttnArgs &a, int rows_tile, int num_sms, cudaStream_t s) {
   const int nt = rows_tile / 8;
   switch (a.cache.D) {
     case 256: return nt == 1 ? launch<256, 1>(a, num_sms, s) : launch<256, 2>(a, num_sms, s);
     case 128: return nt == 1 ? launch<128, 1>(a, num_sms, s) : nt == 2 ? launch<128, 2>(a, num_sms, s) : launch<128, 4>(a, num_sms, s);
-    default:
-      return nt == 1 ? launch<64, 1>(a, num_sms, s) : nt == 2 ? launch<64, 2>(a, num_sms, s)
-             : nt == 4 ? launch<64, 4>(a, num_sms, s) : launch<64, 8>(a, num_sms, s);
+    default: return nt == 1 ? launch<64, 1>(a, num_sms, s) : nt == 2 ? launch<64, 2>(a, num_sms, s) : launch<64, 4>(a, num_sms, s);
   }
 }
 
