@@ -21,6 +21,8 @@
 // row, an equal range of them to each block.  A unit (sequence, key head, row
 // tile) that lies in several ranges leaves partial results, which a second
 // launch joins.
+#include <algorithm>
+
 #include "cache_device.cuh"
 #include "tma_host.h"
 #include "umma.cuh"
@@ -94,13 +96,13 @@ __device__ __forceinline__ long long warp_sum_incl(long long v, int lane) {
 
 // The length of all the work, and where position pos = index * share lies;
 // for the whole block.  share: an equal part for each of `parts`, `least` at
-// least; whole != 0: a unit counts as one slab.
+// least; whole != 0: a unit counts as one slab.  of >= 0: in_seq is where sequence `of` starts instead.
 struct Located {
   long long total, share;
   int b;              // sequence at pos, -1: none
   long long in_seq;   // position there
 };
-__device__ Located locate(const AttnArgs &a, int rows_tile, int slab, int index, int parts, int least, bool whole) {
+__device__ Located locate(const AttnArgs &a, int rows_tile, int slab, int index, int parts, int least, bool whole, int of = -1) {
   __shared__ long long sums[kWarps], base;
   __shared__ int bad, at_b;
   __shared__ long long at_in;
@@ -144,6 +146,24 @@ __device__ Located locate(const AttnArgs &a, int rows_tile, int slab, int index,
   }
   r.share = max(div_up(r.total, parts), (long long)least);
   const long long pos = r.share * index;
+  if (of >= 0) {
+    long long lower = 0;  // before sequence `of`
+    if (one && tid == of) at_in = before;
+    if (!one) {
+      for (int b = tid; b < of; b += kThreads) lower += len_of(b);
+      lower = warp_sum_incl(lower, lane);
+      __syncthreads();
+      if (lane == 31) sums[warp] = lower;
+    }
+    __syncthreads();
+    r.b = of;
+    if (one) {
+      r.in_seq = at_in;
+    } else {
+      for (int w = 0; w < kWarps; ++w) r.in_seq += sums[w];
+    }
+    return r;
+  }
   if (pos >= r.total) return r;
   if (one) {
     if (pos >= before && pos < before + mine) {
@@ -234,45 +254,57 @@ struct RowAt {
   int head;
 };
 
-// q of a row tile as mma operands: element (row n, dim 64 c + 16 t + 4 s + e) is in k step 4 c + s, lane 4 (n % 8) + t,
+// A warp's rows of q, n = warp + kWarps i: 4 elements to a lane, 128 apart.
+template <int D, int NT>
+struct QRows {
+  static constexpr int kOf = 8 * NT / kWarps, kParts = D == 256 ? 2 : 1;
+  uint2 w[kOf][kParts];
+};
+template <int D, int NT>
+__device__ __forceinline__ void fetch_q(const AttnArgs &a, const Seq &s, int hk, int first, int count, QRows<D, NT> &q) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < QRows<D, NT>::kOf; ++i) {
+    const int n = warp + kWarps * i, rr = first + n, tok = rr / a.r;
+    const __nv_bfloat16 *const src =
+        static_cast<const __nv_bfloat16 *>(a.q) + (s.row0 + (long long)tok) * a.ldq + (hk * a.r + rr - tok * a.r) * D + 4 * lane;
+#pragma unroll
+    for (int u = 0; u < QRows<D, NT>::kParts; ++u)
+      q.w[i][u] = n < count && 4 * lane < D ? *reinterpret_cast<const uint2 *>(src + 128 * u) : make_uint2(0, 0);
+  }
+}
+// q as mma operands: element (row n, dim 64 c + 16 t + 4 s + e) is in k step 4 c + s, lane 4 (n % 8) + t,
 // times a power of two that brings the row's largest into [2^14, 2^15).
 template <int D, int NT>
-__device__ __forceinline__ void load_q(const AttnArgs &a, int count, const RowAt *at_row, uint8_t *sq, float *qscale) {
+__device__ __forceinline__ void store_q(const AttnArgs &a, const QRows<D, NT> &q, uint8_t *sq, float *qscale) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll 2
-  for (int n = warp; n < 8 * NT; n += kWarps) {
-    const bool real = n < count;
-    const __nv_bfloat16 *const src = static_cast<const __nv_bfloat16 *>(a.q) + (real ? at_row[n].token * a.ldq + at_row[n].head * D : 0);
-    constexpr int G = D / 4;  // groups of 4 elements
-    float2 x[(G + 31) / 32][2];
-    float top = 0.f;
-    bool bad = false;
+  constexpr int kOf = QRows<D, NT>::kOf, kParts = QRows<D, NT>::kParts;
+  uint32_t top[kOf];  // bits of the largest size: those of NaN are above infinity's
 #pragma unroll
-    for (int i = 0; i < (G + 31) / 32; ++i) {
-      const int gr = lane + 32 * i;
-      uint2 w = make_uint2(0, 0);
-      if (real && gr < G) w = *reinterpret_cast<const uint2 *>(src + 4 * gr);
-      x[i][0] = unpack_bf16(w.x);
-      x[i][1] = unpack_bf16(w.y);
+  for (int i = 0; i < kOf; ++i) {
+    top[i] = 0;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        top = fmaxf(top, fmaxf(fabsf(x[i][u].x), fabsf(x[i][u].y)));
-        bad |= !(fabsf(x[i][u].x) < INFINITY) || !(fabsf(x[i][u].y) < INFINITY);
-      }
+    for (int u = 0; u < kParts; ++u) {
+      const uint32_t x = q.w[i][u].x & 0x7fff7fffu, y = q.w[i][u].y & 0x7fff7fffu;
+      top[i] = max(top[i], max(max(x & 0xffffu, x >> 16), max(y & 0xffffu, y >> 16)));
     }
+  }
 #pragma unroll
-    for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    bad = __any_sync(0xffffffffu, bad);
-    const int e = top > 0.f && !bad ? min(14 - ((int)(__float_as_uint(top) >> 23) - 127), 120) : 0;
+  for (int i = 0; i < kOf; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
+#pragma unroll
+  for (int i = 0; i < kOf; ++i) {
+    const int n = warp + kWarps * i;
+    const bool bad = top[i] >= 0x7f80u;
+    const int e = top[i] > 0 && !bad ? min(14 - ((int)(top[i] >> 7) - 127), 120) : 0;
     const float up = bad ? __int_as_float(0x7fc00000) : __uint_as_float((uint32_t)(e + 127) << 23);
 #pragma unroll
-    for (int i = 0; i < (G + 31) / 32; ++i) {
-      const int gr = lane + 32 * i;
-      if (gr >= G) break;
+    for (int u = 0; u < kParts; ++u) {
+      const int gr = lane + 32 * u;  // group of 4 elements
+      if (4 * lane >= D) break;
       const int kstep = (gr >> 4) * 4 + (gr & 3), t = (gr >> 2) & 3;
       const uint32_t at = ((kstep * NT + (n >> 3)) * 32 + (n & 7) * 4 + t) * 8;
-      *reinterpret_cast<uint2 *>(sq + at) =
-          make_uint2(pack2_sat(x[i][0].x * up, x[i][0].y * up), pack2_sat(x[i][1].x * up, x[i][1].y * up));
+      const float2 x = unpack_bf16(q.w[i][u].x), y = unpack_bf16(q.w[i][u].y);
+      *reinterpret_cast<uint2 *>(sq + at) = make_uint2(pack2_sat(x.x * up, x.y * up), pack2_sat(y.x * up, y.y * up));
     }
     if (lane == 0) qscale[n] = __uint_as_float((uint32_t)(127 - e) << 23) * (a.scale * kLog2e);
   }
@@ -342,8 +374,16 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
     };
     int pg[2];
     float2 sc[2];
+    QRows<D, NT> rows;
     pg[0] = load_page(lane);
     pg[1] = load_page(lane + 32);
+    fetch_q<D, NT>(a, q.s, hk, first, count, rows);  // ahead of the copies, which would hold it up
+    if (tid < RT) {
+      const int rr = first + tid, tok = rr / a.r;
+      at_row[tid] = RowAt{(long long)q.s.row0 + tok, hk * a.r + rr - tok * a.r};
+    }
+    sc[0] = load_scales(pg[0]);
+    sc[1] = load_scales(pg[1]);
     // Lane 8 sub + 0 .. 3 copies 4 tokens each of 16 tokens' k, 4 .. 7 of their v.  What has no page is copied
     // from page 0 and not looked at.
     const uint8_t *const copy_src = (lane & 4 ? c.v : c.k) + ((long long)hk * page + 4 * (lane & 3)) * D;
@@ -364,14 +404,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
       issue(i, __shfl_sync(0xffffffffu, pg[0], (i * SUB + (lane >> 3)) & 31), in_slot);
       in_slot = in_slot + 1 == G::kDepth ? 0 : in_slot + 1;
     }
-    if (tid < RT) {
-      const int rr = first + tid, tok = rr / a.r;
-      at_row[tid] = RowAt{(long long)q.s.row0 + tok, hk * a.r + rr - tok * a.r};
-    }
-    sc[0] = load_scales(pg[0]);
-    sc[1] = load_scales(pg[1]);
-    __syncthreads();
-    load_q<D, NT>(a, count, at_row, sq, qscale);
+    store_q<D, NT>(a, rows, sq, qscale);
     __syncthreads();
 
     constexpr bool kQRegs = D * NT <= 256;
@@ -661,6 +694,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
       }
     __syncthreads();
     const int part = 2 * blockIdx.x + (starts ? 1 : 0);
+#pragma unroll 4
     for (int x = tid; x < count * (D / 2); x += kThreads) {
       const int row = x / (D / 2), dim = x % (D / 2) * 2;
       const int at = D >= 128 ? merge_at<D>((dim >> 4) & 7, (dim >> 7) * 8 + ((dim >> 1) & 7)) : dim;
@@ -687,30 +721,50 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
   }
 }
 
-// Joins the parts of the unit in which boundary blockIdx.x + 1 between the blocks' ranges is the first, for
-// row blockIdx.y of its tile:  o = sum 2^(m_p - m) o_p / sum 2^(m_p - m) l_p.  The threads stand side by side
-// over 4 columns each and over the parts.
+// Joins a unit's parts:  o = sum 2^(m_p - m) o_p / sum 2^(m_p - m) l_p.  by_unit: block x takes unit x (of
+// tiles_max Hk to a sequence); else the unit in which boundary x + 1 between the blocks' ranges is the first.
+// Rows of its tile over blockIdx.y; the threads stand side by side over 4 columns each and over the parts.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) attn_few_join(const AttnArgs a, int least, int parts) {
-  constexpr int RT = 8 * NT, kCols = D / 4, kSide = kThreads / kCols;
+__global__ void __launch_bounds__(kThreads) attn_few_join(const AttnArgs a, int least, int parts, int tiles_max, int by_unit) {
+  constexpr int RT = 8 * NT, kCols = D / 4, kSide = kThreads / kCols, kSlab = Geo<D, NT>::kSlab;
   __shared__ float4 sums[kSide][kCols];
-  __shared__ float side_l[kSide];
-  const int i = blockIdx.x + 1, row = blockIdx.y, col = threadIdx.x % kCols, side = threadIdx.x / kCols;
-  const Located loc = locate(a, RT, Geo<D, NT>::kSlab, i, parts, least, false);
+  __shared__ float side_l[kSide], side_m[kSide];
+  const int col = threadIdx.x % kCols, side = threadIdx.x / kCols;
+  SeqLen q{};
+  long long start = 0, share = 0;  // of the unit, in slabs; a block's range
+  int unit = 0;
+  if (by_unit) {
+    const int per = tiles_max * a.cache.Hk, b = blockIdx.x / per, x = blockIdx.x % per;
+    const Located loc = locate(a, RT, kSlab, 0, parts, least, false, b);
+    q = seq_len(a, b, RT, kSlab);
+    const int hk = x / tiles_max, tile = x % tiles_max;
+    unit = hk * q.tiles + tile;
+    share = loc.share;
+    start = loc.in_seq + (long long)unit * q.slabs;
+    if (loc.total == 0 || q.len == 0 || tile >= q.tiles) share = 0;
+  } else {
+    const Located loc = locate(a, RT, kSlab, blockIdx.x + 1, parts, least, false);
+    if (loc.b >= 0) {
+      q = seq_len(a, loc.b, RT, kSlab);
+      unit = quotient(loc.in_seq, q.slabs);
+      const int slab = (int)(loc.in_seq - (long long)unit * q.slabs);
+      if (slab > 0 && slab <= loc.share) share = loc.share;  // else between two units, or not the first boundary inside
+      start = loc.share * (blockIdx.x + 1) - slab;
+    }
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial results are written (no block ends before that)
-  if (loc.b < 0) return;
-  const SeqLen q = seq_len(a, loc.b, RT, Geo<D, NT>::kSlab);
-  const int unit = quotient(loc.in_seq, q.slabs), slab = (int)(loc.in_seq - (long long)unit * q.slabs);
-  if (slab == 0 || slab > loc.share) return;  // between two units, or not the first boundary inside
-  const int c1 = (int)((loc.share * i - slab + q.slabs - 1) / loc.share);
-  const int hk = unit / q.tiles, first = unit % q.tiles * RT, rr = first + row;
-  if (rr >= q.s.n * a.r) return;
-  const auto slot_of = [&](int c) { return 2 * c + (c == i - 1 ? 1 : 0); };
+  if (share == 0) return;
+  const int c0 = quotient(start, (int)share), c1 = quotient(start + q.slabs - 1, (int)share);
+  if (c0 == c1) return;  // in one range: written already
+  const int hk = unit / q.tiles, first = unit % q.tiles * RT, rows = min(RT, q.s.n * a.r - first);
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+  const int rr = first + row;
+  const auto slot_of = [&](int c) { return 2 * c + (c == c0 ? 1 : 0); };  // its first part starts it
   float m = kNone, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   // Each side with a maximum of its own; 4 parts' loads in flight.
 #pragma unroll 1
-  for (int c = i - 1 + side; c <= c1; c += 4 * kSide) {
+  for (int c = c0 + side; c <= c1; c += 4 * kSide) {
     float2 ml[4];
     float4 v[4];
 #pragma unroll
@@ -737,7 +791,6 @@ __global__ void __launch_bounds__(kThreads) attn_few_join(const AttnArgs a, int 
       o.x += w * v[u].x, o.y += w * v[u].y, o.z += w * v[u].z, o.w += w * v[u].w;
     }
   }
-  __shared__ float side_m[kSide];
   if (col == 0) side_m[side] = m;
   __syncthreads();
   float top = kNone;
@@ -747,19 +800,22 @@ __global__ void __launch_bounds__(kThreads) attn_few_join(const AttnArgs a, int 
   sums[side][col] = make_float4(o.x * w, o.y * w, o.z * w, o.w * w);
   if (col == 0) side_l[side] = l * w;
   __syncthreads();
-  if (side != 0) return;
-  float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
-  float ls = 0.f;
+  if (side == 0) {
+    float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
+    float ls = 0.f;
 #pragma unroll
-  for (int u = 0; u < kSide; ++u) {
-    const float4 v = sums[u][col];
-    all.x += v.x, all.y += v.y, all.z += v.z, all.w += v.w;
-    ls += side_l[u];
+    for (int u = 0; u < kSide; ++u) {
+      const float4 v = sums[u][col];
+      all.x += v.x, all.y += v.y, all.z += v.z, all.w += v.w;
+      ls += side_l[u];
+    }
+    const float inv = ls == 0.f ? 0.f : 1.f / ls;
+    __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.o) + (long long)(q.s.row0 + rr / a.r) * a.ldo +
+                               (long long)(hk * a.r + rr % a.r) * D + 4 * col;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(all.x * inv, all.y * inv), pack_bf16(all.z * inv, all.w * inv));
   }
-  const float inv = ls == 0.f ? 0.f : 1.f / ls;
-  __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.o) + (long long)(q.s.row0 + rr / a.r) * a.ldo +
-                             (long long)(hk * a.r + rr % a.r) * D + 4 * col;
-  *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(all.x * inv, all.y * inv), pack_bf16(all.z * inv, all.w * inv));
+  __syncthreads();
+  }
 }
 
 template <int D, int NT>
@@ -777,7 +833,12 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t s) {
   if (e != cudaSuccess || !a.ws) return e;
   // The join comes up while the last pieces end, and waits for them.
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks - 1, 8 * NT);
+  const int tiles_max = (int)(((long long)a.seq.max_new * a.r + 8 * NT - 1) / (8 * NT));
+  const long long units = (long long)a.seq.B * tiles_max * a.cache.Hk;
+  const int by_unit = units < blocks;
+  // rows of a tile side by side, as many as are all up at once
+  cfg.gridDim = dim3(by_unit ? (unsigned)units : blocks - 1);
+  cfg.gridDim.y = std::max(1u, std::min(8u * NT, 8u * num_sms / cfg.gridDim.x));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr{};
@@ -785,7 +846,7 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_few_join<D, NT>, a, kLeast, blocks);
+  e = cudaLaunchKernelEx(&cfg, attn_few_join<D, NT>, a, kLeast, blocks, tiles_max, by_unit);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
