@@ -821,14 +821,17 @@ __global__ void __launch_bounds__(kThreads) attn_few_join(const AttnArgs a, int 
 template <int D, int NT>
 struct FewTag {};
 
-constexpr int kLeast = kWarps;  // slabs of a block's range: one per warp
+// Slabs of a block's range at least: one per warp, and 128 tokens (1 token over 4096, 4 heads of 256, in a graph:
+// 64 tokens 18.6 us, 128 16.3, 256 16.4, 512 19.3; heads of 64 and 128 lose with every slab beyond one per warp).
+template <int D, int NT>
+constexpr int kLeast = Geo<D, NT>::kSlab * kWarps >= 128 ? kWarps : 128 / Geo<D, NT>::kSlab;
 
 template <int D, int NT>
 cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t s) {
   cudaError_t e = allow_smem<FewTag<D, NT>>(attn_few_kernel<D, NT>, Geo<D, NT>::kBytes);
   if (e != cudaSuccess) return e;
   const int blocks = kBlocksSM * num_sms;
-  attn_few_kernel<D, NT><<<blocks, kThreads, Geo<D, NT>::kBytes, s>>>(a, kLeast);
+  attn_few_kernel<D, NT><<<blocks, kThreads, Geo<D, NT>::kBytes, s>>>(a, kLeast<D, NT>);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.ws) return e;
   // The join comes up while the last pieces end, and waits for them.
@@ -846,7 +849,7 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_few_join<D, NT>, a, kLeast, blocks, tiles_max, by_unit);
+  e = cudaLaunchKernelEx(&cfg, attn_few_join<D, NT>, a, kLeast<D, NT>, blocks, tiles_max, by_unit);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

@@ -73,16 +73,21 @@ gdn_status check_rows(const void *p, long long ld, long long width, size_t el) {
 
 // How a call of gdn_attn runs, and the workspace it makes use of.
 struct AttnPlan {
-  int few_rows;  // rows of a tile of attn_few.cu; 0: attn_rows.cu
+  int few_rows;  // rows of a tile of attn_few.cu, or 0
+  bool tile;     // attn_tile.cu; neither: attn_rows.cu
   int splits;    // attn_rows.cu: ranges of the tokens side by side
   size_t bytes;
 };
 AttnPlan attn_plan(const gdn_attn_shape *s, bool packed, long long rows, int max_kv, int sms) {
   const int r = s->Hq / s->Hk;
-  AttnPlan p{0, 1, 0};
+  AttnPlan p{0, false, 1, 0};
   if (s->io_dtype == GDN_BF16) p.few_rows = gdn::attn_few_rows(s->D, (long long)bound_new(s, packed) * r);
   if (p.few_rows) {
     p.bytes = gdn::attn_few_ws_bytes(s->D, p.few_rows, sms);
+    return p;
+  }
+  if (s->io_dtype == GDN_BF16) {
+    p.tile = true;
     return p;
   }
   // enough blocks to fill the GPU twice, none with less than 64 tokens
@@ -174,6 +179,7 @@ gdn_status gdn_attn(const gdn_attn_shape *shape, const gdn_attn_io *io, void *st
   }
   a.splits = plan.splits;
   const cudaError_t e = plan.few_rows ? gdn::launch_attn_few(a, plan.few_rows, dev.sms, (cudaStream_t)stream)
+                        : plan.tile   ? gdn::launch_attn_tile(a, (cudaStream_t)stream)
                                       : gdn::launch_attn_rows(a, shape->io_dtype == GDN_BF16, (cudaStream_t)stream);
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

@@ -253,6 +253,7 @@ cudaError_t launch_attn_rows(const AttnArgs &a, bool bf16, cudaStream_t s);
 int attn_few_rows(int D, long long rows);
 size_t attn_few_ws_bytes(int D, int rows_tile, int num_sms);
 cudaError_t launch_attn_few(const AttnArgs &a, int rows_tile, int num_sms, cudaStream_t s);
+cudaError_t launch_attn_tile(const AttnArgs &a, cudaStream_t s);  // bf16 io, many rows
 
 // Device error bits (the error word is OR-ed).
 constexpr unsigned int kErrTimeout = 1u;  // a bounded wait gave up
