@@ -13,9 +13,11 @@
 // so far, enters p as a term of the exponent, and leaves the row's sum again as a
 // factor on the page's part of it: no product per element.
 //
-// Warps: 0-3 softmax (thread = row), 4-7 values, 8 keys (TMA), 9 products.  For a
-// tile of 64 tokens and D = 256 the products take 1024 cycles, a row's 64
-// exponentials and what goes with them some 700.
+// Warps: 0-3 and 4-7 softmax (thread = row; even and odd tiles), 8-11 values, 12
+// keys (TMA), 13 products.  For a tile of 64 tokens and D = 256 the products take
+// 1024 cycles; a tile's way through one group of softmax warps is longer than
+// that, so that two take turns.  The running maximum goes from one to the other
+// as soon as it is known, ahead of the exponentials; each keeps a sum of its own.
 #include <algorithm>
 
 #include "cache_device.cuh"
@@ -30,12 +32,14 @@ using namespace umma;
 constexpr int kRows = 128;    // of a CTA
 constexpr int kTile = 64;     // tokens
 constexpr int kSubs = kTile / 16;
-constexpr int kThreads = 320;
+constexpr int kThreads = 448;
+constexpr int kValueWarp = 8, kKeyWarp = 12, kProductWarp = 13;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -1.7e38f;
 constexpr float kSlack = 4.f;   // p may reach 2^kSlack before the running maximum moves
 constexpr float kPExp = 11.f;   // p stands times 2^11 in fp16
 constexpr float kMinRatio = -60.f;
+constexpr float kNoRef = -200.f;  // the logarithm of the value scales where there is none above 0
 
 template <int D>
 struct Geo {
@@ -65,6 +69,30 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const __half2 t = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&t);
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t x, y, z, w;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(w) : "l"(x), "l"(y), "l"(z));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(w));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t x, y, w;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(w) : "l"(x), "l"(y));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(w));
+  return r;
+}
 __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w, int high) {
   uint32_t o;
   if (high)
@@ -76,20 +104,24 @@ __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w, int high) {
 
 struct Bars {
   uint64_t k_full[4], k_empty[4], v_full[2], v_empty[2], s_full[2], p_full[2];
+  uint64_t moved[2][4];  // the running maximum after a tile, per warp
 };
 
-// The 4 pages of a tile, one per lane 0-3 (others none): -1 where the tokens are not seen or the table has none.
+// Entries of the table for the 16 tokens `sub` of a tile.  ask() loads one (kUnseen: its tokens are not looked
+// at); a tile or two later page() says what it is worth, so that nothing waits for the load.
+constexpr int kUnseen = -0x40000000;
 struct TilePages {
   const CacheArgs &c;
   const int *table;
-  int seen, ntiles;
+  int seen;
   unsigned int *err;
-  __device__ __forceinline__ int operator()(int tile, int sub) const {
+  __device__ __forceinline__ int ask(int tile, int sub) const {
     const int tok = tile * kTile + sub * 16;
-    if (tile >= ntiles || tok >= seen) return -1;
-    const int p = table[tok >> c.page_shift];
-    if (p >= 0 && p < c.n_pages) return p;
-    atomicOr(err, kErrSeqlens);
+    return tok < seen ? table[tok >> c.page_shift] : kUnseen;
+  }
+  __device__ __forceinline__ int page(int entry) const {
+    if ((unsigned)entry < (unsigned)c.n_pages) return entry;
+    if (entry != kUnseen) atomicOr(err, kErrSeqlens);
     return -1;
   }
 };
@@ -101,6 +133,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
   __shared__ Bars bars;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int gave_up;
+  __shared__ float2 moved[2][kRows];  // running maximum and largest value scale after a tile, even and odd
+  __shared__ float2 other[2][kRows];  // maximum and sum of each group at the end
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const CacheArgs &c = a.cache;
   int local = 0;
@@ -125,10 +159,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
       bar_init(&bars.v_empty[i], 1);
       bar_init(&bars.s_full[i], 1);
       bar_init(&bars.p_full[i], 128);
+      for (int w = 0; w < 4; ++w) bar_init(&bars.moved[i][w], 32);
     }
     gave_up = 0;
   }
-  if (warp == 9) tmem_alloc(&tmem_slot, G::kCols);
+  if (warp == kProductWarp) tmem_alloc(&tmem_slot, G::kCols);
   fence_before();
   __syncthreads();
   fence_after();
@@ -143,22 +178,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
         atomicOr(a.seq.err, kErrTimeout);
       }
   };
-  const TilePages pages{c, c.table + (long long)s.b * c.table_ld, seen, ntiles, a.seq.err};
+  const TilePages pages{c, c.table + (long long)s.b * c.table_ld, seen, a.seq.err};
   const int page = 1 << c.page_shift;
 
-  if (warp < 4) {
+  if (warp < kValueWarp) {
     // ---------------------------------------------------------------- softmax
-    const int row = tid, rr = first + row, tok = rr / a.r;
+    const int group = warp >> 2, quarter = warp & 3, row = tid & (kRows - 1), rr = first + row, tok = rr / a.r;
     const bool real = row < count;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-    // q as hi + lo, times a power of two that brings the row's largest into [2^7, 2^8)
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    // q as hi + lo, times a power of two that brings the row's largest into [2^7, 2^8); half the columns to a group
     const __nv_bfloat16 *const src = static_cast<const __nv_bfloat16 *>(a.q) + (s.row0 + (long long)tok) * a.ldq +
                                      (long long)(hk * a.r + rr - tok * a.r) * D;
-    const float sign = a.scale < 0.f ? -1.f : 1.f;
     float f;  // on a score, without its page's scale
     {
       uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll 8
       for (int d = 0; d < D; d += 8) {
         const uint4 w = real ? *reinterpret_cast<const uint4 *>(src + d) : make_uint4(0, 0, 0, 0);
         const uint32_t x[4] = {w.x & 0x7fff7fffu, w.y & 0x7fff7fffu, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu};
@@ -167,13 +201,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
       }
       const bool bad = top >= 0x7f80u;
       const int e = top > 0 && !bad ? min(7 - ((int)(top >> 7) - 127), 120) : 0;
-      const float up = sign * __uint_as_float((uint32_t)(e + 127) << 23);
+      const float up = (a.scale < 0.f ? -1.f : 1.f) * __uint_as_float((uint32_t)(e + 127) << 23);
       f = bad ? __int_as_float(0x7fc00000) : __uint_as_float((uint32_t)(127 - e) << 23) * (fabsf(a.scale) * kLog2e);
 #pragma unroll 1
-      for (int d = 0; d < D; d += 64) {
-        uint32_t hi[16], lo[16];
+      for (int d = group * (D / 2); d < (group + 1) * (D / 2); d += 32) {
+        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
           const uint4 w = real && !bad ? *reinterpret_cast<const uint4 *>(src + d + 8 * i) : make_uint4(0, 0, 0, 0);
           const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -187,45 +221,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
           }
         }
         __syncwarp();
-        tmem_st16w_nw(lanes + G::kQ + d / 4, hi);
-        tmem_st16w_nw(lanes + G::kQ + D / 4 + d / 4, lo);
+        tmem_st8w_nw(lanes + G::kQ + d / 4, hi);
+        tmem_st8w_nw(lanes + G::kQ + D / 4 + d / 4, lo);
       }
       tmem_wait_st();
     }
     fence_before();
     __syncwarp();
-    asm volatile("bar.sync 1, 160;" ::: "memory");  // with the products' warp: Q is in place
+    asm volatile("bar.sync 1, 288;" ::: "memory");  // with the products' warp: Q is in place
     const int last = !real ? -1 : a.causal ? s.kv - s.n + tok : s.kv - 1;
     const int all_see = a.causal ? s.kv - s.n + first / a.r : s.kv - 1;
-    float m = kNone, l = 0.f, ref = 0.f;
-    int pg = pages(0, lane & 3), pg_next = pages(1, lane & 3);
+    float m = kNone, l = 0.f, lref = kNoRef;  // m: what l is relative to; the largest value scale's logarithm
+    // Lane u of four has page u of a tile: its key scale, and its value scale's logarithm.
     auto scales = [&](int p) {
       if (p < 0) return make_float2(0.f, 0.f);
       const long long at = (long long)p * c.Hk + hk;
       return make_float2(c.ks[at], c.vs[at]);
     };
+    int pg = pages.page(pages.ask(group, lane & 3)), entry = pages.ask(group + 2, lane & 3);
     float2 sc = scales(pg);
 #pragma unroll 1
-    for (int j = 0; j < ntiles; ++j) {
-      const float2 now = sc;
+    for (int j = group; j < ntiles; j += 2) {
+      const float ks = sc.x, lvs = fmaxf(__log2f(sc.y), kNoRef);  // fmaxf: of 0, and of a NaN, which `odd` looks after
       const uint32_t gone = __ballot_sync(0xffffffffu, pg < 0) & ((1u << kSubs) - 1);
-      pg = pg_next;
+      const uint32_t no_v = __ballot_sync(0xffffffffu, sc.y != sc.y) & ((1u << kSubs) - 1);
+      pg = pages.page(entry);
+      entry = pages.ask(j + 4, lane & 3);
       sc = scales(pg);
-      pg_next = pages(j + 2, lane & 3);
-      float fs[kSubs], vs[kSubs], vtop = 0.f;
+      float fs[kSubs], ltop = lvs;
 #pragma unroll
-      for (int u = 0; u < kSubs; ++u) {
-        fs[u] = f * __shfl_sync(0xffffffffu, now.x, u);
-        vs[u] = __shfl_sync(0xffffffffu, now.y, u);
-        vtop = fmaxf(vtop, vs[u]);
-      }
-      const int buf = j & 1;
-      wait(&bars.s_full[buf], (j >> 1) & 1);
+      for (int u = 0; u < kSubs; ++u) fs[u] = f * __shfl_sync(0xffffffffu, ks, u);
+      ltop = fmaxf(ltop, __shfl_xor_sync(0xffffffffu, ltop, 1));
+      ltop = fmaxf(ltop, __shfl_xor_sync(0xffffffffu, ltop, 2));
+      wait(&bars.s_full[group], (j >> 1) & 1);
       __syncwarp();
       fence_after();
       uint32_t x0[32], x1[32];
-      tmem_ld32_nw(lanes + G::kS + buf * kTile, x0);
-      tmem_ld32_nw(lanes + G::kS + buf * kTile + 32, x1);
+      tmem_ld32_nw(lanes + G::kS + group * kTile, x0);
+      tmem_ld32_nw(lanes + G::kS + group * kTile + 32, x1);
       tmem_wait_ld();
       float y[kTile];
 #pragma unroll
@@ -234,32 +267,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
         y[32 + i] = __uint_as_float(x1[i]);
       }
       const int tok0 = j * kTile;
-      const bool masked = gone != 0 || tok0 + kTile - 1 > all_see;
-      if (masked) {  // scores in full, so that a scale (NaN, 0) does not bring back what is not seen
+      if ((gone | no_v) != 0 || tok0 + kTile - 1 > all_see) {
+        // Some row does not see all, or some value scale is NaN: here the scores get their scales, so that a scale
+        // (NaN, 0) does not bring back what is not seen, and a NaN value scale reaches what is.
 #pragma unroll
-        for (int i = 0; i < kTile; ++i)
-          y[i] = tok0 + i <= last && !(gone >> (i / 16) & 1) ? y[i] * fs[i / 16] : -INFINITY;
+        for (int i = 0; i < kTile; ++i) {
+          const float x = (no_v >> (i / 16)) & 1 ? __int_as_float(0x7fc00000) : y[i] * fs[i / 16];
+          y[i] = tok0 + i <= last && !(gone >> (i / 16) & 1) ? x : -INFINITY;
+        }
 #pragma unroll
         for (int u = 0; u < kSubs; ++u) fs[u] = 1.f;
       }
       float top = -INFINITY;
 #pragma unroll
       for (int u = 0; u < kSubs; ++u) {
-        float t = y[16 * u];
+        float t0 = fmaxf(y[16 * u], y[16 * u + 1]), t1 = fmaxf(y[16 * u + 2], y[16 * u + 3]);
 #pragma unroll
-        for (int i = 1; i < 16; ++i) t = fmaxf(t, y[16 * u + i]);
-        top = fmaxf(top, t * fs[u]);
-      }
-      if (__any_sync(0xffffffffu, top > m + kSlack || vtop > ref)) {
-        float shrink = 1.f;
-        if (vtop > ref) {
-          shrink = ref / vtop;
-          ref = vtop;
+        for (int i = 4; i < 16; i += 4) {
+          t0 = fmaxf(fmaxf(t0, y[16 * u + i]), y[16 * u + i + 1]);
+          t1 = fmaxf(fmaxf(t1, y[16 * u + i + 2]), y[16 * u + i + 3]);
         }
-        const float mn = fmaxf(m, top), al = ex2(m - mn);
-        m = mn;
-        l *= al;
-        shrink *= al;
+        top = fmaxf(top, fmaxf(t0, t1) * fs[u]);
+      }
+      // the other group's word on the tile before
+      float mc = kNone;
+      if (j > 0) {
+        wait(&bars.moved[group ^ 1][quarter], ((j - 1) >> 1) & 1);
+        const float2 x = moved[group ^ 1][row];
+        mc = x.x;
+        lref = x.y;
+      }
+      if (__any_sync(0xffffffffu, top > mc + kSlack || ltop > lref)) {
+        const float mn = fmaxf(mc, top), ln = fmaxf(lref, ltop), shrink = ex2(mc - mn + (lref - ln));
+        mc = mn;
+        lref = ln;
         if (j > 0) {
           wait(&bars.v_empty[(j - 1) % G::kVStages], ((j - 1) / G::kVStages) & 1);  // the products so far are in O
           __syncwarp();
@@ -275,45 +316,53 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
           }
         }
       }
+      moved[group][row] = make_float2(mc, lref);
+      bar_arrive(&bars.moved[group][quarter]);
+      l *= ex2(m - mc);
+      m = mc;
+      // the value scale over the largest, in the exponent
+      const float lr = fmaxf(lvs - lref, kMinRatio), back = ex2(-lr - kPExp), base = kPExp - m;
       uint32_t p[kTile / 2];
 #pragma unroll
       for (int u = 0; u < kSubs; ++u) {
-        if (masked && (tok0 + 16 * u > last || (gone >> u & 1))) {  // nothing seen, whatever the scales are
-#pragma unroll
-          for (int i = 0; i < 8; ++i) p[8 * u + i] = 0;
-          continue;
-        }
-        // the value scale over the largest, in the exponent (a NaN goes on)
-        const float ratio = ref > 0.f ? vs[u] / ref : vs[u] * 0.f;
-        const float lr = ratio < 0x1p-60f ? kMinRatio : __log2f(ratio), shift = lr + kPExp - m;
-        float sum = 0.f;
+        const float shift = __shfl_sync(0xffffffffu, lr, u) + base, undo = __shfl_sync(0xffffffffu, back, u);
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-          float p0 = ex2(fmaf(y[16 * u + i], fs[u], shift)), p1 = ex2(fmaf(y[16 * u + i + 1], fs[u], shift));
-          if (masked) {
-            if (tok0 + 16 * u + i > last) p0 = 0.f;
-            if (tok0 + 16 * u + i + 1 > last) p1 = 0.f;
-          }
-          sum += p0 + p1;
-          p[8 * u + i / 2] = pack2_sat(p0, p1);
+          float2 e = fma2(make_float2(y[16 * u + i], y[16 * u + i + 1]), make_float2(fs[u], fs[u]), make_float2(shift, shift));
+          e.x = ex2(e.x);
+          e.y = ex2(e.y);
+          sum = add2(sum, e);
+          p[8 * u + i / 2] = pack2(e.x, e.y);
         }
-        l = fmaf(sum, ex2(-lr - kPExp), l);
+        l = fmaf(sum.x + sum.y, undo, l);
       }
       __syncwarp();
-      tmem_st32w_nw(lanes + G::kS + buf * kTile, p);
+      tmem_st32w_nw(lanes + G::kS + group * kTile, p);
       tmem_wait_st();
       fence_before();
-      bar_arrive(&bars.p_full[buf]);
+      bar_arrive(&bars.p_full[group]);
     }
-    // ---- out
+    // ---- out: the groups' sums together, half the columns to each
+    if (ntiles > 0) {
+      const int g_last = (ntiles - 1) & 1;
+      wait(&bars.moved[g_last][quarter], ((ntiles - 1) >> 1) & 1);
+      const float2 x = moved[g_last][row];
+      l *= ex2(m - x.x);
+      m = x.x;
+      lref = x.y;
+    }
+    other[group][row] = make_float2(m, l);
+    asm volatile("bar.sync 2, 256;" ::: "memory");
+    l += other[group ^ 1][row].y;
     if (ntiles > 0) wait(&bars.v_empty[(ntiles - 1) % G::kVStages], ((ntiles - 1) / G::kVStages) & 1);
     __syncwarp();
     fence_after();
-    const float inv = l == 0.f ? 0.f : (ref * ex2(-kPExp)) / l;
+    const float inv = l == 0.f ? 0.f : ex2(lref - kPExp) / l;
     __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.o) + (s.row0 + (long long)tok) * a.ldo +
                                (long long)(hk * a.r + rr - tok * a.r) * D;
 #pragma unroll 1
-    for (int d = 0; d < D; d += 32) {
+    for (int d = group * (D / 2); d < (group + 1) * (D / 2); d += 32) {
       uint32_t w[32];
       __syncwarp();
       tmem_ld32_nw(lanes + G::kO + d, w);
@@ -330,10 +379,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
       }
     }
     fence_before();
-  } else if (warp < 8) {
+  } else if (warp < kKeyWarp) {
     // ----------------------------------------------------------------- values
     // 16 tokens to a warp: lane / 4 (and 8 more), 16 dimensions at lane % 4 of every 64.
-    const int w = warp - 4, t8 = lane >> 2, d16 = lane & 3;
+    const int w = warp - kValueWarp, t8 = lane >> 2, d16 = lane & 3;
     constexpr int kLoads = 2 * (D / 64);
     uint4 x[kLoads];
     auto load = [&](int j, int p) {
@@ -346,8 +395,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
           x[i] = *reinterpret_cast<const uint4 *>(c.v + (((long long)p * c.Hk + hk) * page + (tok & (page - 1)) + t) * D + (i >> 1) * 64 + d16 * 16);
       }
     };
-    int pg = pages(1, w);
-    load(0, pages(0, w));
+    int entry = pages.ask(1, w);
+    load(0, pages.page(pages.ask(0, w)));
 #pragma unroll 1
     for (int j = 0; j < ntiles; ++j) {
       const int slot = j % G::kVStages;
@@ -366,18 +415,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
         *reinterpret_cast<uint4 *>(tile + mnmaj(dim, k, kTile)) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4 *>(tile + mnmaj(dim + 8, k, kTile)) = make_uint4(h[4], h[5], h[6], h[7]);
       }
-      if (j + 1 < ntiles) load(j + 1, pg);
-      pg = pages(j + 2, w);
+      load(j + 1, pages.page(entry));
+      entry = pages.ask(j + 2, w);
       fence_smem_to_async();
       bar_arrive(&bars.v_full[slot]);
     }
-  } else if (warp == 8) {
+  } else if (warp == kKeyWarp) {
     // ------------------------------------------------------------------- keys
-    int pg = pages(0, lane & 3);
+    int entry = pages.ask(0, lane & 3), entry_next = pages.ask(1, lane & 3);
 #pragma unroll 1
     for (int j = 0; j < ntiles; ++j) {
-      const int slot = j % G::kKStages, now = lane < kSubs ? pg : -1;
-      pg = pages(j + 1, lane & 3);
+      const int slot = j % G::kKStages, now = lane < kSubs ? pages.page(entry) : -1;
+      entry = entry_next;
+      entry_next = pages.ask(j + 2, lane & 3);
       if (j >= G::kKStages) wait(&bars.k_empty[slot], (j / G::kKStages - 1) & 1);
       __syncwarp();
       const uint32_t there = __ballot_sync(0xffffffffu, now >= 0);
@@ -396,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
     // --------------------------------------------------------------- products
     constexpr uint32_t id_s = idesc(kRows, kTile, 0, 0), id_o = idesc(kRows, D, 0, 1);
     __syncwarp();
-    asm volatile("bar.sync 1, 160;" ::: "memory");
+    asm volatile("bar.sync 1, 288;" ::: "memory");
     fence_after();
     auto scores = [&](int j) {
       const int slot = j % G::kKStages;
@@ -438,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 9) tmem_dealloc(tmem, G::kCols);
+  if (warp == kProductWarp) tmem_dealloc(tmem, G::kCols);
 }
 
 template <int D>
