@@ -13,10 +13,11 @@
 // so far, enters p as a term of the exponent, and leaves the row's sum again as a
 // factor on the page's part of it: no product per element.
 //
-// Warps: 0-3 and 4-7 softmax (thread = row; even and odd tiles), 8-11 values, 12
-// keys (TMA), 13 products.  For a tile of 64 tokens and D = 256 the products take
-// 1024 cycles; a tile's way through one group of softmax warps is longer than
-// that, so that two take turns.  The running maximum goes from one to the other
+// Warps: groups of 4 for the softmax (thread = row), which take tiles in turns, 4
+// for the values, one for the keys (TMA) and one for the products.  For a tile of
+// 64 tokens and D = 256 the products take 1024 cycles; a tile's way through one
+// group of softmax warps is longer than that: two groups, and four for narrower
+// heads.  The running maximum goes from one to the other
 // as soon as it is known, ahead of the exponentials; each keeps a sum of its own.
 #include <algorithm>
 
@@ -32,8 +33,7 @@ using namespace umma;
 constexpr int kRows = 128;    // of a CTA
 constexpr int kTile = 64;     // tokens
 constexpr int kSubs = kTile / 16;
-constexpr int kThreads = 448;
-constexpr int kValueWarp = 8, kKeyWarp = 12, kProductWarp = 13;
+constexpr int kRing = 8;      // tiles whose scales are kept
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -1.7e38f;
 constexpr float kSlack = 4.f;   // p may reach 2^kSlack before the running maximum moves
@@ -43,23 +43,46 @@ constexpr float kNoRef = -200.f;  // the logarithm of the value scales where the
 
 template <int D>
 struct Geo {
-  static constexpr int kKStages = 4, kVStages = 2;
+  // Groups of softmax warps, and buffers of S, which they take in turns.
+  static constexpr int kGroups = 2;
+  static constexpr int kValueWarp = 4 * kGroups, kKeyWarp = kValueWarp + 4, kProductWarp = kKeyWarp + 1;
+  static constexpr int kThreads = 32 * (kProductWarp + 1);
+  // A softmax warp that waits for the products of tile j - 1 knows those of tile j - 1 - kGroups to be done, from the
+  // scores that followed them: a slot of V, whose phases it tells apart by their parity, comes round no sooner.
+  static constexpr int kKStages = 4, kVStages = kGroups;
   static constexpr int kKBytes = kTile * D, kVBytes = kTile * D * 2;
-  static constexpr int kSmem = kKStages * kKBytes + kVStages * kVBytes + 1024;
+  // the rows of q, then of o, on their way between global memory and the threads that have a row each
+  static constexpr int kPitch = (D == 256 ? 2 : 4) * D + 16;
+  static constexpr int kStage = kKStages * kKBytes + kVStages * kVBytes;
+  static constexpr int kSmem = kStage + kRows * kPitch + 1024;
   // TMEM columns
   static constexpr int kQ = 0, kO = D / 2, kS = kO + D;
-  static constexpr int kCols = kS + 2 * kTile <= 256 ? 256 : 512;
+  static constexpr int kCols = 512;
   // K-major rows of 128 bytes (D = 64: 64) with the swizzle of that width
   static constexpr int kRowBytes = D >= 128 ? 128 : 64;
 };
 
-// tcgen05.mma of e4m3 operands, A in TMEM (4 bytes along K to a column: a K step of 32 advances 8), by lane 0 of a converged warp.
-__device__ __forceinline__ void mma_f8_ta_w(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t.reg .u32 l;\n\tmov.u32 l, %%laneid;\n\tsetp.eq.u32 e, l, 0;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(id), "r"(accumulate));
+// One lane of a converged warp.  Instructions that a warp issues once (products, commits) stand in a branch on it: the
+// compiler then knows that a single lane is there and keeps their operands uniform (a predicate per product on the
+// lane's number takes twice the issue time, which bounds a tile: 8192 over 24576 4.4 ms, so 3.5).
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
+// tcgen05.mma with A in TMEM: e4m3 operands (4 bytes along K to a column: a K step of 32 advances 8), or fp16 ones.
+template <bool kF8, bool kAccumulate>
+__device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t id) {
+  if constexpr (kF8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], b, %4, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(id), "n"(kAccumulate ? 1 : 0));
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(id), "n"(kAccumulate ? 1 : 0));
 }
 __device__ __forceinline__ void bar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -103,8 +126,8 @@ __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w, int high) {
 }
 
 struct Bars {
-  uint64_t k_full[4], k_empty[4], v_full[2], v_empty[2], s_full[2], p_full[2];
-  uint64_t moved[2][4];  // the running maximum after a tile, per warp
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[4], p_full[4], scales[kRing];
+  uint64_t moved[4][4];  // the running maximum after a tile, per warp
 };
 
 // Entries of the table for the 16 tokens `sub` of a tile.  ask() loads one (kUnseen: its tokens are not looked
@@ -113,10 +136,10 @@ constexpr int kUnseen = -0x40000000;
 struct TilePages {
   const CacheArgs &c;
   const int *table;
-  int seen;
+  int base, seen;  // tile 0, the tokens looked at
   unsigned int *err;
   __device__ __forceinline__ int ask(int tile, int sub) const {
-    const int tok = tile * kTile + sub * 16;
+    const int tok = (base + tile) * kTile + sub * 16;
     return tok < seen ? table[tok >> c.page_shift] : kUnseen;
   }
   __device__ __forceinline__ int page(int entry) const {
@@ -126,15 +149,31 @@ struct TilePages {
   }
 };
 
+// Parts of a block's rows where their tokens are cut: [items][Hk][parts][128] rows of D values, then their (maximum, sum).
+__device__ __forceinline__ long long part_row(const AttnArgs &a, long long item, int hk, int part, int parts) {
+  return ((item * a.cache.Hk + hk) * parts + part) * kRows;
+}
+__device__ __forceinline__ float *part_ml(const AttnArgs &a, long long items, int parts, int D) {
+  return static_cast<float *>(a.ws) + items * a.cache.Hk * parts * kRows * D;
+}
+
+// What the softmax needs of a tile's 4 pages: key scales and logarithms of value scales.
+struct Scales {
+  float4 ks, lvs;
+  uint32_t flags;  // a byte per page: 1 none, 2 a NaN value scale
+};
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap) {
+__global__ void __launch_bounds__(Geo<D>::kThreads, 1) attn_tile_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap) {
   using G = Geo<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bars;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int gave_up;
-  __shared__ float2 moved[2][kRows];  // running maximum and largest value scale after a tile, even and odd
-  __shared__ float2 other[2][kRows];  // maximum and sum of each group at the end
+  __shared__ float2 moved[G::kGroups][kRows];  // running maximum and largest value scale after a group's tile
+  __shared__ Scales ring[kRing];
+  __shared__ long long row_q[kRows], row_o[kRows];  // elements before a row
+  __shared__ float other[G::kGroups][kRows];  // sum of each group at the end
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const CacheArgs &c = a.cache;
   int local = 0;
@@ -145,25 +184,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
   if (count <= 0) return;
   const int hk = blockIdx.y;
   const int seen = a.causal ? min(s.kv, max(0, s.kv - s.n + (first + count - 1) / a.r + 1)) : s.kv;
-  const int ntiles = (seen + kTile - 1) / kTile;
+  // this block's tiles: base .. base + ntiles - 1 of the rows'
+  const int all = (seen + kTile - 1) / kTile, part = (all + (int)gridDim.z - 1) / (int)gridDim.z, base = part * (int)blockIdx.z;
+  const int ntiles = max(0, min(part, all - base));
 
   uint8_t *const smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  uint8_t *const sk = smem, *const sv = smem + G::kKStages * G::kKBytes;
+  uint8_t *const sk = smem, *const sv = smem + G::kKStages * G::kKBytes, *const stage = smem + G::kStage;
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       bar_init(&bars.k_full[i], 1);
       bar_init(&bars.k_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      bar_init(&bars.v_full[i], 128);
-      bar_init(&bars.v_empty[i], 1);
       bar_init(&bars.s_full[i], 1);
       bar_init(&bars.p_full[i], 128);
       for (int w = 0; w < 4; ++w) bar_init(&bars.moved[i][w], 32);
+      bar_init(&bars.v_full[i], 128);
+      bar_init(&bars.v_empty[i], 1);
     }
+    for (int i = 0; i < kRing; ++i) bar_init(&bars.scales[i], 4);
     gave_up = 0;
   }
-  if (warp == kProductWarp) tmem_alloc(&tmem_slot, G::kCols);
+  if (warp == G::kProductWarp) tmem_alloc(&tmem_slot, G::kCols);
   fence_before();
   __syncthreads();
   fence_after();
@@ -178,23 +218,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
         atomicOr(a.seq.err, kErrTimeout);
       }
   };
-  const TilePages pages{c, c.table + (long long)s.b * c.table_ld, seen, a.seq.err};
+  const TilePages pages{c, c.table + (long long)s.b * c.table_ld, base, min(seen, (base + ntiles) * kTile), a.seq.err};
   const int page = 1 << c.page_shift;
 
-  if (warp < kValueWarp) {
+  auto sync_softmax = [] { asm volatile("bar.sync 2, %0;" ::"n"(128 * G::kGroups) : "memory"); };
+  auto sync_products = [] { asm volatile("bar.sync 1, %0;" ::"n"(128 * G::kGroups + 32) : "memory"); };
+  if (warp < G::kValueWarp) {
     // ---------------------------------------------------------------- softmax
     const int group = warp >> 2, quarter = warp & 3, row = tid & (kRows - 1), rr = first + row, tok = rr / a.r;
     const bool real = row < count;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    // q as hi + lo, times a power of two that brings the row's largest into [2^7, 2^8); half the columns to a group
-    const __nv_bfloat16 *const src = static_cast<const __nv_bfloat16 *>(a.q) + (s.row0 + (long long)tok) * a.ldq +
-                                     (long long)(hk * a.r + rr - tok * a.r) * D;
+    constexpr int kChunks = D / 8;  // 16 bytes each, of a row
+    if (group == 0) {
+      row_q[row] = (s.row0 + (long long)tok) * a.ldq + (long long)(hk * a.r + rr - tok * a.r) * D;
+      row_o[row] = (s.row0 + (long long)tok) * a.ldo + (long long)(hk * a.r + rr - tok * a.r) * D;
+    }
+    sync_softmax();
+#pragma unroll 8
+    for (int x = tid; x < kRows * kChunks; x += 128 * G::kGroups) {
+      const int rw = x / kChunks, ch = x % kChunks;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (rw < count) w = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + row_q[rw] + ch * 8);
+      *reinterpret_cast<uint4 *>(stage + rw * G::kPitch + ch * 16) = w;
+    }
+    sync_softmax();
+    // q as hi + lo, times a power of two that brings the row's largest into [2^7, 2^8); half the columns to each of two groups
+    uint8_t *const mine = stage + row * G::kPitch;
     float f;  // on a score, without its page's scale
     {
       uint32_t top = 0;
 #pragma unroll 8
       for (int d = 0; d < D; d += 8) {
-        const uint4 w = real ? *reinterpret_cast<const uint4 *>(src + d) : make_uint4(0, 0, 0, 0);
+        const uint4 w = *reinterpret_cast<const uint4 *>(mine + 2 * d);
         const uint32_t x[4] = {w.x & 0x7fff7fffu, w.y & 0x7fff7fffu, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu};
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = max(top, max(x[i] & 0xffffu, x[i] >> 16));
@@ -204,11 +259,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
       const float up = (a.scale < 0.f ? -1.f : 1.f) * __uint_as_float((uint32_t)(e + 127) << 23);
       f = bad ? __int_as_float(0x7fc00000) : __uint_as_float((uint32_t)(127 - e) << 23) * (fabsf(a.scale) * kLog2e);
 #pragma unroll 1
-      for (int d = group * (D / 2); d < (group + 1) * (D / 2); d += 32) {
+      for (int d = group * (D / 2); group < 2 && d < (group + 1) * (D / 2); d += 32) {
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 w = real && !bad ? *reinterpret_cast<const uint4 *>(src + d + 8 * i) : make_uint4(0, 0, 0, 0);
+          const uint4 w = bad ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(mine + 2 * d + 16 * i);
           const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -228,72 +283,61 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
     }
     fence_before();
     __syncwarp();
-    asm volatile("bar.sync 1, 288;" ::: "memory");  // with the products' warp: Q is in place
+    sync_products();  // with the products' warp: Q is in place
     const int last = !real ? -1 : a.causal ? s.kv - s.n + tok : s.kv - 1;
     const int all_see = a.causal ? s.kv - s.n + first / a.r : s.kv - 1;
     float m = kNone, l = 0.f, lref = kNoRef;  // m: what l is relative to; the largest value scale's logarithm
-    // Lane u of four has page u of a tile: its key scale, and its value scale's logarithm.
-    auto scales = [&](int p) {
-      if (p < 0) return make_float2(0.f, 0.f);
-      const long long at = (long long)p * c.Hk + hk;
-      return make_float2(c.ks[at], c.vs[at]);
-    };
-    int pg = pages.page(pages.ask(group, lane & 3)), entry = pages.ask(group + 2, lane & 3);
-    float2 sc = scales(pg);
 #pragma unroll 1
-    for (int j = group; j < ntiles; j += 2) {
-      const float ks = sc.x, lvs = fmaxf(__log2f(sc.y), kNoRef);  // fmaxf: of 0, and of a NaN, which `odd` looks after
-      const uint32_t gone = __ballot_sync(0xffffffffu, pg < 0) & ((1u << kSubs) - 1);
-      const uint32_t no_v = __ballot_sync(0xffffffffu, sc.y != sc.y) & ((1u << kSubs) - 1);
-      pg = pages.page(entry);
-      entry = pages.ask(j + 4, lane & 3);
-      sc = scales(pg);
-      float fs[kSubs], ltop = lvs;
-#pragma unroll
-      for (int u = 0; u < kSubs; ++u) fs[u] = f * __shfl_sync(0xffffffffu, ks, u);
-      ltop = fmaxf(ltop, __shfl_xor_sync(0xffffffffu, ltop, 1));
-      ltop = fmaxf(ltop, __shfl_xor_sync(0xffffffffu, ltop, 2));
-      wait(&bars.s_full[group], (j >> 1) & 1);
+    for (int j = group; j < ntiles; j += G::kGroups) {
+      const uint32_t turn = j / G::kGroups;
+      wait(&bars.scales[j % kRing], (j / kRing) & 1);
+      const Scales &sc = ring[j % kRing];
+      const float4 ks4 = sc.ks, lvs = sc.lvs;
+      const float ltop = fmaxf(fmaxf(lvs.x, lvs.y), fmaxf(lvs.z, lvs.w));
+      const uint32_t flags = sc.flags;
+      float fs[kSubs] = {f * ks4.x, f * ks4.y, f * ks4.z, f * ks4.w};
+      wait(&bars.s_full[group], turn & 1);
       __syncwarp();
       fence_after();
-      uint32_t x0[32], x1[32];
-      tmem_ld32_nw(lanes + G::kS + group * kTile, x0);
-      tmem_ld32_nw(lanes + G::kS + group * kTile + 32, x1);
-      tmem_wait_ld();
-      float y[kTile];
+      const uint32_t scores = lanes + G::kS + group * kTile;
+      const int tok0 = (base + j) * kTile;
+      // Some row does not see all, or some value scale is NaN: then scores get their scales first, so that a scale
+      // (NaN, 0) does not bring back what is not seen, and a NaN value scale reaches what is.
+      const bool odd = flags != 0 || tok0 + kTile - 1 > all_see;
+      auto one_by_one = [&](uint32_t (&x)[32], int h) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        y[i] = __uint_as_float(x0[i]);
-        y[32 + i] = __uint_as_float(x1[i]);
-      }
-      const int tok0 = j * kTile;
-      if ((gone | no_v) != 0 || tok0 + kTile - 1 > all_see) {
-        // Some row does not see all, or some value scale is NaN: here the scores get their scales, so that a scale
-        // (NaN, 0) does not bring back what is not seen, and a NaN value scale reaches what is.
-#pragma unroll
-        for (int i = 0; i < kTile; ++i) {
-          const float x = (no_v >> (i / 16)) & 1 ? __int_as_float(0x7fc00000) : y[i] * fs[i / 16];
-          y[i] = tok0 + i <= last && !(gone >> (i / 16) & 1) ? x : -INFINITY;
+        for (int i = 0; i < 32; ++i) {
+          const int u = 2 * h + i / 16;
+          const float y = flags >> (8 * u + 1) & 1 ? __int_as_float(0x7fc00000) : __uint_as_float(x[i]) * fs[u];
+          x[i] = __float_as_uint(tok0 + 32 * h + i <= last && !(flags >> (8 * u) & 1) ? y : -INFINITY);
         }
-#pragma unroll
-        for (int u = 0; u < kSubs; ++u) fs[u] = 1.f;
-      }
+      };
       float top = -INFINITY;
 #pragma unroll
-      for (int u = 0; u < kSubs; ++u) {
-        float t0 = fmaxf(y[16 * u], y[16 * u + 1]), t1 = fmaxf(y[16 * u + 2], y[16 * u + 3]);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x[32];
+        tmem_ld32_nw(scores + 32 * h, x);
+        tmem_wait_ld();
+        if (odd) one_by_one(x, h);
 #pragma unroll
-        for (int i = 4; i < 16; i += 4) {
-          t0 = fmaxf(fmaxf(t0, y[16 * u + i]), y[16 * u + i + 1]);
-          t1 = fmaxf(fmaxf(t1, y[16 * u + i + 2]), y[16 * u + i + 3]);
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t *const y = x + 16 * v;
+          float t0 = fmaxf(__uint_as_float(y[0]), __uint_as_float(y[1])), t1 = fmaxf(__uint_as_float(y[2]), __uint_as_float(y[3]));
+#pragma unroll
+          for (int i = 4; i < 16; i += 4) {
+            t0 = fmaxf(fmaxf(t0, __uint_as_float(y[i])), __uint_as_float(y[i + 1]));
+            t1 = fmaxf(fmaxf(t1, __uint_as_float(y[i + 2])), __uint_as_float(y[i + 3]));
+          }
+          top = fmaxf(top, odd ? fmaxf(t0, t1) : fmaxf(t0, t1) * fs[2 * h + v]);
         }
-        top = fmaxf(top, fmaxf(t0, t1) * fs[u]);
+        __syncwarp();
       }
       // the other group's word on the tile before
       float mc = kNone;
       if (j > 0) {
-        wait(&bars.moved[group ^ 1][quarter], ((j - 1) >> 1) & 1);
-        const float2 x = moved[group ^ 1][row];
+        const int before = group == 0 ? G::kGroups - 1 : group - 1;
+        wait(&bars.moved[before][quarter], ((j - 1) / G::kGroups) & 1);
+        const float2 x = moved[before][row];
         mc = x.x;
         lref = x.y;
       }
@@ -320,92 +364,136 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
       bar_arrive(&bars.moved[group][quarter]);
       l *= ex2(m - mc);
       m = mc;
-      // the value scale over the largest, in the exponent
-      const float lr = fmaxf(lvs - lref, kMinRatio), back = ex2(-lr - kPExp), base = kPExp - m;
-      uint32_t p[kTile / 2];
+      // the value scales over the largest, in the exponent
+      const float up2 = kPExp - m;
+      const float lr[kSubs] = {fmaxf(lvs.x - lref, kMinRatio), fmaxf(lvs.y - lref, kMinRatio), fmaxf(lvs.z - lref, kMinRatio),
+                               fmaxf(lvs.w - lref, kMinRatio)};
+      // the scores once more, half a tile at a time: fewer registers, and more of them for what runs side by side
 #pragma unroll
-      for (int u = 0; u < kSubs; ++u) {
-        const float shift = __shfl_sync(0xffffffffu, lr, u) + base, undo = __shfl_sync(0xffffffffu, back, u);
-        float2 sum = make_float2(0.f, 0.f);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x[32], p[16];
+        __syncwarp();
+        tmem_ld32_nw(scores + 32 * h, x);
+        tmem_wait_ld();
+        if (odd) one_by_one(x, h);
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          float2 e = fma2(make_float2(y[16 * u + i], y[16 * u + i + 1]), make_float2(fs[u], fs[u]), make_float2(shift, shift));
-          e.x = ex2(e.x);
-          e.y = ex2(e.y);
-          sum = add2(sum, e);
-          p[8 * u + i / 2] = pack2(e.x, e.y);
+        for (int v = 0; v < 2; ++v) {
+          const int u = 2 * h + v;
+          const float shift = lr[u] + up2, fu = odd ? 1.f : fs[u];
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            float2 e = fma2(make_float2(__uint_as_float(x[16 * v + i]), __uint_as_float(x[16 * v + i + 1])), make_float2(fu, fu),
+                            make_float2(shift, shift));
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            sum = add2(sum, e);
+            p[8 * v + i / 2] = pack2(e.x, e.y);
+          }
+          l = fmaf(sum.x + sum.y, ex2(-lr[u] - kPExp), l);
         }
-        l = fmaf(sum.x + sum.y, undo, l);
+        __syncwarp();
+        tmem_st16w_nw(scores + 16 * h, p);  // in the place of scores that have been read
       }
-      __syncwarp();
-      tmem_st32w_nw(lanes + G::kS + group * kTile, p);
       tmem_wait_st();
       fence_before();
       bar_arrive(&bars.p_full[group]);
     }
     // ---- out: the groups' sums together, half the columns to each
     if (ntiles > 0) {
-      const int g_last = (ntiles - 1) & 1;
-      wait(&bars.moved[g_last][quarter], ((ntiles - 1) >> 1) & 1);
+      const int g_last = (ntiles - 1) % G::kGroups;
+      wait(&bars.moved[g_last][quarter], ((ntiles - 1) / G::kGroups) & 1);
       const float2 x = moved[g_last][row];
       l *= ex2(m - x.x);
       m = x.x;
       lref = x.y;
     }
-    other[group][row] = make_float2(m, l);
-    asm volatile("bar.sync 2, 256;" ::: "memory");
-    l += other[group ^ 1][row].y;
+    other[group][row] = l;
+    sync_softmax();
+    l = 0.f;
+#pragma unroll
+    for (int g = 0; g < G::kGroups; ++g) l += other[g][row];
     if (ntiles > 0) wait(&bars.v_empty[(ntiles - 1) % G::kVStages], ((ntiles - 1) / G::kVStages) & 1);
     __syncwarp();
     fence_after();
-    const float inv = l == 0.f ? 0.f : ex2(lref - kPExp) / l;
-    __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.o) + (s.row0 + (long long)tok) * a.ldo +
-                               (long long)(hk * a.r + rr - tok * a.r) * D;
+    if (gridDim.z > 1) {  // a part: fp32, relative to m
+      const long long at = part_row(a, item, hk, blockIdx.z, gridDim.z) + row;
+      if (group == 0) reinterpret_cast<float2 *>(part_ml(a, gridDim.x, gridDim.z, D))[at] = make_float2(ntiles > 0 ? m : -INFINITY, l);
+      const float un = ex2(lref - kPExp);
+      constexpr int kRounds = D == 256 ? 2 : 1, kCols = D / (2 * kRounds);  // of a group in a round
 #pragma unroll 1
-    for (int d = group * (D / 2); d < (group + 1) * (D / 2); d += 32) {
+      for (int h = 0; ntiles > 0 && h < kRounds; ++h) {
+#pragma unroll 1
+        for (int d = 0; group < 2 && d < kCols; d += 32) {
+          uint32_t w[32];
+          __syncwarp();
+          tmem_ld32_nw(lanes + G::kO + group * (D / 2) + h * kCols + d, w);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4 *>(mine + (group * kCols + d + i) * 4) =
+                make_float4(__uint_as_float(w[i]) * un, __uint_as_float(w[i + 1]) * un, __uint_as_float(w[i + 2]) * un,
+                            __uint_as_float(w[i + 3]) * un);
+        }
+        sync_softmax();
+        float *const dst = static_cast<float *>(a.ws) + (at - row) * D + h * kCols;
+#pragma unroll 4
+        for (int x = tid; x < count * (kCols / 2); x += 128 * G::kGroups) {
+          const int rw = x / (kCols / 2), ch = x % (kCols / 2), g = ch / (kCols / 4), col = ch % (kCols / 4) * 4;
+          *reinterpret_cast<float4 *>(dst + (long long)rw * D + g * (D / 2) + col) =
+              *reinterpret_cast<const float4 *>(stage + rw * G::kPitch + ch * 16);
+        }
+        sync_softmax();
+      }
+    } else {
+    const float inv = l == 0.f ? 0.f : ex2(lref - kPExp) / l;
+#pragma unroll 1
+    for (int d = group * (D / 2); group < 2 && d < (group + 1) * (D / 2); d += 32) {
       uint32_t w[32];
       __syncwarp();
       tmem_ld32_nw(lanes + G::kO + d, w);
       tmem_wait_ld();
-      if (real) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          uint32_t o[4];
+      for (int i = 0; i < 32; i += 8) {
+        uint32_t o[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            o[k] = ntiles > 0 ? pack_bf16(__uint_as_float(w[i + 2 * k]) * inv, __uint_as_float(w[i + 2 * k + 1]) * inv) : 0u;
-          *reinterpret_cast<uint4 *>(dst + d + i) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+        for (int k = 0; k < 4; ++k)
+          o[k] = ntiles > 0 ? pack_bf16(__uint_as_float(w[i + 2 * k]) * inv, __uint_as_float(w[i + 2 * k + 1]) * inv) : 0u;
+        *reinterpret_cast<uint4 *>(mine + 2 * (d + i)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
+    sync_softmax();
+#pragma unroll 8
+    for (int x = tid; x < count * kChunks; x += 128 * G::kGroups) {
+      const int rw = x / kChunks, ch = x % kChunks;
+      *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + row_o[rw] + ch * 8) =
+          *reinterpret_cast<const uint4 *>(stage + rw * G::kPitch + ch * 16);
+    }
+    }
     fence_before();
-  } else if (warp < kKeyWarp) {
+  } else if (warp < G::kKeyWarp) {
     // ----------------------------------------------------------------- values
     // 16 tokens to a warp: lane / 4 (and 8 more), 16 dimensions at lane % 4 of every 64.
-    const int w = warp - kValueWarp, t8 = lane >> 2, d16 = lane & 3;
+    const int w = warp - G::kValueWarp, t8 = lane >> 2, d16 = lane & 3;
     constexpr int kLoads = 2 * (D / 64);
-    uint4 x[kLoads];
-    auto load = [&](int j, int p) {
-      const int tok = j * kTile + 16 * w;
+    uint4 x[2][kLoads];  // of the next two tiles
+    auto load = [&](int j, int p, uint4 (&r)[kLoads]) {
+      const int tok = (base + j) * kTile + 16 * w;
+      const uint8_t *const src = c.v + (((long long)max(p, 0) * c.Hk + hk) * page + (tok & (page - 1)) + t8) * D + d16 * 16;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int t = t8 + 8 * (i & 1);
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (p >= 0 && tok + t < s.kv)
-          x[i] = *reinterpret_cast<const uint4 *>(c.v + (((long long)p * c.Hk + hk) * page + (tok & (page - 1)) + t) * D + (i >> 1) * 64 + d16 * 16);
+        r[i] = make_uint4(0, 0, 0, 0);
+        if (p >= 0 && tok + t8 + 8 * (i & 1) < s.kv) r[i] = *reinterpret_cast<const uint4 *>(src + 8 * (i & 1) * D + (i >> 1) * 64);
       }
     };
-    int entry = pages.ask(1, w);
-    load(0, pages.page(pages.ask(0, w)));
-#pragma unroll 1
-    for (int j = 0; j < ntiles; ++j) {
+    auto put = [&](int j, const uint4 (&r)[kLoads]) {
       const int slot = j % G::kVStages;
       if (j >= G::kVStages) wait(&bars.v_empty[slot], (j / G::kVStages - 1) & 1);
       uint8_t *const tile = sv + slot * G::kVBytes;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const int k = 16 * w + t8 + 8 * (i & 1), dim = (i >> 1) * 64 + d16 * 16;
-        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        const uint32_t u[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
         uint32_t h[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -415,80 +503,186 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tile_kernel(const AttnArgs a
         *reinterpret_cast<uint4 *>(tile + mnmaj(dim, k, kTile)) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4 *>(tile + mnmaj(dim + 8, k, kTile)) = make_uint4(h[4], h[5], h[6], h[7]);
       }
-      load(j + 1, pages.page(entry));
-      entry = pages.ask(j + 2, w);
       fence_smem_to_async();
       bar_arrive(&bars.v_full[slot]);
+    };
+    // A tile's loads are asked for two tiles ahead, behind the fence, which would wait for them; the pages and scales of
+    // 32 tiles at a time, one per lane, 32 ahead.  The scales go to the softmax warps two tiles ahead as well: the place
+    // of tile j + 2 in the ring was tile j - 6's, which they have done when the products of tile j - 3 are.
+    auto scales = [&](int p) {
+      if (p < 0) return make_float2(0.f, 0.f);
+      const long long at = (long long)p * c.Hk + hk;
+      return make_float2(c.ks[at], c.vs[at]);
+    };
+    int pg = pages.page(pages.ask(lane, w)), pg_next = -1, entry = pages.ask(32 + lane, w);
+    float2 sc = scales(pg), sc_next = make_float2(0.f, 0.f);
+    auto prepare = [&](int j, uint4 (&r)[kLoads]) {  // of the batch of 32 at hand
+      const int p = __shfl_sync(0xffffffffu, pg, j & 31);
+      const float ks = __shfl_sync(0xffffffffu, sc.x, j & 31), vs = __shfl_sync(0xffffffffu, sc.y, j & 31);
+      load(j, p, r);
+      if (lane == 0 && j < ntiles) {
+        Scales &out = ring[j % kRing];
+        reinterpret_cast<float *>(&out.ks)[w] = ks;
+        reinterpret_cast<float *>(&out.lvs)[w] = fmaxf(__log2f(vs), kNoRef);  // fmaxf: of 0, and of a NaN, which the flag tells of
+        reinterpret_cast<uint8_t *>(&out.flags)[w] = (p < 0 ? 1 : 0) | (vs != vs ? 2 : 0);
+        bar_arrive(&bars.scales[j % kRing]);
+      }
+      __syncwarp();
+    };
+    prepare(0, x[0]);
+    prepare(1, x[1]);
+#pragma unroll 1
+    for (int j = 0; j < ntiles; j += 2) {
+      if ((j & 31) == 16) {
+        pg_next = pages.page(entry);
+        sc_next = scales(pg_next);
+      }
+      if ((j & 31) == 30) {  // what follows is of the next batch
+        pg = pg_next;
+        sc = sc_next;
+        entry = pages.ask(j + 34 + lane, w);
+      }
+      put(j, x[0]);
+      prepare(j + 2, x[0]);
+      if (j + 1 < ntiles) put(j + 1, x[1]);
+      prepare(j + 3, x[1]);
     }
-  } else if (warp == kKeyWarp) {
+  } else if (warp == G::kKeyWarp) {
     // ------------------------------------------------------------------- keys
-    int entry = pages.ask(0, lane & 3), entry_next = pages.ask(1, lane & 3);
+    // Lane 4 i + u has page u of tile i of a batch of 8; those of the next are asked for when one begins.
+    int pg = pages.page(pages.ask(lane >> 2, lane & 3)), entry = pages.ask(8 + (lane >> 2), lane & 3);
 #pragma unroll 1
     for (int j = 0; j < ntiles; ++j) {
-      const int slot = j % G::kKStages, now = lane < kSubs ? pages.page(entry) : -1;
-      entry = entry_next;
-      entry_next = pages.ask(j + 2, lane & 3);
+      const int i = j & 7, slot = j % G::kKStages;
+      if (i == 0 && j > 0) {
+        pg = pages.page(entry);
+        entry = pages.ask(j + 8 + (lane >> 2), lane & 3);
+      }
+      const int p = __shfl_sync(0xffffffffu, pg, 4 * i + (lane & 3));
+      const uint32_t there = __ballot_sync(0xffffffffu, p >= 0) & ((1u << kSubs) - 1);
       if (j >= G::kKStages) wait(&bars.k_empty[slot], (j / G::kKStages - 1) & 1);
       __syncwarp();
-      const uint32_t there = __ballot_sync(0xffffffffu, now >= 0);
       if (lane == 0) bar_expect_tx(&bars.k_full[slot], __popc(there) * 16 * D);
       __syncwarp();
-      if (now >= 0) {
+      if (lane < kSubs && p >= 0) {
         const uint32_t dst = smem_u32(sk + slot * G::kKBytes) + lane * 16 * G::kRowBytes;
-        const int tok = (j * kTile + lane * 16) & (page - 1);
+        const int tok = ((base + j) * kTile + lane * 16) & (page - 1);
 #pragma unroll
         for (int b = 0; b < (D + 127) / 128; ++b)
-          tma_load_3d(dst + b * kTile * 128, &kmap, b * 128, hk * page + tok, now, &bars.k_full[slot]);
+          tma_load_3d(dst + b * kTile * 128, &kmap, b * 128, hk * page + tok, p, &bars.k_full[slot]);
       }
       __syncwarp();
     }
   } else {
     // --------------------------------------------------------------- products
     constexpr uint32_t id_s = idesc(kRows, kTile, 0, 0), id_o = idesc(kRows, D, 0, 1);
+    // Descriptors' halves: address and leading stride, group stride, version and swizzle (keys of 64 bytes a row: the
+    // swizzle of that width, 8 rows in 512 bytes).
+    constexpr uint32_t k_hi = D >= 128 ? 1024 >> 4 | 1 << 14 | 2u << 29 : 512 >> 4 | 1 << 14 | 4u << 29;
+    constexpr uint32_t v_hi = 1024 >> 4 | 1 << 14 | 2u << 29;
+    const uint32_t k_lo = smem_u32(sk) >> 4 | 1 << 16, v_lo = smem_u32(sv) >> 4 | (uint32_t)(kTile / 8 * 1024 >> 4) << 16;
     __syncwarp();
-    asm volatile("bar.sync 1, 288;" ::: "memory");
+    sync_products();
     fence_after();
     auto scores = [&](int j) {
       const int slot = j % G::kKStages;
       wait(&bars.k_full[slot], (j / G::kKStages) & 1);
       __syncwarp();
       fence_after();
-      const uint32_t kb = smem_u32(sk + slot * G::kKBytes), d = tmem + G::kS + (j & 1) * kTile;
+      if (elect()) {
+        const uint32_t lo = k_lo + slot * (G::kKBytes >> 4), d = tmem + G::kS + (j % G::kGroups) * kTile;
 #pragma unroll
-      for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < 2; ++part)
 #pragma unroll
-        for (int ks = 0; ks < D / 32; ++ks) {
-          uint64_t b;
-          if constexpr (D >= 128)
-            b = desc_k(kb, ks, kTile);
-          else  // rows of 64 bytes: 64-byte swizzle, 8 rows in 512 bytes
-            b = (uint64_t)(((kb + ks * 32) >> 4) & 0x3FFF) | ((uint64_t)1 << 16) | ((uint64_t)(512 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)4 << 61);
-          mma_f8_ta_w(d, tmem + G::kQ + part * (D / 4) + ks * 8, b, id_s, part + ks > 0);
-        }
-      commit_w(&bars.s_full[j & 1]);
-      commit_w(&bars.k_empty[slot]);
+          for (int ks = 0; ks < D / 32; ++ks) {
+            const uint32_t at = lo + (((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4), q = tmem + G::kQ + part * (D / 4) + ks * 8;
+            if (part + ks == 0)
+              mma_ta<true, false>(d, q, at, k_hi, id_s);
+            else
+              mma_ta<true, true>(d, q, at, k_hi, id_s);
+          }
+        commit(&bars.s_full[j % G::kGroups]);
+        commit(&bars.k_empty[slot]);
+      }
+      __syncwarp();
     };
-    if (ntiles > 0) scores(0);
-    if (ntiles > 1) scores(1);
+#pragma unroll 1
+    for (int j = 0; j < min(ntiles, G::kGroups); ++j) scores(j);
 #pragma unroll 1
     for (int j = 0; j < ntiles; ++j) {
       const int slot = j % G::kVStages;
       wait(&bars.v_full[slot], (j / G::kVStages) & 1);
-      wait(&bars.p_full[j & 1], (j >> 1) & 1);
+      wait(&bars.p_full[j % G::kGroups], (j / G::kGroups) & 1);
       __syncwarp();
       fence_after();
-      const uint32_t vb = smem_u32(sv + slot * G::kVBytes), p = tmem + G::kS + (j & 1) * kTile;
+      if (elect()) {
+        const uint32_t lo = v_lo + slot * (G::kVBytes >> 4), p = tmem + G::kS + (j % G::kGroups) * kTile;
+        if (j == 0)
+          mma_ta<false, false>(tmem + G::kO, p, lo, v_hi, id_o);
+        else
+          mma_ta<false, true>(tmem + G::kO, p, lo, v_hi, id_o);
 #pragma unroll
-      for (int ks = 0; ks < kTile / 16; ++ks)
-        mma_ta_w(tmem + G::kO, p + ks * 8, desc_mn(vb, ks, kTile), id_o, j + ks > 0);
-      commit_w(&bars.v_empty[slot]);
-      if (j + 2 < ntiles) scores(j + 2);
+        for (int ks = 1; ks < kTile / 16; ++ks) mma_ta<false, true>(tmem + G::kO, p + ks * 8, lo + ks * (2048 >> 4), v_hi, id_o);
+        commit(&bars.v_empty[slot]);
+      }
+      __syncwarp();
+      if (j + G::kGroups < ntiles) scores(j + G::kGroups);  // where P was: products follow each other
     }
   }
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == kProductWarp) tmem_dealloc(tmem, G::kCols);
+  if (warp == G::kProductWarp) tmem_dealloc(tmem, G::kCols);
+}
+
+// Joins the parts of an item's rows: o = sum 2^(m_p - m) o_p / sum 2^(m_p - m) l_p.  A thread has 4 columns of a row.
+constexpr int kJoinRows = 16;
+template <int D>
+__global__ void __launch_bounds__(256) attn_tile_join(const AttnArgs a, int parts) {
+  int local = 0;
+  const Seq s = find_seq(a.seq, blockIdx.x, a.r, kRows, 1, &local);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written (no block ends before that)
+  if (s.b < 0) return;
+  const int hk = blockIdx.y, row0 = blockIdx.z * kJoinRows, first = local * kRows + row0;
+  const int count = (int)min((long long)kJoinRows, (long long)s.n * a.r - first);
+  const float *const o = static_cast<const float *>(a.ws);
+  const float2 *const ml = reinterpret_cast<const float2 *>(part_ml(a, gridDim.x, parts, D));
+  const long long base = part_row(a, blockIdx.x, hk, 0, parts) + row0;
+  for (int x = threadIdx.x; x < count * (D / 4); x += 256) {
+    const int row = x / (D / 4), d = x % (D / 4) * 4, rr = first + row, tok = rr / a.r;
+    float m = kNone, l = 0.f;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = 0; p < parts; p += 8) {  // 8 parts' loads in flight
+      float2 z[8];
+      float4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        z[u] = make_float2(-INFINITY, 0.f);
+        if (p + u < parts) {
+          z[u] = ml[base + (p + u) * kRows + row];
+          v[u] = *reinterpret_cast<const float4 *>(o + (base + (p + u) * kRows + row) * D + d);
+        }
+      }
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) mn = fmaxf(mn, z[u].x);
+      const float old = ex2(m - mn);
+      m = mn;
+      l *= old;
+      sum.x *= old, sum.y *= old, sum.z *= old, sum.w *= old;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (z[u].x != -INFINITY) {  // else a part without tokens, which left no values
+          const float w = ex2(z[u].x - m);
+          l += w * z[u].y;
+          sum.x += w * v[u].x, sum.y += w * v[u].y, sum.z += w * v[u].z, sum.w += w * v[u].w;
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.o) + (s.row0 + (long long)tok) * a.ldo +
+                               (long long)(hk * a.r + rr - tok * a.r) * D + d;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
+  }
 }
 
 template <int D>
@@ -510,12 +704,56 @@ cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
              D >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)item_count(a.seq, a.r, kRows, 1), c.Hk);
-  attn_tile_kernel<D><<<grid, kThreads, G::kSmem, s>>>(a, map);
-  return cudaGetLastError();
+  const int parts = a.ws ? a.splits : 1;
+  const dim3 grid((unsigned)item_count(a.seq, a.r, kRows, 1), c.Hk, parts);
+  attn_tile_kernel<D><<<grid, G::kThreads, G::kSmem, s>>>(a, map);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || parts < 2) return e;
+  // The join comes up while the last blocks end, and waits for them.
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid.x, grid.y, kRows / kJoinRows);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attn_tile_join<D>, a, parts);
+  return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace
+
+// The most parts that attn_tile_parts takes for so many tokens or fewer: none has less than 8 tiles, and no more
+// than fill the GPU once, or are two where the blocks alone do not.
+int attn_tile_most_parts(long long blocks, long long max_kv, int num_sms) {
+  return blocks >= num_sms ? 1 : (int)std::max(1LL, std::min({32LL, max_kv / (8 * kTile), (num_sms + blocks - 1) / blocks + 1}));
+}
+// A block takes a tile's time per tile and about that of kEnds to start and end, one block to an SM at a time; a
+// part's values cost kPart more, a join kJoin: the number of parts with the least time.
+int attn_tile_parts(long long blocks, long long max_kv, int num_sms) {
+  constexpr int kEnds = 10, kPart = 8, kJoin = 6;
+  const long long tiles = (max_kv + kTile - 1) / kTile;
+  const int most = attn_tile_most_parts(blocks, max_kv, num_sms);
+  int best = 1;
+  long long least = 0;
+  for (int p = 1; p <= most; ++p) {
+    const long long time =
+        (blocks * p + num_sms - 1) / num_sms * ((tiles + p - 1) / p + kEnds + (p > 1 ? kPart : 0)) + (p > 1 ? kJoin + p / 4 : 0);
+    if (p == 1 || time < least) {
+      least = time;
+      best = p;
+    }
+  }
+  return best;
+}
+
+size_t attn_tile_ws_bytes(long long blocks, int D, int parts) {
+  return parts < 2 ? 0 : (size_t)blocks * parts * kRows * (D + 2) * sizeof(float);
+}
+
+long long attn_tile_blocks(const SeqArgs &q, int r, int Hk) { return item_count(q, r, kRows, 1) * Hk; }
 
 cudaError_t launch_attn_tile(const AttnArgs &a, cudaStream_t s) {
   return a.cache.D == 64 ? launch<64>(a, s) : a.cache.D == 128 ? launch<128>(a, s) : launch<256>(a, s);

@@ -71,26 +71,31 @@ gdn_status check_rows(const void *p, long long ld, long long width, size_t el) {
   return aligned16(p) && ld * el % 16 == 0 ? GDN_OK : GDN_ERR_ALIGNMENT;
 }
 
-// How a call of gdn_attn runs, and the workspace it makes use of.
+// How a call of gdn_attn runs, and the workspace it makes use of.  `room`: the
+// workspace of any call with this shape and max_kv tokens or fewer (a table may
+// allow fewer than the shape says).
 struct AttnPlan {
   int few_rows;  // rows of a tile of attn_few.cu, or 0
   bool tile;     // attn_tile.cu; neither: attn_rows.cu
-  int splits;    // attn_rows.cu: ranges of the tokens side by side
+  int splits;    // ranges of the tokens side by side (attn_few.cu cuts by itself)
   size_t bytes;
 };
-AttnPlan attn_plan(const gdn_attn_shape *s, bool packed, long long rows, int max_kv, int sms) {
-  const int r = s->Hq / s->Hk;
+AttnPlan attn_plan(const gdn_attn_shape *s, bool packed, long long rows, int max_kv, int sms, bool room) {
+  const int r = s->Hq / s->Hk, cu = 0;
   AttnPlan p{0, false, 1, 0};
-  if (s->io_dtype == GDN_BF16) p.few_rows = gdn::attn_few_rows(s->D, (long long)bound_new(s, packed) * r);
-  if (p.few_rows) {
-    p.bytes = gdn::attn_few_ws_bytes(s->D, p.few_rows, sms);
-    return p;
-  }
   if (s->io_dtype == GDN_BF16) {
+    p.few_rows = gdn::attn_few_rows(s->D, (long long)bound_new(s, packed) * r);
+    if (p.few_rows) {
+      p.bytes = gdn::attn_few_ws_bytes(s->D, p.few_rows, sms);
+      return p;
+    }
     p.tile = true;
+    const long long blocks = gdn::attn_tile_blocks(gdn::SeqArgs{s->B, s->T, 0, 0, packed ? &cu : nullptr, nullptr, nullptr}, r, s->Hk);
+    p.splits = room ? gdn::attn_tile_most_parts(blocks, max_kv, sms) : gdn::attn_tile_parts(blocks, max_kv, sms);
+    p.bytes = gdn::attn_tile_ws_bytes(blocks, s->D, p.splits);
     return p;
   }
-  // enough blocks to fill the GPU twice, none with less than 64 tokens
+  // fp32: enough blocks to fill the GPU twice, none with less than 64 tokens
   const long long blocks = (packed ? rows * r / 16 + s->B : ((long long)s->T * r / 16 + 1) * s->B) * s->Hk;
   p.splits = (int)std::max(1LL, std::min({(2LL * sms + blocks - 1) / blocks, (max_kv + 63LL) / 64, 64LL}));
   if (p.splits > 1) p.bytes = (size_t)p.splits * rows * s->Hq * (s->D + 2) * sizeof(float);
@@ -137,7 +142,7 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_shape *shape, int packed) {
   DeviceInfo dev;
   if (!shape || check_attn_shape(shape, packed != 0, &rows) != GDN_OK || check_heads(shape) != GDN_OK || device_info(&dev) != GDN_OK)
     return 0;
-  return attn_plan(shape, packed != 0, rows, bound_kv(shape, 1 << 30), dev.sms).bytes;
+  return attn_plan(shape, packed != 0, rows, bound_kv(shape, 1 << 30), dev.sms, true).bytes;
 }
 
 gdn_status gdn_attn(const gdn_attn_shape *shape, const gdn_attn_io *io, void *stream) {
@@ -172,7 +177,7 @@ gdn_status gdn_attn(const gdn_attn_shape *shape, const gdn_attn_io *io, void *st
   a.ldo = io->ldo;
   a.causal = io->causal != 0;
   a.scale = io->scale != 0.f ? io->scale : 1.0f / std::sqrt((float)shape->D);
-  const AttnPlan plan = attn_plan(shape, packed, rows, a.seq.max_kv, dev.sms);
+  const AttnPlan plan = attn_plan(shape, packed, rows, a.seq.max_kv, dev.sms, false);
   if (io->workspace && plan.bytes) {
     if (io->workspace_bytes < plan.bytes) return GDN_ERR_INVALID_ARG;
     a.ws = io->workspace;

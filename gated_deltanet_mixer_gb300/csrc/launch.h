@@ -253,7 +253,12 @@ cudaError_t launch_attn_rows(const AttnArgs &a, bool bf16, cudaStream_t s);
 int attn_few_rows(int D, long long rows);
 size_t attn_few_ws_bytes(int D, int rows_tile, int num_sms);
 cudaError_t launch_attn_few(const AttnArgs &a, int rows_tile, int num_sms, cudaStream_t s);
-cudaError_t launch_attn_tile(const AttnArgs &a, cudaStream_t s);  // bf16 io, many rows
+// bf16 io, many rows: the blocks of a call, the parts that its tokens are cut into, the partial results' bytes.
+long long attn_tile_blocks(const SeqArgs &q, int r, int Hk);
+int attn_tile_parts(long long blocks, long long max_kv, int num_sms);
+int attn_tile_most_parts(long long blocks, long long max_kv, int num_sms);
+size_t attn_tile_ws_bytes(long long blocks, int D, int parts);
+cudaError_t launch_attn_tile(const AttnArgs &a, cudaStream_t s);
 
 // Device error bits (the error word is OR-ed).
 constexpr unsigned int kErrTimeout = 1u;  // a bounded wait gave up
