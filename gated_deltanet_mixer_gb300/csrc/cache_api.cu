@@ -266,7 +266,6 @@ gdn_status gdn_rope(int tokens, int D, int io_dtype, const gdn_rope_plan *plan, 
     rx[i] = range_of(x[i].x, rows_bytes(tokens, x[i].ldx, width, el));
     ry[i] = range_of(x[i].y, rows_bytes(tokens, x[i].ldy, width, el));
     a.x[i] = gdn::RopeX{x[i].x, x[i].y, x[i].ldx, x[i].ldy, x[i].heads};
-    a.heads += x[i].heads;
   }
   for (int i = 0; i < n_x; ++i) {
     if (overlap(ry[i], rp)) return GDN_ERR_ALIAS;
@@ -284,7 +283,7 @@ gdn_status gdn_rope(int tokens, int D, int io_dtype, const gdn_rope_plan *plan, 
   DeviceInfo dev;
   const gdn_status st = device_info(&dev);
   if (st != GDN_OK) return st;
-  return gdn::launch_rope(a, io_dtype == GDN_BF16, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return gdn::launch_rope(a, io_dtype == GDN_BF16, dev.sms, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 gdn_status gdn_kv_pages(const gdn_kv_pages_io *io, void *stream) {

@@ -16,15 +16,16 @@ struct Seq {
   int kv;    // tokens in all
 };
 
-// The lengths of sequence b whose rows start at row0; b = -1 where they are out of range.
-__device__ __forceinline__ Seq load_seq(const SeqArgs &g, int b, int row0, int n) {
-  Seq s{b, row0, n, g.kv_lens[b]};
+// Sequence b with n rows from row0 on and kv tokens in all; b = -1 where the lengths are out of range.
+__device__ __forceinline__ Seq checked_seq(const SeqArgs &g, int b, int row0, int n, int kv) {
+  Seq s{b, row0, n, kv};
   if (n < 0 || n > g.max_new || s.kv < 0 || s.kv > g.max_kv) {
     atomicOr(g.err, kErrSeqlens);
     s.b = -1;
   }
   return s;
 }
+__device__ __forceinline__ Seq load_seq(const SeqArgs &g, int b, int row0, int n) { return checked_seq(g, b, row0, n, g.kv_lens[b]); }
 
 // Work items are numbered over the sequences without a prefix sum: those of
 // sequence b from base(b) = floor(cu[b] mul / div) + c b on, which leaves room for
@@ -45,30 +46,30 @@ __device__ __forceinline__ Seq find_seq(const SeqArgs &g, long long item, int mu
     *local = (int)(item % per);
     return load_seq(g, b, b * g.T, g.T);
   }
-  __shared__ int found, bad;
+  __shared__ Seq found;
+  __shared__ int bad;
   if (threadIdx.x == 0) {
-    found = -1;
+    found.b = -1;
     bad = 0;
   }
   __syncthreads();
   for (int b = threadIdx.x; b < g.B; b += blockDim.x) {
-    const int lo = g.cu[b], hi = g.cu[b + 1];
+    const int lo = g.cu[b], hi = g.cu[b + 1], kv = g.kv_lens[b];
     if (lo < 0 || hi < lo || hi > g.T) {
       bad = 1;
     } else if (item >= item_base(lo, b, mul, div, c) && item < item_base(hi, b + 1, mul, div, c)) {
-      found = b;
+      found = Seq{b, lo, hi - lo, kv};
     }
   }
   __syncthreads();
-  const int b = found;
+  const Seq s = found;
   if (bad) {
     if (threadIdx.x == 0) atomicOr(g.err, kErrSeqlens);
     return Seq{-1, 0, 0, 0};
   }
-  if (b < 0) return Seq{-1, 0, 0, 0};
-  const int lo = g.cu[b];
-  *local = (int)(item - item_base(lo, b, mul, div, c));
-  return load_seq(g, b, lo, g.cu[b + 1] - lo);
+  if (s.b < 0) return s;
+  *local = (int)(item - item_base(s.row0, s.b, mul, div, c));
+  return checked_seq(g, s.b, s.row0, s.n, s.kv);
 }
 
 // The page of block j of sequence b, or -1 (recorded) where the table has none.
@@ -103,8 +104,8 @@ template <>
 struct Io<true> {
   static constexpr int V = 8;
   using T = __nv_bfloat16;
-  static __device__ __forceinline__ void load(const T *p, float (&x)[8]) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+  static __device__ __forceinline__ void load(const T *p, float (&x)[8]) { unpack(*reinterpret_cast<const uint4 *>(p), x); }
+  static __device__ __forceinline__ void unpack(const uint4 &w, float (&x)[8]) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -124,9 +125,9 @@ template <>
 struct Io<false> {
   static constexpr int V = 4;
   using T = float;
-  static __device__ __forceinline__ void load(const T *p, float (&x)[4]) {
-    const float4 w = *reinterpret_cast<const float4 *>(p);
-    x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+  static __device__ __forceinline__ void load(const T *p, float (&x)[4]) { unpack(*reinterpret_cast<const uint4 *>(p), x); }
+  static __device__ __forceinline__ void unpack(const uint4 &w, float (&x)[4]) {
+    x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
   }
   static __device__ __forceinline__ void store(T *p, const float (&x)[4]) {
     *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);

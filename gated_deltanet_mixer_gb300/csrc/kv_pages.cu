@@ -67,12 +67,19 @@ __global__ void __launch_bounds__(1024) kv_pages_kernel(const PagesArgs a) {
     }
     if (lane == 31) warp_sums[warp] = sum;
     __syncthreads();
-    Sums before = total;
-    for (int w = 0; w < nwarps; ++w) {
-      const Sums s = warp_sums[w];
-      if (w < warp) before.tokens += s.tokens, before.pages += s.pages;
-      total.tokens += s.tokens, total.pages += s.pages;
+    // each warp scans the warps' sums for itself
+    Sums all = lane < nwarps ? warp_sums[lane] : Sums{0, 0};
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const Sums up = shfl_up(all, d);
+      if (lane >= d) all.tokens += up.tokens, all.pages += up.pages;
     }
+    Sums before = total;
+    const int prev = max(warp - 1, 0);
+    const long long t = __shfl_sync(0xffffffffu, all.tokens, prev), g = __shfl_sync(0xffffffffu, all.pages, prev);
+    if (warp > 0) before.tokens += t, before.pages += g;
+    total.tokens += __shfl_sync(0xffffffffu, all.tokens, 31);
+    total.pages += __shfl_sync(0xffffffffu, all.pages, 31);
     if (b < a.B) {  // sums past 31 bits make the call fail below
       tok_of[b] = (int)(before.tokens + sum.tokens - own.tokens);
       page_of[b] = (int)(before.pages + sum.pages - own.pages);

@@ -227,7 +227,7 @@ struct RopeX {
 };
 constexpr int kRopeMaxX = 4, kRopeMaxPairs = 128;
 struct RopeArgs {
-  int tokens, D, rot, interleaved, n_x, heads;  // heads: of all x
+  int tokens, D, rot, interleaved, n_x;
   int vec;                                      // 16-byte accesses allowed
   float m, sign;
   const int *positions;
@@ -245,7 +245,7 @@ struct PagesArgs {
 };
 constexpr int kPagesMaxB = 16384;
 cudaError_t launch_kv_pages(const PagesArgs &a, cudaStream_t s);
-cudaError_t launch_rope(const RopeArgs &a, bool bf16, cudaStream_t s);
+cudaError_t launch_rope(const RopeArgs &a, bool bf16, int num_sms, cudaStream_t s);
 cudaError_t launch_kv_append(const AppendArgs &a, bool bf16, cudaStream_t s);
 cudaError_t launch_attn_rows(const AttnArgs &a, bool bf16, cudaStream_t s);
 // bf16 io, few rows: the rows of a tile that hold `rows` rows of a sequence and

@@ -1,103 +1,159 @@
 // rope.cu -- rotary positions: the pair (a, b) of index i at position p becomes
 //   m (a cos x - b sin x, b cos x + a sin x),   x = p f_i.
 // The angle is kept as a 64-bit fraction of a turn, p * turns_i modulo 2^64: an
-// integer product has no error that grows with p, and its upper bits are the
-// angle in [-pi, pi) to fp32's precision for sincospi.
+// integer product has no error that grows with p, and its upper 32 bits are the
+// angle in [-pi, pi) to 2^-32 of a turn for sincospi.
 //
-// Bound by memory traffic: a block first forms the cosines and sines of its
-// tokens (shared by all heads), then its threads take 16-byte vectors.
+// Bound by memory traffic (in place that of the rotated elements alone).  A block
+// first forms the cosines and sines of its tokens, which all heads share; then
+// its threads take items of 16 bytes (or, where an address or a width does not
+// allow that, single pairs), two at a time, the first two asked for before that.
+#include <algorithm>
+
 #include "cache_device.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAtOnce = 2;
+
+// n / d for n < 2^22, d <= 2^10 (and for n < d <= 2^11): n m / 2^32 with m = floor(2^32 / d) + 1 is too large by
+// n (m d - 2^32) / (d 2^32) <= n / 2^32 < 1 / d.  (heads <= 2^12, D <= 2^10; a block of several tokens has at most 2^11
+// items.)
+struct FastDiv {
+  uint32_t d, m;
+};
+FastDiv fast_div(uint32_t d) { return FastDiv{d, d == 1 ? 0u : (uint32_t)((1ull << 32) / d + 1)}; }
+__device__ __forceinline__ uint32_t quotient(uint32_t n, FastDiv f) { return f.d == 1 ? n : __umulhi(n, f.m); }
+
+struct Items {
+  FastDiv of_token;            // items of a token, over all tensors
+  FastDiv of_head[kRopeMaxX];  // of a head: pairs' vectors, then (out of place) those of the elements that stay
+  int begin[kRopeMaxX];        // a tensor's first item of a token
+  int rot;                     // items of a head that turn
+  int per_block;               // tokens
+};
 
 template <bool kBf16, bool kVec>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, int per_block) {
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Items n) {
   using X = Io<kBf16>;
   using T = typename X::T;
   constexpr int V = kVec ? X::V : 1;
   extern __shared__ float2 turn[];  // [per_block][rot / 2]: m cos, m sin
   const int pairs = a.rot >> 1;
-  const long long t0 = (long long)blockIdx.x * per_block;
-  const int nt = (int)min((long long)per_block, a.tokens - t0);
+  const int t0 = blockIdx.x * n.per_block, nt = min(n.per_block, a.tokens - t0);
+  const uint32_t total = (uint32_t)nt * n.of_token.d;
+  const T *src[kAtOnce];
+  T *dst[kAtOnce];
+  int what[kAtOnce];  // the item of its head, -1: none
+  uint32_t token[kAtOnce];
+  uint4 lo[kAtOnce], hi[kAtOnce];
+  auto load = [&](uint32_t it0) {
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const uint32_t it = it0 + u * kThreads;
+      what[u] = -1;
+      if (it >= total) continue;
+      const uint32_t t = nt == 1 ? 0 : quotient(it, n.of_token), r = it - t * n.of_token.d;
+      int xi = 0;
+      while (xi + 1 < a.n_x && (int)r >= n.begin[xi + 1]) ++xi;
+      const uint32_t in = r - n.begin[xi], h = quotient(in, n.of_head[xi]);
+      const int j = (int)(in - h * n.of_head[xi].d);
+      src[u] = static_cast<const T *>(a.x[xi].x) + (long long)(t0 + t) * a.x[xi].ldx + (long long)h * a.D;
+      dst[u] = static_cast<T *>(a.x[xi].y) + (long long)(t0 + t) * a.x[xi].ldy + (long long)h * a.D;
+      what[u] = j;
+      token[u] = t;
+      if constexpr (kVec) {
+        const int at = j < n.rot ? j * V : a.rot + (j - n.rot) * V;
+        lo[u] = *reinterpret_cast<const uint4 *>(src[u] + at);
+        if (!a.interleaved && j < n.rot) hi[u] = *reinterpret_cast<const uint4 *>(src[u] + pairs + at);
+      }
+    }
+  };
+  load(threadIdx.x);  // on the way while the angles are formed
   for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
-    const unsigned long long f = (unsigned long long)(long long)a.positions[t0 + i / pairs] * a.turns[i % pairs];
+    const int t = i / pairs;
+    const unsigned long long x = (unsigned long long)(long long)a.positions[t0 + t] * a.turns[i - t * pairs];
     float s, c;
-    sincospif((float)(long long)f * 0x1p-63f, &s, &c);
+    sincospif((float)(int)((x + (1ull << 31)) >> 32) * 0x1p-31f, &s, &c);
     turn[i] = make_float2(a.m * c, a.m * a.sign * s);
   }
   __syncthreads();
-  // items of a head: vectors of pairs (half: V pairs from two places; interleaved: V elements), then, out of place,
-  // vectors of the elements that stay
-  const int items_rot = !kVec ? pairs : a.interleaved ? a.rot / V : pairs / V;
-  const int items_all = items_rot + (a.D - a.rot) / V;
-  int xi = 0, h0 = 0;
-  const int total = nt * a.heads * items_all;
-  for (int it = threadIdx.x; it < total; it += kThreads) {
-    const int j = it % items_all, th = it / items_all, h = th % a.heads, t = th / a.heads;
-    for (xi = 0, h0 = 0; h - h0 >= a.x[xi].heads; ++xi) h0 += a.x[xi].heads;
-    const RopeX &r = a.x[xi];
-    const T *const x = static_cast<const T *>(r.x) + (t0 + t) * r.ldx + (long long)(h - h0) * a.D;
-    T *const y = static_cast<T *>(r.y) + (t0 + t) * r.ldy + (long long)(h - h0) * a.D;
-    if (j >= items_rot) {
-      if (x == y) continue;
-      const int e = a.rot + (j - items_rot) * V;
-      if constexpr (kVec)
-        *reinterpret_cast<uint4 *>(y + e) = *reinterpret_cast<const uint4 *>(x + e);
-      else
-        y[e] = x[e];
-      continue;
-    }
-    const float2 *const cs = turn + t * pairs;
-    if constexpr (kVec) {
-      float u[V], w[V];
-      if (a.interleaved) {
-        X::load(x + j * V, u);
+  for (uint32_t it0 = threadIdx.x; it0 < total; it0 += kThreads * kAtOnce) {
+    if (it0 != threadIdx.x) load(it0);
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          const float2 f = cs[(j * V + i) >> 1];
-          w[i] = u[i] * f.x - u[i + 1] * f.y;
-          w[i + 1] = u[i + 1] * f.x + u[i] * f.y;
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int j = what[u];
+      if (j < 0) continue;
+      T *const y = dst[u];
+      const float2 *const cs = turn + token[u] * pairs;
+      if constexpr (kVec) {
+        if (j >= n.rot) {
+          *reinterpret_cast<uint4 *>(y + a.rot + (j - n.rot) * V) = lo[u];
+        } else if (a.interleaved) {
+          float x[V], w[V];
+          X::unpack(lo[u], x);
+#pragma unroll
+          for (int i = 0; i < V; i += 2) {
+            const float2 f = cs[(j * V + i) >> 1];
+            w[i] = x[i] * f.x - x[i + 1] * f.y;
+            w[i + 1] = x[i + 1] * f.x + x[i] * f.y;
+          }
+          X::store(y + j * V, w);
+        } else {
+          float x[V], w[V];
+          X::unpack(lo[u], x);
+          X::unpack(hi[u], w);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float2 f = cs[j * V + i];
+            const float p = x[i] * f.x - w[i] * f.y;
+            w[i] = w[i] * f.x + x[i] * f.y;
+            x[i] = p;
+          }
+          X::store(y + j * V, x);
+          X::store(y + pairs + j * V, w);
         }
-        X::store(y + j * V, w);
+      } else if (j >= n.rot) {
+        y[a.rot + j - n.rot] = src[u][a.rot + j - n.rot];
       } else {
-        X::load(x + j * V, u);
-        X::load(x + pairs + j * V, w);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float2 f = cs[j * V + i];
-          const float p = u[i] * f.x - w[i] * f.y;
-          w[i] = w[i] * f.x + u[i] * f.y;
-          u[i] = p;
-        }
-        X::store(y + j * V, u);
-        X::store(y + pairs + j * V, w);
+        const int ia = a.interleaved ? 2 * j : j, ib = a.interleaved ? 2 * j + 1 : j + pairs;
+        const float x = X::get(src[u] + ia), w = X::get(src[u] + ib);
+        const float2 f = cs[j];
+        X::put(y + ia, x * f.x - w * f.y);
+        X::put(y + ib, w * f.x + x * f.y);
       }
-    } else {
-      const int ia = a.interleaved ? 2 * j : j, ib = a.interleaved ? 2 * j + 1 : j + pairs;
-      const float u = X::get(x + ia), w = X::get(x + ib);
-      const float2 f = cs[j];
-      X::put(y + ia, u * f.x - w * f.y);
-      X::put(y + ib, w * f.x + u * f.y);
     }
   }
 }
 
 template <bool kBf16, bool kVec>
-cudaError_t launch(const RopeArgs &a, cudaStream_t s) {
-  const int per_block = a.tokens >= 4096 ? 4 : 1;
-  const long long blocks = ((long long)a.tokens + per_block - 1) / per_block;
-  rope_kernel<kBf16, kVec><<<(unsigned)blocks, kThreads, (size_t)per_block * (a.rot / 2) * sizeof(float2), s>>>(a, per_block);
+cudaError_t launch(const RopeArgs &a, int num_sms, cudaStream_t s) {
+  constexpr int V = kVec ? Io<kBf16>::V : 1;
+  Items n{};
+  n.rot = !kVec ? a.rot / 2 : a.interleaved ? a.rot / V : a.rot / (2 * V);
+  int all = 0;
+  for (int i = 0; i < a.n_x; ++i) {
+    const int of_head = n.rot + (a.x[i].x == a.x[i].y ? 0 : (a.D - a.rot) / V);
+    n.of_head[i] = fast_div(of_head);
+    n.begin[i] = all;
+    all += a.x[i].heads * of_head;
+  }
+  n.of_token = fast_div(all);
+  // Tokens of a block: what its threads take at once, if that leaves the GPU enough blocks.
+  const int want = std::max(1, kAtOnce * kThreads / all), spread = std::max(1, a.tokens / (4 * num_sms));
+  n.per_block = std::min({want, spread, 32});
+  const int blocks = (a.tokens + n.per_block - 1) / n.per_block;
+  rope_kernel<kBf16, kVec><<<blocks, kThreads, (size_t)n.per_block * (a.rot / 2) * sizeof(float2), s>>>(a, n);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeArgs &a, bool bf16, cudaStream_t s) {
-  return bf16 ? (a.vec ? launch<true, true>(a, s) : launch<true, false>(a, s))
-              : (a.vec ? launch<false, true>(a, s) : launch<false, false>(a, s));
+cudaError_t launch_rope(const RopeArgs &a, bool bf16, int num_sms, cudaStream_t s) {
+  return bf16 ? (a.vec ? launch<true, true>(a, num_sms, s) : launch<true, false>(a, num_sms, s))
+              : (a.vec ? launch<false, true>(a, num_sms, s) : launch<false, false>(a, num_sms, s));
 }
 
 }  // namespace gdn
