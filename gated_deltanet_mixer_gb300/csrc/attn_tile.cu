@@ -13,11 +13,11 @@
 // so far, enters p as a term of the exponent, and leaves the row's sum again as a
 // factor on the page's part of it: no product per element.
 //
-// Warps: groups of 4 for the softmax (thread = row), which take tiles in turns, 4
-// for the values, one for the keys (TMA) and one for the products.  For a tile of
-// 64 tokens and D = 256 the products take 1024 cycles; a tile's way through one
-// group of softmax warps is longer than that: two groups, and four for narrower
-// heads.  The running maximum goes from one to the other
+// Warps: 4 for the softmax (thread = row), 4 for the values, one for the keys
+// (TMA) and one for the products.  For a tile of 64 tokens and D = 256 the products
+// take 1024 cycles; a tile's way through the softmax is longer than that: two groups
+// of warps, which take tiles in turns.  Narrower heads have two blocks to an SM for
+// that.  The running maximum goes from one to the other
 // as soon as it is known, ahead of the exponentials; each keeps a sum of its own.
 #include <algorithm>
 
@@ -43,21 +43,24 @@ constexpr float kNoRef = -200.f;  // the logarithm of the value scales where the
 
 template <int D>
 struct Geo {
-  // Groups of softmax warps, and buffers of S, which they take in turns.
-  static constexpr int kGroups = 2;
+  // Blocks of an SM, and groups of softmax warps (as many as buffers of S, which they take in turns) of a block.  Where
+  // TMEM holds two blocks they take turns by themselves, and one works while the other starts or ends.
+  static constexpr int kBlocks = D == 256 ? 1 : 2, kGroups = D == 256 ? 2 : 1;
   static constexpr int kValueWarp = 4 * kGroups, kKeyWarp = kValueWarp + 4, kProductWarp = kKeyWarp + 1;
   static constexpr int kThreads = 32 * (kProductWarp + 1);
   // A softmax warp that waits for the products of tile j - 1 knows those of tile j - 1 - kGroups to be done, from the
   // scores that followed them: a slot of V, whose phases it tells apart by their parity, comes round no sooner.
-  static constexpr int kKStages = 4, kVStages = kGroups;
+  static constexpr int kKStages = 4, kVStages = 2;
+  static_assert(kVStages >= kGroups, "phases of V");
   static constexpr int kKBytes = kTile * D, kVBytes = kTile * D * 2;
   // the rows of q, then of o, on their way between global memory and the threads that have a row each
-  static constexpr int kPitch = (D == 256 ? 2 : 4) * D + 16;
+  static constexpr int kPitch = 2 * D + 16;
   static constexpr int kStage = kKStages * kKBytes + kVStages * kVBytes;
   static constexpr int kSmem = kStage + kRows * kPitch + 1024;
   // TMEM columns
   static constexpr int kQ = 0, kO = D / 2, kS = kO + D;
-  static constexpr int kCols = 512;
+  static constexpr int kCols = 512 / kBlocks;
+  static_assert(kS + kGroups * kTile <= kCols, "TMEM");
   // K-major rows of 128 bytes (D = 64: 64) with the swizzle of that width
   static constexpr int kRowBytes = D >= 128 ? 128 : 64;
 };
@@ -125,9 +128,15 @@ __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w, int high) {
   return o;
 }
 
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 struct Bars {
-  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[4], p_full[4], scales[kRing];
-  uint64_t moved[4][4];  // the running maximum after a tile, per warp
+  uint64_t k_full[4], k_empty[4], v_full[2], v_empty[2], s_full[2], p_full[2], scales[kRing];
+  uint64_t moved[2][4];  // the running maximum after a tile, per warp
 };
 
 // Entries of the table for the 16 tokens `sub` of a tile.  ask() loads one (kUnseen: its tokens are not looked
@@ -164,7 +173,7 @@ struct Scales {
 };
 
 template <int D>
-__global__ void __launch_bounds__(Geo<D>::kThreads, 1) attn_tile_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap) {
+__global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap) {
   using G = Geo<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars bars;
@@ -194,6 +203,8 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) attn_tile_kernel(const At
     for (int i = 0; i < 4; ++i) {
       bar_init(&bars.k_full[i], 1);
       bar_init(&bars.k_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       bar_init(&bars.s_full[i], 1);
       bar_init(&bars.p_full[i], 128);
       for (int w = 0; w < 4; ++w) bar_init(&bars.moved[i][w], 32);
@@ -202,6 +213,11 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) attn_tile_kernel(const At
     }
     for (int i = 0; i < kRing; ++i) bar_init(&bars.scales[i], 4);
     gave_up = 0;
+  }
+  if (tid < kRows) {
+    const int rr = first + tid, tok = rr / a.r;
+    row_q[tid] = (s.row0 + (long long)tok) * a.ldq + (long long)(hk * a.r + rr - tok * a.r) * D;
+    row_o[tid] = (s.row0 + (long long)tok) * a.ldo + (long long)(hk * a.r + rr - tok * a.r) * D;
   }
   if (warp == G::kProductWarp) tmem_alloc(&tmem_slot, G::kCols);
   fence_before();
@@ -229,21 +245,16 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) attn_tile_kernel(const At
     const bool real = row < count;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     constexpr int kChunks = D / 8;  // 16 bytes each, of a row
-    if (group == 0) {
-      row_q[row] = (s.row0 + (long long)tok) * a.ldq + (long long)(hk * a.r + rr - tok * a.r) * D;
-      row_o[row] = (s.row0 + (long long)tok) * a.ldo + (long long)(hk * a.r + rr - tok * a.r) * D;
-    }
-    sync_softmax();
-#pragma unroll 8
-    for (int x = tid; x < kRows * kChunks; x += 128 * G::kGroups) {
+#pragma unroll
+    for (int x = tid; x < kRows * kChunks; x += 128 * G::kGroups) {  // rows that are none become 0
       const int rw = x / kChunks, ch = x % kChunks;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (rw < count) w = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + row_q[rw] + ch * 8);
-      *reinterpret_cast<uint4 *>(stage + rw * G::kPitch + ch * 16) = w;
+      copy16(stage + rw * G::kPitch + ch * 16, static_cast<const __nv_bfloat16 *>(a.q) + (rw < count ? row_q[rw] + ch * 8 : 0), rw < count);
     }
+    copies_done();
     sync_softmax();
-    // q as hi + lo, times a power of two that brings the row's largest into [2^7, 2^8); half the columns to each of two groups
+    // q as hi + lo, times a power of two that brings the row's largest into [2^7, 2^8); a share of the columns to each group
     uint8_t *const mine = stage + row * G::kPitch;
+    constexpr int kShare = D / G::kGroups;
     float f;  // on a score, without its page's scale
     {
       uint32_t top = 0;
@@ -258,8 +269,8 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) attn_tile_kernel(const At
       const int e = top > 0 && !bad ? min(7 - ((int)(top >> 7) - 127), 120) : 0;
       const float up = (a.scale < 0.f ? -1.f : 1.f) * __uint_as_float((uint32_t)(e + 127) << 23);
       f = bad ? __int_as_float(0x7fc00000) : __uint_as_float((uint32_t)(127 - e) << 23) * (fabsf(a.scale) * kLog2e);
-#pragma unroll 1
-      for (int d = group * (D / 2); group < 2 && d < (group + 1) * (D / 2); d += 32) {
+#pragma unroll 2
+      for (int d = group * kShare; d < (group + 1) * kShare; d += 32) {
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -399,7 +410,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) attn_tile_kernel(const At
       fence_before();
       bar_arrive(&bars.p_full[group]);
     }
-    // ---- out: the groups' sums together, half the columns to each
+    // ---- out: the groups' sums together, a share of the columns to each
     if (ntiles > 0) {
       const int g_last = (ntiles - 1) % G::kGroups;
       wait(&bars.moved[g_last][quarter], ((ntiles - 1) / G::kGroups) & 1);
@@ -420,14 +431,14 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) attn_tile_kernel(const At
       const long long at = part_row(a, item, hk, blockIdx.z, gridDim.z) + row;
       if (group == 0) reinterpret_cast<float2 *>(part_ml(a, gridDim.x, gridDim.z, D))[at] = make_float2(ntiles > 0 ? m : -INFINITY, l);
       const float un = ex2(lref - kPExp);
-      constexpr int kRounds = D == 256 ? 2 : 1, kCols = D / (2 * kRounds);  // of a group in a round
+      constexpr int kRounds = 2, kCols = kShare / kRounds;  // of a group in a round
 #pragma unroll 1
       for (int h = 0; ntiles > 0 && h < kRounds; ++h) {
 #pragma unroll 1
-        for (int d = 0; group < 2 && d < kCols; d += 32) {
+        for (int d = 0; d < kCols; d += 32) {
           uint32_t w[32];
           __syncwarp();
-          tmem_ld32_nw(lanes + G::kO + group * (D / 2) + h * kCols + d, w);
+          tmem_ld32_nw(lanes + G::kO + group * kShare + h * kCols + d, w);
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
@@ -438,9 +449,9 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) attn_tile_kernel(const At
         sync_softmax();
         float *const dst = static_cast<float *>(a.ws) + (at - row) * D + h * kCols;
 #pragma unroll 4
-        for (int x = tid; x < count * (kCols / 2); x += 128 * G::kGroups) {
-          const int rw = x / (kCols / 2), ch = x % (kCols / 2), g = ch / (kCols / 4), col = ch % (kCols / 4) * 4;
-          *reinterpret_cast<float4 *>(dst + (long long)rw * D + g * (D / 2) + col) =
+        for (int x = tid; x < count * (D / 8); x += 128 * G::kGroups) {
+          const int rw = x / (D / 8), ch = x % (D / 8), g = ch / (kCols / 4), col = ch % (kCols / 4) * 4;
+          *reinterpret_cast<float4 *>(dst + (long long)rw * D + g * kShare + col) =
               *reinterpret_cast<const float4 *>(stage + rw * G::kPitch + ch * 16);
         }
         sync_softmax();
@@ -448,7 +459,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, 1) attn_tile_kernel(const At
     } else {
     const float inv = l == 0.f ? 0.f : ex2(lref - kPExp) / l;
 #pragma unroll 1
-    for (int d = group * (D / 2); group < 2 && d < (group + 1) * (D / 2); d += 32) {
+    for (int d = group * kShare; d < (group + 1) * kShare; d += 32) {
       uint32_t w[32];
       __syncwarp();
       tmem_ld32_nw(lanes + G::kO + d, w);
