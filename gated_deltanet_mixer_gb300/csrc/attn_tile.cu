@@ -4,7 +4,7 @@
 // over the tokens in tiles of 64 on the tensor cores, one pass with the running
 // maximum and sum of each row:
 //   S = Q K^T   e4m3 products straight on the cache's bytes, which TMA brings from
-//               the pages.  Q stands in TMEM as two e4m3 values per element, hi +
+//               the pages.  Q stands in TMEM (or shared memory) as two e4m3 values per element, hi +
 //               lo of q times a power of two per row (8 bits of a bf16 where it is
 //               within 2^10 of its row's largest; 2^-19 of that largest at worst).
 //   O += P V    fp16 products: P, rounded to fp16, in TMEM where S was; V's bytes
@@ -43,24 +43,26 @@ constexpr float kNoRef = -200.f;  // the logarithm of the value scales where the
 
 template <int D>
 struct Geo {
-  // Blocks of an SM, and groups of softmax warps (as many as buffers of S, which they take in turns) of a block.  Where
-  // TMEM holds two blocks they take turns by themselves, and one works while the other starts or ends.
-  static constexpr int kBlocks = D == 256 ? 1 : 2, kGroups = D == 256 ? 2 : 1;
+  // Blocks of an SM, groups of softmax warps of a block, which take tiles in turns, and buffers of S.  Where TMEM holds
+  // two blocks (Q is in shared memory then) they take turns by themselves, and one works while the other starts or ends.
+  static constexpr int kBlocks = D == 256 ? 1 : 2, kGroups = D == 256 ? 2 : 1, kBufs = 2;
+  static constexpr bool kQSmem = D < 256;
   static constexpr int kValueWarp = 4 * kGroups, kKeyWarp = kValueWarp + 4, kProductWarp = kKeyWarp + 1;
   static constexpr int kThreads = 32 * (kProductWarp + 1);
-  // A softmax warp that waits for the products of tile j - 1 knows those of tile j - 1 - kGroups to be done, from the
+  // A softmax warp that waits for the products of tile j - 1 knows those of tile j - 1 - kBufs to be done, from the
   // scores that followed them: a slot of V, whose phases it tells apart by their parity, comes round no sooner.
   static constexpr int kKStages = 4, kVStages = 2;
-  static_assert(kVStages >= kGroups, "phases of V");
-  static constexpr int kKBytes = kTile * D, kVBytes = kTile * D * 2;
-  // the rows of q, then of o, on their way between global memory and the threads that have a row each
-  static constexpr int kPitch = 2 * D + 16;
-  static constexpr int kStage = kKStages * kKBytes + kVStages * kVBytes;
-  static constexpr int kSmem = kStage + kRows * kPitch + 1024;
+  static_assert(kVStages >= kBufs, "phases of V");
+  static constexpr int kKBytes = kTile * D, kVBytes = kTile * D * 2, kQBytes = kQSmem ? 2 * kRows * D : 0;
+  // The rows of q, then of o, between global memory and the threads that have a row each: where V is before and after.
+  static constexpr int kRowPitch = 2 * D;
+  static_assert(kRows * kRowPitch <= kVStages * kVBytes, "rows");
+  static constexpr int kSmem = kKStages * kKBytes + kVStages * kVBytes + kQBytes + 1024;
   // TMEM columns
-  static constexpr int kQ = 0, kO = D / 2, kS = kO + D;
+  [[maybe_unused]] static constexpr int kQ = 0;
+  static constexpr int kO = kQSmem ? 0 : D / 2, kS = kO + D;
   static constexpr int kCols = 512 / kBlocks;
-  static_assert(kS + kGroups * kTile <= kCols, "TMEM");
+  static_assert(kS + kBufs * kTile <= kCols, "TMEM");
   // K-major rows of 128 bytes (D = 64: 64) with the swizzle of that width
   static constexpr int kRowBytes = D >= 128 ? 128 : 64;
 };
@@ -86,6 +88,14 @@ __device__ __forceinline__ void mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_
         "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}\n" ::"r"(d_tmem),
         "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(id), "n"(kAccumulate ? 1 : 0));
+}
+// The same of e4m3 operands, both in shared memory with the same strides.
+template <bool kAccumulate>
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t id) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(id), "n"(kAccumulate ? 1 : 0));
 }
 __device__ __forceinline__ void bar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -128,6 +138,16 @@ __device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w, int high) {
   return o;
 }
 
+// 16-byte chunk `ch` of a row of q or o in shared memory, turned so that neither rows nor chunks side by side share banks.
+template <int D>
+__device__ __forceinline__ uint32_t row_at(int row, int ch) {
+  return (uint32_t)(row * Geo<D>::kRowPitch + ((ch ^ (row & 7)) << 4));
+}
+// 16 e4m3 values of a row as an operand with K contiguous: rows of 128 bytes (64 for D = 64) with the swizzle of that width.
+template <int D>
+__device__ __forceinline__ uint32_t f8_at(int row, int ch) {
+  return D >= 128 ? (uint32_t)(row * 128 + ((ch ^ (row & 7)) << 4)) : (uint32_t)(row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
+}
 // 16 bytes from global to shared memory, or zeros.
 __device__ __forceinline__ void copy16(void *dst, const void *src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -135,7 +155,7 @@ __device__ __forceinline__ void copy16(void *dst, const void *src, bool there) {
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 struct Bars {
-  uint64_t k_full[4], k_empty[4], v_full[2], v_empty[2], s_full[2], p_full[2], scales[kRing];
+  uint64_t q_read, k_full[4], k_empty[4], v_full[2], v_empty[2], s_full[2], p_full[2], scales[kRing];
   uint64_t moved[2][4];  // the running maximum after a tile, per warp
 };
 
@@ -198,7 +218,8 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
   const int ntiles = max(0, min(part, all - base));
 
   uint8_t *const smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  uint8_t *const sk = smem, *const sv = smem + G::kKStages * G::kKBytes, *const stage = smem + G::kStage;
+  uint8_t *const sk = smem, *const sv = smem + G::kKStages * G::kKBytes, *const sq = sv + G::kVStages * G::kVBytes;
+  uint8_t *const stage = sv;
   if (tid == 0) {
     for (int i = 0; i < 4; ++i) {
       bar_init(&bars.k_full[i], 1);
@@ -212,6 +233,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
       bar_init(&bars.v_empty[i], 1);
     }
     for (int i = 0; i < kRing; ++i) bar_init(&bars.scales[i], 4);
+    bar_init(&bars.q_read, 128 * G::kGroups);
     gave_up = 0;
   }
   if (tid < kRows) {
@@ -248,19 +270,18 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
 #pragma unroll
     for (int x = tid; x < kRows * kChunks; x += 128 * G::kGroups) {  // rows that are none become 0
       const int rw = x / kChunks, ch = x % kChunks;
-      copy16(stage + rw * G::kPitch + ch * 16, static_cast<const __nv_bfloat16 *>(a.q) + (rw < count ? row_q[rw] + ch * 8 : 0), rw < count);
+      copy16(stage + row_at<D>(rw, ch), static_cast<const __nv_bfloat16 *>(a.q) + (rw < count ? row_q[rw] + ch * 8 : 0), rw < count);
     }
     copies_done();
     sync_softmax();
     // q as hi + lo, times a power of two that brings the row's largest into [2^7, 2^8); a share of the columns to each group
-    uint8_t *const mine = stage + row * G::kPitch;
     constexpr int kShare = D / G::kGroups;
     float f;  // on a score, without its page's scale
     {
       uint32_t top = 0;
 #pragma unroll 8
       for (int d = 0; d < D; d += 8) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(mine + 2 * d);
+        const uint4 w = *reinterpret_cast<const uint4 *>(stage + row_at<D>(row, d / 8));
         const uint32_t x[4] = {w.x & 0x7fff7fffu, w.y & 0x7fff7fffu, w.z & 0x7fff7fffu, w.w & 0x7fff7fffu};
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = max(top, max(x[i] & 0xffffu, x[i] >> 16));
@@ -274,7 +295,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
         uint32_t hi[8], lo[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint4 w = bad ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(mine + 2 * d + 16 * i);
+          const uint4 w = bad ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(stage + row_at<D>(row, d / 8 + i));
           const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -286,13 +307,28 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
             lo[2 * i + k] = float2_to_e4m3(v[0] - b0.x, v[1] - b0.y) | float2_to_e4m3(v[2] - b1.x, v[3] - b1.y) << 16;
           }
         }
-        __syncwarp();
-        tmem_st8w_nw(lanes + G::kQ + d / 4, hi);
-        tmem_st8w_nw(lanes + G::kQ + D / 4 + d / 4, lo);
+        if constexpr (G::kQSmem) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t at = f8_at<D>(row, d / 16 + i);
+            *reinterpret_cast<uint4 *>(sq + at) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+            *reinterpret_cast<uint4 *>(sq + kRows * D + at) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+          }
+        } else {
+          __syncwarp();
+          tmem_st8w_nw(lanes + G::kQ + d / 4, hi);
+          tmem_st8w_nw(lanes + G::kQ + D / 4 + d / 4, lo);
+        }
       }
-      tmem_wait_st();
+      if constexpr (G::kQSmem) {
+        fence_smem_to_async();
+      } else {
+        __syncwarp();
+        tmem_wait_st();
+      }
     }
     fence_before();
+    bar_arrive(&bars.q_read);  // V may come
     __syncwarp();
     sync_products();  // with the products' warp: Q is in place
     const int last = !real ? -1 : a.causal ? s.kv - s.n + tok : s.kv - 1;
@@ -300,17 +336,17 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
     float m = kNone, l = 0.f, lref = kNoRef;  // m: what l is relative to; the largest value scale's logarithm
 #pragma unroll 1
     for (int j = group; j < ntiles; j += G::kGroups) {
-      const uint32_t turn = j / G::kGroups;
+      const int buf = j % G::kBufs;
       wait(&bars.scales[j % kRing], (j / kRing) & 1);
       const Scales &sc = ring[j % kRing];
       const float4 ks4 = sc.ks, lvs = sc.lvs;
       const float ltop = fmaxf(fmaxf(lvs.x, lvs.y), fmaxf(lvs.z, lvs.w));
       const uint32_t flags = sc.flags;
       float fs[kSubs] = {f * ks4.x, f * ks4.y, f * ks4.z, f * ks4.w};
-      wait(&bars.s_full[group], turn & 1);
+      wait(&bars.s_full[buf], (j / G::kBufs) & 1);
       __syncwarp();
       fence_after();
-      const uint32_t scores = lanes + G::kS + group * kTile;
+      const uint32_t scores = lanes + G::kS + buf * kTile;
       const int tok0 = (base + j) * kTile;
       // Some row does not see all, or some value scale is NaN: then scores get their scales first, so that a scale
       // (NaN, 0) does not bring back what is not seen, and a NaN value scale reaches what is.
@@ -343,14 +379,14 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
         }
         __syncwarp();
       }
-      // the other group's word on the tile before
-      float mc = kNone;
-      if (j > 0) {
-        const int before = group == 0 ? G::kGroups - 1 : group - 1;
-        wait(&bars.moved[before][quarter], ((j - 1) / G::kGroups) & 1);
-        const float2 x = moved[before][row];
-        mc = x.x;
-        lref = x.y;
+      float mc = m;
+      if constexpr (G::kGroups > 1) {
+        if (j > 0) {  // the other group's word on the tile before
+          wait(&bars.moved[group ^ 1][quarter], ((j - 1) / G::kGroups) & 1);
+          const float2 x = moved[group ^ 1][row];
+          mc = x.x;
+          lref = x.y;
+        }
       }
       if (__any_sync(0xffffffffu, top > mc + kSlack || ltop > lref)) {
         const float mn = fmaxf(mc, top), ln = fmaxf(lref, ltop), shrink = ex2(mc - mn + (lref - ln));
@@ -371,8 +407,10 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
           }
         }
       }
-      moved[group][row] = make_float2(mc, lref);
-      bar_arrive(&bars.moved[group][quarter]);
+      if constexpr (G::kGroups > 1) {
+        moved[group][row] = make_float2(mc, lref);
+        bar_arrive(&bars.moved[group][quarter]);
+      }
       l *= ex2(m - mc);
       m = mc;
       // the value scales over the largest, in the exponent
@@ -408,22 +446,22 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
       }
       tmem_wait_st();
       fence_before();
-      bar_arrive(&bars.p_full[group]);
+      bar_arrive(&bars.p_full[buf]);
     }
     // ---- out: the groups' sums together, a share of the columns to each
-    if (ntiles > 0) {
-      const int g_last = (ntiles - 1) % G::kGroups;
-      wait(&bars.moved[g_last][quarter], ((ntiles - 1) / G::kGroups) & 1);
-      const float2 x = moved[g_last][row];
-      l *= ex2(m - x.x);
-      m = x.x;
-      lref = x.y;
+    if constexpr (G::kGroups > 1) {
+      if (ntiles > 0) {
+        const int g_last = (ntiles - 1) % G::kGroups;
+        wait(&bars.moved[g_last][quarter], ((ntiles - 1) / G::kGroups) & 1);
+        const float2 x = moved[g_last][row];
+        l *= ex2(m - x.x);
+        m = x.x;
+        lref = x.y;
+      }
+      other[group][row] = l;
+      sync_softmax();
+      l += other[group ^ 1][row];
     }
-    other[group][row] = l;
-    sync_softmax();
-    l = 0.f;
-#pragma unroll
-    for (int g = 0; g < G::kGroups; ++g) l += other[g][row];
     if (ntiles > 0) wait(&bars.v_empty[(ntiles - 1) % G::kVStages], ((ntiles - 1) / G::kVStages) & 1);
     __syncwarp();
     fence_after();
@@ -442,7 +480,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4 *>(mine + (group * kCols + d + i) * 4) =
+            *reinterpret_cast<float4 *>(stage + row_at<D>(row, (group * kCols + d + i) / 4)) =
                 make_float4(__uint_as_float(w[i]) * un, __uint_as_float(w[i + 1]) * un, __uint_as_float(w[i + 2]) * un,
                             __uint_as_float(w[i + 3]) * un);
         }
@@ -452,7 +490,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
         for (int x = tid; x < count * (D / 8); x += 128 * G::kGroups) {
           const int rw = x / (D / 8), ch = x % (D / 8), g = ch / (kCols / 4), col = ch % (kCols / 4) * 4;
           *reinterpret_cast<float4 *>(dst + (long long)rw * D + g * kShare + col) =
-              *reinterpret_cast<const float4 *>(stage + rw * G::kPitch + ch * 16);
+              *reinterpret_cast<const float4 *>(stage + row_at<D>(rw, ch));
         }
         sync_softmax();
       }
@@ -470,7 +508,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           o[k] = ntiles > 0 ? pack_bf16(__uint_as_float(w[i + 2 * k]) * inv, __uint_as_float(w[i + 2 * k + 1]) * inv) : 0u;
-        *reinterpret_cast<uint4 *>(mine + 2 * (d + i)) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(stage + row_at<D>(row, (d + i) / 8)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
     sync_softmax();
@@ -478,7 +516,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
     for (int x = tid; x < count * kChunks; x += 128 * G::kGroups) {
       const int rw = x / kChunks, ch = x % kChunks;
       *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + row_o[rw] + ch * 8) =
-          *reinterpret_cast<const uint4 *>(stage + rw * G::kPitch + ch * 16);
+          *reinterpret_cast<const uint4 *>(stage + row_at<D>(rw, ch));
     }
     }
     fence_before();
@@ -542,6 +580,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
     };
     prepare(0, x[0]);
     prepare(1, x[1]);
+    wait(&bars.q_read, 0);
 #pragma unroll 1
     for (int j = 0; j < ntiles; j += 2) {
       if ((j & 31) == 16) {
@@ -591,7 +630,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
     // swizzle of that width, 8 rows in 512 bytes).
     constexpr uint32_t k_hi = D >= 128 ? 1024 >> 4 | 1 << 14 | 2u << 29 : 512 >> 4 | 1 << 14 | 4u << 29;
     constexpr uint32_t v_hi = 1024 >> 4 | 1 << 14 | 2u << 29;
-    const uint32_t k_lo = smem_u32(sk) >> 4 | 1 << 16, v_lo = smem_u32(sv) >> 4 | (uint32_t)(kTile / 8 * 1024 >> 4) << 16;
+    const uint32_t q_lo = smem_u32(sq) >> 4 | 1 << 16, k_lo = smem_u32(sk) >> 4 | 1 << 16, v_lo = smem_u32(sv) >> 4 | (uint32_t)(kTile / 8 * 1024 >> 4) << 16;
     __syncwarp();
     sync_products();
     fence_after();
@@ -601,33 +640,42 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
       __syncwarp();
       fence_after();
       if (elect()) {
-        const uint32_t lo = k_lo + slot * (G::kKBytes >> 4), d = tmem + G::kS + (j % G::kGroups) * kTile;
+        const uint32_t lo = k_lo + slot * (G::kKBytes >> 4), d = tmem + G::kS + (j % G::kBufs) * kTile;
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int ks = 0; ks < D / 32; ++ks) {
-            const uint32_t at = lo + (((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4), q = tmem + G::kQ + part * (D / 4) + ks * 8;
-            if (part + ks == 0)
-              mma_ta<true, false>(d, q, at, k_hi, id_s);
-            else
-              mma_ta<true, true>(d, q, at, k_hi, id_s);
+            const uint32_t at = lo + (((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4);
+            if constexpr (G::kQSmem) {
+              const uint32_t q = q_lo + ((part * kRows * D + ks * 32) >> 4);
+              if (part + ks == 0)
+                mma_f8_ss<false>(d, q, at, k_hi, id_s);
+              else
+                mma_f8_ss<true>(d, q, at, k_hi, id_s);
+            } else {
+              const uint32_t q = tmem + G::kQ + part * (D / 4) + ks * 8;
+              if (part + ks == 0)
+                mma_ta<true, false>(d, q, at, k_hi, id_s);
+              else
+                mma_ta<true, true>(d, q, at, k_hi, id_s);
+            }
           }
-        commit(&bars.s_full[j % G::kGroups]);
+        commit(&bars.s_full[j % G::kBufs]);
         commit(&bars.k_empty[slot]);
       }
       __syncwarp();
     };
 #pragma unroll 1
-    for (int j = 0; j < min(ntiles, G::kGroups); ++j) scores(j);
+    for (int j = 0; j < min(ntiles, G::kBufs); ++j) scores(j);
 #pragma unroll 1
     for (int j = 0; j < ntiles; ++j) {
       const int slot = j % G::kVStages;
       wait(&bars.v_full[slot], (j / G::kVStages) & 1);
-      wait(&bars.p_full[j % G::kGroups], (j / G::kGroups) & 1);
+      wait(&bars.p_full[j % G::kBufs], (j / G::kBufs) & 1);
       __syncwarp();
       fence_after();
       if (elect()) {
-        const uint32_t lo = v_lo + slot * (G::kVBytes >> 4), p = tmem + G::kS + (j % G::kGroups) * kTile;
+        const uint32_t lo = v_lo + slot * (G::kVBytes >> 4), p = tmem + G::kS + (j % G::kBufs) * kTile;
         if (j == 0)
           mma_ta<false, false>(tmem + G::kO, p, lo, v_hi, id_o);
         else
@@ -637,7 +685,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
         commit(&bars.v_empty[slot]);
       }
       __syncwarp();
-      if (j + G::kGroups < ntiles) scores(j + G::kGroups);  // where P was: products follow each other
+      if (j + G::kBufs < ntiles) scores(j + G::kBufs);  // where P was: products follow each other
     }
   }
   fence_before();
