@@ -439,13 +439,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
     const uint32_t k_at0 = gr0 * G::kGroup + 2 * bg * D + 16 * t, k_at1 = gr1 * G::kGroup + (2 * bg + 1) * D + 16 * t;
 
     auto wait = [&](uint32_t slot, uint32_t phase) {
-      if (bar_try_wait(bar + slot, phase)) return;
-      const uint64_t t0 = global_ns();
-      while (!gave_up && !bar_try_wait(bar + slot, phase))
-        if (global_ns() - t0 > 1000000000ull) {
-          gave_up = 1;  // what follows is not right, and stays in its bounds
-          atomicOr(a.seq.err, kErrTimeout);
-        }
+      if (!bar_try_wait(bar + slot, phase)) {
+        const uint64_t t0 = global_ns();
+        while (!gave_up && !bar_try_wait(bar + slot, phase))
+          if (global_ns() - t0 > 1000000000ull) {
+            gave_up = 1;  // what follows is not right, and stays in its bounds
+            atomicOr(a.seq.err, kErrTimeout);
+          }
+      }
+      __syncwarp();
     };
     // S^T of a slab; 16 tokens alone in two chains of products
     auto scores = [&](uint32_t slot, float (&st)[SUB][NT][4]) {

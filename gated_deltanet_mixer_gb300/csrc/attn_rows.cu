@@ -48,9 +48,9 @@ __device__ __forceinline__ float2 *part_ml(const AttnArgs &a, int splits, int z,
   return reinterpret_cast<float2 *>(static_cast<float *>(a.ws) + splits * rows * D) + z * rows + row;
 }
 
-template <bool kBf16, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnArgs a, int chunk) {
-  using X = Io<kBf16>;
+  using X = Io<false>;
   using T = typename X::T;
   constexpr int C = D / 32;  // columns of a lane: 2 lane + 64 i, two at a time
   extern __shared__ float4 smem4[];
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnArgs a, i
     if (row < span.count)
       X::load(static_cast<const T *>(a.q) + (long long)(s.row0 + rr / a.r) * a.ldq + (long long)(hk * a.r + rr % a.r) * D + col, x);
 #pragma unroll
-    for (int u = 0; u < X::V; ++u) sq[row * D + col + u] = x[u];
+    for (int u = 0; u < X::V; ++u) sq[row * D + col + u] = fabsf(x[u]) < INFINITY ? x[u] : __int_as_float(0x7fc00000);
   }
   int last[kRowsWarp];  // of the tokens each row sees
   float m[kRowsWarp], l[kRowsWarp], o[kRowsWarp][C];
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnArgs a, i
       const long long head = (long long)p * c.Hk + hk;
       if (p >= 0)
         w = *reinterpret_cast<const uint4 *>((is_v ? c.v : c.k) + (head * page + (t & (page - 1))) * D + col);
-      if (col == 0) {  // NaN: a token that is not there
+      if (col == 0) {  // a key scale below 0: a token that is not there
         if (is_v)
           svs[tok] = p >= 0 ? c.vs[head] : 0.f;
         else
@@ -131,7 +131,6 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnArgs a, i
     const int t = t0 + lane;
 #pragma unroll
     for (int i = 0; i < kRowsWarp; ++i) {
-      // A k scale below 0 stands for a missing page (a NaN one is seen).
       const bool sees = t <= last[i] && t < hi && !(ks < 0.f);
       const float x = sees ? sc[i] * scale * ks : -INFINITY;
       float top = x;
@@ -192,9 +191,9 @@ __global__ void __launch_bounds__(kThreads) attn_rows_kernel(const AttnArgs a, i
 }
 
 // Joins the partial results of a block's rows: o = sum_z 2^(m_z - m) o_z / sum_z 2^(m_z - m) l_z.
-template <bool kBf16, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) attn_rows_join(const AttnArgs a, int splits) {
-  using X = Io<kBf16>;
+  using X = Io<false>;
   using T = typename X::T;
   constexpr int C = D / 32;
   const RowSpan span = row_span(a);
@@ -227,31 +226,26 @@ __global__ void __launch_bounds__(kThreads) attn_rows_join(const AttnArgs a, int
   }
 }
 
-template <bool kBf16, int D>
+template <int D>
 struct RowsTag {};
 
-template <bool kBf16, int D>
+template <int D>
 cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
-  cudaError_t e = allow_smem<RowsTag<kBf16, D>>(attn_rows_kernel<kBf16, D>, smem_bytes<D>());
+  cudaError_t e = allow_smem<RowsTag<D>>(attn_rows_kernel<D>, smem_bytes<D>());
   if (e != cudaSuccess) return e;
   const int splits = a.ws ? a.splits : 1;
   const int chunk = ((a.seq.max_kv + splits - 1) / splits + kTile - 1) / kTile * kTile;
   const dim3 grid((unsigned)item_count(a.seq, a.r, kRows, 1), a.cache.Hk, splits);
-  attn_rows_kernel<kBf16, D><<<grid, kThreads, smem_bytes<D>(), s>>>(a, chunk);
+  attn_rows_kernel<D><<<grid, kThreads, smem_bytes<D>(), s>>>(a, chunk);
   e = cudaGetLastError();
   if (e != cudaSuccess || splits < 2) return e;
-  attn_rows_join<kBf16, D><<<dim3(grid.x, grid.y), kThreads, 0, s>>>(a, splits);
+  attn_rows_join<D><<<dim3(grid.x, grid.y), kThreads, 0, s>>>(a, splits);
   return cudaGetLastError();
 }
-template <bool kBf16>
-cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
-  return a.cache.D == 64 ? launch<kBf16, 64>(a, s) : a.cache.D == 128 ? launch<kBf16, 128>(a, s) : launch<kBf16, 256>(a, s);
-}
-
 }  // namespace
 
-cudaError_t launch_attn_rows(const AttnArgs &a, bool bf16, cudaStream_t s) {
-  return bf16 ? launch<true>(a, s) : launch<false>(a, s);
+cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t s) {
+  return a.cache.D == 64 ? launch<64>(a, s) : a.cache.D == 128 ? launch<128>(a, s) : launch<256>(a, s);
 }
 
 }  // namespace gdn

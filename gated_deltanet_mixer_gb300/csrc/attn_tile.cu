@@ -259,8 +259,14 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
   const TilePages pages{c, c.table + (long long)s.b * c.table_ld, base, min(seen, (base + ntiles) * kTile), a.seq.err};
   const int page = 1 << c.page_shift;
 
-  auto sync_softmax = [] { asm volatile("bar.sync 2, %0;" ::"n"(128 * G::kGroups) : "memory"); };
-  auto sync_products = [] { asm volatile("bar.sync 1, %0;" ::"n"(128 * G::kGroups + 32) : "memory"); };
+  auto sync_softmax = [] {
+    __syncwarp();
+    asm volatile("bar.sync 2, %0;" ::"n"(128 * G::kGroups) : "memory");
+  };
+  auto sync_products = [] {
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"n"(128 * G::kGroups + 32) : "memory");
+  };
   if (warp < G::kValueWarp) {
     // ---------------------------------------------------------------- softmax
     const int group = warp >> 2, quarter = warp & 3, row = tid & (kRows - 1), rr = first + row, tok = rr / a.r;

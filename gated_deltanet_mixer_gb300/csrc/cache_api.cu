@@ -145,6 +145,20 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_shape *shape, int packed) {
   return attn_plan(shape, packed != 0, rows, bound_kv(shape, 1 << 30), dev.sms, true).bytes;
 }
 
+gdn_status gdn_selftest_attn_form(const gdn_attn_shape *shape, int packed, int workspace, gdn_attn_form *form) {
+  if (!shape || !form) return GDN_ERR_INVALID_ARG;
+  long long rows = 0;
+  DeviceInfo dev;
+  gdn_status st = check_attn_shape(shape, packed != 0, &rows);
+  if (st == GDN_OK) st = check_heads(shape);
+  if (st == GDN_OK) st = device_info(&dev);
+  if (st != GDN_OK) return st;
+  const AttnPlan p = attn_plan(shape, packed != 0, rows, bound_kv(shape, 1 << 30), dev.sms, false);
+  *form = gdn_attn_form{p.few_rows ? GDN_ATTN_FEW : p.tile ? GDN_ATTN_TILE : GDN_ATTN_ROWS, p.few_rows ? p.few_rows : p.tile ? 128 : 16,
+                        p.few_rows ? 0 : workspace ? p.splits : 1};
+  return GDN_OK;
+}
+
 gdn_status gdn_attn(const gdn_attn_shape *shape, const gdn_attn_io *io, void *stream) {
   if (!shape || !io || !io->q || !io->o) return GDN_ERR_INVALID_ARG;
   const bool packed = io->cu_seqlens != nullptr;
@@ -185,7 +199,7 @@ gdn_status gdn_attn(const gdn_attn_shape *shape, const gdn_attn_io *io, void *st
   a.splits = plan.splits;
   const cudaError_t e = plan.few_rows ? gdn::launch_attn_few(a, plan.few_rows, dev.sms, (cudaStream_t)stream)
                         : plan.tile   ? gdn::launch_attn_tile(a, (cudaStream_t)stream)
-                                      : gdn::launch_attn_rows(a, shape->io_dtype == GDN_BF16, (cudaStream_t)stream);
+                                      : gdn::launch_attn_rows(a, (cudaStream_t)stream);
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -247,7 +247,7 @@ constexpr int kPagesMaxB = 16384;
 cudaError_t launch_kv_pages(const PagesArgs &a, cudaStream_t s);
 cudaError_t launch_rope(const RopeArgs &a, bool bf16, int num_sms, cudaStream_t s);
 cudaError_t launch_kv_append(const AppendArgs &a, bool bf16, cudaStream_t s);
-cudaError_t launch_attn_rows(const AttnArgs &a, bool bf16, cudaStream_t s);
+cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t s);  // fp32 io
 // bf16 io, few rows: the rows of a tile that hold `rows` rows of a sequence and
 // key head (0: too many), the partial results' bytes, the launches.
 int attn_few_rows(int D, long long rows);

@@ -104,6 +104,10 @@ class gdn_attn_io(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
+class gdn_attn_form(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("kernel", "rows", "parts")]
+
+
 class gdn_rope_plan_t(ctypes.Structure):  # gdn_rope_plan of the header
     _fields_ = [("rot", ctypes.c_int), ("layout", ctypes.c_int), ("m", ctypes.c_float), ("turns", ctypes.c_ulonglong * 128)]
 
@@ -176,6 +180,8 @@ def lib():
             getattr(L, name).argtypes = [vp, vp, vp]  # structures by reference, or packed bytes
         L.gdn_attn_workspace_bytes.restype = ctypes.c_size_t
         L.gdn_attn_workspace_bytes.argtypes = [ctypes.POINTER(gdn_attn_shape), ctypes.c_int]
+        L.gdn_selftest_attn_form.restype = ctypes.c_int
+        L.gdn_selftest_attn_form.argtypes = [ctypes.POINTER(gdn_attn_shape), ctypes.c_int, ctypes.c_int, ctypes.POINTER(gdn_attn_form)]
         L.gdn_rope_plan_init.restype = ctypes.c_int
         L.gdn_rope_plan_init.argtypes = [ctypes.POINTER(gdn_rope_spec), ctypes.POINTER(gdn_rope_plan_t)]
         L.gdn_rope.restype = ctypes.c_int
@@ -630,6 +636,15 @@ def gdn_attn_workspace_bytes(B, T, Hq, Hk, D, *, max_new=0, max_kv=0, packed=Tru
     """Workspace bytes of gdn_attn (packed: T is the total token count)."""
     sh = gdn_attn_shape(B, T, Hq, Hk, D, GDN_BF16 if io_dtype is None else io_dtype, max_new, max_kv)
     return lib().gdn_attn_workspace_bytes(ctypes.byref(sh), 1 if packed else 0)
+
+
+def gdn_selftest_attn_form(B, T, Hq, Hk, D, *, max_new=0, max_kv=0, packed=True, workspace=True, io_dtype=None):
+    """How gdn_attn runs this shape (gdn_selftest_attn_form)."""
+    sh, f = gdn_attn_shape(B, T, Hq, Hk, D, GDN_BF16 if io_dtype is None else io_dtype, max_new, max_kv), gdn_attn_form()
+    st = lib().gdn_selftest_attn_form(ctypes.byref(sh), int(packed), int(workspace), ctypes.byref(f))
+    if st != GDN_OK:
+        raise GdnError(st, "gdn_selftest_attn_form")
+    return f
 
 
 def gdn_rope_plan(rot, *, base=10000.0, layout="half", scaling=None):

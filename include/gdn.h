@@ -475,7 +475,7 @@ gdn_status gdn_selftest_linattn_form(const gdn_shape *shape, int packed, int wor
  */
 typedef struct {
   int B, T;
-  int Hq, Hk;     /* query heads, key heads; Hq % Hk == 0, at most 64 query heads to a key head */
+  int Hq, Hk;     /* query heads, key heads; Hq % Hk == 0, at most 64 query heads to a key head, Hk <= 1024 */
   int D;
   int io_dtype;   /* gdn_dtype of q, k, v and o */
   int max_new, max_kv;
@@ -531,8 +531,13 @@ gdn_status gdn_kv_append(const gdn_attn_shape *shape, const gdn_kv_append_io *io
  * v scale is NaN gives NaN.  Scales are 0 <= s <= 2^7.  In the bytes there is no
  * NaN (0x7f, 0xff; gdn_kv_append writes none): where there is one among the
  * tokens seen, what it is taken for is not specified.
- * bf16 io: products of exact 16-bit operands on the tensor cores, p rounded to
- * 16 bits, sums and softmax in fp32.  fp32 io: fp32 throughout.
+ * bf16 io: products on the tensor cores, of the bytes themselves, of q (for many
+ * rows to within 2^-19 of the largest of its row and head) and of p rounded to
+ * fp16; scores, softmax and sums in fp32.  fp32 io: fp32 throughout.  A NaN or
+ * infinity in a head of q makes that row and head NaN.
+ * max_new and max_kv choose how the call runs: a few rows (new tokens x Hq / Hk) of
+ * each sequence and key head side by side, or tiles of 128 rows.  A batch of
+ * prompts and of single tokens is faster as two calls.
  */
 typedef struct {
   const void *q;
@@ -552,6 +557,22 @@ gdn_status gdn_attn(const gdn_attn_shape *shape, const gdn_attn_io *io, void *st
  * for gdn_linattn_workspace_bytes); 0 where the call uses none or the shape is
  * invalid. */
 size_t gdn_attn_workspace_bytes(const gdn_attn_shape *shape, int packed);
+
+/* How gdn_attn runs a shape on the current device (packed as above; workspace !=
+ * 0: the call has one; max_kv 0 stands for long sequences), for tests that mean one form. */
+typedef enum {
+  GDN_ATTN_ROWS = 0, /* fp32 arithmetic (fp32 io) */
+  GDN_ATTN_FEW = 1,  /* bf16, few rows: work cut evenly over the GPU */
+  GDN_ATTN_TILE = 2  /* bf16, tiles of 128 rows */
+} gdn_attn_kernel;
+
+typedef struct {
+  int kernel; /* gdn_attn_kernel */
+  int rows;   /* of a tile */
+  int parts;  /* ranges of the tokens side by side; FEW: 0, they follow from the lengths */
+} gdn_attn_form;
+
+gdn_status gdn_selftest_attn_form(const gdn_attn_shape *shape, int packed, int workspace, gdn_attn_form *form);
 
 /*
  * Rotary positions on the first `rot` elements of every head ("How Qwen3.5
