@@ -267,7 +267,6 @@ gdn_status gdn_rope(int tokens, int D, int io_dtype, const gdn_rope_plan *plan, 
   a.m = plan->m;
   a.sign = inverse ? -1.f : 1.f;
   a.positions = positions;
-  std::memcpy(a.turns, plan->turns, sizeof a.turns);
   a.vec = D % V == 0 && plan->rot % (a.interleaved ? V : 2 * V) == 0;
   Range rx[gdn::kRopeMaxX], ry[gdn::kRopeMaxX];
   const Range rp = range_of(positions, (size_t)tokens * 4);
@@ -297,7 +296,7 @@ gdn_status gdn_rope(int tokens, int D, int io_dtype, const gdn_rope_plan *plan, 
   DeviceInfo dev;
   const gdn_status st = device_info(&dev);
   if (st != GDN_OK) return st;
-  return gdn::launch_rope(a, io_dtype == GDN_BF16, dev.sms, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return gdn::launch_rope(a, plan->turns, io_dtype == GDN_BF16, dev.sms, (cudaStream_t)stream) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 gdn_status gdn_kv_pages(const gdn_kv_pages_io *io, void *stream) {

@@ -226,13 +226,17 @@ struct RopeX {
   int heads;
 };
 constexpr int kRopeMaxX = 4, kRopeMaxPairs = 128;
+// The frequencies of a launch: its parameters are copied per call, so most calls take the short form.
+template <int kPairs>
+struct RopeTurns {
+  unsigned long long at[kPairs];
+};
 struct RopeArgs {
   int tokens, D, rot, interleaved, n_x;
   int vec;                                      // 16-byte accesses allowed
   float m, sign;
   const int *positions;
   RopeX x[kRopeMaxX];
-  unsigned long long turns[kRopeMaxPairs];
 };
 struct PagesArgs {
   int B, page_shift, max_blocks, n_free;
@@ -245,7 +249,7 @@ struct PagesArgs {
 };
 constexpr int kPagesMaxB = 16384;
 cudaError_t launch_kv_pages(const PagesArgs &a, cudaStream_t s);
-cudaError_t launch_rope(const RopeArgs &a, bool bf16, int num_sms, cudaStream_t s);
+cudaError_t launch_rope(const RopeArgs &a, const unsigned long long *turns, bool bf16, int num_sms, cudaStream_t s);
 cudaError_t launch_kv_append(const AppendArgs &a, bool bf16, cudaStream_t s);
 cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t s);  // fp32 io
 // bf16 io, few rows: the rows of a tile that hold `rows` rows of a sequence and

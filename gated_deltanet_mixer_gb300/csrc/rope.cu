@@ -35,8 +35,9 @@ struct Items {
   int per_block;               // tokens
 };
 
-template <bool kBf16, bool kVec>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Items n) {
+template <bool kBf16, bool kVec, int kPairs>
+__global__ void __launch_bounds__(kThreads)
+    rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Items n, const __grid_constant__ RopeTurns<kPairs> turns) {
   using X = Io<kBf16>;
   using T = typename X::T;
   constexpr int V = kVec ? X::V : 1;
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   load(threadIdx.x);  // on the way while the angles are formed
   for (int i = threadIdx.x; i < nt * pairs; i += kThreads) {
     const int t = i / pairs;
-    const unsigned long long x = (unsigned long long)(long long)a.positions[t0 + t] * a.turns[i - t * pairs];
+    const unsigned long long x = (unsigned long long)(long long)a.positions[t0 + t] * turns.at[i - t * pairs];
     float s, c;
     sincospif((float)(int)((x + (1ull << 31)) >> 32) * 0x1p-31f, &s, &c);
     turn[i] = make_float2(a.m * c, a.m * a.sign * s);
@@ -128,8 +129,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   }
 }
 
-template <bool kBf16, bool kVec>
-cudaError_t launch(const RopeArgs &a, int num_sms, cudaStream_t s) {
+template <bool kBf16, bool kVec, int kPairs>
+cudaError_t launch(const RopeArgs &a, const unsigned long long *turns, int num_sms, cudaStream_t s) {
   constexpr int V = kVec ? Io<kBf16>::V : 1;
   Items n{};
   n.rot = !kVec ? a.rot / 2 : a.interleaved ? a.rot / V : a.rot / (2 * V);
@@ -145,15 +146,21 @@ cudaError_t launch(const RopeArgs &a, int num_sms, cudaStream_t s) {
   const int want = std::max(1, kAtOnce * kThreads / all), spread = std::max(1, a.tokens / (4 * num_sms));
   n.per_block = std::min({want, spread, 32});
   const int blocks = (a.tokens + n.per_block - 1) / n.per_block;
-  rope_kernel<kBf16, kVec><<<blocks, kThreads, (size_t)n.per_block * (a.rot / 2) * sizeof(float2), s>>>(a, n);
+  RopeTurns<kPairs> f{};
+  std::copy(turns, turns + a.rot / 2, f.at);
+  rope_kernel<kBf16, kVec, kPairs><<<blocks, kThreads, (size_t)n.per_block * (a.rot / 2) * sizeof(float2), s>>>(a, n, f);
   return cudaGetLastError();
+}
+template <bool kBf16, bool kVec>
+cudaError_t launch(const RopeArgs &a, const unsigned long long *turns, int num_sms, cudaStream_t s) {
+  return a.rot <= 64 ? launch<kBf16, kVec, 32>(a, turns, num_sms, s) : launch<kBf16, kVec, kRopeMaxPairs>(a, turns, num_sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeArgs &a, bool bf16, int num_sms, cudaStream_t s) {
-  return bf16 ? (a.vec ? launch<true, true>(a, num_sms, s) : launch<true, false>(a, num_sms, s))
-              : (a.vec ? launch<false, true>(a, num_sms, s) : launch<false, false>(a, num_sms, s));
+cudaError_t launch_rope(const RopeArgs &a, const unsigned long long *turns, bool bf16, int num_sms, cudaStream_t s) {
+  return bf16 ? (a.vec ? launch<true, true>(a, turns, num_sms, s) : launch<true, false>(a, turns, num_sms, s))
+              : (a.vec ? launch<false, true>(a, turns, num_sms, s) : launch<false, false>(a, turns, num_sms, s));
 }
 
 }  // namespace gdn

@@ -555,31 +555,46 @@ def _int32(t, n, what):
 
 def _table(t, B):
     """(pointer, elements between rows, blocks of a row) of a block table [B, blocks]."""
-    if t.dtype != _I32 or t.dim() != 2 or t.shape[0] != B or t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape = t.shape
+    if t.dtype != _I32 or len(shape) != 2 or shape[0] != B or shape[1] < 1:
         raise ValueError("block_table is int32 [B, blocks]")
-    return t.data_ptr(), t.stride(0) if B > 1 else max(t.stride(0), t.shape[1]), t.shape[1]
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError("block_table: rows must be contiguous")
+    return t.data_ptr(), ld if B > 1 else max(ld, shape[1]), shape[1]
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens):
-    """(packed gdn_kv_cache, B, Hk, D)."""
-    P, Hk, page, D = k_cache.shape
-    for t in (k_cache, v_cache):
-        if t.dtype not in _CACHE_BYTES or t.shape != k_cache.shape or not t.is_contiguous():
-            raise ValueError("k_cache and v_cache are contiguous [pages, Hk, page, D] of float8_e4m3fn or uint8")
-    _fp32(k_scale, P * Hk, "k_scale")
-    _fp32(v_scale, P * Hk, "v_scale")
+    """(packed gdn_kv_cache, B, Hk, D).  Written out, like what follows: a single token's call is mostly this."""
+    shape = k_cache.shape
+    if (len(shape) != 4 or v_cache.shape != shape or k_cache.dtype not in _CACHE_BYTES or v_cache.dtype not in _CACHE_BYTES or
+            not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache are contiguous [pages, Hk, page, D] of float8_e4m3fn or uint8")
+    P, Hk, page, D = shape
+    n = P * Hk
+    if (k_scale.dtype != _F32 or v_scale.dtype != _F32 or k_scale.numel() != n or v_scale.numel() != n or
+            not k_scale.is_contiguous() or not v_scale.is_contiguous()):
+        raise ValueError("k_scale and v_scale: %d contiguous float32 values are wanted" % n)
     B = kv_lens.numel()
     table, ld, blocks = _table(block_table, B)
+    if kv_lens.dtype != _I32 or not kv_lens.is_contiguous():
+        raise ValueError("kv_lens: contiguous int32 values are wanted")
     return _PACK_CACHE.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, page, table,
-                            ld, blocks, _int32(kv_lens, B, "kv_lens")), B, Hk, D
+                            ld, blocks, kv_lens.data_ptr()), B, Hk, D
 
 
 def _new_rows(t, B, cu_seqlens, what):
     """(rows of a sequence or in all, width, stride) of the new tokens' tensor."""
-    Bt, T, C, ld = _token_rows(t, what)
-    if (cu_seqlens is None) != (t.dim() == 3) or (Bt and Bt != B):
+    shape = t.shape
+    if cu_seqlens is not None and len(shape) == 2:
+        T, C = shape
+        ld, one = t.stride()
+        if one != 1:
+            raise ValueError("%s: the last dimension must be contiguous" % what)
+        return T, C, ld if T > 1 else (C + 7) // 8 * 8
+    if cu_seqlens is not None or len(shape) != 3 or shape[0] != B:
         raise ValueError("%s is [B, T, heads * D], or packed [tokens, heads * D] with cu_seqlens" % what)
-    return T, C, ld
+    return _token_rows(t, what)[1:]
 
 
 def gdn_kv_append(k, v, kv_lens, block_table, k_cache, v_cache, k_scale, v_scale, *, cu_seqlens=None, max_new=0, max_kv=0,
@@ -676,13 +691,13 @@ def gdn_rope(plan, positions, tensors, *, D, inverse=False, stream=None):
     packed = []
     for x, y in tensors:
         B, T, C, ldx = _token_rows(x, "x")
-        By, Ty, Cy, ldy = _token_rows(y, "y")
+        By, Ty, Cy, ldy = (B, T, C, ldx) if y is x else _token_rows(y, "y")
         if x.dtype != dtype or y.dtype != dtype:
             raise TypeError("the tensors have one dtype")
         if (B or 1) * T != tokens or (By or 1) * Ty != tokens or C != Cy or C % D:
             raise ValueError("x and y are [.., heads * D] over the tokens of positions")
         packed.append(_PACK_ROPE_X.pack(x.data_ptr(), y.data_ptr(), ldx, ldy, C // D))
-    st = (_lib or lib()).gdn_rope(tokens, D, _IO_CODES[dtype], ctypes.byref(plan), _int32(positions, tokens, "positions"),
+    st = (_lib or lib()).gdn_rope(tokens, D, _IO_CODES[dtype], plan, _int32(positions, tokens, "positions"),
                                   len(packed), b"".join(packed), 1 if inverse else 0, _raw_stream(stream, positions))
     if st != GDN_OK:
         raise GdnError(st, "gdn_rope")
