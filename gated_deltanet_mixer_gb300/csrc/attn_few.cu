@@ -55,9 +55,11 @@ struct Geo {
   static constexpr int kSlabBytes = 2 * kK * kSub;
   static constexpr int kDepth = D == 256 ? 3 : kSub == 1 ? 5 : D == 64 && kSub == 2 ? 5 : 3;
   static constexpr int kRing = kWarps * kDepth * kSlabBytes;
-  static constexpr int kPitch = D + 4;                        // of a row of the merge, in floats
-  static constexpr int kMerge = kWarps * kRows * kPitch * 4;  // takes the ring's place when a piece ends
-  static constexpr int kBig = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kPitch = D + 4;  // of a row of the merge, in floats
+  // A warp's results at the end of a piece take the first slots of its ring.
+  static constexpr int kMergeSlots = (kRows * kPitch * 4 + kSlabBytes - 1) / kSlabBytes;
+  static_assert(kMergeSlots < kDepth, "no slot is left for the next piece");
+  static constexpr int kBig = kRing;
   static constexpr int kQ = (D / 16) * NT * 256;
   static constexpr int kBytes = kBig + kQ;
 };
@@ -236,9 +238,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
-__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 // Bytes 4w .. 4w+3 of a 16-byte word.
 __device__ __forceinline__ uint32_t word(const uint4 &v, int w) { return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w; }
 
@@ -317,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *const sq = smem + G::kBig;
   __shared__ __align__(8) uint64_t bars[kWarps][G::kDepth];
-  __shared__ RowAt at_row[RT];
+  __shared__ RowAt at_row[2][RT];  // of the piece at hand, and of the one whose results go out
   __shared__ float qscale[RT], wm[kWarps][RT], wl[kWarps][RT], row_m[RT], row_l[RT];
   __shared__ volatile int gave_up;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -333,77 +332,83 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
   int slab0 = whole ? 0 : (int)(loc.in_seq - (long long)unit * q.slabs);
   uint8_t *const ring = smem + warp * (G::kDepth * G::kSlabBytes);
   uint64_t *const bar = bars[warp];
-  uint32_t slot_at = 0, phase_at = 0;  // of the ring, where the next slab goes
+  uint32_t parity = 0;  // bit i: of slot i's next phase
   const int page = 1 << c.page_shift;
   const long long page_bytes = (long long)c.Hk * page * D;
+  constexpr int kStep = kWarps * G::kSlab;  // tokens from one of a warp's slabs to the next
 
-  while (left > 0) {
-    if (unit >= q.tiles * c.Hk) {  // the next sequence that has rows
-      for (int nb = q.s.b + 1;; ++nb) {
-        if (nb >= a.seq.B) return;
-        q = seq_len(a, nb, RT, G::kSlab);
-        if (q.len > 0) break;
-      }
-      unit = 0;
-      slab0 = 0;
-    }
-    const int hk = unit / q.tiles, tile = unit % q.tiles, first = tile * RT;
-    const int count = min(RT, q.s.n * a.r - first);
-    const int slab1 = whole ? q.slabs : (int)min((long long)q.slabs, slab0 + left);
-    const bool starts = slab0 == 0, ends = slab1 == q.slabs;
-    const int seen = a.causal ? min(q.s.kv, max(0, q.s.kv - q.s.n + (first + count - 1) / a.r + 1)) : q.s.kv;
+  // The piece of work at hand: rows first .. first + count - 1 of a key head, slabs slab0 .. slab1 - 1 of their tokens.
+  // A warp's are slab0 + warp + kWarps i, i < mine; the pages and scales of 32 of their 16 tokens at a time, one per lane.
+  int hk, first, count, seen, mine, tok_first, slab1, turn = 0;
+  bool starts, ends;
+  const int *table;
+  const uint8_t *copy_src;
+  int pg[2];
+  float2 sc[2];
+  QRows<D, NT> rows;
+  auto load_page = [&](int x) -> int {  // x: 16 tokens, SUB to a slab
+    const int i = x / SUB, tok = tok_first + i * kStep + (x % SUB) * 16;
+    if (i >= mine || tok >= seen) return -1;
+    const int p = table[tok >> c.page_shift];
+    if (p >= 0 && p < c.n_pages) return p;
+    atomicOr(a.seq.err, kErrSeqlens);
+    return -1;
+  };
+  auto load_scales = [&](int p) -> float2 {
+    if (p < 0) return make_float2(0.f, 0.f);
+    const long long at = (long long)p * c.Hk + hk;
+    return make_float2(c.ks[at], c.vs[at]);
+  };
+  // Makes the piece at (q, unit, slab0) the one at hand and asks for its pages, queries (ahead of the copies, which
+  // would hold them up) and scales.
+  auto open = [&] {
+    const int tile = unit % q.tiles;
+    hk = unit / q.tiles;
+    first = tile * RT;
+    count = min(RT, q.s.n * a.r - first);
+    slab1 = whole ? q.slabs : (int)min((long long)q.slabs, slab0 + left);
+    starts = slab0 == 0;
+    ends = slab1 == q.slabs;
+    seen = a.causal ? min(q.s.kv, max(0, q.s.kv - q.s.n + (first + count - 1) / a.r + 1)) : q.s.kv;
     const int slab_hi = min(slab1, (seen + G::kSlab - 1) / G::kSlab);
-    // this warp's slabs: slab0 + warp + kWarps i, i < mine; the pages and scales of 32 of their 16 tokens at a
-    // time, one per lane
-    const int mine = slab_hi - slab0 > warp ? (slab_hi - slab0 - warp + kWarps - 1) / kWarps : 0;
-    const int *const table = c.table + (long long)q.s.b * c.table_ld;
-    const int tok_first = (slab0 + warp) * G::kSlab;
-    constexpr int kStep = kWarps * G::kSlab;  // tokens from one of them to the next
-    auto load_page = [&](int x) -> int {      // x: 16 tokens, SUB to a slab
-      const int i = x / SUB, tok = tok_first + i * kStep + (x % SUB) * 16;
-      if (i >= mine || tok >= seen) return -1;
-      const int p = table[tok >> c.page_shift];
-      if (p >= 0 && p < c.n_pages) return p;
-      atomicOr(a.seq.err, kErrSeqlens);
-      return -1;
-    };
-    auto load_scales = [&](int p) -> float2 {
-      if (p < 0) return make_float2(0.f, 0.f);
-      const long long at = (long long)p * c.Hk + hk;
-      return make_float2(c.ks[at], c.vs[at]);
-    };
-    int pg[2];
-    float2 sc[2];
-    QRows<D, NT> rows;
+    mine = slab_hi - slab0 > warp ? (slab_hi - slab0 - warp + kWarps - 1) / kWarps : 0;
+    table = c.table + (long long)q.s.b * c.table_ld;
+    tok_first = (slab0 + warp) * G::kSlab;
+    // Lane 8 sub + 0 .. 3 copies 4 tokens each of 16 tokens' k, 4 .. 7 of their v.  What has no page is copied
+    // from page 0 and not looked at.
+    copy_src = (lane & 4 ? c.v : c.k) + ((long long)hk * page + 4 * (lane & 3)) * D;
+    turn ^= 1;
     pg[0] = load_page(lane);
     pg[1] = load_page(lane + 32);
-    fetch_q<D, NT>(a, q.s, hk, first, count, rows);  // ahead of the copies, which would hold it up
+    fetch_q<D, NT>(a, q.s, hk, first, count, rows);
     if (tid < RT) {
       const int rr = first + tid, tok = rr / a.r;
-      at_row[tid] = RowAt{(long long)q.s.row0 + tok, hk * a.r + rr - tok * a.r};
+      at_row[turn][tid] = RowAt{(long long)q.s.row0 + tok, hk * a.r + rr - tok * a.r};
     }
     sc[0] = load_scales(pg[0]);
     sc[1] = load_scales(pg[1]);
-    // Lane 8 sub + 0 .. 3 copies 4 tokens each of 16 tokens' k, 4 .. 7 of their v.  What has no page is copied
-    // from page 0 and not looked at.
-    const uint8_t *const copy_src = (lane & 4 ? c.v : c.k) + ((long long)hk * page + 4 * (lane & 3)) * D;
-    const uint32_t copy_dst = (lane >> 3) * 2 * G::kK + (lane & 7) * G::kGroup;
-    auto issue = [&](int i, int p, uint32_t slot) {  // the copies of slab i into the ring; p: the lane's page
-      uint64_t *const b = bar + slot;
-      if (lane == 0) bar_expect_tx(b, SUB * 8 * 4 * D);
-      __syncwarp();
-      if (lane < 8 * SUB) {
-        const int tok = (tok_first + i * kStep + (lane >> 3) * 16) & (page - 1);
-        bulk_load(smem_u32(ring + slot * G::kSlabBytes) + copy_dst, copy_src + max(p, 0) * page_bytes + tok * D, 4 * D, b);
-      }
-      __syncwarp();
-    };
-    uint32_t in_slot = slot_at;
-#pragma unroll 1
-    for (int i = 0; i < min(mine, G::kDepth); ++i) {
-      issue(i, __shfl_sync(0xffffffffu, pg[0], (i * SUB + (lane >> 3)) & 31), in_slot);
-      in_slot = in_slot + 1 == G::kDepth ? 0 : in_slot + 1;
+  };
+  const uint32_t copy_dst = (lane >> 3) * 2 * G::kK + (lane & 7) * G::kGroup;
+  auto issue = [&](int i, int p, uint32_t slot) {  // the copies of slab i into the ring; p: the lane's page
+    uint64_t *const b = bar + slot;
+    if (lane == 0) bar_expect_tx(b, SUB * 8 * 4 * D);
+    __syncwarp();
+    if (lane < 8 * SUB) {
+      const int tok = (tok_first + i * kStep + (lane >> 3) * 16) & (page - 1);
+      bulk_load(smem_u32(ring + slot * G::kSlabBytes) + copy_dst, copy_src + max(p, 0) * page_bytes + tok * D, 4 * D, b);
     }
+    __syncwarp();
+  };
+  // A piece's slabs go round the ring from behind the slots that the last piece's results are merged in.
+  auto issue_first = [&](int i0, int i1) {
+#pragma unroll 1
+    for (int i = i0; i < min(mine, i1); ++i)
+      issue(i, __shfl_sync(0xffffffffu, pg[0], (i * SUB + (lane >> 3)) & 31), (uint32_t)(i + G::kMergeSlots) % G::kDepth);
+  };
+
+  open();
+  issue_first(0, G::kDepth);
+  while (true) {
     store_q<D, NT>(a, rows, sq, qscale);
     __syncthreads();
 
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
       }
     auto last_of = [&](int j, int u) {  // the last token that a row sees
       const int row = 8 * j + 2 * t + u;
-      return row >= count ? -1 : a.causal ? q.s.kv - q.s.n + (int)(at_row[row].token - q.s.row0) : q.s.kv - 1;
+      return row >= count ? -1 : a.causal ? q.s.kv - q.s.n + (int)(at_row[turn][row].token - q.s.row0) : q.s.kv - 1;
     };
     // Tokens up to this one are seen by every row (rows that are none may see them too: nothing reads those).
     const int all_see = a.causal ? q.s.kv - q.s.n + first / a.r : q.s.kv - 1;
@@ -438,7 +443,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
     const int in0 = 4 * gr0 + 2 * bg, in1 = 4 * gr1 + 2 * bg + 1;
     const uint32_t k_at0 = gr0 * G::kGroup + 2 * bg * D + 16 * t, k_at1 = gr1 * G::kGroup + (2 * bg + 1) * D + 16 * t;
 
-    auto wait = [&](uint32_t slot, uint32_t phase) {
+    auto wait = [&](uint32_t slot) {
+      const uint32_t phase = parity >> slot & 1;
+      parity ^= 1u << slot;
       if (!bar_try_wait(bar + slot, phase)) {
         const uint64_t t0 = global_ns();
         while (!gave_up && !bar_try_wait(bar + slot, phase))
@@ -492,9 +499,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
     };
 
     float st[SUB][NT][4];
-    uint32_t slot = slot_at, phase = phase_at;
+    uint32_t slot = G::kMergeSlots % G::kDepth;
     if (mine > 0) {
-      wait(slot, phase);
+      wait(slot);
       scores(slot, st);
     }
 #pragma unroll 1
@@ -514,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
         vs[u] = __shfl_sync(0xffffffffu, sc[0].y, in * SUB + u);
         vtop = fmaxf(vtop, vs[u]);
       }
-      const uint32_t next = slot + 1 == G::kDepth ? 0 : slot + 1, next_phase = phase ^ (next == 0 ? 1u : 0u);
+      const uint32_t next = slot + 1 == G::kDepth ? 0 : slot + 1;
       const int tok0 = tok_first + i * kStep;
       float y[SUB][NT][4];
 #pragma unroll
@@ -525,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
           for (int e = 0; e < 4; ++e) y[u][j][e] = st[u][j][e] * (qs[j][e & 1] * ks[u]);
       // The next slab's scores are on their way while this one's weights are formed.
       if (i + 1 < mine) {
-        wait(next, next_phase);
+        wait(next);
         scores(next, st);
       }
       // Tokens that some row does not see, or that have no page.
@@ -650,10 +657,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
         issue(i + G::kDepth, x / 32 == i / kBatch ? p0 : p1, slot);
       }
       slot = next;
-      phase = next_phase;
     }
-    slot_at = slot;
-    phase_at = phase;
 
     // ---- the warps' results together
 #pragma unroll
@@ -671,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
       }
     asm volatile("griddepcontrol.launch_dependents;");  // the join may come up
     __syncthreads();  // every warp is through with its ring
-    float *const merge = reinterpret_cast<float *>(smem) + warp * RT * G::kPitch;
+    float *const merge = reinterpret_cast<float *>(ring);
     if (tid < RT) {
       float top = kNone, sum = 0.f;
 #pragma unroll
@@ -694,32 +698,51 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
         for (int i2 = 0; i2 < MT; ++i2)
           *reinterpret_cast<float2 *>(merge + row * G::kPitch + merge_at<D>(g, i2)) = make_float2(acc[i2][j][u] * f, acc[i2][j][2 + u] * f);
       }
+    // The next piece is asked for while this one's results go out.
+    const bool whole_unit = starts && ends;
+    const int part = 2 * blockIdx.x + (starts ? 1 : 0), out_rows = count;
+    const RowAt *const out_at = at_row[turn];
+    left -= whole ? 1 : slab1 - slab0;
+    slab0 = 0;
+    ++unit;
+    bool more = left > 0;
+    if (more && unit >= q.tiles * c.Hk) {  // the next sequence that has rows
+      unit = 0;
+      for (int nb = q.s.b + 1;; ++nb) {
+        more = nb < a.seq.B;
+        if (!more) break;
+        q = seq_len(a, nb, RT, G::kSlab);
+        if (q.len > 0) break;
+      }
+    }
+    if (more) {
+      open();
+      issue_first(0, G::kDepth - G::kMergeSlots);
+    }
     __syncthreads();
-    const int part = 2 * blockIdx.x + (starts ? 1 : 0);
 #pragma unroll 4
-    for (int x = tid; x < count * (D / 2); x += kThreads) {
+    for (int x = tid; x < out_rows * (D / 2); x += kThreads) {
       const int row = x / (D / 2), dim = x % (D / 2) * 2;
       const int at = D >= 128 ? merge_at<D>((dim >> 4) & 7, (dim >> 7) * 8 + ((dim >> 1) & 7)) : dim;
       float2 o = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float2 v = *reinterpret_cast<const float2 *>(reinterpret_cast<const float *>(smem) + (w * RT + row) * G::kPitch + at);
+        const float2 v = *reinterpret_cast<const float2 *>(smem + w * (G::kDepth * G::kSlabBytes) + (row * G::kPitch + at) * 4);
         o.x += v.x, o.y += v.y;
       }
-      if (starts && ends) {
+      if (whole_unit) {
         const float ls = row_l[row], inv = ls == 0.f ? 0.f : 1.f / ls;
-        __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.o) + at_row[row].token * a.ldo + at_row[row].head * D + dim;
+        __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.o) + out_at[row].token * a.ldo + out_at[row].head * D + dim;
         *reinterpret_cast<uint32_t *>(dst) = pack_bf16(o.x * inv, o.y * inv);
       } else {
         *reinterpret_cast<float2 *>(part_o(a.ws, part, RT, D) + row * D + dim) = o;
         if (dim == 0) part_ml(a.ws, 2 * gridDim.x, part, RT, D)[row] = make_float2(row_m[row], row_l[row]);
       }
     }
+    if (!more) return;
     fence_smem_to_async();  // before the next copies into what was written here
     __syncthreads();
-    left -= whole ? 1 : slab1 - slab0;
-    slab0 = 0;
-    ++unit;
+    issue_first(G::kDepth - G::kMergeSlots, G::kDepth);
   }
 }
 
