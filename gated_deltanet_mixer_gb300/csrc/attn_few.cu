@@ -41,6 +41,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // fp16 times kPScale finite, and normal from 2^-25 on.
 constexpr float kSlack = 4.f;
 constexpr float kPScale = 2048.f;
+constexpr float kLeastRef = 0x1p-100f;  // what value scales are relative to at least
 
 // A slab's copies: kSub times 16 tokens, of a page each, in a ring of kDepth slabs per warp.  More tokens at a
 // time spread what a slab costs whatever its width (waits, votes, copies; some 250 instructions of a warp with
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
     };
     // Tokens up to this one are seen by every row (rows that are none may see them too: nothing reads those).
     const int all_see = a.causal ? q.s.kv - q.s.n + first / a.r : q.s.kv - 1;
-    float ref = 0.f, inv_ref = 0.f;  // the largest value scale so far, kPScale over it
+    float ref = kLeastRef, inv_ref = kPScale / kLeastRef;  // the largest value scale so far, kPScale over it
     // Rows g and g + 8 of S^T are these tokens of 16.
     const int tg = g >> 1, bg = g & 1, gr0 = (tg + 2 * bg) & 3, gr1 = (tg + 2 * bg + 1) & 3;
     const int in0 = 4 * gr0 + 2 * bg, in1 = 4 * gr1 + 2 * bg + 1;
@@ -592,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
       }
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
-        const float pv = vs[u] * inv_ref;  // NaN where the scale is, 0 where none is above 0
+        const float pv = vs[u] * inv_ref;  // NaN where the scale is
         uint32_t pb[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
@@ -738,11 +739,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
         if (dim == 0) part_ml(a.ws, 2 * gridDim.x, part, RT, D)[row] = make_float2(row_m[row], row_l[row]);
       }
     }
-    if (!more) return;
+    if (!more) break;
     fence_smem_to_async();  // before the next copies into what was written here
     __syncthreads();
     issue_first(G::kDepth - G::kMergeSlots, G::kDepth);
   }
+  if (gave_up) settle();
 }
 
 // Joins a unit's parts:  o = sum 2^(m_p - m) o_p / sum 2^(m_p - m) l_p.  by_unit: block x takes unit x (of

@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
     if (gridDim.z > 1) {  // a part: fp32, relative to m
       const long long at = part_row(a, item, hk, blockIdx.z, gridDim.z) + row;
       if (group == 0) reinterpret_cast<float2 *>(part_ml(a, gridDim.x, gridDim.z, D))[at] = make_float2(ntiles > 0 ? m : -INFINITY, l);
-      const float un = ex2(lref - kPExp);
+      const float un = ex2(-kPExp), scale = ex2(lref);
       constexpr int kRounds = 2, kCols = kShare / kRounds;  // of a group in a round
 #pragma unroll 1
       for (int h = 0; ntiles > 0 && h < kRounds; ++h) {
@@ -487,8 +487,8 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
             *reinterpret_cast<float4 *>(stage + row_at<D>(row, (group * kCols + d + i) / 4)) =
-                make_float4(__uint_as_float(w[i]) * un, __uint_as_float(w[i + 1]) * un, __uint_as_float(w[i + 2]) * un,
-                            __uint_as_float(w[i + 3]) * un);
+                make_float4(__uint_as_float(w[i]) * un * scale, __uint_as_float(w[i + 1]) * un * scale,
+                            __uint_as_float(w[i + 2]) * un * scale, __uint_as_float(w[i + 3]) * un * scale);
         }
         sync_softmax();
         float *const dst = static_cast<float *>(a.ws) + (at - row) * D + h * kCols;
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
         sync_softmax();
       }
     } else {
-    const float inv = l == 0.f ? 0.f : ex2(lref - kPExp) / l;
+    const float inv = l == 0.f ? 0.f : ex2(-kPExp) / l, scale = ex2(lref);  // the smallest scales first would be lost
 #pragma unroll 1
     for (int d = group * kShare; d < (group + 1) * kShare; d += 32) {
       uint32_t w[32];
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
         uint32_t o[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          o[k] = ntiles > 0 ? pack_bf16(__uint_as_float(w[i + 2 * k]) * inv, __uint_as_float(w[i + 2 * k + 1]) * inv) : 0u;
+          o[k] = ntiles > 0 ? pack_bf16(__uint_as_float(w[i + 2 * k]) * inv * scale, __uint_as_float(w[i + 2 * k + 1]) * inv * scale) : 0u;
         *reinterpret_cast<uint4 *>(stage + row_at<D>(row, (d + i) / 8)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
       __syncwarp();
       if (lane == 0) bar_expect_tx(&bars.k_full[slot], __popc(there) * 16 * D);
       __syncwarp();
-      if (lane < kSubs && p >= 0) {
+      if (lane < kSubs && p >= 0 && !gave_up) {
         const uint32_t dst = smem_u32(sk + slot * G::kKBytes) + lane * 16 * G::kRowBytes;
         const int tok = ((base + j) * kTile + lane * 16) & (page - 1);
 #pragma unroll
@@ -694,6 +694,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
       if (j + G::kBufs < ntiles) scores(j + G::kBufs);  // where P was: products follow each other
     }
   }
+  if (gave_up) settle();
   fence_before();
   __syncthreads();
   fence_after();

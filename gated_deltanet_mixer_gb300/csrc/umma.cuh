@@ -144,6 +144,12 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity,
     if (global_ns() - t0 > limit_ns) return false;
   return true;
 }
+// After a wait that gave up: time for the copies and products in flight to land, before their memory goes to others.
+__device__ __forceinline__ void settle() {
+  const uint64_t t0 = global_ns();
+  while (global_ns() - t0 < 5000000ull) {
+  }
+}
 // Arrive on `bar` announcing `bytes` of asynchronous copies to complete on it.
 __device__ __forceinline__ void bar_expect_tx(uint64_t *bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes)

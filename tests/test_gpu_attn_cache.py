@@ -148,6 +148,7 @@ def test_rows_that_see_nothing(dt):
     """Causal rows before the first cached token give 0."""
     cache = R.Cache([3, 0, 20], 2, 128, 16, device="cuda").fill()
     check(cache, [5, 4, 150], 4, dt)
+    check(R.Cache([3, 0, 1, 70], 2, 128, 16, device="cuda").fill(), [5, 4, 3, 5], 2, dt)
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
@@ -201,6 +202,20 @@ def test_value_scales_far_apart(dt, new):
     cache.v8[int(cache.table[0, 3])] = 0
     cache.sv[int(cache.table[0, 3])] = 2.0 ** -120
     check(cache, [new], 4, dt)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("new", [1, 6, 140])
+@pytest.mark.parametrize("least", [2.0 ** -120, 2.0 ** -99, 0.0])
+def test_least_scales(dt, new, least):
+    """Values (or keys) that are all zeros, as of padding, or as small as they go."""
+    for what in ("v", "k"):
+        for zero in (True, False):
+            cache = R.Cache([new + 90], 2, 128, 16, device="cuda").fill()
+            getattr(cache, "s" + what)[cache.table[0].long()] = least
+            if zero:
+                getattr(cache, what + "8")[cache.table[0].long()] = 0
+            check(cache, [new], 4, dt)
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
@@ -590,7 +605,7 @@ def pages_by_hand(kv, new, free, used, table, page):
 
 
 @pytest.mark.parametrize("B,top,most,page", [(1, 0, 1, 16), (1, 0, 5000, 16), (5, 40, 3, 16), (64, 100, 1, 32), (300, 30, 9, 64),
-                                             (1024, 10, 4, 16), (1500, 20, 20, 128), (3000, 0, 2, 16)])
+                                             (1024, 10, 4, 16), (1500, 20, 20, 128), (3000, 0, 2, 16), (16384, 5, 1, 16)])
 @pytest.mark.parametrize("in_place", [True, False])
 def test_pages(B, top, most, page, in_place):
     g = torch.Generator().manual_seed(B)
