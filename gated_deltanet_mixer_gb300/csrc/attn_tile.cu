@@ -541,13 +541,14 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
         if (p >= 0 && tok + t8 + 8 * (i & 1) < s.kv) r[i] = *reinterpret_cast<const uint4 *>(src + 8 * (i & 1) * D + (i >> 1) * 64);
       }
     };
+    // where a lane's 16 dimensions go, as an operand with the dimensions contiguous; what follows is a fixed way on
+    uint8_t *const put_lo = sv + mnmaj(d16 * 16, 16 * w + t8, kTile), *const put_hi = sv + mnmaj(d16 * 16 + 8, 16 * w + t8, kTile);
     auto put = [&](int j, const uint4 (&r)[kLoads]) {
       const int slot = j % G::kVStages;
       if (j >= G::kVStages) wait(&bars.v_empty[slot], (j / G::kVStages - 1) & 1);
-      uint8_t *const tile = sv + slot * G::kVBytes;
+      uint8_t *const lo = put_lo + slot * G::kVBytes, *const hi = put_hi + slot * G::kVBytes;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int k = 16 * w + t8 + 8 * (i & 1), dim = (i >> 1) * 64 + d16 * 16;
         const uint32_t u[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
         uint32_t h[8];
 #pragma unroll
@@ -555,8 +556,9 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
           h[2 * e] = e4m3x2_to_h2(u[e], 0);
           h[2 * e + 1] = e4m3x2_to_h2(u[e], 1);
         }
-        *reinterpret_cast<uint4 *>(tile + mnmaj(dim, k, kTile)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4 *>(tile + mnmaj(dim + 8, k, kTile)) = make_uint4(h[4], h[5], h[6], h[7]);
+        constexpr int kBlock = kTile * 128;  // 64 dimensions of a tile
+        *reinterpret_cast<uint4 *>(lo + (i >> 1) * kBlock + (i & 1) * 1024) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(hi + (i >> 1) * kBlock + (i & 1) * 1024) = make_uint4(h[4], h[5], h[6], h[7]);
       }
       fence_smem_to_async();
       bar_arrive(&bars.v_full[slot]);
