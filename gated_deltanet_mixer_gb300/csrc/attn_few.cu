@@ -1,11 +1,13 @@
 // attn_few.cu -- attention of few rows over the paged 8-bit cache (bf16 io): one
 // new token of a sequence, or a handful, times the query heads of a key head.
 //
-// Bound by the cache's bytes, which the rows of a key head share.  The products
+// Bound by the cache's bytes, which the rows of a key head share (64 x 1 token over
+// 8192, 24/4 heads of 256: 171 us, 6.3 TB/s; 16 x 4 tokens, ragged, 32/8 heads of 128,
+// 87 MB: 37 us, of which some 10 are a block's start, end and the join).  The products
 // run transposed, so that the cache is the operand with 16 rows and the queries
 // the one with 8 columns:  S^T = K q^T  and  O^T = V^T P^T  by
 // mma.m16n8k16 in fp16, whose e4m3 operands are exact; q enters with a power of
-// two per row, p with one that keeps it normal down to 2^-29 (11 bits of p
+// two per row, p with one that keeps it normal down to 2^-25 (11 bits of p
 // where bf16 would keep 8).
 //
 // A slab is 16 tokens: its k and v are two contiguous blocks of a page, and its

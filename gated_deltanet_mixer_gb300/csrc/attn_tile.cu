@@ -13,12 +13,17 @@
 // so far, enters p as a term of the exponent, and leaves the row's sum again as a
 // factor on the page's part of it: no product per element.
 //
+// Bound by the products for heads of 256 (8192 tokens over 24576, 24/4 heads: 3.45 to
+// 3.65 ms, 1.6 PFLOP/s of bf16's 1.7 sustained; the products of q's two parts are twice those
+// of one, at twice the rate), by the softmax's instructions for narrower ones (2048 over 8192,
+// 32/4 heads of 128: 266 us, 1.16 PFLOP/s).
+//
 // Warps: 4 for the softmax (thread = row), 4 for the values, one for the keys
 // (TMA) and one for the products.  For a tile of 64 tokens and D = 256 the products
 // take 1024 cycles; a tile's way through the softmax is longer than that: two groups
 // of warps, which take tiles in turns.  Narrower heads have two blocks to an SM for
-// that.  The running maximum goes from one to the other
-// as soon as it is known, ahead of the exponentials; each keeps a sum of its own.
+// that.  The running maximum goes from one group to the other as soon as it is known,
+// ahead of the exponentials; each keeps a sum of its own.
 #include <algorithm>
 
 #include "cache_device.cuh"
