@@ -4,9 +4,10 @@
 // over the tokens in tiles of 64 on the tensor cores, one pass with the running
 // maximum and sum of each row:
 //   S = Q K^T   e4m3 products straight on the cache's bytes, which TMA brings from
-//               the pages.  Q stands in TMEM (or shared memory) as two e4m3 values per element, hi +
-//               lo of q times a power of two per row (8 bits of a bf16 where it is
-//               within 2^10 of its row's largest; 2^-19 of that largest at worst).
+//               the pages.  Q stands in TMEM (or shared memory) as two e4m3 values
+//               per element, hi + lo of q times a power of two per row: all 8 bits of
+//               a bf16 that is not below 2^-9 of its row's largest, and never off by
+//               more than 2^-17 of that largest.
 //   O += P V    fp16 products: P, rounded to fp16, in TMEM where S was; V's bytes
 //               become fp16 (exact) on the way through a group of four warps.
 // A page's key scale multiplies its scores.  Its value scale, over the largest

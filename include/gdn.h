@@ -532,7 +532,7 @@ gdn_status gdn_kv_append(const gdn_attn_shape *shape, const gdn_kv_append_io *io
  * NaN (0x7f, 0xff; gdn_kv_append writes none): where there is one among the
  * tokens seen, what it is taken for is not specified.
  * bf16 io: products on the tensor cores, of the bytes themselves, of q (for many
- * rows to within 2^-19 of the largest of its row and head) and of p rounded to
+ * rows to within 2^-17 of the largest of its row and head) and of p rounded to
  * fp16; scores, softmax and sums in fp32.  fp32 io: fp32 throughout.  A NaN or
  * infinity in a head of q makes that row and head NaN.
  * max_new and max_kv choose how the call runs: a few rows (new tokens x Hq / Hk) of
