@@ -541,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
       const uint32_t gone = (__ballot_sync(0xffffffffu, pg[0] < 0) >> (in * SUB)) & ((1u << SUB) - 1);  // bit u: no page
       const bool masked = gone != 0 || tok0 + G::kSlab - 1 > all_see;
       if (masked) {
+        vtop = 0.f;  // not yet: a row that does not see the larger values' page would lose bits to them
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -595,6 +596,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
       }
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
+        if (masked && vs[u] > ref) {  // page by page: who sees this one has seen those before it
+          const float shrink = ref / vs[u];
+          ref = vs[u];
+          inv_ref = kPScale / vs[u];
+#pragma unroll
+          for (int i2 = 0; i2 < MT; ++i2)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i2][j][e] *= shrink;
+        }
         const float pv = vs[u] * inv_ref;  // NaN where the scale is
         uint32_t pb[NT][2];
 #pragma unroll

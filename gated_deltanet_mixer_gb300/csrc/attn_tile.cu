@@ -11,8 +11,9 @@
 //   O += P V    fp16 products: P, rounded to fp16, in TMEM where S was; V's bytes
 //               become fp16 (exact) on the way through a group of four warps.
 // A page's key scale multiplies its scores.  Its value scale, over the largest
-// so far, enters p as a term of the exponent, and leaves the row's sum again as a
-// factor on the page's part of it: no product per element.
+// that the row has seen, enters p as a term of the exponent, and leaves the row's sum
+// again as a factor on the page's part of it: no product per element.  In fp16 p has
+// 11 bits down to 2^-25 of the largest, and is within 2^-36 of it below that.
 //
 // Bound by the products for heads of 256 (8192 tokens over 24576, 24/4 heads: 3.45 to
 // 3.65 ms, 1.6 PFLOP/s of bf16's 1.7 sustained; the products of q's two parts are twice those
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
       wait(&bars.scales[j % kRing], (j / kRing) & 1);
       const Scales &sc = ring[j % kRing];
       const float4 ks4 = sc.ks, lvs = sc.lvs;
-      const float ltop = fmaxf(fmaxf(lvs.x, lvs.y), fmaxf(lvs.z, lvs.w));
+      float ltop = fmaxf(fmaxf(lvs.x, lvs.y), fmaxf(lvs.z, lvs.w));
       const uint32_t flags = sc.flags;
       float fs[kSubs] = {f * ks4.x, f * ks4.y, f * ks4.z, f * ks4.w};
       wait(&bars.s_full[buf], (j / G::kBufs) & 1);
@@ -363,6 +364,13 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
       // Some row does not see all, or some value scale is NaN: then scores get their scales first, so that a scale
       // (NaN, 0) does not bring back what is not seen, and a NaN value scale reaches what is.
       const bool odd = flags != 0 || tok0 + kTile - 1 > all_see;
+      if (odd) {  // of the pages that the row sees: it would lose bits to larger values behind its last token
+        const float of[kSubs] = {lvs.x, lvs.y, lvs.z, lvs.w};
+        ltop = kNoRef;
+#pragma unroll
+        for (int u = 0; u < kSubs; ++u)
+          if (tok0 + 16 * u <= last) ltop = fmaxf(ltop, of[u]);
+      }
       auto one_by_one = [&](uint32_t (&x)[32], int h) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {

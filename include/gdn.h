@@ -447,8 +447,8 @@ gdn_status gdn_selftest_linattn_form(const gdn_shape *shape, int packed, int wor
 
 /*
  * Softmax attention over a paged cache in 8 bits: the layer of the hybrid
- * decoders that stands between the linear ones (node kv of "Qwen3.8-27B", page
- * size 16; "How Qwen3.5 works" sections 10 and 13), from the output of its
+ * decoders that stands between the linear ones (page "Qwen3.8-27B": pages of 16
+ * tokens; "How Qwen3.5 works" sections 10 and 13), from the output of its
  * in-projection to the input of its out-projection.
  *
  * The cache of a layer: n_pages pages of `page` tokens (16, 32, 64 or 128)
@@ -533,8 +533,10 @@ gdn_status gdn_kv_append(const gdn_attn_shape *shape, const gdn_kv_append_io *io
  * tokens seen, what it is taken for is not specified.
  * bf16 io: products on the tensor cores, of the bytes themselves, of q (for many
  * rows to within 2^-17 of the largest of its row and head) and of p rounded to
- * fp16; scores, softmax and sums in fp32.  fp32 io: fp32 throughout.  A NaN or
- * infinity in a head of q makes that row and head NaN.
+ * fp16; scores, softmax and sums in fp32.  p has its page's value scale with it
+ * there: 11 bits down to 2^-25 of the largest weight times scale that the row
+ * has seen, and what is smaller to within 2^-36 of that.  fp32 io: fp32
+ * throughout.  A NaN or infinity in a head of q makes that row and head NaN.
  * max_new and max_kv choose how the call runs: a few rows (new tokens x Hq / Hk) of
  * each sequence and key head side by side, or tiles of 128 rows.  A batch of
  * prompts and of single tokens is faster as two calls.

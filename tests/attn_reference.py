@@ -95,6 +95,20 @@ def attend(q, k, v, n, causal, scale):
     return torch.einsum("hnk,khd->nhd", p, v), torch.einsum("hnk,khd->nhd", p, v.abs()), size.T
 
 
+def least(cache, b, n, kv, Hq, causal):
+    """What bf16 io may be off by however small a weight is: weights stand in fp16 with the page's value scale as
+    a factor, so that the row's largest weight so far under the largest scale so far (2^-100 at least) is 2^11 or more,
+    and fp16 rounds to within 2^-25: 2^-36 of that weight and scale for each token's value over its scale.  The sum of
+    weights that they are divided by is no less than the row's largest weight."""
+    p = cache.table[b, :-(-kv // cache.page)].long()
+    codes = cache.v8.view(torch.float8_e4m3fn)[p].double().abs().nan_to_num(0.0).transpose(1, 2).reshape(-1, cache.Hk, cache.D)[:kv]
+    scales = cache.sv[p].double().nan_to_num(0.0).clamp(min=2.0 ** -100).repeat_interleave(cache.page, 0)[:kv]
+    x = 2.0 ** -36 * scales.cummax(0).values[:, :, None] * codes.cumsum(0) if kv else codes
+    last = torch.full((n,), kv - 1) if not causal else kv - n + torch.arange(n)
+    x = torch.cat((torch.zeros_like(x[:1]) if kv else codes.new_zeros(1, cache.Hk, cache.D), x))
+    return x[(last + 1).clamp(min=0).to(x.device)].repeat_interleave(Hq // cache.Hk, 1)
+
+
 def append(k, v, cache, lens, new):
     """The cache behind new tokens k, v (lists of [n, Hk, D] per sequence), in place, in 64 bits."""
     for b, (kv, n) in enumerate(zip(lens, new)):

@@ -66,6 +66,8 @@ def check_rows(got, q, cache, b, n, kv, Hq, causal, scale, dt, k=None, v=None):
     want, S, A = R.attend(q.reshape(n, Hq, D), k, v, n, causal, scale)
     hp = H[BF] if dt == BF else 0.0
     tol = (hp + 4 * (D + 8) * 2.0 ** -24 * A[:, :, None] + 2 * (kv + 8) * 2.0 ** -24) * S + H[dt] * want.abs()
+    if dt == BF:
+        tol = tol + R.least(cache, b, n, kv, Hq, causal)
     err = (got.reshape(n, Hq, D).double() - want).abs()
     assert bool((err <= tol + 1e-37).all()), "off by %.3g of the tolerance" % float((err / (tol + 1e-37)).max())
 
@@ -202,6 +204,31 @@ def test_value_scales_far_apart(dt, new):
     cache.v8[int(cache.table[0, 3])] = 0
     cache.sv[int(cache.table[0, 3])] = 2.0 ** -120
     check(cache, [new], 4, dt)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new,kv,steps", [(2, 49, (0, 0, 0, 60)), (2, 17, (0, 60)), (7, 70, (0, 0, 0, 40, 80)), (20, 33, (0, 50, 100)),
+                                          (140, 160, tuple(range(0, 120, 12)))])
+def test_larger_values_of_later_tokens_do_not_reach_a_row(dt, D, new, kv, steps):
+    """The value scales grow from page to page, up to 2^60 times, right behind what a row sees."""
+    cache = R.Cache([kv], 2, D, 16, device="cuda").fill()
+    for j, e in enumerate(steps):
+        cache.sv[int(cache.table[0, j])] = 2.0 ** (e - 100)
+    check(cache, [new], 8, dt)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("new", [2, 30, 140])
+def test_weights_far_below_the_largest(dt, new):
+    """Dimensions whose value is zero at the token with nearly all the weight: what is left of the others'."""
+    cache = R.Cache([new + 60], 2, 128, 16, device="cuda").fill(mean=0.0)
+    cache.v8[int(cache.table[0, 0]), :, 3] = 0
+    cache.sk[cache.table[0].long()] = 2.0 ** -6
+    cache.k8[int(cache.table[0, 0]), :, 3] = torch.full((128,), 60.0).to(torch.float8_e4m3fn).view(torch.uint8).to("cuda")
+    for size in (16.0, 20.0, 24.0, 28.0):  # weights of e^-size next to it, about
+        q = torch.full((new, 4 * 128), size * 64 / 60 / 128 ** 0.5, device="cuda").to(dt)
+        check(cache, [new], 4, dt, q=q)
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
