@@ -467,11 +467,12 @@ gdn_status gdn_selftest_linattn_form(const gdn_shape *shape, int packed, int wor
  * the last of the sequence: row i of n is at position kv_lens[b] - n + i.
  *   max_new   packed: no sequence has more new tokens (0: T)
  *   max_kv    no sequence has more tokens in all (0: max_blocks * page)
- * Lengths and tables are read on the device.  A sequence with offsets out of
- * order or range, or with more tokens than max_new, max_kv or its table allow,
- * is skipped (its outputs stay untouched); an entry of the table that is used
- * and is not a page of the cache is left out.  Both record GDN_ERR_INVALID_ARG
- * for gdn_device_status.
+ * Lengths and tables are read on the device.  A sequence with more tokens than
+ * max_new, max_kv or its table allow is skipped (its outputs stay untouched); with
+ * offsets out of order or range all are; an entry of the table that is used and
+ * is not a page of the cache is left out.  Each records GDN_ERR_INVALID_ARG for
+ * gdn_device_status.
+ * B <= 65536, 2^24 token rows, Hq <= 4096, 2^27 pages, max_blocks * page <= 2^30.
  */
 typedef struct {
   int B, T;
@@ -528,9 +529,9 @@ gdn_status gdn_kv_append(const gdn_attn_shape *shape, const gdn_kv_append_io *io
  *     may overlap in time.
  * What the cache holds behind a row's last token does not reach it, whatever it
  * is, but for its page's scales: a row that sees a token of a page whose k or
- * v scale is NaN gives NaN.  Scales are 0 <= s <= 2^7.  In the bytes there is no
- * NaN (0x7f, 0xff; gdn_kv_append writes none): where there is one among the
- * tokens seen, what it is taken for is not specified.
+ * v scale is NaN gives NaN.  Scales are 0 <= s <= 2^7.  The bytes of a sequence's
+ * kv_lens tokens hold no NaN (0x7f, 0xff; gdn_kv_append writes none): with one
+ * there, what its rows give, those before that token too, is not specified.
  * bf16 io: products on the tensor cores, of the bytes themselves, of q (for many
  * rows to within 2^-17 of the largest of its row and head) and of p rounded to
  * fp16; scores, softmax and sums in fp32.  p has its page's value scale with it
@@ -660,7 +661,7 @@ gdn_status gdn_rope(int tokens, int D, int io_dtype, const gdn_rope_plan *plan, 
  * nothing, and leaves cu_seqlens all 0, every slot -1, kv_lens_out and
  * free_used_out as if no token were new (the other calls then have nothing to do).
  * An entry of the table that is already there is not checked.
- * page: 16, 32, 64 or 128; n_free may be 0; B <= 65536.
+ * page: 16, 32, 64 or 128; n_free may be 0; B <= 16384, max_tokens <= 2^30.
  */
 typedef struct {
   int B, page, max_blocks, n_free;
