@@ -15,8 +15,8 @@
 // again as a factor on the page's part of it: no product per element.  In fp16 p has
 // 11 bits down to 2^-25 of the largest, and is within 2^-36 of it below that.
 //
-// Bound by the products for heads of 256 (8192 tokens over 24576, 24/4 heads: 3.45 to
-// 3.65 ms, 1.6 PFLOP/s of bf16's 1.7 sustained; the products of q's two parts are twice those
+// Bound by the products for heads of 256 (8192 tokens over 24576, 24/4 heads: 3.49
+// ms, 1.66 PFLOP/s of bf16's 1.7 sustained; the products of q's two parts are twice those
 // of one, at twice the rate), by the softmax's instructions for narrower ones (2048 over 8192,
 // 32/4 heads of 128: 266 us, 1.16 PFLOP/s).
 //
@@ -185,12 +185,116 @@ struct TilePages {
   }
 };
 
-// Parts of a block's rows where their tokens are cut: [items][Hk][parts][128] rows of D values, then their (maximum, sum).
-__device__ __forceinline__ long long part_row(const AttnArgs &a, long long item, int hk, int part, int parts) {
-  return ((item * a.cache.Hk + hk) * parts + part) * kRows;
+// The last blocks' tokens may be cut into a.splits parts (all blocks' where they do not fill the GPU): a part is a
+// block from number a.whole on, and leaves 128 rows of D values; behind those of all parts their (maximum, sum).
+__device__ __forceinline__ long long part_row(long long part) { return part * kRows; }
+__device__ __forceinline__ float *part_ml(const AttnArgs &a, long long parts, int D) { return static_cast<float *>(a.ws) + parts * kRows * D; }
+
+// Blocks start with the tiles that see the most, whatever sequence and head they are of, so that what runs last is
+// short (12 prompts: 73.6 us, in the sequences' order 76.5).  Tile t of a sequence counts as P + t, P the 128s of rows
+// that its cached tokens would have been; of all tiles this finds number `rank` from the largest down (equal ones in the
+// sequences' order), for the whole block: how many are above a size is a sum over the sequences, which one warp forms,
+// and the range of sizes is quartered until one is left.  More sequences than 4 to a lane are taken in order, the
+// last first.
+constexpr int kSeqsLane = 4;
+__device__ __forceinline__ Seq find_largest(const AttnArgs &a, int rank, int ranks, int *local) {
+  const SeqArgs &g = a.seq;
+  if (g.B == 1) {  // nothing to search
+    const int lo = g.cu ? g.cu[0] : 0, hi = g.cu ? g.cu[1] : g.T, kv = g.kv_lens[0];
+    if (lo < 0 || hi < lo || hi > g.T) {
+      if (threadIdx.x == 0) atomicOr(g.err, kErrSeqlens);
+      return Seq{-1, 0, 0, 0};
+    }
+    *local = (int)(((long long)(hi - lo) * a.r + kRows - 1) / kRows) - 1 - rank;
+    Seq s = checked_seq(g, 0, lo, hi - lo, kv);
+    if (*local < 0) s.b = -1;
+    return s;
+  }
+  if (g.B > 32 * kSeqsLane) return find_seq(g, ranks - 1 - rank, a.r, kRows, 1, local);
+  __shared__ Seq found;
+  __shared__ int at;
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int row0[kSeqsLane], n[kSeqsLane], kv[kSeqsLane], from[kSeqsLane], tiles[kSeqsLane];
+    bool bad = false, out = false;
+#pragma unroll
+    for (int k = 0; k < kSeqsLane; ++k) {
+      const int b = lane + 32 * k;
+      row0[k] = n[k] = kv[k] = 0;
+      if (b < g.B) {
+        row0[k] = g.cu ? g.cu[b] : b * g.T;
+        n[k] = g.cu ? g.cu[b + 1] : g.T;
+        kv[k] = g.kv_lens[b];
+      }
+    }
+    int end = 0;
+#pragma unroll
+    for (int k = 0; k < kSeqsLane; ++k) {
+      if (g.cu) {
+        bad |= row0[k] < 0 || n[k] < row0[k] || n[k] > g.T;
+        n[k] -= row0[k];
+      }
+      const bool use = n[k] <= g.max_new && kv[k] >= 0 && kv[k] <= g.max_kv;
+      out |= !use;
+      tiles[k] = use && lane + 32 * k < g.B ? (int)(((long long)n[k] * a.r + kRows - 1) / kRows) : 0;
+      from[k] = (int)((long long)max(0, kv[k] - n[k]) * a.r / kRows);
+      end = max(end, tiles[k] > 0 ? from[k] + tiles[k] : 0);
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (__any_sync(0xffffffffu, out || bad) && lane == 0) atomicOr(g.err, kErrSeqlens);
+    const bool one = g.B <= 32;
+    auto above = [&](int x) {  // tiles of size x or more
+      int c = min(max(from[0] + tiles[0] - x, 0), tiles[0]);
+      if (!one)
+#pragma unroll
+        for (int k = 1; k < kSeqsLane; ++k) c += min(max(from[k] + tiles[k] - x, 0), tiles[k]);
+      return __reduce_add_sync(0xffffffffu, c);
+    };
+    int lo = 0, hi = __reduce_max_sync(0xffffffffu, end);
+    if (lane == 0) found.b = -1;
+    __syncwarp();
+    if (!bad && rank < above(0)) {
+      while (hi - lo > 1) {
+        const int q = (hi - lo + 3) >> 2, x1 = lo + q, x2 = min(x1 + q, hi), x3 = min(x2 + q, hi);
+        const int c1 = above(x1), c2 = above(x2), c3 = above(x3);
+        if (c3 > rank) {
+          lo = x3;
+        } else if (c2 > rank) {
+          lo = x2;
+          hi = x3;
+        } else if (c1 > rank) {
+          lo = x1;
+          hi = x2;
+        } else {
+          hi = x1;
+        }
+      }
+      int rest = rank - above(hi);  // among those of size lo
+#pragma unroll
+      for (int k = 0; k < kSeqsLane; ++k) {
+        const bool here = from[k] <= lo && lo < from[k] + tiles[k];
+        const uint32_t all = __ballot_sync(0xffffffffu, here);
+        if (here && __popc(all & ((1u << lane) - 1)) == rest) {
+          found = Seq{lane + 32 * k, row0[k], n[k], kv[k]};
+          at = lo - from[k];
+        }
+        rest -= __popc(all);
+      }
+    }
+  }
+  __syncthreads();
+  *local = at;
+  return found;
 }
-__device__ __forceinline__ float *part_ml(const AttnArgs &a, long long items, int parts, int D) {
-  return static_cast<float *>(a.ws) + items * a.cache.Hk * parts * kRows * D;
+
+// Block `n` of a call: a tile of a key head.  The heads of a tile start side by side; but those of one sequence whose
+// keys and values would not all stay in a die's half of the L2 one after the other (8192 tokens over 24576, 67 MB:
+// 3.66 ms, side by side 3.71).
+__device__ __forceinline__ Seq find_block(const AttnArgs &a, int n, int *hk, int *local) {
+  const int Hk = a.cache.Hk, ranks = a.blocks / Hk;
+  const bool apart = a.seq.B == 1 && 2ll * a.seq.kv_lens[0] * Hk * a.cache.D > (48 << 20);
+  *hk = apart ? n / ranks : n % Hk;
+  return find_largest(a, apart ? n % ranks : n / Hk, ranks, local);
 }
 
 // What the softmax needs of a tile's 4 pages: key scales and logarithms of value scales.
@@ -213,15 +317,16 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const CacheArgs &c = a.cache;
   int local = 0;
-  const long long item = (long long)gridDim.x - 1 - blockIdx.x;  // the later rows of a prompt, which see more, first
-  const Seq s = find_seq(a.seq, item, a.r, kRows, 1, &local);
+  const int split = (int)blockIdx.x < a.whole ? 1 : a.splits, part_no = (int)blockIdx.x - a.whole;
+  const int z = split > 1 ? part_no % split : 0;
+  int hk = 0;
+  const Seq s = find_block(a, split > 1 ? a.whole + part_no / split : (int)blockIdx.x, &hk, &local);
   if (s.b < 0) return;
   const int first = local * kRows, count = (int)min((long long)kRows, (long long)s.n * a.r - first);
   if (count <= 0) return;
-  const int hk = blockIdx.y;
   const int seen = a.causal ? min(s.kv, max(0, s.kv - s.n + (first + count - 1) / a.r + 1)) : s.kv;
   // this block's tiles: base .. base + ntiles - 1 of the rows'
-  const int all = (seen + kTile - 1) / kTile, part = (all + (int)gridDim.z - 1) / (int)gridDim.z, base = part * (int)blockIdx.z;
+  const int all = (seen + kTile - 1) / kTile, part = (all + split - 1) / split, base = part * z;
   const int ntiles = max(0, min(part, all - base));
 
   uint8_t *const smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -485,9 +590,9 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
     if (ntiles > 0) wait(&bars.v_empty[(ntiles - 1) % G::kVStages], ((ntiles - 1) / G::kVStages) & 1);
     __syncwarp();
     fence_after();
-    if (gridDim.z > 1) {  // a part: fp32, relative to m
-      const long long at = part_row(a, item, hk, blockIdx.z, gridDim.z) + row;
-      if (group == 0) reinterpret_cast<float2 *>(part_ml(a, gridDim.x, gridDim.z, D))[at] = make_float2(ntiles > 0 ? m : -INFINITY, l);
+    if (split > 1) {  // a part: fp32, relative to m
+      const long long at = part_row(part_no) + row;
+      if (group == 0) reinterpret_cast<float2 *>(part_ml(a, (int)gridDim.x - a.whole, D))[at] = make_float2(ntiles > 0 ? m : -INFINITY, l);
       const float un = ex2(-kPExp), scale = ex2(lref);
       constexpr int kRounds = 2, kCols = kShare / kRounds;  // of a group in a round
 #pragma unroll 1
@@ -720,16 +825,17 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
 // Joins the parts of an item's rows: o = sum 2^(m_p - m) o_p / sum 2^(m_p - m) l_p.  A thread has 4 columns of a row.
 constexpr int kJoinRows = 16;
 template <int D>
-__global__ void __launch_bounds__(256) attn_tile_join(const AttnArgs a, int parts) {
-  int local = 0;
-  const Seq s = find_seq(a.seq, blockIdx.x, a.r, kRows, 1, &local);
+__global__ void __launch_bounds__(256) attn_tile_join(const AttnArgs a) {
+  const int parts = a.splits;
+  int local = 0, hk = 0;
+  const Seq s = find_block(a, a.whole + blockIdx.x, &hk, &local);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are written (no block ends before that)
   if (s.b < 0) return;
-  const int hk = blockIdx.y, row0 = blockIdx.z * kJoinRows, first = local * kRows + row0;
+  const int row0 = blockIdx.y * kJoinRows, first = local * kRows + row0;
   const int count = (int)min((long long)kJoinRows, (long long)s.n * a.r - first);
   const float *const o = static_cast<const float *>(a.ws);
-  const float2 *const ml = reinterpret_cast<const float2 *>(part_ml(a, gridDim.x, parts, D));
-  const long long base = part_row(a, blockIdx.x, hk, 0, parts) + row0;
+  const float2 *const ml = reinterpret_cast<const float2 *>(part_ml(a, (long long)gridDim.x * parts, D));
+  const long long base = part_row((long long)blockIdx.x * parts) + row0;
   for (int x = threadIdx.x; x < count * (D / 4); x += 256) {
     const int row = x / (D / 4), d = x % (D / 4) * 4, rr = first + row, tok = rr / a.r;
     float m = kNone, l = 0.f;
@@ -786,14 +892,13 @@ cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
              D >= 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  const int parts = a.ws ? a.splits : 1;
-  const dim3 grid((unsigned)item_count(a.seq, a.r, kRows, 1), c.Hk, parts);
-  attn_tile_kernel<D><<<grid, G::kThreads, G::kSmem, s>>>(a, map);
+  const int cut = a.blocks - a.whole;
+  attn_tile_kernel<D><<<a.whole + cut * a.splits, G::kThreads, G::kSmem, s>>>(a, map);
   e = cudaGetLastError();
-  if (e != cudaSuccess || parts < 2) return e;
+  if (e != cudaSuccess || cut == 0) return e;
   // The join comes up while the last blocks end, and waits for them.
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid.x, grid.y, kRows / kJoinRows);
+  cfg.gridDim = dim3(cut, kRows / kJoinRows);
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr{};
@@ -801,41 +906,57 @@ cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_tile_join<D>, a, parts);
+  e = cudaLaunchKernelEx(&cfg, attn_tile_join<D>, a);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
 }  // namespace
 
-// The most parts that attn_tile_parts takes for so many tokens or fewer: none has less than 8 tiles, and no more
-// than fill the GPU once, or are two where the blocks alone do not.
-int attn_tile_most_parts(long long blocks, long long max_kv, int num_sms) {
-  return blocks >= num_sms ? 1 : (int)std::max(1LL, std::min({32LL, max_kv / (8 * kTile), (num_sms + blocks - 1) / blocks + 1}));
+// Tiles of a call and key heads, at most (packed: of any lengths).
+static long long tile_blocks(const SeqArgs &q, int r, int Hk) {
+  const long long each = ((long long)q.T * r + kRows - 1) / kRows;
+  return (q.B > 32 * kSeqsLane ? item_count(q, r, kRows, 1) : !q.cu || q.B == 1 ? each * q.B : (long long)q.T * r / kRows + q.B) * Hk;
 }
-// A block takes a tile's time per tile and about that of kEnds to start and end, one block to an SM at a time; a
-// part's values cost kPart more, a join kJoin: the number of parts with the least time.
-int attn_tile_parts(long long blocks, long long max_kv, int num_sms) {
+// Where blocks do not fill the GPU all are cut: a block takes a tile's time per tile and about that of kEnds to start
+// and end, one block to an SM at a time; a part's values cost kPart more, a join kJoin: the number of parts with
+// the least time.  Where they fill it some times over, and all have about the same length (one sequence, or fixed
+// lengths; others' blocks get shorter to the end), those that are left for the last time are cut into as many parts
+// as fill it once more, if the time saved is more than those cost (8192 tokens over 24576, 10.1 times: 3.65 to
+// 3.49 ms; 1.03 times, 2048 tokens, heads of 256: 62 to 53 us).  `most`: the most parts for so many tokens or fewer;
+// none has less than 8 tiles.
+TileCut attn_tile_cut(const SeqArgs &q, int r, int Hk, int D, int max_kv, int num_sms, bool most) {
   constexpr int kEnds = 10, kPart = 8, kJoin = 6;
-  const long long tiles = (max_kv + kTile - 1) / kTile;
-  const int most = attn_tile_most_parts(blocks, max_kv, num_sms);
-  int best = 1;
+  const long long blocks = tile_blocks(q, r, Hk);
+  const int tiles = (int)(((long long)max_kv + kTile - 1) / kTile), slots = num_sms * (D == 256 ? Geo<256>::kBlocks : Geo<128>::kBlocks);
+  TileCut c{(int)blocks, (int)blocks, 1};
+  if (blocks >= num_sms) {
+    const int left = (int)(blocks % slots), parts = left ? std::min({slots / left, tiles / 8, 32}) : 1;
+    const bool even = !q.cu || q.B == 1;
+    if (even && blocks > slots && parts > 1 &&
+        (most || tiles + kEnds > (tiles + parts - 1) / parts + kEnds + kPart + kJoin + parts / 4)) {
+      c.whole = (int)blocks - left;
+      c.parts = parts;
+    }
+    return c;
+  }
+  const int up_to = (int)std::max(1LL, std::min({32LL, (long long)max_kv / (8 * kTile), (num_sms + blocks - 1) / blocks + 1}));
   long long least = 0;
-  for (int p = 1; p <= most; ++p) {
+  for (int p = 1; p <= up_to; ++p) {
     const long long time =
         (blocks * p + num_sms - 1) / num_sms * ((tiles + p - 1) / p + kEnds + (p > 1 ? kPart : 0)) + (p > 1 ? kJoin + p / 4 : 0);
     if (p == 1 || time < least) {
       least = time;
-      best = p;
+      c.parts = p;
     }
   }
-  return best;
+  if (most) c.parts = up_to;
+  if (c.parts > 1) c.whole = 0;
+  return c;
 }
 
-size_t attn_tile_ws_bytes(long long blocks, int D, int parts) {
-  return parts < 2 ? 0 : (size_t)blocks * parts * kRows * (D + 2) * sizeof(float);
+size_t attn_tile_ws_bytes(const TileCut &c, int D) {
+  return (size_t)(c.blocks - c.whole) * c.parts * kRows * (D + 2) * sizeof(float);
 }
-
-long long attn_tile_blocks(const SeqArgs &q, int r, int Hk) { return item_count(q, r, kRows, 1) * Hk; }
 
 cudaError_t launch_attn_tile(const AttnArgs &a, cudaStream_t s) {
   return a.cache.D == 64 ? launch<64>(a, s) : a.cache.D == 128 ? launch<128>(a, s) : launch<256>(a, s);

@@ -79,10 +79,11 @@ struct AttnPlan {
   bool tile;     // attn_tile.cu; neither: attn_rows.cu
   int splits;    // ranges of the tokens side by side (attn_few.cu cuts by itself)
   size_t bytes;
+  gdn::TileCut cut;  // attn_tile.cu
 };
 AttnPlan attn_plan(const gdn_attn_shape *s, bool packed, long long rows, int max_kv, int sms, bool room) {
   const int r = s->Hq / s->Hk, cu = 0;
-  AttnPlan p{0, false, 1, 0};
+  AttnPlan p{0, false, 1, 0, {}};
   if (s->io_dtype == GDN_BF16) {
     p.few_rows = gdn::attn_few_rows(s->D, (long long)bound_new(s, packed) * r);
     if (p.few_rows) {
@@ -90,9 +91,9 @@ AttnPlan attn_plan(const gdn_attn_shape *s, bool packed, long long rows, int max
       return p;
     }
     p.tile = true;
-    const long long blocks = gdn::attn_tile_blocks(gdn::SeqArgs{s->B, s->T, 0, 0, packed ? &cu : nullptr, nullptr, nullptr}, r, s->Hk);
-    p.splits = room ? gdn::attn_tile_most_parts(blocks, max_kv, sms) : gdn::attn_tile_parts(blocks, max_kv, sms);
-    p.bytes = gdn::attn_tile_ws_bytes(blocks, s->D, p.splits);
+    p.cut = gdn::attn_tile_cut(gdn::SeqArgs{s->B, s->T, 0, 0, packed ? &cu : nullptr, nullptr, nullptr}, r, s->Hk, s->D, max_kv, sms, room);
+    p.splits = p.cut.parts;
+    p.bytes = gdn::attn_tile_ws_bytes(p.cut, s->D);
     return p;
   }
   // fp32: enough blocks to fill the GPU twice, none with less than 64 tokens
@@ -196,7 +197,9 @@ gdn_status gdn_attn(const gdn_attn_shape *shape, const gdn_attn_io *io, void *st
     if (io->workspace_bytes < plan.bytes) return GDN_ERR_INVALID_ARG;
     a.ws = io->workspace;
   }
-  a.splits = plan.splits;
+  a.splits = a.ws ? plan.splits : 1;
+  a.blocks = plan.cut.blocks;
+  a.whole = a.ws ? plan.cut.whole : plan.cut.blocks;
   const cudaError_t e = plan.few_rows ? gdn::launch_attn_few(a, plan.few_rows, dev.sms, (cudaStream_t)stream)
                         : plan.tile   ? gdn::launch_attn_tile(a, (cudaStream_t)stream)
                                       : gdn::launch_attn_rows(a, (cudaStream_t)stream);

@@ -218,6 +218,7 @@ struct AttnArgs {
   float scale;
   void *ws;  // may be null
   int splits;  // ranges of the tokens side by side, with ws
+  int blocks, whole;  // attn_tile.cu: tiles of rows and key heads, and those whose tokens are not cut
 };
 struct RopeX {
   const void *x;
@@ -258,10 +259,11 @@ int attn_few_rows(int D, long long rows);
 size_t attn_few_ws_bytes(int D, int rows_tile, int num_sms);
 cudaError_t launch_attn_few(const AttnArgs &a, int rows_tile, int num_sms, cudaStream_t s);
 // bf16 io, many rows: the blocks of a call, the parts that its tokens are cut into, the partial results' bytes.
-long long attn_tile_blocks(const SeqArgs &q, int r, int Hk);
-int attn_tile_parts(long long blocks, long long max_kv, int num_sms);
-int attn_tile_most_parts(long long blocks, long long max_kv, int num_sms);
-size_t attn_tile_ws_bytes(long long blocks, int D, int parts);
+struct TileCut {
+  int blocks, whole, parts;  // the blocks from number `whole` on in so many parts each
+};
+TileCut attn_tile_cut(const SeqArgs &q, int r, int Hk, int D, int max_kv, int num_sms, bool most);
+size_t attn_tile_ws_bytes(const TileCut &c, int D);
 cudaError_t launch_attn_tile(const AttnArgs &a, cudaStream_t s);
 
 // Device error bits (the error word is OR-ed).

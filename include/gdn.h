@@ -572,7 +572,7 @@ typedef enum {
 typedef struct {
   int kernel; /* gdn_attn_kernel */
   int rows;   /* of a tile */
-  int parts;  /* ranges of the tokens side by side; FEW: 0, they follow from the lengths */
+  int parts;  /* ranges of the tokens side by side (TILE: of the last blocks, or all); FEW: 0, they follow from the lengths */
 } gdn_attn_form;
 
 gdn_status gdn_selftest_attn_form(const gdn_attn_shape *shape, int packed, int workspace, gdn_attn_form *form);

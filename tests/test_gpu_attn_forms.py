@@ -61,6 +61,76 @@ def test_tiles_whole(D):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+def test_last_tiles_in_parts(D, causal):
+    """Two tiles more than the GPU takes at once: those in parts, of a packed sequence and of fixed lengths; and fewer new
+    tokens than the call says, so that other tiles, or none, are the last."""
+    slots = torch.cuda.get_device_properties(0).multi_processor_count * (1 if D == 256 else 2)
+    tokens = 16 * (slots // 2 + 1)  # of two tiles of 128 rows each, with 8 query heads to each of 2 key heads
+    n, kv = tokens - 5, tokens + 700
+    f = form([n], 16, 2, D, BF, kv)
+    assert f.kernel == TILE and f.parts > 1 and form([n], 16, 2, D, BF, kv, ws=False).parts == 1
+    cache = R.Cache([kv], 2, D, 16, device="cuda").fill()
+    q, o = attend(cache, [n], 16, BF, causal=causal, max_kv=kv)
+    ok()
+    for at in (0, 16, n - 40):  # the first rows are the last tiles
+        if causal:
+            k, v = cache.rows(0, kv - n + at + 40)
+            check_rows(o[at:at + 40], q[at:at + 40], cache, 0, 40, kv - n + at + 40, 16, True, D ** -0.5, BF, k=k, v=v)
+        else:
+            check_rows(o[at:at + 40], q[at:at + 40], cache, 0, 40, kv, 16, False, D ** -0.5, BF)
+    _, whole = attend(cache, [n], 16, BF, causal=causal, max_kv=kv, q=q, ws=False)
+    assert float((whole.float() - o.float()).abs().max()) <= 2 * 2.0 ** -8 * float(whole.float().abs().max())
+    both = R.Cache([kv, kv - 3], 1, D, 16, device="cuda").fill()
+    q2 = q[:n, :8 * D].repeat(2, 1).reshape(2, n, 8 * D).contiguous()
+    kw = dict(causal=causal, max_kv=kv)
+    o2 = torch.full_like(q2, math.nan)
+    w = workspace(2, n, 8, 1, D, BF, packed=False, max_kv=kv)
+    assert w.numel() > 0
+    gdn.gdn_attn(q2, o2, *both.args(), Hq=8, workspace=w, **kw)
+    ok()
+    o3 = torch.full_like(q2, math.nan)
+    gdn.gdn_attn(q2, o3, *both.args(), Hq=8, **kw)
+    ok()
+    assert float((o2.float() - o3.float()).abs().max()) <= 2 * 2.0 ** -8 * float(o3.float().abs().max())
+    for fewer in (1, 300, n - 200):
+        w = workspace(1, n, 16, 2, D, BF, max_new=n, max_kv=kv)
+        o4 = torch.full((n, 16 * D), math.nan, device="cuda", dtype=BF)
+        gdn.gdn_attn(q[:n].contiguous(), o4, *cache.args(), Hq=16, cu_seqlens=offsets([fewer]), max_new=n, workspace=w, **kw)
+        ok()
+        assert bool(o4[fewer:].isnan().all())
+        top = min(fewer, 40)
+        if causal:
+            k, v = cache.rows(0, kv - fewer + top)
+            check_rows(o4[:top], q[:top], cache, 0, top, kv - fewer + top, 16, True, D ** -0.5, BF, k=k, v=v)
+        else:
+            check_rows(o4[:top], q[:top], cache, 0, top, kv, 16, False, D ** -0.5, BF)
+
+
+@pytest.mark.parametrize("B", [1, 31, 33, 128, 129, 300])
+@pytest.mark.parametrize("ws", [True, False])
+def test_many_sequences_of_tiles(B, ws):
+    """Tiles are taken by their size over all sequences, up to some number of them; ties, sequences without new tokens,
+    one that the call's bounds skip."""
+    new = [(29 * i) % 90 for i in range(B)]
+    new[0] = 61
+    lens = [n + (131 * i) % 400 for i, n in enumerate(new)]
+    cache = R.Cache(lens, 1, 64, 16, device="cuda").fill()
+    check(cache, new, 8, BF, ws=ws, max_kv=max(lens))
+    if B > 1:
+        q, o = attend(cache, new, 8, BF, ws=ws, max_new=max(new) - 1, max_kv=max(lens))
+        torch.cuda.synchronize()
+        assert gdn.gdn_device_status(reset=True) == gdn.GDN_ERR_INVALID_ARG
+        at = 0
+        for b, n in enumerate(new):
+            if n == max(new):
+                assert bool(o[at:at + n].isnan().all())
+            elif n:
+                check_rows(o[at:at + n], q[at:at + n], cache, b, n, lens[b], 8, True, 64 ** -0.5, BF)
+            at += n
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("n", [1, 20])
 def test_fp32_in_parts(D, n):
     f = form([n], 4, 2, D, F32, 3000)
