@@ -3,7 +3,7 @@
 //
 // Bound by the cache's bytes, which the rows of a key head share (64 x 1 token over
 // 8192, 24/4 heads of 256: 171 us, 6.3 TB/s; 16 x 4 tokens, ragged, 32/8 heads of 128,
-// 87 MB: 37 us, of which some 10 are a block's start, end and the join).  The products
+// 87 MB: 33 us, of which some 10 are a block's start, end and the join).  The products
 // run transposed, so that the cache is the operand with 16 rows and the queries
 // the one with 8 columns:  S^T = K q^T  and  O^T = V^T P^T  by
 // mma.m16n8k16 in fp16, whose e4m3 operands are exact; q enters with a power of
@@ -20,9 +20,9 @@
 // bank.
 //
 // Work is cut evenly: the slabs of all sequences, key heads and row tiles in a
-// row, an equal range of them to each block.  A unit (sequence, key head, row
-// tile) that lies in several ranges leaves partial results, which a second
-// launch joins.
+// row, an equal range of them to each block (a unit - sequence, key head, row
+// tile - counts as some slabs more than it has).  A unit that lies in several
+// ranges leaves partial results, which a second launch joins.
 #include <algorithm>
 
 #include "cache_device.cuh"
@@ -64,23 +64,33 @@ struct Geo {
   static_assert(kMergeSlots < kDepth, "no slot is left for the next piece");
   static constexpr int kQ = (D / 16) * NT * 256;
   static constexpr int kBytes = kRing + kQ;
+  // What going on to another unit costs a block, in slabs (some 7 us): counted with the unit's own where the work is
+  // cut.  32 x 1 token over 200 to 15,000, 4 heads of 256: 47 us, with half of it 51, without 67; heads of 64 26, with
+  // twice as much 26.3, without 37; 300 x 1 over 500 the same but for heads of 128: 50, without 47.
+  static constexpr int kStart = D == 64 ? 32 / kSub : 16;
 };
 
 struct SeqLen {
   Seq s;
   int slabs, tiles;
+  int each;       // of a unit: what its start costs, and its slabs
   long long len;  // of the sequence's units together
 };
-__device__ __forceinline__ SeqLen seq_len(const AttnArgs &a, int b, int rows_tile, int slab) {
+// What the kernels of a tile have in common: its rows, a slab's tokens, a unit's start in slabs.
+struct Cut {
+  int rows_tile, slab, start;
+};
+__device__ __forceinline__ SeqLen seq_len(const AttnArgs &a, int b, const Cut &cut) {
   SeqLen x{};
   const int lo = a.seq.cu ? a.seq.cu[b] : b * a.seq.T, n = a.seq.cu ? a.seq.cu[b + 1] - lo : a.seq.T;
   x.s = Seq{-1, lo, n, 0};
   if (lo < 0 || n < 0 || (a.seq.cu && (long long)lo + n > a.seq.T)) return x;  // recorded by the scan
   x.s = load_seq(a.seq, b, lo, n);
   if (x.s.b < 0 || n == 0) return x;
-  x.slabs = max(1, (x.s.kv + slab - 1) / slab);
-  x.tiles = (n * a.r + rows_tile - 1) / rows_tile;
-  x.len = (long long)x.slabs * x.tiles * a.cache.Hk;
+  x.slabs = max(1, (x.s.kv + cut.slab - 1) / cut.slab);
+  x.each = x.slabs + cut.start;
+  x.tiles = (n * a.r + cut.rows_tile - 1) / cut.rows_tile;
+  x.len = (long long)x.each * x.tiles * a.cache.Hk;
   return x;
 }
 
@@ -106,7 +116,9 @@ struct Located {
   int b;              // sequence at pos, -1: none
   long long in_seq;   // position there
 };
-__device__ Located locate(const AttnArgs &a, int rows_tile, int slab, int index, int parts, int least, bool whole, int of = -1) {
+template <int kThreads>
+__device__ Located locate(const AttnArgs &a, const Cut &cut, int index, int parts, int least, bool whole, int of = -1) {
+  constexpr int kWarps = kThreads / 32;
   __shared__ long long sums[kWarps], base;
   __shared__ int bad, at_b;
   __shared__ long long at_in;
@@ -126,7 +138,7 @@ __device__ Located locate(const AttnArgs &a, int rows_tile, int slab, int index,
         return 0;
       }
     }
-    const SeqLen x = seq_len(a, b, rows_tile, slab);
+    const SeqLen x = seq_len(a, b, cut);
     return whole ? (long long)x.tiles * a.cache.Hk : x.len;
   };
   Located r{};
@@ -326,12 +338,21 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
   if (tid < kWarps * G::kDepth) bar_init(&bars[tid / G::kDepth][tid % G::kDepth], 1);
   if (tid == 0) gave_up = 0;
   const bool whole = a.ws == nullptr;
-  const Located loc = locate(a, RT, G::kSlab, blockIdx.x, gridDim.x, whole ? 1 : least, whole);
+  constexpr Cut cut{RT, G::kSlab, G::kStart};
+  const Located loc = locate<kThreads>(a, cut, blockIdx.x, gridDim.x, whole ? 1 : least, whole);
   if (loc.b < 0) return;
-  long long left = min(loc.share, loc.total - loc.share * blockIdx.x);
-  SeqLen q = seq_len(a, loc.b, RT, G::kSlab);
-  int unit = whole ? (int)loc.in_seq : quotient(loc.in_seq, q.slabs);
-  int slab0 = whole ? 0 : (int)(loc.in_seq - (long long)unit * q.slabs);
+  long long left = min(loc.share, loc.total - loc.share * blockIdx.x);  // of the range, from the next slab on
+  SeqLen q = seq_len(a, loc.b, cut);
+  int unit = whole ? (int)loc.in_seq : quotient(loc.in_seq, q.each);
+  int slab0 = 0;
+  if (!whole) {
+    slab0 = (int)(loc.in_seq - (long long)unit * q.each) - cut.start;
+    if (slab0 < 0) {  // the range starts with a unit's start
+      left += slab0;
+      slab0 = 0;
+      if (left <= 0) return;
+    }
+  }
   uint8_t *const ring = smem + warp * (G::kDepth * G::kSlabBytes);
   uint64_t *const bar = bars[warp];
   uint32_t parity = 0;  // bit i: of slot i's next phase
@@ -716,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
     const bool whole_unit = starts && ends;
     const int part = 2 * blockIdx.x + (starts ? 1 : 0), out_rows = count;
     const RowAt *const out_at = at_row[turn];
-    left -= whole ? 1 : slab1 - slab0;
+    left -= whole ? 1 : slab1 - slab0 + cut.start;
     slab0 = 0;
     ++unit;
     bool more = left > 0;
@@ -725,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
       for (int nb = q.s.b + 1;; ++nb) {
         more = nb < a.seq.B;
         if (!more) break;
-        q = seq_len(a, nb, RT, G::kSlab);
+        q = seq_len(a, nb, cut);
         if (q.len > 0) break;
       }
     }
@@ -764,31 +785,34 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
 // Joins a unit's parts:  o = sum 2^(m_p - m) o_p / sum 2^(m_p - m) l_p.  by_unit: block x takes unit x (of
 // tiles_max Hk to a sequence); else the unit in which boundary x + 1 between the blocks' ranges is the first.
 // Rows of its tile over blockIdx.y; the threads stand side by side over 4 columns each and over the parts.
+constexpr int kJoinThreads = 128;
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) attn_few_join(const AttnArgs a, int least, int parts, int tiles_max, int by_unit) {
-  constexpr int RT = 8 * NT, kCols = D / 4, kSide = kThreads / kCols, kSlab = Geo<D, NT>::kSlab;
+__global__ void __launch_bounds__(kJoinThreads) attn_few_join(const AttnArgs a, int least, int parts, int tiles_max, int by_unit) {
+  using G = Geo<D, NT>;
+  constexpr int RT = 8 * NT, kCols = D / 4, kSide = kJoinThreads / kCols;
+  constexpr Cut cut{RT, G::kSlab, G::kStart};
   __shared__ float4 sums[kSide][kCols];
   __shared__ float side_l[kSide], side_m[kSide];
   const int col = threadIdx.x % kCols, side = threadIdx.x / kCols;
   SeqLen q{};
-  long long start = 0, share = 0;  // of the unit, in slabs; a block's range
+  long long start = 0, share = 0;  // of the unit's first slab; a block's range
   int unit = 0;
   if (by_unit) {
     const int per = tiles_max * a.cache.Hk, b = blockIdx.x / per, x = blockIdx.x % per;
-    const Located loc = locate(a, RT, kSlab, 0, parts, least, false, b);
-    q = seq_len(a, b, RT, kSlab);
+    const Located loc = locate<kJoinThreads>(a, cut, 0, parts, least, false, b);
+    q = seq_len(a, b, cut);
     const int hk = x / tiles_max, tile = x % tiles_max;
     unit = hk * q.tiles + tile;
     share = loc.share;
-    start = loc.in_seq + (long long)unit * q.slabs;
+    start = loc.in_seq + (long long)unit * q.each + cut.start;
     if (loc.total == 0 || q.len == 0 || tile >= q.tiles) share = 0;
   } else {
-    const Located loc = locate(a, RT, kSlab, blockIdx.x + 1, parts, least, false);
+    const Located loc = locate<kJoinThreads>(a, cut, blockIdx.x + 1, parts, least, false);
     if (loc.b >= 0) {
-      q = seq_len(a, loc.b, RT, kSlab);
-      unit = quotient(loc.in_seq, q.slabs);
-      const int slab = (int)(loc.in_seq - (long long)unit * q.slabs);
-      if (slab > 0 && slab <= loc.share) share = loc.share;  // else between two units, or not the first boundary inside
+      q = seq_len(a, loc.b, cut);
+      unit = quotient(loc.in_seq, q.each);
+      const int slab = (int)(loc.in_seq - (long long)unit * q.each) - cut.start;
+      if (slab > 0 && slab <= loc.share) share = loc.share;  // else before the slabs, or not the first boundary inside
       start = loc.share * (blockIdx.x + 1) - slab;
     }
   }
@@ -862,7 +886,7 @@ template <int D, int NT>
 struct FewTag {};
 
 // Slabs of a block's range at least: one per warp, and 128 tokens (1 token over 4096, 4 heads of 256, in a graph:
-// 64 tokens 18.6 us, 128 16.3, 256 16.4, 512 19.3; heads of 64 and 128 lose with every slab beyond one per warp).
+// 64 tokens 15.8 us, 128 13.7, 256 13.9, 512 17.1; heads of 64 and 128 lose with every slab beyond one per warp).
 template <int D, int NT>
 constexpr int kLeast = Geo<D, NT>::kSlab * kWarps >= 128 ? kWarps : 128 / Geo<D, NT>::kSlab;
 
@@ -882,7 +906,7 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t s) {
   // rows of a tile side by side, as many as are all up at once
   cfg.gridDim = dim3(by_unit ? (unsigned)units : blocks - 1);
   cfg.gridDim.y = std::max(1u, std::min(8u * NT, 8u * num_sms / cfg.gridDim.x));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
