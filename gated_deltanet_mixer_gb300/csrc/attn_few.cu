@@ -123,6 +123,36 @@ __device__ Located locate(const AttnArgs &a, const Cut &cut, int index, int part
   __shared__ int bad, at_b;
   __shared__ long long at_in;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (a.seq.B <= 32) {  // each warp for itself, without a barrier (1 token over 4096: 13.2 us, with them 13.7)
+    bool wrong = false;
+    long long len = 0;
+    if (lane < a.seq.B) {
+      if (a.seq.cu) {
+        const int lo = a.seq.cu[lane], hi = a.seq.cu[lane + 1];
+        wrong = lo < 0 || hi < lo || hi > a.seq.T;
+      }
+      const SeqLen x = seq_len(a, lane, cut);
+      len = whole ? (long long)x.tiles * a.cache.Hk : x.len;
+    }
+    Located r{};
+    r.b = -1;
+    if (__any_sync(0xffffffffu, wrong)) {
+      if (tid == 0) atomicOr(a.seq.err, kErrSeqlens);
+      return r;
+    }
+    const long long incl = warp_sum_incl(len, lane);
+    r.total = __shfl_sync(0xffffffffu, incl, 31);
+    r.share = max(div_up(r.total, parts), (long long)least);
+    const long long pos = r.share * index;
+    const uint32_t at = __ballot_sync(0xffffffffu, pos >= incl - len && pos < incl);
+    const int from = of >= 0 ? of : at ? __ffs(at) - 1 : 0;
+    const long long before = __shfl_sync(0xffffffffu, incl - len, from);
+    if (of >= 0 || at) {
+      r.b = from;
+      r.in_seq = of >= 0 ? before : pos - before;
+    }
+    return r;
+  }
   if (tid == 0) {
     bad = 0;
     at_b = -1;
@@ -337,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
   const CacheArgs &c = a.cache;
   if (tid < kWarps * G::kDepth) bar_init(&bars[tid / G::kDepth][tid % G::kDepth], 1);
   if (tid == 0) gave_up = 0;
+  __syncthreads();
   const bool whole = a.ws == nullptr;
   constexpr Cut cut{RT, G::kSlab, G::kStart};
   const Located loc = locate<kThreads>(a, cut, blockIdx.x, gridDim.x, whole ? 1 : least, whole);
@@ -785,8 +816,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
 // Joins a unit's parts:  o = sum 2^(m_p - m) o_p / sum 2^(m_p - m) l_p.  by_unit: block x takes unit x (of
 // tiles_max Hk to a sequence); else the unit in which boundary x + 1 between the blocks' ranges is the first.
 // Rows of its tile over blockIdx.y; the threads stand side by side over 4 columns each and over the parts.
-constexpr int kJoinThreads = 128;
-template <int D, int NT>
+template <int D, int NT, int kJoinThreads>
 __global__ void __launch_bounds__(kJoinThreads) attn_few_join(const AttnArgs a, int least, int parts, int tiles_max, int by_unit) {
   using G = Geo<D, NT>;
   constexpr int RT = 8 * NT, kCols = D / 4, kSide = kJoinThreads / kCols;
@@ -885,8 +915,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_few_join(const AttnArgs a, 
 template <int D, int NT>
 struct FewTag {};
 
-// Slabs of a block's range at least: one per warp, and 128 tokens (1 token over 4096, 4 heads of 256, in a graph:
-// 64 tokens 15.8 us, 128 13.7, 256 13.9, 512 17.1; heads of 64 and 128 lose with every slab beyond one per warp).
+// Slabs of a block's range at least: one per warp, and 128 tokens (1 token over 4096, 4 heads of 256, 12 us:
+// 64 tokens take 2.1 more, 256 0.2 and 512 3.4; heads of 64 and 128 lose with every slab beyond one per warp).
 template <int D, int NT>
 constexpr int kLeast = Geo<D, NT>::kSlab * kWarps >= 128 ? kWarps : 128 / Geo<D, NT>::kSlab;
 
@@ -906,14 +936,17 @@ cudaError_t launch(const AttnArgs &a, int num_sms, cudaStream_t s) {
   // rows of a tile side by side, as many as are all up at once
   cfg.gridDim = dim3(by_unit ? (unsigned)units : blocks - 1);
   cfg.gridDim.y = std::max(1u, std::min(8u * NT, 8u * num_sms / cfg.gridDim.x));
-  cfg.blockDim = dim3(kJoinThreads);
+  // Few units have many parts each: 8 side by side (1 token over 16384, heads of 256, in a graph: 20.0 us with 2, 17.2
+  // with 8; 16 x 4 tokens, whose parts are few, 34.9 and 47).
+  const bool wide = units * 8 * NT <= num_sms;
+  cfg.blockDim = dim3(wide ? 2 * D : kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, attn_few_join<D, NT>, a, kLeast<D, NT>, blocks, tiles_max, by_unit);
+  e = cudaLaunchKernelEx(&cfg, wide ? attn_few_join<D, NT, 2 * D> : attn_few_join<D, NT, kThreads>, a, kLeast<D, NT>, blocks, tiles_max, by_unit);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
