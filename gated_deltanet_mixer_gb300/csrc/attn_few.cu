@@ -7,8 +7,11 @@
 // run transposed, so that the cache is the operand with 16 rows and the queries
 // the one with 8 columns:  S^T = K q^T  and  O^T = V^T P^T  by
 // mma.m16n8k16 in fp16, whose e4m3 operands are exact; q enters with a power of
-// two per row, p with one that keeps it normal down to 2^-25 (11 bits of p
-// where bf16 would keep 8).
+// two per row, p with its page's value scale and one that keeps the product normal
+// down to 2^-25 of the row's largest (11 bits of p where bf16 would keep 8).  What O
+// is relative to is the running maximum of these products, apart from that of p
+// alone, which the sum of the weights is relative to: a page of large values and
+// hardly any weight costs the others no bits.
 //
 // A slab is 16 tokens: its k and v are two contiguous blocks of a page, and its
 // scales two numbers.  Each warp copies its own slabs ahead into its own ring
@@ -38,12 +41,14 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kBlocksSM = 2;
 constexpr float kNone = -1.7e38f;  // the running maximum of a row that has seen nothing
 constexpr float kLog2e = 1.4426950408889634f;
-// The reference of a row's exponents is its running maximum, moved only when a
-// score passes it by kSlack (in powers of 2): p stays below 2^kSlack, and in
-// fp16 times kPScale finite, and normal from 2^-25 on.
+// The references of a row's exponents are its running maxima, less kLift and moved only
+// when a score passes them by kSlack (in powers of 2).  Weights stay below 2^(kSlack + kLift),
+// and what is far below the largest, but has larger values, does not vanish before it
+// gets its scale (2^-120 to 2^7; the exponential ends at 2^-126); their products with the
+// scales stay below 2^(kSlack + kPExp) in fp16, finite, and normal from 2^-25 on.
 constexpr float kSlack = 4.f;
-constexpr float kPScale = 2048.f;
-constexpr float kLeastRef = 0x1p-100f;  // what value scales are relative to at least
+constexpr float kLift = 30.f;
+constexpr float kPExp = 11.f;
 
 // A slab's copies: kSub times 16 tokens, of a page each, in a ring of kDepth slabs per warp.  More tokens at a
 // time spread what a slab costs whatever its width (waits, votes, copies; some 250 instructions of a warp with
@@ -474,13 +479,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
 #pragma unroll
         for (int j = 0; j < NT; ++j) qr[k][j] = *reinterpret_cast<const uint2 *>(sq + ((k * NT + j) * 32 + lane) * 8);
     }
-    float acc[MT][NT][4], m[NT][2], l[NT][2], qs[NT][2];
+    // m, l: what the weights are relative to, their sum; mv: what acc is, in weight times value scale; up: 2^(m - mv) as fp16 has it
+    float acc[MT][NT][4], m[NT][2], l[NT][2], mv[NT][2], up[NT][2], qs[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        m[j][u] = kNone;
-        l[j][u] = 0.f;
+        m[j][u] = mv[j][u] = kNone;
+        l[j][u] = up[j][u] = 0.f;
         qs[j][u] = qscale[8 * j + 2 * t + u];
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[i][j][u] = acc[i][j][2 + u] = 0.f;
@@ -491,7 +497,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
     };
     // Tokens up to this one are seen by every row (rows that are none may see them too: nothing reads those).
     const int all_see = a.causal ? q.s.kv - q.s.n + first / a.r : q.s.kv - 1;
-    float ref = kLeastRef, inv_ref = kPScale / kLeastRef;  // the largest value scale so far, kPScale over it
     // Rows g and g + 8 of S^T are these tokens of 16.
     const int tg = g >> 1, bg = g & 1, gr0 = (tg + 2 * bg) & 3, gr1 = (tg + 2 * bg + 1) & 3;
     const int in0 = 4 * gr0 + 2 * bg, in1 = 4 * gr1 + 2 * bg + 1;
@@ -568,12 +573,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
         pg[1] = load_page((i + kBatch) * SUB + lane);
       }
       if (in == kBatch / 2 && i > kBatch) sc[1] = load_scales(pg[1]);
-      float ks[SUB], vs[SUB], vtop = 0.f;
+      float ks[SUB], vs[SUB], lv[SUB];
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
         ks[u] = __shfl_sync(0xffffffffu, sc[0].x, in * SUB + u);
         vs[u] = __shfl_sync(0xffffffffu, sc[0].y, in * SUB + u);
-        vtop = fmaxf(vtop, vs[u]);
+        lv[u] = __log2f(vs[u]);  // of 0: below all; of NaN: passed over by the maxima
       }
       const uint32_t next = slot + 1 == G::kDepth ? 0 : slot + 1;
       const int tok0 = tok_first + i * kStep;
@@ -593,7 +598,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
       const uint32_t gone = (__ballot_sync(0xffffffffu, pg[0] < 0) >> (in * SUB)) & ((1u << SUB) - 1);  // bit u: no page
       const bool masked = gone != 0 || tok0 + G::kSlab - 1 > all_see;
       if (masked) {
-        vtop = 0.f;  // not yet: a row that does not see the larger values' page would lose bits to them
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -605,37 +609,38 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
               if (tok0 + 16 * u + in1 > last) y[u][j][2 + e] = -INFINITY;
             }
       }
-      float top[NT][2], high = -INFINITY;
+      float top[NT][2], topv[NT][2], high = -INFINITY;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           top[j][e] = fmaxf(y[0][j][e], y[0][j][2 + e]);
+          topv[j][e] = top[j][e] + lv[0];
 #pragma unroll
-          for (int u = 1; u < SUB; ++u) top[j][e] = fmaxf(top[j][e], fmaxf(y[u][j][e], y[u][j][2 + e]));
-          high = fmaxf(high, top[j][e] - m[j][e]);
+          for (int u = 1; u < SUB; ++u) {
+            const float x = fmaxf(y[u][j][e], y[u][j][2 + e]);
+            top[j][e] = fmaxf(top[j][e], x);
+            topv[j][e] = fmaxf(topv[j][e], x + lv[u]);
+          }
+          high = fmaxf(high, fmaxf(top[j][e] - m[j][e], topv[j][e] - mv[j][e]));
         }
-      if (__any_sync(0xffffffffu, high > kSlack || vtop > ref)) {
-        float shrink = 1.f;  // on the values so far, where a larger value scale sets in
-        if (vtop > ref) {
-          shrink = ref / vtop;
-          ref = vtop;
-          inv_ref = kPScale / vtop;
-        }
+      if (__any_sync(0xffffffffu, high > kSlack + kLift)) {
+        auto over_lanes = [](float x) {
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        };
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           float al[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x = top[j][e];
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            x = fmaxf(x, m[j][e]);
-            al[e] = ex2(m[j][e] - x);
-            l[j][e] *= al[e];
+            const float x = fmaxf(over_lanes(top[j][e]) - kLift, m[j][e]), z = fmaxf(over_lanes(topv[j][e]) - kLift, mv[j][e]);
+            l[j][e] *= ex2(m[j][e] - x);
+            al[e] = ex2(mv[j][e] - z);
             m[j][e] = x;
-            al[e] *= shrink;
+            mv[j][e] = z;
+            up[j][e] = ex2(fminf(x - z + (kPExp - kLift), 120.f));  // at most 2^105 where a value scale is above 0
           }
 #pragma unroll
           for (int i2 = 0; i2 < MT; ++i2) {
@@ -648,27 +653,16 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
       }
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
-        if (masked && vs[u] > ref) {  // page by page: who sees this one has seen those before it
-          const float shrink = ref / vs[u];
-          ref = vs[u];
-          inv_ref = kPScale / vs[u];
-#pragma unroll
-          for (int i2 = 0; i2 < MT; ++i2)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i2][j][e] *= shrink;
-        }
-        const float pv = vs[u] * inv_ref;  // NaN where the scale is
         uint32_t pb[NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
+          const float pv[2] = {vs[u] * up[j][0], vs[u] * up[j][1]};  // NaN where the scale is
           float pp[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float w = ex2(y[u][j][e] - m[j][e & 1]);
             l[j][e & 1] += w;
-            pp[e] = w * pv;
+            pp[e] = w * pv[e & 1];
             if (masked && y[u][j][e] == -INFINITY) pp[e] = 0.f;  // whatever the scale is
           }
           pb[j][0] = transpose8(pack2_sat(pp[0], pp[1]));
@@ -759,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
         float top = kNone;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, wm[w][row]);
-        const float f = ex2(m[j][u] - top) * (ref * (1.f / kPScale));
+        const float f = ex2(mv[j][u] - top + (kLift - kPExp));  // never below 2^-110: a value scale is above 2^-121, or all are 0
 #pragma unroll
         for (int i2 = 0; i2 < MT; ++i2)
           *reinterpret_cast<float2 *>(merge + row * G::kPitch + merge_at<D>(g, i2)) = make_float2(acc[i2][j][u] * f, acc[i2][j][2 + u] * f);

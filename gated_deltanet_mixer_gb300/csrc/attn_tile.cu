@@ -10,10 +10,11 @@
 //               more than 2^-17 of that largest.
 //   O += P V    fp16 products: P, rounded to fp16, in TMEM where S was; V's bytes
 //               become fp16 (exact) on the way through a group of four warps.
-// A page's key scale multiplies its scores.  Its value scale, over the largest
-// that the row has seen, enters p as a term of the exponent, and leaves the row's sum
-// again as a factor on the page's part of it: no product per element.  In fp16 p has
-// 11 bits down to 2^-25 of the largest, and is within 2^-36 of it below that.
+// A page's key scale multiplies its scores.  Its value scale enters p as a term of the
+// exponent, and leaves the row's sum again as a factor on the page's part of it: no
+// product per element.  What O is relative to is the running maximum of weight times
+// value scale, apart from that of the weights alone: in fp16 p has 11 bits down to 2^-25
+// of the row's largest product, and is within 2^-36 of it below that.
 //
 // Bound by the products for heads of 256 (8192 tokens over 24576, 24/4 heads: 3.49
 // ms, 1.66 PFLOP/s of bf16's 1.7 sustained; the products of q's two parts are twice those
@@ -46,7 +47,7 @@ constexpr float kNone = -1.7e38f;
 constexpr float kSlack = 4.f;   // p may reach 2^kSlack before the running maximum moves
 constexpr float kPExp = 11.f;   // p stands times 2^11 in fp16
 constexpr float kMinRatio = -60.f;
-constexpr float kNoRef = -200.f;  // the logarithm of the value scales where there is none above 0
+constexpr float kNoScale = -200.f;  // the logarithm of a value scale of 0
 
 template <int D>
 struct Geo {
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
   __shared__ Bars bars;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int gave_up;
-  __shared__ float2 moved[G::kGroups][kRows];  // running maximum and largest value scale after a group's tile
+  __shared__ float2 moved[G::kGroups][kRows];  // running maxima, of scores and with value scales, after a group's tile
   __shared__ Scales ring[kRing];
   __shared__ long long row_q[kRows], row_o[kRows];  // elements before a row
   __shared__ float other[G::kGroups][kRows];  // sum of each group at the end
@@ -451,16 +452,15 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
     sync_products();  // with the products' warp: Q is in place
     const int last = !real ? -1 : a.causal ? s.kv - s.n + tok : s.kv - 1;
     const int all_see = a.causal ? s.kv - s.n + first / a.r : s.kv - 1;
-    float m = kNone, l = 0.f, lref = kNoRef;  // m: what l is relative to; the largest value scale's logarithm
+    float m = kNone, l = 0.f, mv = kNone;  // what the weights' sum l is relative to, and O: the largest weight times value scale
 #pragma unroll 1
     for (int j = group; j < ntiles; j += G::kGroups) {
       const int buf = j % G::kBufs;
       wait(&bars.scales[j % kRing], (j / kRing) & 1);
       const Scales &sc = ring[j % kRing];
       const float4 ks4 = sc.ks, lvs = sc.lvs;
-      float ltop = fmaxf(fmaxf(lvs.x, lvs.y), fmaxf(lvs.z, lvs.w));
       const uint32_t flags = sc.flags;
-      float fs[kSubs] = {f * ks4.x, f * ks4.y, f * ks4.z, f * ks4.w};
+      const float fs[kSubs] = {f * ks4.x, f * ks4.y, f * ks4.z, f * ks4.w}, lv[kSubs] = {lvs.x, lvs.y, lvs.z, lvs.w};
       wait(&bars.s_full[buf], (j / G::kBufs) & 1);
       __syncwarp();
       fence_after();
@@ -469,13 +469,6 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
       // Some row does not see all, or some value scale is NaN: then scores get their scales first, so that a scale
       // (NaN, 0) does not bring back what is not seen, and a NaN value scale reaches what is.
       const bool odd = flags != 0 || tok0 + kTile - 1 > all_see;
-      if (odd) {  // of the pages that the row sees: it would lose bits to larger values behind its last token
-        const float of[kSubs] = {lvs.x, lvs.y, lvs.z, lvs.w};
-        ltop = kNoRef;
-#pragma unroll
-        for (int u = 0; u < kSubs; ++u)
-          if (tok0 + 16 * u <= last) ltop = fmaxf(ltop, of[u]);
-      }
       auto one_by_one = [&](uint32_t (&x)[32], int h) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
@@ -484,7 +477,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
           x[i] = __float_as_uint(tok0 + 32 * h + i <= last && !(flags >> (8 * u) & 1) ? y : -INFINITY);
         }
       };
-      float top = -INFINITY;
+      float top = -INFINITY, topv = -INFINITY;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t x[32];
@@ -500,7 +493,9 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
             t0 = fmaxf(fmaxf(t0, __uint_as_float(y[i])), __uint_as_float(y[i + 1]));
             t1 = fmaxf(fmaxf(t1, __uint_as_float(y[i + 2])), __uint_as_float(y[i + 3]));
           }
-          top = fmaxf(top, odd ? fmaxf(t0, t1) : fmaxf(t0, t1) * fs[2 * h + v]);
+          const float t = odd ? fmaxf(t0, t1) : fmaxf(t0, t1) * fs[2 * h + v];
+          top = fmaxf(top, t);
+          topv = fmaxf(topv, t + lv[2 * h + v]);
         }
         __syncwarp();
       }
@@ -510,13 +505,13 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
           wait(&bars.moved[group ^ 1][quarter], ((j - 1) / G::kGroups) & 1);
           const float2 x = moved[group ^ 1][row];
           mc = x.x;
-          lref = x.y;
+          mv = x.y;
         }
       }
-      if (__any_sync(0xffffffffu, top > mc + kSlack || ltop > lref)) {
-        const float mn = fmaxf(mc, top), ln = fmaxf(lref, ltop), shrink = ex2(mc - mn + (lref - ln));
-        mc = mn;
-        lref = ln;
+      if (__any_sync(0xffffffffu, top > mc + kSlack || topv > mv + kSlack)) {
+        const float mvn = fmaxf(mv, topv), shrink = ex2(mv - mvn);
+        mc = fmaxf(mc, top);
+        mv = mvn;
         if (j > 0) {
           wait(&bars.v_empty[(j - 1) % G::kVStages], ((j - 1) / G::kVStages) & 1);  // the products so far are in O
           __syncwarp();
@@ -533,15 +528,16 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
         }
       }
       if constexpr (G::kGroups > 1) {
-        moved[group][row] = make_float2(mc, lref);
+        moved[group][row] = make_float2(mc, mv);
         bar_arrive(&bars.moved[group][quarter]);
       }
       l *= ex2(m - mc);
       m = mc;
-      // the value scales over the largest, in the exponent
-      const float up2 = kPExp - m;
-      const float lr[kSubs] = {fmaxf(lvs.x - lref, kMinRatio), fmaxf(lvs.y - lref, kMinRatio), fmaxf(lvs.z - lref, kMinRatio),
-                               fmaxf(lvs.w - lref, kMinRatio)};
+      // the value scales, over what brings the largest product to 1, in the exponent: at least so much that weights which
+      // count in the sum do not vanish (as products they do, in fp16)
+      const float up2 = kPExp - m, ratio = mv - m;
+      const float lr[kSubs] = {fmaxf(lv[0] - ratio, kMinRatio), fmaxf(lv[1] - ratio, kMinRatio), fmaxf(lv[2] - ratio, kMinRatio),
+                               fmaxf(lv[3] - ratio, kMinRatio)};
       // the scores once more, half a tile at a time: fewer registers, and more of them for what runs side by side
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -581,7 +577,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
         const float2 x = moved[g_last][row];
         l *= ex2(m - x.x);
         m = x.x;
-        lref = x.y;
+        mv = x.y;
       }
       other[group][row] = l;
       sync_softmax();
@@ -593,7 +589,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
     if (split > 1) {  // a part: fp32, relative to m
       const long long at = part_row(part_no) + row;
       if (group == 0) reinterpret_cast<float2 *>(part_ml(a, (int)gridDim.x - a.whole, D))[at] = make_float2(ntiles > 0 ? m : -INFINITY, l);
-      const float un = ex2(-kPExp), scale = ex2(lref);
+      const float un = ex2(-kPExp), scale = ex2(mv - m);
       constexpr int kRounds = 2, kCols = kShare / kRounds;  // of a group in a round
 #pragma unroll 1
       for (int h = 0; ntiles > 0 && h < kRounds; ++h) {
@@ -620,7 +616,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
         sync_softmax();
       }
     } else {
-    const float inv = l == 0.f ? 0.f : ex2(-kPExp) / l, scale = ex2(lref);  // the smallest scales first would be lost
+    const float inv = l == 0.f ? 0.f : ex2(-kPExp) / l, scale = ex2(mv - m);  // the smallest scales first would be lost
 #pragma unroll 1
     for (int d = group * kShare; d < (group + 1) * kShare; d += 32) {
       uint32_t w[32];
@@ -699,7 +695,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
       if (lane == 0 && j < ntiles) {
         Scales &out = ring[j % kRing];
         reinterpret_cast<float *>(&out.ks)[w] = ks;
-        reinterpret_cast<float *>(&out.lvs)[w] = fmaxf(__log2f(vs), kNoRef);  // fmaxf: of 0, and of a NaN, which the flag tells of
+        reinterpret_cast<float *>(&out.lvs)[w] = fmaxf(__log2f(vs), kNoScale);  // fmaxf: of 0, and of a NaN, which the flag tells of
         reinterpret_cast<uint8_t *>(&out.flags)[w] = (p < 0 ? 1 : 0) | (vs != vs ? 2 : 0);
         bar_arrive(&bars.scales[j % kRing]);
       }

@@ -529,14 +529,15 @@ gdn_status gdn_kv_append(const gdn_attn_shape *shape, const gdn_kv_append_io *io
  *     may overlap in time.
  * What the cache holds behind a row's last token does not reach it, whatever it
  * is, but for its page's scales: a row that sees a token of a page whose k or
- * v scale is NaN gives NaN.  Scales are 0 <= s <= 2^7.  The bytes of a sequence's
- * kv_lens tokens hold no NaN (0x7f, 0xff; gdn_kv_append writes none): with one
- * there, what its rows give, those before that token too, is not specified.
+ * v scale is NaN gives NaN.  Scales are 0 <= s <= 2^7 (below 2^-126 they may count
+ * as 0).  The bytes of a sequence's kv_lens tokens hold no NaN (0x7f, 0xff;
+ * gdn_kv_append writes none): with one there, what its rows give, those before
+ * that token too, is not specified.
  * bf16 io: products on the tensor cores, of the bytes themselves, of q (for many
  * rows to within 2^-17 of the largest of its row and head) and of p rounded to
  * fp16; scores, softmax and sums in fp32.  p has its page's value scale with it
- * there: 11 bits down to 2^-25 of the largest weight times scale that the row
- * has seen, and what is smaller to within 2^-36 of that.  fp32 io: fp32
+ * there: 11 bits down to 2^-25 of the largest product of a weight and its scale that
+ * the row has seen, and what is smaller to within 2^-36 of that.  fp32 io: fp32
  * throughout.  A NaN or infinity in a head of q makes that row and head NaN.
  * max_new and max_kv choose how the call runs: a few rows (new tokens x Hq / Hk) of
  * each sequence and key head side by side, or tiles of 128 rows.  A batch of
