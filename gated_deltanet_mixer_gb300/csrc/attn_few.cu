@@ -257,14 +257,6 @@ __device__ __forceinline__ float2 *part_ml(void *ws, int slots, int slot, int ro
   return reinterpret_cast<float2 *>(static_cast<float *>(ws) + (long long)slots * rows * D) + (long long)slot * rows;
 }
 
-__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w, int high) {
-  uint32_t o;
-  if (high)
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(o) : "r"(w));
-  else
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(o) : "r"(w));
-  return o;
-}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -275,11 +267,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -846,63 +833,63 @@ __global__ void __launch_bounds__(kJoinThreads) attn_few_join(const AttnArgs a, 
   if (c0 == c1) return;  // in one range: written already
   const int hk = unit / q.tiles, first = unit % q.tiles * RT, rows = min(RT, q.s.n * a.r - first);
   for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-  const int rr = first + row;
-  const auto slot_of = [&](int c) { return 2 * c + (c == c0 ? 1 : 0); };  // its first part starts it
-  float m = kNone, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  // Each side with a maximum of its own; 4 parts' loads in flight.
+    const int rr = first + row;
+    const auto slot_of = [&](int c) { return 2 * c + (c == c0 ? 1 : 0); };  // its first part starts it
+    float m = kNone, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    // Each side with a maximum of its own; 4 parts' loads in flight.
 #pragma unroll 1
-  for (int c = c0 + side; c <= c1; c += 4 * kSide) {
-    float2 ml[4];
-    float4 v[4];
+    for (int c = c0 + side; c <= c1; c += 4 * kSide) {
+      float2 ml[4];
+      float4 v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int cu = c + u * kSide;
-      ml[u] = make_float2(kNone, 0.f);
-      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (cu <= c1) {
-        ml[u] = part_ml(a.ws, 2 * parts, slot_of(cu), RT, D)[row];
-        v[u] = *reinterpret_cast<const float4 *>(part_o(a.ws, slot_of(cu), RT, D) + row * D + 4 * col);
+      for (int u = 0; u < 4; ++u) {
+        const int cu = c + u * kSide;
+        ml[u] = make_float2(kNone, 0.f);
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (cu <= c1) {
+          ml[u] = part_ml(a.ws, 2 * parts, slot_of(cu), RT, D)[row];
+          v[u] = *reinterpret_cast<const float4 *>(part_o(a.ws, slot_of(cu), RT, D) + row * D + 4 * col);
+        }
+      }
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) mn = fmaxf(mn, ml[u].x);
+      const float w0 = ex2(m - mn);
+      l *= w0;
+      o.x *= w0, o.y *= w0, o.z *= w0, o.w *= w0;
+      m = mn;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float w = ex2(ml[u].x - mn);
+        l += w * ml[u].y;
+        o.x += w * v[u].x, o.y += w * v[u].y, o.z += w * v[u].z, o.w += w * v[u].w;
       }
     }
-    float mn = m;
+    if (col == 0) side_m[side] = m;
+    __syncthreads();
+    float top = kNone;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) mn = fmaxf(mn, ml[u].x);
-    const float w0 = ex2(m - mn);
-    l *= w0;
-    o.x *= w0, o.y *= w0, o.z *= w0, o.w *= w0;
-    m = mn;
+    for (int u = 0; u < kSide; ++u) top = fmaxf(top, side_m[u]);
+    const float w = ex2(m - top);
+    sums[side][col] = make_float4(o.x * w, o.y * w, o.z * w, o.w * w);
+    if (col == 0) side_l[side] = l * w;
+    __syncthreads();
+    if (side == 0) {
+      float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
+      float ls = 0.f;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float w = ex2(ml[u].x - mn);
-      l += w * ml[u].y;
-      o.x += w * v[u].x, o.y += w * v[u].y, o.z += w * v[u].z, o.w += w * v[u].w;
+      for (int u = 0; u < kSide; ++u) {
+        const float4 v = sums[u][col];
+        all.x += v.x, all.y += v.y, all.z += v.z, all.w += v.w;
+        ls += side_l[u];
+      }
+      const float inv = ls == 0.f ? 0.f : 1.f / ls;
+      __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.o) + (long long)(q.s.row0 + rr / a.r) * a.ldo +
+                                 (long long)(hk * a.r + rr % a.r) * D + 4 * col;
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(all.x * inv, all.y * inv), pack_bf16(all.z * inv, all.w * inv));
     }
-  }
-  if (col == 0) side_m[side] = m;
-  __syncthreads();
-  float top = kNone;
-#pragma unroll
-  for (int u = 0; u < kSide; ++u) top = fmaxf(top, side_m[u]);
-  const float w = ex2(m - top);
-  sums[side][col] = make_float4(o.x * w, o.y * w, o.z * w, o.w * w);
-  if (col == 0) side_l[side] = l * w;
-  __syncthreads();
-  if (side == 0) {
-    float4 all = make_float4(0.f, 0.f, 0.f, 0.f);
-    float ls = 0.f;
-#pragma unroll
-    for (int u = 0; u < kSide; ++u) {
-      const float4 v = sums[u][col];
-      all.x += v.x, all.y += v.y, all.z += v.z, all.w += v.w;
-      ls += side_l[u];
-    }
-    const float inv = ls == 0.f ? 0.f : 1.f / ls;
-    __nv_bfloat16 *const dst = static_cast<__nv_bfloat16 *>(a.o) + (long long)(q.s.row0 + rr / a.r) * a.ldo +
-                               (long long)(hk * a.r + rr % a.r) * D + 4 * col;
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(all.x * inv, all.y * inv), pack_bf16(all.z * inv, all.w * inv));
-  }
-  __syncthreads();
+    __syncthreads();
   }
 }
 

@@ -108,11 +108,6 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint32_t a_lo, uint32
 __device__ __forceinline__ void bar_arrive(uint64_t *bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __half2 t = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t *>(&t);
@@ -136,14 +131,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 r;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(w));
   return r;
-}
-__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w, int high) {
-  uint32_t o;
-  if (high)
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(o) : "r"(w));
-  else
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(o) : "r"(w));
-  return o;
 }
 
 // 16-byte chunk `ch` of a row of q or o in shared memory, turned so that neither rows nor chunks side by side share banks.
@@ -616,29 +603,29 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
         sync_softmax();
       }
     } else {
-    const float inv = l == 0.f ? 0.f : ex2(-kPExp) / l, scale = ex2(mv - m);  // the smallest scales first would be lost
+      const float inv = l == 0.f ? 0.f : ex2(-kPExp) / l, scale = ex2(mv - m);  // the smallest scales first would be lost
 #pragma unroll 1
-    for (int d = group * kShare; d < (group + 1) * kShare; d += 32) {
-      uint32_t w[32];
-      __syncwarp();
-      tmem_ld32_nw(lanes + G::kO + d, w);
-      tmem_wait_ld();
+      for (int d = group * kShare; d < (group + 1) * kShare; d += 32) {
+        uint32_t w[32];
+        __syncwarp();
+        tmem_ld32_nw(lanes + G::kO + d, w);
+        tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) {
-        uint32_t o[4];
+        for (int i = 0; i < 32; i += 8) {
+          uint32_t o[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          o[k] = ntiles > 0 ? pack_bf16(__uint_as_float(w[i + 2 * k]) * inv * scale, __uint_as_float(w[i + 2 * k + 1]) * inv * scale) : 0u;
-        *reinterpret_cast<uint4 *>(stage + row_at<D>(row, (d + i) / 8)) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int k = 0; k < 4; ++k)
+            o[k] = ntiles > 0 ? pack_bf16(__uint_as_float(w[i + 2 * k]) * inv * scale, __uint_as_float(w[i + 2 * k + 1]) * inv * scale) : 0u;
+          *reinterpret_cast<uint4 *>(stage + row_at<D>(row, (d + i) / 8)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
       }
-    }
-    sync_softmax();
+      sync_softmax();
 #pragma unroll 8
-    for (int x = tid; x < count * kChunks; x += 128 * G::kGroups) {
-      const int rw = x / kChunks, ch = x % kChunks;
-      *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + row_o[rw] + ch * 8) =
-          *reinterpret_cast<const uint4 *>(stage + row_at<D>(rw, ch));
-    }
+      for (int x = tid; x < count * kChunks; x += 128 * G::kGroups) {
+        const int rw = x / kChunks, ch = x % kChunks;
+        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + row_o[rw] + ch * 8) =
+            *reinterpret_cast<const uint4 *>(stage + row_at<D>(rw, ch));
+      }
     }
     fence_before();
   } else if (warp < G::kKeyWarp) {

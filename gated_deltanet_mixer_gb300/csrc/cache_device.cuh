@@ -92,9 +92,25 @@ __device__ __forceinline__ float2 e4m3_to_float2(uint32_t pair) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)pair, __NV_E4M3);
   return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
+// Two of a word's four e4m3 bytes, the lower or the upper ones, as fp16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w, int upper) {
+  uint32_t o;
+  if (upper)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(o) : "r"(w));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(o) : "r"(w));
+  return o;
+}
 // Two floats as e4m3 bytes, to nearest even, saturated to +-448.
 __device__ __forceinline__ uint32_t float2_to_e4m3(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+// 2^x to about 2^-22, 0 below 2^-126.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // V consecutive elements (16 bytes) of an io tensor as floats.
