@@ -592,9 +592,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int last = gone >> u & 1 ? -1 : last_of(j, e);
-              if (tok0 + 16 * u + in0 > last) y[u][j][e] = -INFINITY;
-              if (tok0 + 16 * u + in1 > last) y[u][j][2 + e] = -INFINITY;
+              y[u][j][e] = tok0 + 16 * u + in0 > last ? -INFINITY : y[u][j][e];
+              y[u][j][2 + e] = tok0 + 16 * u + in1 > last ? -INFINITY : y[u][j][2 + e];
             }
+        __syncwarp();
       }
       float top[NT][2], topv[NT][2], high = -INFINITY;
 #pragma unroll
@@ -649,8 +650,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
           for (int e = 0; e < 4; ++e) {
             const float w = ex2(y[u][j][e] - m[j][e & 1]);
             l[j][e & 1] += w;
-            pp[e] = w * pv[e & 1];
-            if (masked && y[u][j][e] == -INFINITY) pp[e] = 0.f;  // whatever the scale is
+            pp[e] = masked && y[u][j][e] == -INFINITY ? 0.f : w * pv[e & 1];  // 0 whatever the scale is
           }
           pb[j][0] = transpose8(pack2_sat(pp[0], pp[1]));
           pb[j][1] = transpose8(pack2_sat(pp[2], pp[3]));
@@ -677,10 +677,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksSM) attn_few_kernel(const Att
           if (masked) {  // bytes behind the end, or of no page, may be anything, NaN too
             const int tk[4] = {4 * ga, 4 * gb + 2, 4 * gc + 1, 4 * gd + 3};
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (tok0 + 16 * u + tk[k] >= q.s.kv || (gone >> u & 1))
+            for (int k = 0; k < 4; ++k) {
+              const bool none = tok0 + 16 * u + tk[k] >= q.s.kv || (gone >> u & 1);
 #pragma unroll
-                for (int e = 0; e < W / 4; ++e) w[k][e] = 0;
+              for (int e = 0; e < W / 4; ++e) w[k][e] = none ? 0 : w[k][e];
+            }
+            __syncwarp();  // the lanes' tests are behind: what follows takes the warp
           }
 #pragma unroll
           for (int e = 0; e < W / 4; ++e) {

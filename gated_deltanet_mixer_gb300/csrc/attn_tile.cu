@@ -341,6 +341,7 @@ __global__ void __launch_bounds__(Geo<D>::kThreads, Geo<D>::kBlocks) attn_tile_k
     row_q[tid] = (s.row0 + (long long)tok) * a.ldq + (long long)(hk * a.r + rr - tok * a.r) * D;
     row_o[tid] = (s.row0 + (long long)tok) * a.ldo + (long long)(hk * a.r + rr - tok * a.r) * D;
   }
+  __syncwarp();
   if (warp == G::kProductWarp) tmem_alloc(&tmem_slot, G::kCols);
   fence_before();
   __syncthreads();
