@@ -176,11 +176,14 @@ gdn_status gdn_attn(const gdn_attn_shape *shape, const gdn_attn_io *io, void *st
   if ((st = check_rows(io->q, io->ldq, width, el)) != GDN_OK || (st = check_rows(io->o, io->ldo, width, el)) != GDN_OK) return st;
   if (!aligned_to(io->cu_seqlens, 4) || !aligned_to(io->workspace, 256)) return GDN_ERR_ALIGNMENT;
   const Range ro = range_of(io->o, rows_bytes(rows, io->ldo, width, el)), rw = range_of(io->workspace, io->workspace_bytes);
-  const Range in[] = {range_of(io->q, rows_bytes(rows, io->ldq, width, el)), r.k, r.v, r.ks, r.vs, r.table, r.lens,
-                      range_of(io->cu_seqlens, io->cu_seqlens ? ((size_t)shape->B + 1) * 4 : 0)};
+  const Range rq = range_of(io->q, rows_bytes(rows, io->ldq, width, el));
+  const Range in[] = {r.k, r.v, r.ks, r.vs, r.table, r.lens, range_of(io->cu_seqlens, io->cu_seqlens ? ((size_t)shape->B + 1) * 4 : 0)};
   for (const Range &x : in)
     if (overlap(ro, x) || overlap(rw, x)) return GDN_ERR_ALIAS;
-  if (overlap(ro, rw)) return GDN_ERR_ALIAS;
+  // q and o may be column blocks of one buffer
+  if (overlap(ro, rq) && !(io->ldq == io->ldo && gdn::column_blocks(io->q, width * el, io->o, width * el, (size_t)io->ldo * el)))
+    return GDN_ERR_ALIAS;
+  if (overlap(rw, rq) || overlap(ro, rw)) return GDN_ERR_ALIAS;
   DeviceInfo dev;
   if ((st = device_info(&dev)) != GDN_OK) return st;
   a.seq = seq_args(shape, io->cu_seqlens, &io->cache, dev.err);

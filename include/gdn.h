@@ -519,7 +519,8 @@ gdn_status gdn_kv_append(const gdn_attn_shape *shape, const gdn_kv_append_io *io
  * Attention of the new tokens over the cache (which holds their keys and values
  * already):  o_i = sum_j p_ij v_j,  p_ij = softmax over j of scale q_i . k_j,
  * query head h with key head h / (Hq / Hk).
- *   q, o [rows][ldq], [rows][ldo]   Hq heads of D, io dtype, 16-byte rows
+ *   q, o [rows][ldq], [rows][ldo]   Hq heads of D, io dtype, 16-byte rows; o overlaps
+ *     no input (but q as disjoint column blocks of one buffer: the same stride)
  *   causal != 0: row i at position p sees tokens 0 .. p; 0: it sees all
  *     kv_lens[b] (an encoder's states, say).  A row that sees none gives 0.
  *   scale   0 means 1/sqrt(D)
