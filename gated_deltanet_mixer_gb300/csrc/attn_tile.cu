@@ -901,29 +901,37 @@ static long long tile_blocks(const SeqArgs &q, int r, int Hk) {
   const long long each = ((long long)q.T * r + kRows - 1) / kRows;
   return (q.B > 32 * kSeqsLane ? item_count(q, r, kRows, 1) : !q.cu || q.B == 1 ? each * q.B : (long long)q.T * r / kRows + q.B) * Hk;
 }
+// Parts at most: of the blocks that are left for the last time where blocks fill the GPU, of all where they do not.  None
+// has less than 8 tiles.
+static int slots_of(int D, int num_sms) { return num_sms * (D == 256 ? Geo<256>::kBlocks : Geo<128>::kBlocks); }
+static int most_parts_last(long long blocks, int tiles, int slots) {
+  const int left = (int)(blocks % slots);
+  return blocks > slots && left ? std::min({slots / left, tiles / 8, 32}) : 1;
+}
+static int most_parts_all(long long blocks, int max_kv, int num_sms) {
+  return (int)std::max(1LL, std::min({32LL, (long long)max_kv / (8 * kTile), (num_sms + blocks - 1) / blocks + 1}));
+}
 // Where blocks do not fill the GPU all are cut: a block takes a tile's time per tile and about that of kEnds to start
 // and end, one block to an SM at a time; a part's values cost kPart more, a join kJoin: the number of parts with
 // the least time.  Where they fill it some times over, and all have about the same length (one sequence, or fixed
 // lengths; others' blocks get shorter to the end), those that are left for the last time are cut into as many parts
 // as fill it once more, if the time saved is more than those cost (8192 tokens over 24576, 10.1 times: 3.65 to
-// 3.49 ms; 1.03 times, 2048 tokens, heads of 256: 62 to 53 us).  `most`: the most parts for so many tokens or fewer;
-// none has less than 8 tiles.
-TileCut attn_tile_cut(const SeqArgs &q, int r, int Hk, int D, int max_kv, int num_sms, bool most) {
+// 3.49 ms; 1.03 times, 2048 tokens, heads of 256: 62 to 53 us).
+TileCut attn_tile_cut(const SeqArgs &q, int r, int Hk, int D, int max_kv, int num_sms) {
   constexpr int kEnds = 10, kPart = 8, kJoin = 6;
   const long long blocks = tile_blocks(q, r, Hk);
-  const int tiles = (int)(((long long)max_kv + kTile - 1) / kTile), slots = num_sms * (D == 256 ? Geo<256>::kBlocks : Geo<128>::kBlocks);
+  const int tiles = (int)(((long long)max_kv + kTile - 1) / kTile), slots = slots_of(D, num_sms);
   TileCut c{(int)blocks, (int)blocks, 1};
   if (blocks >= num_sms) {
-    const int left = (int)(blocks % slots), parts = left ? std::min({slots / left, tiles / 8, 32}) : 1;
+    const int parts = most_parts_last(blocks, tiles, slots);
     const bool even = !q.cu || q.B == 1;
-    if (even && blocks > slots && parts > 1 &&
-        (most || tiles + kEnds > (tiles + parts - 1) / parts + kEnds + kPart + kJoin + parts / 4)) {
-      c.whole = (int)blocks - left;
+    if (even && parts > 1 && tiles + kEnds > (tiles + parts - 1) / parts + kEnds + kPart + kJoin + parts / 4) {
+      c.whole = (int)(blocks - blocks % slots);
       c.parts = parts;
     }
     return c;
   }
-  const int up_to = (int)std::max(1LL, std::min({32LL, (long long)max_kv / (8 * kTile), (num_sms + blocks - 1) / blocks + 1}));
+  const int up_to = most_parts_all(blocks, max_kv, num_sms);
   long long least = 0;
   for (int p = 1; p <= up_to; ++p) {
     const long long time =
@@ -933,13 +941,25 @@ TileCut attn_tile_cut(const SeqArgs &q, int r, int Hk, int D, int max_kv, int nu
       c.parts = p;
     }
   }
-  if (most) c.parts = up_to;
   if (c.parts > 1) c.whole = 0;
   return c;
 }
 
 size_t attn_tile_ws_bytes(const TileCut &c, int D) {
   return (size_t)(c.blocks - c.whole) * c.parts * kRows * (D + 2) * sizeof(float);
+}
+
+// Of so many blocks or fewer; from twice the slots on what is left for the last time comes round again.
+size_t attn_tile_room(const SeqArgs &q, int r, int Hk, int D, int max_kv, int num_sms) {
+  const int tiles = (int)(((long long)max_kv + kTile - 1) / kTile), slots = slots_of(D, num_sms);
+  const long long blocks = std::min(tile_blocks(q, r, Hk), 2LL * slots);
+  size_t most = 0;
+  for (long long b = 1; b <= blocks; ++b) {
+    const int parts = b < num_sms ? most_parts_all(b, max_kv, num_sms) : most_parts_last(b, tiles, slots);
+    const long long cut = b < num_sms ? b : b % slots;
+    if (parts > 1) most = std::max(most, attn_tile_ws_bytes(TileCut{(int)cut, 0, parts}, D));
+  }
+  return most;
 }
 
 cudaError_t launch_attn_tile(const AttnArgs &a, cudaStream_t s) {

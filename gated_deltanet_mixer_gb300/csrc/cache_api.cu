@@ -71,9 +71,7 @@ gdn_status check_rows(const void *p, long long ld, long long width, size_t el) {
   return aligned16(p) && ld * el % 16 == 0 ? GDN_OK : GDN_ERR_ALIGNMENT;
 }
 
-// How a call of gdn_attn runs, and the workspace it makes use of.  `room`: the
-// workspace of any call with this shape and max_kv tokens or fewer (a table may
-// allow fewer than the shape says).
+// How a call of gdn_attn runs, and the workspace it makes use of.
 struct AttnPlan {
   int few_rows;  // rows of a tile of attn_few.cu, or 0
   bool tile;     // attn_tile.cu; neither: attn_rows.cu
@@ -81,8 +79,14 @@ struct AttnPlan {
   size_t bytes;
   gdn::TileCut cut;  // attn_tile.cu
 };
-AttnPlan attn_plan(const gdn_attn_shape *s, bool packed, long long rows, int max_kv, int sms, bool room) {
-  const int r = s->Hq / s->Hk, cu = 0;
+const int kPacked = 0;  // stands for offsets where only their being there counts
+gdn::SeqArgs plan_seqs(const gdn_attn_shape *s, bool packed) { return gdn::SeqArgs{s->B, s->T, 0, 0, packed ? &kPacked : nullptr, nullptr, nullptr}; }
+// fp32: ranges of the tokens side by side, enough blocks to fill the GPU twice, none with less than 64 tokens
+int rows_splits(long long blocks, int max_kv, int sms) {
+  return (int)std::max(1LL, std::min({(2LL * sms + blocks - 1) / blocks, (max_kv + 63LL) / 64, 64LL}));
+}
+AttnPlan attn_plan(const gdn_attn_shape *s, bool packed, long long rows, int max_kv, int sms) {
+  const int r = s->Hq / s->Hk;
   AttnPlan p{0, false, 1, 0, {}};
   if (s->io_dtype == GDN_BF16) {
     p.few_rows = gdn::attn_few_rows(s->D, (long long)bound_new(s, packed) * r);
@@ -91,16 +95,36 @@ AttnPlan attn_plan(const gdn_attn_shape *s, bool packed, long long rows, int max
       return p;
     }
     p.tile = true;
-    p.cut = gdn::attn_tile_cut(gdn::SeqArgs{s->B, s->T, 0, 0, packed ? &cu : nullptr, nullptr, nullptr}, r, s->Hk, s->D, max_kv, sms, room);
+    p.cut = gdn::attn_tile_cut(plan_seqs(s, packed), r, s->Hk, s->D, max_kv, sms);
     p.splits = p.cut.parts;
     p.bytes = gdn::attn_tile_ws_bytes(p.cut, s->D);
     return p;
   }
-  // fp32: enough blocks to fill the GPU twice, none with less than 64 tokens
-  const long long blocks = (packed ? rows * r / 16 + s->B : ((long long)s->T * r / 16 + 1) * s->B) * s->Hk;
-  p.splits = (int)std::max(1LL, std::min({(2LL * sms + blocks - 1) / blocks, (max_kv + 63LL) / 64, 64LL}));
+  p.splits = rows_splits((packed ? rows * r / 16 + s->B : ((long long)s->T * r / 16 + 1) * s->B) * s->Hk, max_kv, sms);
   if (p.splits > 1) p.bytes = (size_t)p.splits * rows * s->Hq * (s->D + 2) * sizeof(float);
   return p;
+}
+// The most workspace of this call and of any with these heads and no more sequences, rows, new and cached tokens: what
+// one call uses rises and falls with them, as its parts fill the GPU.
+size_t attn_room(const gdn_attn_shape *s, bool packed, long long rows, int max_kv, int sms) {
+  const int r = s->Hq / s->Hk;
+  size_t most = 0;
+  if (s->io_dtype == GDN_BF16) {
+    bool all_few = true;
+    for (int n = 1, top = bound_new(s, packed); n <= top && all_few; ++n) {
+      const int few = gdn::attn_few_rows(s->D, (long long)n * r);
+      all_few = few > 0;
+      if (few) most = std::max(most, gdn::attn_few_ws_bytes(s->D, few, sms));
+    }
+    return all_few ? most : std::max(most, gdn::attn_tile_room(plan_seqs(s, packed), r, s->Hk, s->D, max_kv, sms));
+  }
+  for (long long n = 1; n <= rows; ++n) {
+    const long long blocks = (n * r + 15) / 16 * s->Hk;  // so many at least, whatever the sequences
+    if (blocks >= 2LL * sms) break;
+    const int splits = rows_splits(blocks, max_kv, sms);
+    if (splits > 1) most = std::max(most, (size_t)(splits * n) * s->Hq * (s->D + 2) * sizeof(float));
+  }
+  return most;
 }
 
 }  // namespace
@@ -143,7 +167,7 @@ size_t gdn_attn_workspace_bytes(const gdn_attn_shape *shape, int packed) {
   DeviceInfo dev;
   if (!shape || check_attn_shape(shape, packed != 0, &rows) != GDN_OK || check_heads(shape) != GDN_OK || device_info(&dev) != GDN_OK)
     return 0;
-  return attn_plan(shape, packed != 0, rows, bound_kv(shape, 1 << 30), dev.sms, true).bytes;
+  return attn_room(shape, packed != 0, rows, bound_kv(shape, 1 << 30), dev.sms);
 }
 
 gdn_status gdn_selftest_attn_form(const gdn_attn_shape *shape, int packed, int workspace, gdn_attn_form *form) {
@@ -154,7 +178,7 @@ gdn_status gdn_selftest_attn_form(const gdn_attn_shape *shape, int packed, int w
   if (st == GDN_OK) st = check_heads(shape);
   if (st == GDN_OK) st = device_info(&dev);
   if (st != GDN_OK) return st;
-  const AttnPlan p = attn_plan(shape, packed != 0, rows, bound_kv(shape, 1 << 30), dev.sms, false);
+  const AttnPlan p = attn_plan(shape, packed != 0, rows, bound_kv(shape, 1 << 30), dev.sms);
   *form = gdn_attn_form{p.few_rows ? GDN_ATTN_FEW : p.tile ? GDN_ATTN_TILE : GDN_ATTN_ROWS, p.few_rows ? p.few_rows : p.tile ? 128 : 16,
                         p.few_rows ? 0 : workspace ? p.splits : 1};
   return GDN_OK;
@@ -195,7 +219,7 @@ gdn_status gdn_attn(const gdn_attn_shape *shape, const gdn_attn_io *io, void *st
   a.ldo = io->ldo;
   a.causal = io->causal != 0;
   a.scale = io->scale != 0.f ? io->scale : 1.0f / std::sqrt((float)shape->D);
-  const AttnPlan plan = attn_plan(shape, packed, rows, a.seq.max_kv, dev.sms, false);
+  const AttnPlan plan = attn_plan(shape, packed, rows, a.seq.max_kv, dev.sms);
   if (io->workspace && plan.bytes) {
     if (io->workspace_bytes < plan.bytes) return GDN_ERR_INVALID_ARG;
     a.ws = io->workspace;

@@ -262,8 +262,9 @@ cudaError_t launch_attn_few(const AttnArgs &a, int rows_tile, int num_sms, cudaS
 struct TileCut {
   int blocks, whole, parts;  // the blocks from number `whole` on in so many parts each
 };
-TileCut attn_tile_cut(const SeqArgs &q, int r, int Hk, int D, int max_kv, int num_sms, bool most);
+TileCut attn_tile_cut(const SeqArgs &q, int r, int Hk, int D, int max_kv, int num_sms);
 size_t attn_tile_ws_bytes(const TileCut &c, int D);
+size_t attn_tile_room(const SeqArgs &q, int r, int Hk, int D, int max_kv, int num_sms);  // of that call and of any smaller one
 cudaError_t launch_attn_tile(const AttnArgs &a, cudaStream_t s);
 
 // Device error bits (the error word is OR-ed).

@@ -648,7 +648,8 @@ def gdn_attn(q, o, kv_lens, block_table, k_cache, v_cache, k_scale, v_scale, *, 
 
 
 def gdn_attn_workspace_bytes(B, T, Hq, Hk, D, *, max_new=0, max_kv=0, packed=True, io_dtype=None):
-    """Workspace bytes of gdn_attn (packed: T is the total token count)."""
+    """Workspace bytes that do for gdn_attn of this shape and of smaller ones
+    (packed: T is the total token count)."""
     sh = gdn_attn_shape(B, T, Hq, Hk, D, GDN_BF16 if io_dtype is None else io_dtype, max_new, max_kv)
     return lib().gdn_attn_workspace_bytes(ctypes.byref(sh), 1 if packed else 0)
 

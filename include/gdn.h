@@ -558,9 +558,12 @@ typedef struct {
 
 gdn_status gdn_attn(const gdn_attn_shape *shape, const gdn_attn_io *io, void *stream);
 
-/* Bytes of workspace of gdn_attn for this shape on the current device (packed as
- * for gdn_linattn_workspace_bytes); 0 where the call uses none or the shape is
- * invalid. */
+/* Bytes of workspace that do for gdn_attn of this shape on the current device (packed
+ * as for gdn_linattn_workspace_bytes), and for every call of the same heads, type and
+ * form, packed or not, with no more sequences, tokens, new tokens (max_new) and tokens in
+ * all (max_kv): sized for the largest batch it serves the smaller ones.  0 where the
+ * shape is invalid or none of these calls uses any.  gdn_attn refuses a workspace that is
+ * smaller than what the call at hand would use. */
 size_t gdn_attn_workspace_bytes(const gdn_attn_shape *shape, int packed);
 
 /* How gdn_attn runs a shape on the current device (packed as above; workspace !=

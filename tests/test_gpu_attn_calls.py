@@ -36,3 +36,34 @@ def test_o_beside_q_in_one_buffer(dt, D, n, ws):
             assert torch.equal(o, apart)
             keep = [i for i in range(3) if i != o_at]
             assert all(torch.equal(one[..., i * Hq * D:(i + 1) * Hq * D], buf[..., i * Hq * D:(i + 1) * Hq * D]) for i in keep)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hk,r", [(1, 1), (2, 8), (1, 24)])
+@pytest.mark.parametrize("packed", [True, False])
+def test_a_workspace_for_the_largest_batch_serves_the_smaller_ones(dt, D, Hk, r, packed):
+    """Sized once: fewer sequences, fewer tokens, shorter tables.  (What a call uses rises and falls with them.)"""
+    B, n, kv = 4, 1500 // max(1, r // 2), 6000
+    cache = R.Cache([kv] * B, Hk, D, 128, device="cuda").fill()
+    Hq = Hk * r
+    io = dict(io_dtype=gdn.GDN_BF16 if dt == BF else gdn.GDN_F32, packed=packed)
+    w = torch.empty(gdn.gdn_attn_workspace_bytes(B, B * n if packed else n, Hq, Hk, D, max_new=n, max_kv=kv, **io), dtype=torch.uint8,
+                    device="cuda")
+    assert w.numel() > 0
+    q = torch.randn(B, n, Hq * D, device="cuda").to(dt)
+    for b in (B, 1, 2):
+        small = R.Cache([kv] * b, Hk, D, 128, device="cuda")
+        small.table, args = cache.table[:b].contiguous(), cache.args()[2:]
+        for m in sorted({n, n - 1, n // 2, n // 3, n // 5, n // 16 or 1, 40, 17, 5, 2, 1}):
+            for top in (kv, 3000, 700, 128):
+                if m > top:
+                    continue
+                x = q[:b, :m].reshape(b * m, -1) if packed else q[:b, :m].contiguous()
+                o = torch.full_like(x, math.nan)
+                kw = dict(cu_seqlens=offsets([m] * b), max_new=m) if packed else {}
+                gdn.gdn_attn(x, o, torch.full((b,), top, dtype=torch.int32, device="cuda"), small.table, *args, Hq=Hq, max_kv=top,
+                             workspace=w, **kw)
+                assert not bool(o.isnan().any())
+                assert gdn.gdn_attn_workspace_bytes(b, b * m if packed else m, Hq, Hk, D, max_new=m if packed else 0, max_kv=top, **io) <= w.numel()
+    ok()
