@@ -1,8 +1,9 @@
 // rope.cu -- rotary positions: the pair (a, b) of index i at position p becomes
 //   m (a cos x - b sin x, b cos x + a sin x),   x = p f_i.
-// The angle is kept as a 64-bit fraction of a turn, p * turns_i modulo 2^64: an
-// integer product has no error that grows with p, and its upper 32 bits are the
-// angle in [-pi, pi) to 2^-32 of a turn for sincospi.
+// The angle is kept as a 64-bit fraction of a turn, p * turns_i modulo 2^64: the
+// integer product rounds nothing, however large p is.  Its upper 32 bits, in fp32
+// half turns for sincospi, are within 2^-26 of a turn (2^-24 pi / 2 of the pair's
+// size: what other fp32 roundings of a turn come to).
 //
 // Bound by memory traffic (in place that of the rotated elements alone; 8192 tokens,
 // 28 heads, 64 of 256 elements, 59 MB: 11.7 us, 5.0 TB/s) and by instruction issue.  A block
