@@ -135,10 +135,14 @@ cudaError_t launch_kv_pages(const PagesArgs &a, cudaStream_t s) {
   const size_t smem = (size_t)a.B * 3 * sizeof(int);
   cudaError_t e = allow_smem<PagesTag>(kv_pages_kernel, (size_t)kPagesMaxB * 3 * sizeof(int));
   if (e != cudaSuccess) return e;
-  const bool small = a.B <= 256 && a.max_tokens <= 1024;
+  // Threads and CTAs cost a start, and save on the scan and the stores (us in a graph, requests / tokens: one CTA of 256
+  // threads, 8 of 512, 8 of 1024):  64/64 3.2, 3.5, 4.2;  256/256 3.5, 3.9, 4.5;  256/843 6.2, 4.0, 4.9;  64/2950 9.7, 3.7,
+  // 4.5;  1024/3470 16, 5.1, 5.3;  1/18995 23, 4.3, 4.7;  512/26431 75, 8.8, 8.0;  4096/4096 27, 10.1, 10.0;
+  // 16384/16384 107, 32, 27.
+  const bool small = a.B <= 256 && a.max_tokens <= 256, large = a.B > 4096 || a.max_tokens > 20480;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.B <= 1024 && a.max_tokens <= 4096 ? 1 : 8);
-  cfg.blockDim = dim3(small ? 256 : 1024);
+  cfg.gridDim = dim3(small ? 1 : 8);
+  cfg.blockDim = dim3(small ? 256 : large ? 1024 : 512);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr{};
