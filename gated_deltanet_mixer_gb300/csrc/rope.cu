@@ -1,9 +1,9 @@
 // rope.cu -- rotary positions: the pair (a, b) of index i at position p becomes
 //   m (a cos x - b sin x, b cos x + a sin x),   x = p f_i.
 // The angle is kept as a 64-bit fraction of a turn, p * turns_i modulo 2^64: the
-// integer product rounds nothing, however large p is.  Its upper 32 bits, in fp32
-// half turns for sincospi, are within 2^-26 of a turn (2^-24 pi / 2 of the pair's
-// size: what other fp32 roundings of a turn come to).
+// integer product rounds nothing, however large p is.  What it has beyond the
+// nearest quarter, an eighth of a turn at most, goes through fp32 to sincospi: within
+// 2^-28 of a turn.
 //
 // Bound by memory traffic (in place that of the rotated elements alone; 8192 tokens,
 // 28 heads, 64 of 256 elements, 59 MB: 11.7 us, 5.0 TB/s) and by instruction issue.  A block
@@ -85,9 +85,11 @@ __global__ void __launch_bounds__(kThreads)
     const unsigned long long f = turns.at[i];
     for (int t = threadIdx.x / wide; t < nt; t += kThreads / wide) {
       const unsigned long long x = (unsigned long long)(long long)a.positions[t0 + t] * f;
+      const uint32_t quarter = (uint32_t)((x + (1ull << 61)) >> 62);  // the nearest quarter of a turn; what is left is small
       float s, c;
-      sincospif((float)(int)((x + (1ull << 31)) >> 32) * 0x1p-31f, &s, &c);
-      turn[t * pairs + i] = make_float2(a.m * c, a.m * a.sign * s);
+      sincospif((float)(int)((x - ((unsigned long long)quarter << 62) + (1ull << 31)) >> 32) * 0x1p-31f, &s, &c);
+      const float c1 = quarter & 1 ? -s : c, s1 = quarter & 1 ? c : s, m = quarter & 2 ? -a.m : a.m;
+      turn[t * pairs + i] = make_float2(m * c1, m * a.sign * s1);
     }
   }
   __syncthreads();

@@ -538,8 +538,10 @@ gdn_status gdn_kv_append(const gdn_attn_shape *shape, const gdn_kv_append_io *io
  * rows to within 2^-17 of the largest of its row and head) and of p rounded to
  * fp16; scores, softmax and sums in fp32.  p has its page's value scale with it
  * there: 11 bits down to 2^-25 of the largest product of a weight and its scale that
- * the row has seen, and what is smaller to within 2^-36 of that.  fp32 io: fp32
- * throughout.  A NaN or infinity in a head of q makes that row and head NaN.
+ * the row has seen, and what is smaller to within 2^-36 of that.  Weights below
+ * 2^-120 of the row's largest, and rows whose products are all below 2^-120 of it, may
+ * count as 0.  fp32 io: fp32 throughout.  A NaN or infinity in a head of q makes
+ * that row and head NaN.
  * max_new and max_kv choose how the call runs: a few rows (new tokens x Hq / Hk) of
  * each sequence and key head side by side, or tiles of 128 rows.  A batch of
  * prompts and of single tokens is faster as two calls.

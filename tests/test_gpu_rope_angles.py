@@ -11,10 +11,11 @@ BF, F32 = torch.bfloat16, torch.float32
 
 
 def turned(x, pos, plan, D, inverse=False, bits=None):
-    """(y, bound) of x [tokens, heads * D] in 64 bits.  The angle is p * turns modulo 2^64, of a turn; as fp32 in half turns,
-    at most 1, it is off by 2^-25: pi 2^-25.  Its sine and cosine are off by 2 steps of 2^-24, m times them by half a step;
-    two products and a sum round by half a step of the pair's size h at most, each: with |a| + |b| <= sqrt(2) h,
-        (pi / 2 + 2 sqrt(2) + sqrt(2) / 2 + 1) 2^-24 m h < 7 2^-24 m h,  8 with the higher orders,
+    """(y, bound) of x [tokens, heads * D] in 64 bits.  The angle is p * turns modulo 2^64, of a turn; beyond the nearest
+    quarter, at most 2^-3 of a turn, as fp32 it is off by 2^-28: pi 2^-27.  Its sine and cosine are off by 2 steps of 2^-24,
+    m times them by half a step; two products and a sum round by half a step of the pair's size h at most, each: with
+    |a| + |b| <= sqrt(2) h,
+        (pi / 8 + 2 sqrt(2) + sqrt(2) / 2 + 1) 2^-24 m h < 5 2^-24 m h,  6 with the higher orders,
     and one rounding to the type.  bits: an angle of so many bits instead, for the bound's own test."""
     n = plan.rot // 2
     f = torch.tensor([plan.turns[i] - (1 << 64 if plan.turns[i] >> 63 else 0) for i in range(n)], dtype=torch.int64, device=x.device)
@@ -27,7 +28,7 @@ def turned(x, pos, plan, D, inverse=False, bits=None):
     ia = torch.arange(n) if plan.layout == 0 else torch.arange(0, 2 * n, 2)
     ib = ia + (n if plan.layout == 0 else 1)
     u, w = y[..., ia], y[..., ib]
-    h = 8 * 2.0 ** -24 * plan.m * torch.hypot(u, w)
+    h = 6 * 2.0 ** -24 * plan.m * torch.hypot(u, w)
     y[..., ia], y[..., ib] = u * c - w * s, w * c + u * s
     bound = torch.zeros_like(y)
     bound[..., ia], bound[..., ib] = h, h
