@@ -14,7 +14,8 @@ Per step, for n_b new tokens of each of B requests, x [tokens, hidden] of the re
     f         = silu(x W_g^T) (x W_u^T)                                  gdn_linear_ex, gated
     x        += f W_d^T          added in place                          gdn_linear_ex
 
-(The norms in front of the two halves are left out: they are the caller's.)  Lengths and tables stay on the GPU: a step of
+(The norms in front of the two halves, those of q and k that such layers have ahead of the rotation, and the gate on o
+are left out: the library has no call for them.)  Lengths and tables stay on the GPU: a step of
 single tokens can be captured into a graph and replayed.  Run as a program it takes prompts of ragged lengths, then
 single tokens from a captured graph, and checks them against the same tokens taken as one prompt.
 """

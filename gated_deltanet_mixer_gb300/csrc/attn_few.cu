@@ -2,7 +2,7 @@
 // new token of a sequence, or a handful, times the query heads of a key head.
 //
 // Bound by the cache's bytes, which the rows of a key head share (64 x 1 token over
-// 8192, 24/4 heads of 256: 171 us, 6.3 TB/s; 16 x 4 tokens, ragged, 32/8 heads of 128,
+// 8192, 24/4 heads of 256: 170 us, 6.3 TB/s; 16 x 4 tokens, ragged, 32/8 heads of 128,
 // 87 MB: 33 us, of which some 10 are a block's start, end and the join).  The products
 // run transposed, so that the cache is the operand with 16 rows and the queries
 // the one with 8 columns:  S^T = K q^T  and  O^T = V^T P^T  by
@@ -70,8 +70,8 @@ struct Geo {
   static constexpr int kQ = (D / 16) * NT * 256;
   static constexpr int kBytes = kRing + kQ;
   // What going on to another unit costs a block, in slabs (some 7 us): counted with the unit's own where the work is
-  // cut.  32 x 1 token over 200 to 15,000, 4 heads of 256: 47 us, with half of it 51, without 67; heads of 64 26, with
-  // twice as much 26.3, without 37; 300 x 1 over 500 the same but for heads of 128: 50, without 47.
+  // cut.  32 x 1 token over 200 to 15,000, 4 heads of 256: 47 us, with half of it 51, without 67; heads of 64 25, with
+  // twice as much 26.3, without 37; 300 x 1 over 500 the same but for heads of 128, which lose: 49.5, without 47.
   static constexpr int kStart = D == 64 ? 32 / kSub : 16;
 };
 

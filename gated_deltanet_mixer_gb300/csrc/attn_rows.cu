@@ -5,9 +5,11 @@
 // A block takes 16 rows (query tokens x the heads of one key head) and a range
 // of tokens; tiles of 32 tokens become floats in shared memory, where a lane is
 // a token for the scores and a set of columns for the values, and each value
-// read serves the 4 rows of its warp.  Bound by fp32 multiply-adds and the
-// loads from shared memory that feed them.  Where rows are few, ranges of the
-// tokens run side by side and a second launch joins them.
+// read serves the 4 rows of its warp.  Bound by the loads from shared memory
+// and the shuffles that feed the multiply-adds: 64 tokens over 2000, 8/2 heads of 64,
+// 128 and 256 take 47, 70 and 111 us, of which the multiply-adds alone are 3.4, 6.7 and 13
+// at the fp32 rate.  Where rows are few, ranges of the tokens run side by side and a
+// second launch joins them (1 token over 5000: 29, 39 and 53 us).
 #include "cache_device.cuh"
 #include "tma_host.h"
 

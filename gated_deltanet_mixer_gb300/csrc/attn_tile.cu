@@ -16,10 +16,10 @@
 // value scale, apart from that of the weights alone: in fp16 p has 11 bits down to 2^-25
 // of the row's largest product, and is within 2^-36 of it below that.
 //
-// Bound by the products for heads of 256 (8192 tokens over 24576, 24/4 heads: 3.49
-// ms, 1.66 PFLOP/s of bf16's 1.7 sustained; the products of q's two parts are twice those
-// of one, at twice the rate), by the softmax's instructions for narrower ones (2048 over 8192,
-// 32/4 heads of 128: 266 us, 1.16 PFLOP/s).
+// Bound by the products for heads of 256 (8192 tokens over 24576, 24/4 heads: 3.3 to
+// 3.6 ms as the power cap leaves it, 1.6 to 1.75 PFLOP/s of bf16's 1.7 sustained; the products of
+// q's two parts are twice those of one, at twice the rate), by the softmax's instructions for
+// narrower ones (2048 over 8192, 32/4 heads of 128: 260 us, 1.19 PFLOP/s; of 64: 235 us, 0.66).
 //
 // Warps: 4 for the softmax (thread = row), 4 for the values, one for the keys
 // (TMA) and one for the products.  For a tile of 64 tokens and D = 256 the products

@@ -6,10 +6,12 @@
 // those that become subnormal are rounded a second time.
 //
 // Bound by memory traffic, of which few warps with a page each in flight do not
-// reach all: 12 prompts (16,000 tokens, 4 heads of 256, 88 MB) take 19 us, 4.7 TB/s.  A warp
+// reach all: 12 prompts (14,000 tokens, 4 heads of 256, 88 MB) take 19 us, 4.6 TB/s.  A warp
 // takes a page and head of k or v, 8 elements to a lane and step; what 16 steps
 // read (a page of 16 tokens at D = 256) stays in registers between the maximum and
-// the rounding.
+// the rounding.  Larger pages are read twice: with 32, 64 and 128 tokens to a page the
+// prompts take 24, 25 and 33 us (fp32 33 with 16, then 39, 42 and 51).  Every block looks
+// at all offsets, which many sequences feel: 4096 of a token each, 2 heads of 64, 94 us.
 #include <algorithm>
 
 #include "cache_device.cuh"

@@ -6,7 +6,8 @@
 // 2^-28 of a turn.
 //
 // Bound by memory traffic (in place that of the rotated elements alone; 8192 tokens,
-// 28 heads, 64 of 256 elements, 59 MB: 11.7 us, 5.0 TB/s) and by instruction issue.  A block
+// 28 heads, 64 of 256 elements, 59 MB: 12 us, 13 where they come from memory, 4.5 to 4.9 TB/s) and
+// by instruction issue (49% active).  A block
 // first forms the cosines and sines of its tokens, which all heads share; then
 // its threads take items of 16 bytes (or, where an address or a width does not
 // allow that, single pairs), two at a time, the first two asked for before that.

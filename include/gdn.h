@@ -503,8 +503,8 @@ typedef struct {
  *   A NaN or infinity among a page's new tokens makes the scale of that page
  *   and head NaN (the new bytes are 0).
  *   Rows of a page behind the sequence's end keep what they hold.
- *   A page that is written belongs to one sequence: where the table gives it to
- *   two, what the two write there is not specified.
+ *   A page that is written belongs to one sequence, once: where the table gives
+ *   it to two, or twice to one, what is written there is not specified.
  */
 typedef struct {
   const void *k, *v;
